@@ -415,7 +415,9 @@ kda_status_t kda_read_device_status(void *workspace, void *stream);
 #define KDA_DEVICE_ERR_TIMEOUT 2u /* a bounded device-side wait expired                   */
 #define KDA_DEVICE_ERR_DECAY 4u   /* a chunk's cumulative log-decay left the supported range */
 #define KDA_DEVICE_ERR_RANGE 8u   /* a value held in fp16 left the fp16 range (two-kernel path) */
-#define KDA_DEVICE_ERR_SLOT 16u   /* a state-pool slot index out of range (the _slots calls)   */
+#define KDA_DEVICE_ERR_SLOT 16u   /* a state-pool or latent-cache slot index out of range      */
+#define KDA_DEVICE_ERR_POSITION 32u /* a position outside the rotation table (latent append)   */
+#define KDA_DEVICE_ERR_PAGE 64u   /* a page index outside the latent cache (latent decode)     */
 kda_status_t kda_prefill_no_alloc(const void *q, const void *k, const void *v,
                                   const float *log_alpha, const float *beta,
                                   const int32_t *cu_seqlens, int32_t num_seqs,
@@ -502,6 +504,131 @@ int32_t kda_prefill_host_segments(const int32_t *cu_seqlens, int32_t num_seqs, i
  * Synchronises `stream`.  KDA_ERR_TIMEOUT if a bounded wait gave up.
  */
 kda_status_t kda_diag_tensor_phases(int32_t pass, int32_t reps, void *workspace, void *stream, double *tflops);
+
+/*
+ * ---------------------------------------------------------------------------------
+ * Latent attention: the layers that a hybrid model runs between its KDA layers ("K3
+ * attention, three-piece set", the three KDA layers to one latent-attention layer
+ * stack).  Keys and values of all heads come from one latent vector of
+ * KDA_LATENT_DIM channels per token, plus one key of KDA_LATENT_PE_DIM position
+ * channels shared by the heads, which is rotated by the token's position or, where
+ * the KDA layers carry the position (NoPE), left as it is.  Three calls:
+ *
+ *   kda_latent_append   the tokens' rows into the paged cache (normalised latent,
+ *                       rotated position key), and the rotation of the queries
+ *   kda_latent_decode   one token per sequence against the cache, absorbed: the
+ *                       queries are already multiplied by the up-projection of the
+ *                       keys, the result is still to be multiplied by that of the
+ *                       values
+ *   kda_latent_prefill  packed prompts, expanded: keys and values per head
+ *
+ * The projections themselves are plain matrix products and the caller's.  All of
+ * them take bf16 or fp32 tensors (kda_dtype_t); bf16 attention runs on the tensor
+ * cores, fp32 on the CUDA cores with exact fp32 products.  Scores, softmax
+ * statistics and sums are fp32.  Strides are in elements and a multiple of 16 bytes,
+ * the last dimension is contiguous, bases are 16-byte aligned.  device_errors is NULL
+ * or a device uint32 that receives KDA_DEVICE_ERR_* bits (or-ed, never cleared).
+ */
+#define KDA_LATENT_DIM 512
+#define KDA_LATENT_PE_DIM 64
+#define KDA_LATENT_HEAD_DIM 128 /* expanded: key channels without position, and value channels */
+
+/* Options of the latent calls (other bits: KDA_ERR_INVALID_ARG). */
+#define KDA_LATENT_INTERLEAVED 1u /* append: rotate the pairs (2i, 2i + 1) instead of (i, i + 32) */
+#define KDA_LATENT_FULL 2u        /* prefill: every query sees every key of its sequence (not causal) */
+
+/*
+ * y = w x / sqrt(mean(x^2) + eps) over the latent channels, rounded once; the position
+ * key rotated; both to cache row slots[t].  In the same launch the queries' position
+ * channels are rotated, into place or elsewhere (the absorbed query of
+ * kda_latent_decode, the expanded one of kda_latent_prefill).
+ *
+ *  latent       [num_tokens, d_latent], row stride latent_stride
+ *  k_pe         [num_tokens, d_pe], row stride k_pe_stride (both may be parts of one
+ *               joint projection's rows)
+ *  norm_weight  [d_latent] dtype, or NULL: the latent is stored as it is
+ *  cos_sin      [num_positions, d_pe] fp32, the cosines of the d_pe / 2 pairs' angles
+ *               and then their sines, or NULL: no rotation
+ *  positions    [num_tokens] int32 device (ignored without cos_sin).  A token whose
+ *               position is outside [0, num_positions) is left out: nothing of it is
+ *               written (KDA_DEVICE_ERR_POSITION)
+ *  q_pe, q_pe_out  [num_tokens, num_heads, d_pe] with token and head strides; both or
+ *               neither; may be the same rows
+ *  latent_out, k_pe_out  the normalised latent and the rotated key again, for the
+ *               expanded form's projections; each may be NULL or its input's rows
+ *  cache        [num_slots, d_latent + d_pe] (pages of any size, one after the other)
+ *  slots        [num_tokens] int32 device, distinct; -1: the row is not cached.  Others
+ *               outside [0, num_slots): not cached, KDA_DEVICE_ERR_SLOT
+ */
+kda_status_t kda_latent_append(const void *latent, int64_t latent_stride, const void *k_pe, int64_t k_pe_stride,
+                               const void *norm_weight, float norm_eps, const float *cos_sin,
+                               int32_t num_positions, const int32_t *positions, const void *q_pe,
+                               int64_t q_token_stride, int64_t q_head_stride, void *q_pe_out,
+                               int64_t out_token_stride, int64_t out_head_stride, void *latent_out,
+                               int64_t latent_out_stride, void *k_pe_out, int64_t k_pe_out_stride,
+                               int32_t num_tokens, int32_t num_heads, int32_t d_latent, int32_t d_pe,
+                               kda_dtype_t dtype, void *cache, int64_t num_slots, const int32_t *slots,
+                               uint32_t *device_errors, void *stream, uint32_t flags);
+
+/*
+ * s_bhj = scale q_bh . cache_bj over all d_latent + d_pe channels, j < seq_lens[b];
+ * o_bh = sum_j softmax_j(s_bh) cache_bj[:d_latent];  lse_bh = log(sum_j exp(s_bhj)).
+ * A sequence of length 0 gives o = 0, lse = -inf.  What cache rows past a sequence's
+ * end hold, NaN included, does not matter.
+ *
+ *  q           [batch, num_heads, d_latent + d_pe], batch and head strides
+ *  cache       [num_pages, page_size, d_latent + d_pe] contiguous; page_size a positive
+ *              multiple of 8
+ *  page_table  [batch, max_pages] int32 device, row stride page_table_stride; position j of
+ *              sequence b is row j % page_size of page page_table[b][j / page_size].
+ *              Entries past a sequence's end are not read.  A page outside
+ *              [0, num_pages) reads as zero rows (KDA_DEVICE_ERR_PAGE)
+ *  seq_lens    [batch] int32 device; lengths below 0 or over max_pages * page_size are
+ *              held to that range (KDA_DEVICE_ERR_SEQLENS)
+ *  o           [batch, num_heads, d_latent] contiguous
+ *  lse         [batch, num_heads] fp32 (natural log), or NULL
+ *  workspace   256-byte aligned, kda_latent_decode_workspace_size(num_heads, dtype) bytes,
+ *              at most KDA_LATENT_DECODE_WORKSPACE_MAX whatever the problem; needs no
+ *              initialisation.  Calls that share it must be ordered
+ * The cache rows are split evenly over the GPU whatever the lengths are, which stay on
+ * the device: a captured call replays with new lengths, pages and contents.  For given
+ * lengths the result is the same bits on every call.
+ */
+#define KDA_LATENT_DECODE_WORKSPACE_MAX 50331648
+size_t kda_latent_decode_workspace_size(int32_t num_heads, kda_dtype_t dtype);
+kda_status_t kda_latent_decode(const void *q, int64_t q_batch_stride, int64_t q_head_stride, const void *cache,
+                               int64_t num_pages, int32_t page_size, const int32_t *page_table,
+                               int64_t page_table_stride, int32_t max_pages, const int32_t *seq_lens,
+                               int32_t batch, int32_t num_heads, int32_t d_latent, int32_t d_pe,
+                               kda_dtype_t dtype, float scale, void *o, float *lse, void *workspace,
+                               size_t workspace_bytes, uint32_t *device_errors, void *stream);
+
+/*
+ * Packed sequences of queries against packed sequences of keys and values:
+ * s_ihj = scale q_ih . [k_nope_jh, k_pe_j];  o_ih = sum_j softmax_j(s_ih) v_jh;  lse as
+ * above.  A sequence of lq queries and lk keys is aligned at its end: query i sees the
+ * keys j <= i + lk - lq, so lk > lq is a chunk of a prompt whose beginning is cached.  A
+ * query that sees no key gives o = 0, lse = -inf.  KDA_LATENT_FULL: it sees all lk keys.
+ * Rows of other sequences, NaN included, do not matter to a sequence; its own must be
+ * finite (a key's zero weight does not undo a value of NaN or infinity).
+ *
+ *  q        [q_tokens, num_heads, d_nope + d_pe], token and head strides
+ *  k_nope   [k_tokens, num_heads, d_nope], v [k_tokens, num_heads, d_v], token and head
+ *           strides (parts of one up-projection's rows, for instance); k_pe
+ *           [k_tokens, d_pe], row stride, shared by the heads
+ *  cu_q, cu_k  [num_seqs + 1] int32 device prefix sums ending at q_tokens and k_tokens.
+ *           cu_k NULL: cu_q (k_tokens == q_tokens); both NULL: one sequence.  A malformed
+ *           array is reported (KDA_DEVICE_ERR_SEQLENS) and held to the buffers; the rows
+ *           that it covers no or several times are unspecified
+ *  o        [q_tokens, num_heads, d_v] contiguous;  lse [q_tokens, num_heads] fp32 or NULL
+ */
+kda_status_t kda_latent_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_nope,
+                                int64_t k_token_stride, int64_t k_head_stride, const void *k_pe,
+                                int64_t k_pe_stride, const void *v, int64_t v_token_stride,
+                                int64_t v_head_stride, const int32_t *cu_q, const int32_t *cu_k,
+                                int32_t num_seqs, int64_t q_tokens, int64_t k_tokens, int32_t num_heads,
+                                int32_t d_nope, int32_t d_pe, int32_t d_v, kda_dtype_t dtype, float scale,
+                                void *o, float *lse, uint32_t *device_errors, void *stream, uint32_t flags);
 
 /* Static, human-readable name of a status code (never NULL). */
 const char *kda_status_string(kda_status_t status);

@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "latent.cuh"
 
 namespace {
 
@@ -15,7 +16,9 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // 1 = supported (compute capability 10.3), -1 = not supported, 0 = unknown.
 int g_device_ok[kMaxDevices];
 
-kda_status_t check_device()
+}  // namespace
+
+kda_status_t kda::check_device()
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
@@ -29,6 +32,10 @@ kda_status_t check_device()
     }
     return g_device_ok[dev] == 1 ? KDA_OK : KDA_ERR_UNSUPPORTED;
 }
+
+namespace {
+
+using kda::check_device;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -1,0 +1,266 @@
+// latent.cuh -- latent attention (one shared latent vector and one position key per token):
+// problem descriptions, the split of the absorbed decode over the CTAs, and device helpers
+// shared by its kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace kda {
+
+// The supported widths (other values are refused by the entry points).
+constexpr int kLatR = KDA_LATENT_DIM;         // latent channels; the values of the absorbed form
+constexpr int kLatP = KDA_LATENT_PE_DIM;      // position channels
+constexpr int kLatC = kLatR + kLatP;          // channels of a cache row = absorbed key width
+constexpr int kLatN = KDA_LATENT_HEAD_DIM;    // expanded key channels without position; value channels
+constexpr int kLatQK = kLatN + kLatP;         // expanded key width
+constexpr float kLn2 = 0.6931471805599453f;   // ln 2: log-sum-exp from log2 units
+constexpr float kLatLog2e = 1.4426950408889634f;
+
+struct LatentAppend {
+    const void *latent, *k_pe, *norm_weight, *q_pe;  // norm_weight, q_pe may be null
+    int64_t latent_stride, k_pe_stride, q_ts, q_hs, qo_ts, qo_hs, lo_stride, ko_stride;  // elements
+    float eps;
+    const float *cos_sin;  // [num_positions, 64]: 32 cosines, 32 sines; null: no rotation
+    const int32_t *positions, *slots;
+    int num_positions, tokens, heads;
+    void *q_pe_out, *latent_out, *k_pe_out, *cache;  // the outputs but the cache may be null
+    int64_t num_slots;
+    bool interleaved;
+    kda_dtype_t dtype;
+    uint32_t *errors;
+    cudaStream_t stream;
+};
+
+struct LatentDecode {
+    const void *q, *cache;
+    int64_t q_bs, q_hs;  // elements
+    int64_t num_pages, table_stride;
+    int page_size, table_width;
+    const int32_t *table, *lens;
+    int batch, heads;
+    float scale_log2;  // softmax scale x log2(e)
+    void *o;
+    float *lse;        // may be null
+    char *workspace;
+    kda_dtype_t dtype;
+    uint32_t *errors;
+    cudaStream_t stream;
+};
+
+struct LatentPrefill {
+    const void *q, *k_nope, *k_pe, *v;
+    int64_t q_ts, q_hs, kn_ts, kn_hs, kp_ts, v_ts, v_hs;  // elements
+    const int32_t *cu_q, *cu_k;  // both null: one sequence
+    int num_seqs;
+    int64_t q_tokens, k_tokens;
+    int heads;
+    float scale_log2;
+    bool causal;
+    void *o;
+    float *lse;  // may be null
+    kda_dtype_t dtype;
+    uint32_t *errors;
+    cudaStream_t stream;
+};
+
+kda_status_t check_device();  // kda_api.cu
+
+cudaError_t launch_latent_append(const LatentAppend &p);
+cudaError_t launch_latent_decode_simt(const LatentDecode &p);
+cudaError_t launch_latent_prefill_simt(const LatentPrefill &p);
+size_t latent_decode_ws_bytes(int heads, kda_dtype_t dtype);
+
+// ---------------------------------------------------------------- absorbed decode: work split
+// The cache rows of all (head group, sequence) units, cut into tiles, are one list of W tiles
+// (head group outermost, so that CTAs working on the same cache rows for different head groups
+// do so at the same time and share them in L2).  CTA c of G' = min(G, W) takes the tiles
+// [c W / G', (c + 1) W / G'): every CTA reads the same number of cache rows whatever the lengths,
+// and the host needs to know no length.  A unit cut by a CTA boundary leaves partial results
+// (the running maximum and sum, and the unnormalised output, fp32): slot 2c for the first unit
+// of CTA c, 2c + 1 for its last.  The CTA after a unit's first boundary records where the unit's
+// parts lie, and the combine kernel joins them in the order of the cache rows.
+constexpr int kLatMaxGrid = 320;  // bound on the decode grid (two CTAs on each of 152 SMs, rounded up)
+constexpr int kLatHeadTile = 64;  // most heads in one tile
+
+struct LatentJoin {  // at the head of the workspace, one per CTA
+    int b, h0;            // sequence and first head; b < 0: nothing to join at this boundary
+    int c_first, c_last;  // CTAs that hold parts
+    int first_slot;       // slot of the first part; the others' are 2 c
+    int pad[3];
+};
+
+constexpr size_t kLatJoinBytes = ((size_t)kLatMaxGrid * sizeof(LatentJoin) + 255) / 256 * 256;
+
+// per slot and head: (maximum in log2 units, sum), then the slots' outputs
+__host__ __device__ inline float *latent_ml(char *ws) { return reinterpret_cast<float *>(ws + kLatJoinBytes); }
+__host__ __device__ inline float *latent_part(char *ws, int head_tile)
+{
+    return latent_ml(ws) + (size_t)2 * kLatMaxGrid * head_tile * 2;
+}
+inline size_t latent_ws_bytes(int head_tile, int grid)
+{
+    return kLatJoinBytes + (size_t)2 * kLatMaxGrid * head_tile * 2 * sizeof(float) +
+           (size_t)2 * grid * head_tile * kLatR * sizeof(float);
+}
+// Joins the parts of the split units; `head_tile` heads per slot.
+cudaError_t launch_latent_join(const LatentDecode &p, int head_tile, int grid);
+
+#ifdef __CUDACC__
+// ---------------------------------------------------------------- expanded prefill: query tiles
+// A tile of one sequence's queries: rows from query q0 (global), the sequence's keys from k0
+// (global), how many of them the tile's last row sees, and the last key (counted from k0) that its
+// first row sees when causal.  rows 0: no tile has this number.
+struct LatentTile {
+    int64_t q0, k0;
+    int rows;
+    int64_t keys, off;
+};
+
+// Sequence n's tiles are numbered from cu_q[n] / m + n, which increases with n and leaves room for
+// all of them, so that bisection finds a tile's sequence without a table.  A malformed cu_q or
+// cu_k is reported and held to the buffers.
+__device__ __forceinline__ LatentTile latent_tile(const LatentPrefill &p, int tile, int m)
+{
+    int n = 0;
+    if (p.cu_q) {
+        int hi = p.num_seqs - 1;
+        while (n < hi) {  // the last sequence whose first tile is not after `tile`
+            const int mid = (n + hi + 1) >> 1;
+            int64_t t0, t1;
+            seq_range(p.cu_q, mid, p.q_tokens, t0, t1);
+            if (t0 / m + mid <= tile) n = mid;
+            else hi = mid - 1;
+        }
+    }
+    LatentTile t;
+    int64_t q0, q1, k0, k1;
+    seq_range(p.cu_q, n, p.q_tokens, q0, q1);
+    seq_range(p.cu_k, n, p.k_tokens, k0, k1);
+    const int64_t first = max(q0, q0 + (tile - (q0 / m + n)) * (int64_t)m);
+    t.q0 = first;
+    t.k0 = k0;
+    t.rows = (int)max((int64_t)0, min((int64_t)m, q1 - first));
+    t.off = (first - q0) + (k1 - k0) - (q1 - q0);
+    t.keys = k1 - k0;
+    if (p.causal) t.keys = max((int64_t)0, min(t.keys, t.off + t.rows));
+    return t;
+}
+
+// Reports a cu array that is not a prefix sum ending at `total`: every thread of one CTA calls it.
+__device__ __forceinline__ void latent_check_cu(const int32_t *cu, int num_seqs, int64_t total, uint32_t *errors)
+{
+    if (!cu || !errors) return;
+    bool bad = threadIdx.x == 0 && (cu[0] != 0 || cu[num_seqs] != total);
+    for (int n = threadIdx.x; n < num_seqs; n += blockDim.x) bad |= cu[n + 1] < cu[n];
+    if (bad) atomicOr(errors, DEV_ERR_SEQLENS);
+}
+
+// ---------------------------------------------------------------- absorbed decode: the walk
+// A sequence's length, held to what its page table can hold; `bad` when that changed it.
+__device__ __forceinline__ int latent_len(const int32_t *lens, int b, int64_t capacity, bool &bad)
+{
+    const int64_t n = lens[b];
+    if (n >= 0 && n <= capacity) return (int)n;
+    bad = true;
+    return n < 0 ? 0 : (int)capacity;
+}
+
+// Position of a CTA in the tile list.
+struct LatentWalk {
+    int64_t g, g_end;   // tile list range of this CTA
+    int64_t total;      // W
+    int cta, ctas;      // c, G'
+    int hg, b, tile;    // head group, sequence and tile of g
+    __device__ __forceinline__ int64_t start_of(int64_t c) const { return c * total / ctas; }
+    __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
+};
+
+// Called by all NT threads of the CTA (contains barriers); s_scan: NT + 4 int64 of shared memory.
+// The first CTAs also clear the outputs of the sequences without cache rows.
+template <int NT, typename IO>
+__device__ __forceinline__ LatentWalk latent_walk(const int32_t *lens, int batch, int64_t capacity, int tile_rows,
+                                                  int head_groups, int heads, IO *o, float *lse, uint32_t *errors,
+                                                  int64_t *s_scan)
+{
+    const int tid = threadIdx.x;
+    const int chunk = (batch + NT - 1) / NT;
+    const int lo = min(tid * chunk, batch), hi = min(lo + chunk, batch);
+    bool bad = false;
+    int64_t sum = 0;
+    for (int b = lo; b < hi; ++b) sum += (latent_len(lens, b, capacity, bad) + tile_rows - 1) / tile_rows;
+    if (bad && errors && blockIdx.x == 0) atomicOr(errors, DEV_ERR_SEQLENS);
+    int64_t inc = sum;  // inclusive scan: within the warp, then over the warps
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, inc, m);
+        if ((tid & 31) >= m) inc += up;
+    }
+    if ((tid & 31) == 31) s_scan[tid >> 5] = inc;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < (tid >> 5)) before += s_scan[w];
+        all += s_scan[w];
+    }
+    const int64_t first = before + inc - sum;  // tiles before this thread's sequences
+    LatentWalk k;
+    k.total = all * head_groups;
+    k.cta = blockIdx.x;
+    k.ctas = (int)min((int64_t)gridDim.x, k.total);
+    k.hg = k.b = k.tile = 0;
+    k.g = k.g_end = 0;
+    if (k.cta < k.ctas) {
+        k.g = k.start_of(k.cta);
+        k.g_end = k.start_of(k.cta + 1);
+        k.hg = (int)(k.g / all);
+        int64_t r = k.g - k.hg * all;
+        if (r >= first && r < first + sum) {
+            r -= first;
+            bool ignore = false;
+            int b = lo;
+            for (; b < hi; ++b) {
+                const int n = (latent_len(lens, b, capacity, ignore) + tile_rows - 1) / tile_rows;
+                if (r < n) break;
+                r -= n;
+            }
+            s_scan[NT / 32] = b;
+            s_scan[NT / 32 + 1] = r;
+        }
+    }
+    __syncthreads();
+    if (k.cta < k.ctas) {
+        k.b = (int)s_scan[NT / 32];
+        k.tile = (int)s_scan[NT / 32 + 1];
+    }
+    for (int b = blockIdx.x; b < batch; b += gridDim.x) {
+        bool ignore = false;
+        if (latent_len(lens, b, capacity, ignore) > 0) continue;
+        for (int64_t e = tid; e < (int64_t)heads * kLatR; e += NT) store_io(o + (size_t)b * heads * kLatR + e, 0.f);
+        if (lse)
+            for (int h = tid; h < heads; h += NT) lse[(size_t)b * heads + h] = -INFINITY;
+    }
+    return k;
+}
+
+// This CTA's record for the combine kernel: one thread, once, with the walk at its start.
+// n0: tiles of the first unit.
+__device__ __forceinline__ void latent_record_join(const LatentWalk &k, int n0, int head_tile, char *ws)
+{
+    LatentJoin j = {-1, 0, 0, 0, 0, {0, 0, 0}};
+    if (k.cta < k.ctas && k.tile > 0) {
+        const int64_t a = k.g - k.tile;
+        const int cf = k.cta_of(a);
+        if (cf == k.cta - 1) {
+            j.b = k.b;
+            j.h0 = k.hg * head_tile;
+            j.c_first = cf;
+            j.c_last = k.cta_of(a + n0 - 1);
+            j.first_slot = k.start_of(cf) >= a ? 2 * cf : 2 * cf + 1;
+        }
+    }
+    reinterpret_cast<LatentJoin *>(ws)[blockIdx.x] = j;
+}
+#endif
+
+}  // namespace kda

@@ -1,0 +1,268 @@
+// latent_decode_simt.cu -- absorbed latent attention for one token per sequence on the CUDA cores
+// (fp32 I/O, exact fp32 products), and the kernel that joins the parts of a split sequence for
+// this form and the tensor-core one.
+//
+//   s_hj = scale q_h . c_j  (576 channels),  o_h = sum_j softmax_j(s_h) c_j[:512],  j < len
+//
+// One pass over the cache rows with a running maximum m and sum l per head (base 2): a tile's rows
+// enter with p = 2^(s - m), and what is held is scaled by 2^(m_old - m) when m rises.
+#include <math.h>
+
+#include "latent.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kT = 256;        // threads
+constexpr int kRows = 32;      // cache rows per tile, one per lane
+constexpr int kHeads = 8;      // heads per tile
+constexpr int kLdK = kLatC + 4;  // row stride (floats) of the tile: 16-byte reads of 8 rows cover all banks
+constexpr int kSpan = kLatC / 8;  // channels of one warp in the score product
+
+struct Smem {
+    float q[kHeads][kLatC];
+    float k[kRows][kLdK];
+    float red[8][kHeads][kRows];
+    float p[kRows][kHeads];
+    float alpha[kHeads];
+    float ml[kHeads][2];
+    int64_t scan[kT / 32 + 2];
+};
+
+// Two CTAs on an SM overlap one's loads with the other's products.  Scores: warp w multiplies
+// channels [72 w, 72 w + 72) for the tile's 32 rows (a lane each) and 8 heads, then the eight
+// partial products are summed.  Output: a thread owns two of the 512 channels for 8 heads.
+template <typename IO>
+__global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentDecode p)
+{
+    extern __shared__ __align__(16) unsigned char raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t capacity = (int64_t)p.table_width * p.page_size;
+    const int groups = (p.heads + kHeads - 1) / kHeads;
+    LatentWalk w = latent_walk<kT, IO>(p.lens, p.batch, capacity, kRows, groups, p.heads, static_cast<IO *>(p.o),
+                                       p.lse, p.errors, sm.scan);
+    if (w.cta >= w.ctas) {
+        if (tid == 0) latent_record_join(w, 0, kHeads, p.workspace);
+        return;
+    }
+    const IO *cache = static_cast<const IO *>(p.cache);
+    bool first_unit = true;
+    while (w.g < w.g_end) {
+        bool ignore = false;
+        const int len = latent_len(p.lens, w.b, capacity, ignore);
+        const int n = (len + kRows - 1) / kRows;
+        if (n == 0) {
+            if (++w.b == p.batch) { w.b = 0; ++w.hg; }
+            continue;
+        }
+        if (first_unit && tid == 0) latent_record_join(w, n, kHeads, p.workspace);
+        const int tile0 = w.tile, tiles = (int)min((int64_t)(n - tile0), w.g_end - w.g);
+        const int h0 = w.hg * kHeads, hs = min(kHeads, p.heads - h0);
+        __syncthreads();  // the previous unit's reads of q
+        for (int e = tid; e < kHeads * kLatC; e += kT) {
+            const int h = e / kLatC, c = e - h * kLatC;
+            sm.q[h][c] = h < hs ? load_io(static_cast<const IO *>(p.q) + w.b * p.q_bs + (h0 + h) * p.q_hs + c) : 0.f;
+        }
+        float m = -INFINITY, l = 0.f;  // of head `warp`, the same on every lane (l: this lane's rows)
+        float acc[kHeads][2];
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) acc[h][0] = acc[h][1] = 0.f;
+        for (int t = tile0; t < tile0 + tiles; ++t) {
+            const int j0 = t * kRows, rows = min(kRows, len - j0);
+            __syncthreads();  // the previous tile's reads of k and p
+            for (int e = tid; e < kRows * (kLatC / 4); e += kT) {
+                const int r = e / (kLatC / 4), c = 4 * (e - r * (kLatC / 4));
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);  // rows past the end count nothing, whatever they hold
+                if (r < rows) {
+                    const int j = j0 + r, page = j / p.page_size;
+                    const int64_t at = p.table[w.b * p.table_stride + page];
+                    if (at >= 0 && at < p.num_pages)
+                        x = load4_io(cache + (at * p.page_size + (j - page * p.page_size)) * kLatC + c);
+                    else if (c == 0 && p.errors)
+                        atomicOr(p.errors, DEV_ERR_PAGE);
+                }
+                *reinterpret_cast<float4 *>(&sm.k[r][c]) = x;
+            }
+            __syncthreads();
+            float s[kHeads];
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) s[h] = 0.f;
+#pragma unroll 6
+            for (int c = warp * kSpan; c < (warp + 1) * kSpan; c += 4) {
+                const float4 k = *reinterpret_cast<const float4 *>(&sm.k[lane][c]);
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    const float4 q = *reinterpret_cast<const float4 *>(&sm.q[h][c]);
+                    s[h] += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) sm.red[warp][h][lane] = s[h];
+            __syncthreads();
+            // head `warp`, row `lane`
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x += sm.red[i][warp][lane];
+            x = lane < rows ? x * p.scale_log2 : -INFINITY;
+            float mx = x;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.f : mn;
+            const float a = exp2f(m - base), e = exp2f(x - base);
+            l = l * a + e;
+            m = mn;
+            sm.p[lane][warp] = e;
+            if (lane == 0) sm.alpha[warp] = a;
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                const float f = sm.alpha[h];
+                acc[h][0] *= f;
+                acc[h][1] *= f;
+            }
+#pragma unroll 8
+            for (int r = 0; r < kRows; ++r) {
+                const float2 v = *reinterpret_cast<const float2 *>(&sm.k[r][2 * tid]);
+                const float4 pa = *reinterpret_cast<const float4 *>(&sm.p[r][0]);
+                const float4 pb = *reinterpret_cast<const float4 *>(&sm.p[r][4]);
+                const float ph[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    acc[h][0] += ph[h] * v.x;
+                    acc[h][1] += ph[h] * v.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (lane == 0) {
+            sm.ml[warp][0] = m;
+            sm.ml[warp][1] = l;
+        }
+        __syncthreads();
+        if (tiles == n) {  // the whole unit
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                if (h >= hs) break;
+                const float inv = sm.ml[h][1] == 0.f ? 0.f : 1.f / sm.ml[h][1];
+                IO *o = static_cast<IO *>(p.o) + ((int64_t)w.b * p.heads + h0 + h) * kLatR + 2 * tid;
+                store_io(o, acc[h][0] * inv);
+                store_io(o + 1, acc[h][1] * inv);
+            }
+            if (p.lse && tid < hs)
+                p.lse[(int64_t)w.b * p.heads + h0 + tid] = sm.ml[tid][0] * kLn2 + logf(sm.ml[tid][1]);
+        } else {
+            const int slot = first_unit ? 2 * w.cta : 2 * w.cta + 1;
+            float *part = latent_part(p.workspace, kHeads) + (size_t)slot * kHeads * kLatR + 2 * tid;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h)
+                *reinterpret_cast<float2 *>(part + h * kLatR) = make_float2(acc[h][0], acc[h][1]);
+            if (tid < kHeads) {
+                float *ml = latent_ml(p.workspace) + ((size_t)slot * kHeads + tid) * 2;
+                ml[0] = sm.ml[tid][0];
+                ml[1] = sm.ml[tid][1];
+            }
+        }
+        first_unit = false;
+        w.g += tiles;
+        w.tile = 0;
+        if (++w.b == p.batch) { w.b = 0; ++w.hg; }
+    }
+}
+
+// Joins one split unit's parts for one head: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
+// over the parts in the order of the cache rows.  One CTA per (CTA boundary, head); most
+// boundaries of a large batch have nothing to join and return at once.
+template <typename IO>
+__global__ void __launch_bounds__(128)
+latent_join_kernel(const char *ws, int head_tile, int heads, IO *o, float *lse)
+{
+    __shared__ float s_w[kLatMaxGrid];
+    __shared__ float s_red[4];
+    const LatentJoin j = reinterpret_cast<const LatentJoin *>(ws)[blockIdx.x];
+    const int hl = blockIdx.y, h = j.h0 + hl, tid = threadIdx.x;
+    if (j.b < 0 || h >= heads) return;
+    const int parts = j.c_last - j.c_first + 1;
+    auto slot = [&](int i) { return i == 0 ? j.first_slot : 2 * (j.c_first + i); };
+    const float *ml = latent_ml(const_cast<char *>(ws));
+    const float *part = latent_part(const_cast<char *>(ws), head_tile);
+    float mx = -INFINITY;
+    for (int i = tid; i < parts; i += 128) mx = fmaxf(mx, ml[((size_t)slot(i) * head_tile + hl) * 2]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    if ((tid & 31) == 0) s_red[tid >> 5] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    __syncthreads();
+    float l = 0.f;
+    for (int i = tid; i < parts; i += 128) {
+        const float *x = ml + ((size_t)slot(i) * head_tile + hl) * 2;
+        const float f = exp2f(x[0] - base);
+        s_w[i] = f;
+        l += f * x[1];
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if ((tid & 31) == 0) s_red[tid >> 5] = l;
+    __syncthreads();
+    l = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(part + ((size_t)slot(i) * head_tile + hl) * kLatR + 4 * tid);
+        const float f = s_w[i];
+        acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float out[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    store_io4(o + ((int64_t)j.b * heads + h) * kLatR + 4 * tid, out);
+    if (lse && tid == 0) lse[(int64_t)j.b * heads + h] = mx * kLn2 + logf(l);
+}
+
+int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
+template <typename IO>
+cudaError_t launch_simt(const LatentDecode &p)
+{
+    const cudaError_t err = cudaFuncSetAttribute(latent_decode_simt_kernel<IO>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    if (err != cudaSuccess) return err;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int grid = 2 * sms < kLatMaxGrid ? 2 * sms : kLatMaxGrid;
+    latent_decode_simt_kernel<IO><<<grid, kT, sizeof(Smem), p.stream>>>(p);
+    const cudaError_t launched = cudaGetLastError();
+    return launched != cudaSuccess ? launched : launch_latent_join(p, kHeads, grid);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_join(const LatentDecode &p, int head_tile, int grid)
+{
+    const dim3 g((unsigned)grid, (unsigned)(p.heads < head_tile ? p.heads : head_tile));
+    if (p.dtype == KDA_DTYPE_BF16)
+        latent_join_kernel<__nv_bfloat16><<<g, 128, 0, p.stream>>>(p.workspace, head_tile, p.heads,
+                                                                    static_cast<__nv_bfloat16 *>(p.o), p.lse);
+    else
+        latent_join_kernel<float><<<g, 128, 0, p.stream>>>(p.workspace, head_tile, p.heads,
+                                                            static_cast<float *>(p.o), p.lse);
+    return cudaGetLastError();
+}
+
+size_t latent_decode_ws_bytes(int heads, kda_dtype_t dtype) { return latent_ws_bytes(kHeads, kLatMaxGrid); }
+
+cudaError_t launch_latent_decode_simt(const LatentDecode &p)
+{
+    return p.dtype == KDA_DTYPE_BF16 ? launch_simt<__nv_bfloat16>(p) : launch_simt<float>(p);
+}
+
+}  // namespace kda

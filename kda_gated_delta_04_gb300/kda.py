@@ -30,6 +30,9 @@ KDA_PATH_CUDA_CORE, KDA_PATH_FUSED, KDA_PATH_TWO_KERNEL, KDA_PATH_SEQ_SPLIT, KDA
     KDA_PATH_STREAMED = range(6)
 CHUNK = 64
 KDA_STREAM_RING_MIN = 8
+KDA_LATENT_DIM, KDA_LATENT_PE_DIM, KDA_LATENT_HEAD_DIM = 512, 64, 128
+KDA_LATENT_INTERLEAVED, KDA_LATENT_FULL = 1, 2
+KDA_LATENT_DECODE_WORKSPACE_MAX = 50331648
 
 _lib = None
 _lock = threading.Lock()
@@ -67,6 +70,18 @@ EXPORTS = {
     "kda_decode_step_slots": (_c.c_int, [_VP, _VP, _VP, _VP, _VP, _c.c_int32, _c.c_int32, _c.c_int32,
                                          _c.c_int32, _c.c_int, _VP, _c.c_int32, _VP, _VP, _VP, _VP,
                                          _c.c_uint32]),
+    "kda_latent_append": (_c.c_int, [_VP, _c.c_int64, _VP, _c.c_int64, _VP, _c.c_float, _VP, _c.c_int32, _VP,
+                                     _VP, _c.c_int64, _c.c_int64, _VP, _c.c_int64, _c.c_int64, _VP, _c.c_int64,
+                                     _VP, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int,
+                                     _VP, _c.c_int64, _VP, _VP, _VP, _c.c_uint32]),
+    "kda_latent_decode_workspace_size": (_c.c_size_t, [_c.c_int32, _c.c_int]),
+    "kda_latent_decode": (_c.c_int, [_VP, _c.c_int64, _c.c_int64, _VP, _c.c_int64, _c.c_int32, _VP, _c.c_int64,
+                                     _c.c_int32, _VP, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int,
+                                     _c.c_float, _VP, _VP, _VP, _c.c_size_t, _VP, _VP]),
+    "kda_latent_prefill": (_c.c_int, [_VP, _c.c_int64, _c.c_int64, _VP, _c.c_int64, _c.c_int64, _VP, _c.c_int64,
+                                      _VP, _c.c_int64, _c.c_int64, _VP, _VP, _c.c_int32, _c.c_int64, _c.c_int64,
+                                      _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int, _c.c_float, _VP,
+                                      _VP, _VP, _VP, _c.c_uint32]),
     "kda_prefill_slots": (_c.c_int, _PREFILL_ARGS[:12] + [_VP, _c.c_int32, _VP, _VP, _VP, _VP,
                                                           _c.c_size_t, _VP, _c.c_uint32]),
 }
@@ -198,6 +213,25 @@ def kda_prefill_host_buffer_size(cu_seqlens, num_seqs, total_tokens, num_heads, 
 
 def kda_prefill_host_segments(cu_seqlens, num_seqs, total_tokens, bounds, max_bounds):
     return lib().kda_prefill_host_segments(cu_seqlens, num_seqs, total_tokens, bounds, max_bounds)
+
+
+def kda_latent_append(*args):
+    """The C entry point; arguments as in include/kda.h."""
+    return lib().kda_latent_append(*args)
+
+
+def kda_latent_decode_workspace_size(num_heads, dtype):
+    return lib().kda_latent_decode_workspace_size(num_heads, dtype)
+
+
+def kda_latent_decode(*args):
+    """The C entry point; arguments as in include/kda.h."""
+    return lib().kda_latent_decode(*args)
+
+
+def kda_latent_prefill(*args):
+    """The C entry point; arguments as in include/kda.h."""
+    return lib().kda_latent_prefill(*args)
 
 
 def kda_diag_tensor_phases(pass_, reps, workspace, stream, tflops):
@@ -480,3 +514,165 @@ def decode_step(q, k, v, log_alpha, beta, state, *, o=None, stream=None, qk_l2no
     if st != KDA_OK:
         raise KdaError(st, "kda_decode_step")
     return o
+
+
+# ------------------------------------------------------------------ latent attention
+def _rows(t, name, shape, like):
+    """Address of a CUDA tensor of `like`'s type and device whose last dimension is contiguous
+    (the others may be strided); shape entries of None are not checked."""
+    if not hasattr(t, "is_cuda") or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, "
+                         f"got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _step(t, dim):
+    """Stride of a dimension; 0 where there is one entry only (torch's is then arbitrary)."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def _flat(t, name, dtype, shape, like):
+    """Address of a contiguous CUDA tensor of a given type and shape on `like`'s device, or None."""
+    if t is None:
+        return None
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return _ptr(t, name, dtype)
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty, owned by the stream that will use it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def latent_append(latent, k_pe, cache, slots, *, norm_weight=None, norm_eps=1e-6, cos_sin=None, positions=None,
+                  interleaved=False, q_pe=None, q_pe_out=None, latent_out=None, k_pe_out=None, errors=None,
+                  stream=None):
+    """The tokens' rows into the latent cache: latent [T, 512] normalised (RMSNorm with norm_weight
+    [512]; stored as it is when that is None), k_pe [T, 64] rotated by cos_sin[positions] (cos_sin
+    [M, 64] fp32: 32 cosines, 32 sines; positions int32 [T]; None: no rotation), to row slots[t] of
+    cache [pages, page_size, 576] (slots int32 [T], distinct; -1: not cached).  q_pe [T, H, 64], the
+    queries' position channels, is rotated in the same launch into q_pe_out (None: in place).
+    latent_out [T, 512] and k_pe_out [T, 64] receive the normalised latent and the rotated key
+    again.  Rows may be strided; all are bf16 or all fp32.  interleaved: the rotated pairs are
+    (2i, 2i + 1) instead of (i, i + 32).  errors: int32 [1] that collects KDA_DEVICE_ERR_* bits."""
+    torch = _torch()
+    T = latent.shape[0]
+    dt = _dtype_code(latent)
+    i32 = torch.int32
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    if (cos_sin is None) != (positions is None):
+        raise ValueError("cos_sin and positions go together")
+    H = qt = qh = ot = oh = lo = ko = 0
+    q = qo = lo_p = ko_p = None
+    if q_pe is not None:
+        H = q_pe.shape[1]
+        q_pe_out = q_pe if q_pe_out is None else q_pe_out
+        q, qo = _rows(q_pe, "q_pe", (T, None, 64), latent), _rows(q_pe_out, "q_pe_out", (T, H, 64), latent)
+        qt, qh = _step(q_pe, 0), _step(q_pe, 1)
+        ot, oh = _step(q_pe_out, 0), _step(q_pe_out, 1)
+    elif q_pe_out is not None:
+        raise ValueError("q_pe_out without q_pe")
+    if latent_out is not None:
+        lo_p, lo = _rows(latent_out, "latent_out", (T, 512), latent), _step(latent_out, 0)
+    if k_pe_out is not None:
+        ko_p, ko = _rows(k_pe_out, "k_pe_out", (T, 64), latent), _step(k_pe_out, 0)
+    st = kda_latent_append(
+        _rows(latent, "latent", (None, 512), latent), _step(latent, 0), _rows(k_pe, "k_pe", (T, 64), latent),
+        _step(k_pe, 0), _flat(norm_weight, "norm_weight", latent.dtype, (512,), latent), norm_eps,
+        None if cos_sin is None else _flat(cos_sin, "cos_sin", torch.float32, (cos_sin.shape[0], 64), latent),
+        0 if cos_sin is None else cos_sin.shape[0], _flat(positions, "positions", i32, (T,), latent),
+        q, qt, qh, qo, ot, oh, lo_p, lo, ko_p, ko, T, H, 512, 64, dt,
+        _rows(cache, "cache", (None, None, 576), latent), cache.shape[0] * cache.shape[1],
+        _flat(slots, "slots", i32, (T,), latent), _flat(errors, "errors", i32, (1,), latent),
+        _stream_handle(stream, latent.device), KDA_LATENT_INTERLEAVED if interleaved else 0)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_latent_append")
+
+
+def latent_decode_workspace_for(num_heads, dtype_code, device):
+    """The scratch buffer of latent_decode, for any batch and lengths."""
+    torch = _torch()
+    return torch.empty(kda_latent_decode_workspace_size(num_heads, dtype_code), dtype=torch.uint8, device=device)
+
+
+def latent_decode(q, cache, page_table, seq_lens, scale, *, o=None, lse=None, workspace=None, errors=None,
+                  stream=None):
+    """Absorbed latent attention, one token per sequence over the paged cache: q [B, H, 576]
+    (batch and head dimensions may be strided), cache [pages, page_size, 576], page_table int32
+    [B, W] (rows may be strided), seq_lens int32 [B] on the device.  Returns (o [B, H, 512],
+    lse [B, H] fp32); a sequence of length 0 gives zeros and -inf.  bf16 or fp32.  The scratch
+    buffer (latent_decode_workspace_for) may be kept by the caller; errors as latent_append."""
+    torch = _torch()
+    B, H = q.shape[:2]
+    dt = _dtype_code(q)
+    i32 = torch.int32
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    if page_table.dtype != i32 or not page_table.is_cuda or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be an int32 CUDA tensor [{B}, *]")
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table's last dimension must be contiguous")
+    if o is None:
+        o = _empty((B, H, 512), q.dtype, q.device, stream)
+    if lse is None:
+        lse = _empty((B, H), torch.float32, q.device, stream)
+    if workspace is None:
+        workspace = _empty((kda_latent_decode_workspace_size(H, dt),), torch.uint8, q.device, stream)
+    width = page_table.shape[1]
+    st = kda_latent_decode(
+        _rows(q, "q", (B, H, 576), q), _step(q, 0), _step(q, 1), _rows(cache, "cache", (None, None, 576), q),
+        cache.shape[0], cache.shape[1], page_table.data_ptr(), _step(page_table, 0), width, _flat(seq_lens, "seq_lens", i32, (B,), q), B, H, 512, 64, dt, scale,
+        _flat(o, "o", q.dtype, (B, H, 512), q), _flat(lse, "lse", torch.float32, (B, H), q),
+        _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _flat(errors, "errors", i32, (1,), q), _stream_handle(stream, q.device))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_latent_decode")
+    return o, lse
+
+
+def latent_prefill(q, k_nope, k_pe, v, scale, cu_q=None, cu_k=None, *, causal=True, o=None, lse=None, errors=None,
+                   stream=None):
+    """Expanded latent attention over packed sequences: q [Tq, H, 192], k_nope [Tk, H, 128], k_pe
+    [Tk, 64] (shared by the heads), v [Tk, H, 128], all but the last dimension strided as they
+    come; cu_q, cu_k int32 [N + 1] CUDA offsets (cu_k None: cu_q; both None: one sequence).
+    Causal, aligned at each sequence's end: with lk > lq keys the queries are the last lq
+    positions.  causal=False: every query sees all keys of its sequence.  Returns (o [Tq, H, 128],
+    lse [Tq, H] fp32); a query without keys gives zeros and -inf.  errors as latent_append."""
+    torch = _torch()
+    Tq, H = q.shape[:2]
+    Tk = k_pe.shape[0]
+    dt = _dtype_code(q)
+    i32 = torch.int32
+    if cu_q is None and cu_k is not None:
+        raise ValueError("cu_k without cu_q")
+    N = 1 if cu_q is None else cu_q.numel() - 1
+    if o is None:
+        o = _empty((Tq, H, 128), q.dtype, q.device, stream)
+    if lse is None:
+        lse = _empty((Tq, H), torch.float32, q.device, stream)
+    st = kda_latent_prefill(
+        _rows(q, "q", (Tq, H, 192), q), _step(q, 0), _step(q, 1), _rows(k_nope, "k_nope", (Tk, H, 128), q),
+        _step(k_nope, 0), _step(k_nope, 1), _rows(k_pe, "k_pe", (Tk, 64), q), _step(k_pe, 0),
+        _rows(v, "v", (Tk, H, 128), q), _step(v, 0), _step(v, 1), _flat(cu_q, "cu_q", i32, (N + 1,), q),
+        _flat(cu_k, "cu_k", i32, (N + 1,), q), N, Tq, Tk, H, 128, 64, 128, dt, scale,
+        _flat(o, "o", q.dtype, (Tq, H, 128), q), _flat(lse, "lse", torch.float32, (Tq, H), q),
+        _flat(errors, "errors", i32, (1,), q), _stream_handle(stream, q.device), 0 if causal else KDA_LATENT_FULL)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_latent_prefill")
+    return o, lse
