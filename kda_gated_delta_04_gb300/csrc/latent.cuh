@@ -68,7 +68,9 @@ kda_status_t check_device();  // kda_api.cu
 cudaError_t launch_latent_append(const LatentAppend &p);
 cudaError_t launch_latent_decode_simt(const LatentDecode &p);
 cudaError_t launch_latent_prefill_simt(const LatentPrefill &p);
-size_t latent_decode_ws_bytes(int heads, kda_dtype_t dtype);
+cudaError_t launch_latent_decode_tc(const LatentDecode &p);  // bf16
+size_t latent_decode_simt_ws_bytes();
+size_t latent_decode_tc_ws_bytes(int heads);
 
 // ---------------------------------------------------------------- absorbed decode: work split
 // The cache rows of all (head group, sequence) units, cut into tiles, are one list of W tiles

@@ -15,6 +15,11 @@ size_t elem_size(kda_dtype_t dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
 
 bool dtype_ok(kda_dtype_t dtype) { return dtype == KDA_DTYPE_BF16 || dtype == KDA_DTYPE_F32; }
 
+size_t workspace_bytes_of(int32_t heads, kda_dtype_t dtype)
+{
+    return dtype == KDA_DTYPE_BF16 ? kda::latent_decode_tc_ws_bytes(heads) : kda::latent_decode_simt_ws_bytes();
+}
+
 }  // namespace
 
 extern "C" {
@@ -66,7 +71,7 @@ kda_status_t kda_latent_append(const void *latent, int64_t latent_stride, const 
 size_t kda_latent_decode_workspace_size(int32_t num_heads, kda_dtype_t dtype)
 {
     if (num_heads <= 0 || !dtype_ok(dtype)) return 0;
-    return kda::latent_decode_ws_bytes(num_heads, dtype);
+    return workspace_bytes_of(num_heads, dtype);
 }
 
 kda_status_t kda_latent_decode(const void *q, int64_t q_batch_stride, int64_t q_head_stride, const void *cache,
@@ -92,7 +97,7 @@ kda_status_t kda_latent_decode(const void *q, int64_t q_batch_stride, int64_t q_
         !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(device_errors, 4))
         return KDA_ERR_INVALID_ARG;
     if (!stride_ok(q_batch_stride, es) || !stride_ok(q_head_stride, es)) return KDA_ERR_INVALID_ARG;
-    if (workspace_bytes < kda::latent_decode_ws_bytes(num_heads, dtype)) return KDA_ERR_INVALID_ARG;
+    if (workspace_bytes < workspace_bytes_of(num_heads, dtype)) return KDA_ERR_INVALID_ARG;
     const kda_status_t st = kda::check_device();
     if (st != KDA_OK) return st;
     kda::LatentDecode p;
@@ -102,7 +107,8 @@ kda_status_t kda_latent_decode(const void *q, int64_t q_batch_stride, int64_t q_
     p.batch = batch; p.heads = num_heads; p.scale_log2 = scale * kda::kLatLog2e;
     p.o = o; p.lse = lse; p.workspace = static_cast<char *>(workspace); p.dtype = dtype;
     p.errors = device_errors; p.stream = static_cast<cudaStream_t>(stream);
-    return kda::launch_latent_decode_simt(p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t err = dtype == KDA_DTYPE_BF16 ? kda::launch_latent_decode_tc(p) : kda::launch_latent_decode_simt(p);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status_t kda_latent_prefill(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_nope,

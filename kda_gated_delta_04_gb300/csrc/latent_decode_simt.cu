@@ -9,9 +9,12 @@
 #include <math.h>
 
 #include "latent.cuh"
+#include "sm100_ptx.cuh"
 
 namespace kda {
 namespace {
+
+using ptx::pdl_wait;
 
 constexpr int kT = 256;        // threads
 constexpr int kRows = 32;      // cache rows per tile, one per lane
@@ -180,6 +183,7 @@ latent_join_kernel(const char *ws, int head_tile, int heads, IO *o, float *lse)
 {
     __shared__ float s_w[kLatMaxGrid];
     __shared__ float s_red[4];
+    pdl_wait();  // launched early behind the kernel that wrote the parts
     const LatentJoin j = reinterpret_cast<const LatentJoin *>(ws)[blockIdx.x];
     const int hl = blockIdx.y, h = j.h0 + hl, tid = threadIdx.x;
     if (j.b < 0 || h >= heads) return;
@@ -248,21 +252,27 @@ cudaError_t launch_simt(const LatentDecode &p)
 
 cudaError_t launch_latent_join(const LatentDecode &p, int head_tile, int grid)
 {
-    const dim3 g((unsigned)grid, (unsigned)(p.heads < head_tile ? p.heads : head_tile));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.heads < head_tile ? p.heads : head_tile));
+    cfg.blockDim = dim3(128);
+    cfg.stream = p.stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
     if (p.dtype == KDA_DTYPE_BF16)
-        latent_join_kernel<__nv_bfloat16><<<g, 128, 0, p.stream>>>(p.workspace, head_tile, p.heads,
-                                                                    static_cast<__nv_bfloat16 *>(p.o), p.lse);
-    else
-        latent_join_kernel<float><<<g, 128, 0, p.stream>>>(p.workspace, head_tile, p.heads,
-                                                            static_cast<float *>(p.o), p.lse);
-    return cudaGetLastError();
+        return cudaLaunchKernelEx(&cfg, latent_join_kernel<__nv_bfloat16>, (const char *)p.workspace, head_tile, p.heads,
+                                  static_cast<__nv_bfloat16 *>(p.o), p.lse);
+    return cudaLaunchKernelEx(&cfg, latent_join_kernel<float>, (const char *)p.workspace, head_tile, p.heads,
+                              static_cast<float *>(p.o), p.lse);
 }
 
-size_t latent_decode_ws_bytes(int heads, kda_dtype_t dtype) { return latent_ws_bytes(kHeads, kLatMaxGrid); }
+size_t latent_decode_simt_ws_bytes() { return latent_ws_bytes(kHeads, kLatMaxGrid); }
 
 cudaError_t launch_latent_decode_simt(const LatentDecode &p)
 {
-    return p.dtype == KDA_DTYPE_BF16 ? launch_simt<__nv_bfloat16>(p) : launch_simt<float>(p);
+    return launch_simt<float>(p);
 }
 
 }  // namespace kda

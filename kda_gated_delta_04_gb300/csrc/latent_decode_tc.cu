@@ -1,0 +1,599 @@
+// latent_decode_tc.cu -- absorbed latent attention for one token per sequence on the tensor cores
+// (bf16 I/O).
+//
+//   s_hj = scale q_h . c_j  (576 channels),  o_h = sum_j softmax_j(s_h) c_j[:512],  j < len
+//
+// All heads read the same cache rows, so a row is worth one read: 1,152 bytes against
+// 2 x 1,088 x H operations.  Up to about 128 heads the cache's bytes are the bound.  Both products
+// are computed transposed, cache rows (or channels) as the M dimension and heads as N:
+//
+//   S^T [64 rows x H]   = C [64 x 576] Q^T            (M = 64, N = H, 36 steps of K = 16)
+//   O^T [512 x H]      += C[:, :512]^T P^T [64 x H]   (4 x M = 128, N = H, 4 steps of K = 16)
+//
+// so that no part of a matrix instruction is spent on padding a few heads to a tile of 128: a
+// tile's cost is reading it from shared memory twice, below the time HBM takes to deliver it.  O^T
+// stays in tensor memory for the whole of a sequence (4 H columns), the two S^T buffers beside it.
+//
+// One CTA per SM, 256 threads: warp 0 copies (TMA), warp 1 issues the matrix instructions, warps 2
+// and 3 bring a sequence's queries in, warps 4 to 7 do the softmax.  The cache rows arrive as 64-row
+// panels of 64 channels in rings of pieces: the position channels (read by S^T only, freed early)
+// in one, pairs of latent panels (read by both products) in the other.  S^T of tile t + 1 is issued
+// before O^T of tile t, so the softmax of one tile runs beside the products of its neighbours, and
+// the rings hold 2 to 2.7 tiles: while one is worked on, the others are in flight (100 KB and more a
+// SM; 45 KB cover HBM's latency at its full rate).
+#include <math.h>
+
+#include "latent.cuh"
+#include "tc_common.cuh"
+
+namespace kda {
+namespace {
+
+using namespace ptx;
+using tc::kdesc;
+
+constexpr int kT = 256;
+constexpr int kRows = 64;                 // cache rows per tile
+constexpr uint32_t kPanel = kRows * 128;  // bytes of a panel: 64 rows x 64 channels
+constexpr uint32_t kPair = 2 * kPanel;
+constexpr int kSmemMax = 232448;          // 227 KB, the most a CTA can have
+constexpr uint64_t kWait = tc::kWaitNs;
+constexpr float kSlack = 8.f;  // log2: how far scores may pass the held maximum before it is moved
+
+template <int NH>
+struct Cfg {
+    static constexpr int NP = NH == 64 ? 1 : 2;  // P buffers (one where a second would cost a piece of the ring)
+    static constexpr int NB = NH == 64 ? 2 : (NH == 32 ? 2 : 3);    // position-panel slots
+    static constexpr int NA = NH == 64 ? 8 : (NH == 32 ? 10 : 11);  // latent-pair slots (4 a tile)
+    static constexpr uint32_t Q = 0;
+    static constexpr uint32_t P = Q + 9 * NH * 128;
+    static constexpr uint32_t A = P + NP * NH * 128;
+    static constexpr uint32_t B = A + NA * kPair;
+    static constexpr uint32_t MISC = B + NB * kPanel;
+    static constexpr uint32_t COLS = NH == 64 ? 512 : (NH == 32 ? 256 : 128);  // 6 NH columns, a power of two
+    static constexpr uint32_t SCOL = 4 * NH;                                   // S^T buffers after O^T
+};
+
+template <int NH>
+struct Misc {
+    uint64_t full_a[Cfg<NH>::NA], empty_a[Cfg<NH>::NA], full_b[Cfg<NH>::NB], empty_b[Cfg<NH>::NB];
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, q_empty, o_full, o_empty, drained;
+    uint32_t tmem;
+    int abort;
+    float red[2][4][NH];  // per warp: a tile's column maxima (by tile parity), at the end the sums
+    float fac[NH];        // rescaling factors, at the end 1 / sum
+    int64_t scan[kT / 32 + 2];
+};
+
+// Waits for a phase; gives up after kWait ns or as soon as another role has.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWait) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// The units of this CTA, in order, as each role walks them.
+struct Units {
+    const LatentDecode &p;
+    LatentWalk w;
+    int64_t capacity;
+    int len, n, tile0, tiles;  // current unit: rows, tiles, this CTA's part
+    bool first;
+    __device__ __forceinline__ Units(const LatentDecode &p_, const LatentWalk &w_)
+        : p(p_), w(w_), capacity((int64_t)p_.table_width * p_.page_size), len(0), n(0), tile0(0), tiles(0), first(true)
+    {
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (tiles > 0) {
+            first = false;
+            advance();
+        }
+        while (w.g < w.g_end) {
+            bool ignore = false;
+            len = latent_len(p.lens, w.b, capacity, ignore);
+            n = (len + kRows - 1) / kRows;
+            if (n > 0) {
+                tile0 = w.tile;
+                tiles = (int)min((int64_t)(n - tile0), w.g_end - w.g);
+                w.g += tiles;
+                return true;
+            }
+            advance();
+        }
+        return false;
+    }
+    __device__ __forceinline__ void advance()
+    {
+        w.tile = 0;
+        if (++w.b == p.batch) {
+            w.b = 0;
+            ++w.hg;
+        }
+    }
+};
+
+// Reduces r[0..n) over 16 lanes (a half warp), splitting the values among them: afterwards r[0..)
+// of a lane holds the results of the columns starting at the returned index, `per` of them.
+template <int N, bool MAX>
+__device__ __forceinline__ int half_warp_reduce(float (&r)[N], int lane)
+{
+    int at = 0, cnt = N;
+#pragma unroll
+    for (int m = 8; m; m >>= 1) {
+        if (cnt > 1) {
+            const int half = cnt / 2;
+            const bool up = lane & m;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (i >= half) break;
+                const float send = up ? r[i] : r[i + half], keep = up ? r[i + half] : r[i];
+                const float got = __shfl_xor_sync(0xffffffffu, send, m);
+                r[i] = MAX ? fmaxf(keep, got) : keep + got;
+            }
+            at += up ? half : 0;
+            cnt = half;
+        } else {
+            const float got = __shfl_xor_sync(0xffffffffu, r[0], m);
+            r[0] = MAX ? fmaxf(r[0], got) : r[0] + got;
+        }
+    }
+    return at;
+}
+
+// This thread's half of a row of S^T: N columns (16 lanes a warp hold rows, two threads each).
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t t, float (&s)[N])
+{
+    if constexpr (N == 8) {
+        tmem_ld16x2_x8<8>(t, s);
+    } else if constexpr (N == 16) {
+        tmem_ld16x2_x16<16>(t, s);
+    } else {
+        static_assert(N == 32, "");
+        tmem_ld16x2_x16<32>(t, *reinterpret_cast<float(*)[16]>(&s[0]));
+        tmem_ld16x2_x16<32>(t + 16, *reinterpret_cast<float(*)[16]>(&s[16]));
+    }
+}
+
+template <int NH>
+__device__ __forceinline__ void copy_role(unsigned char *sm, Misc<NH> &mi, const LatentDecode &p, Units u,
+                                          const CUtensorMap &tm, int piece_rows, int lane)
+{
+    using C = Cfg<NH>;
+    const int pieces = kRows / piece_rows;  // copies per panel: 1, 2, 4 or 8
+    const int batch = 32 / pieces;          // tiles whose pages the warp looks up at once
+    const int64_t outside = max(p.num_pages * (int64_t)p.page_size, (int64_t)1);  // past the cache: copied as zeros
+    int ts = 0, na = 0, nb = 0;
+    volatile int *abort = &mi.abort;
+    while (u.next()) {
+        // row of the cache at which piece (lane % pieces) of tile (t + lane / pieces) starts
+        auto look_up = [&](int t) -> int {
+            const int j = (u.tile0 + t + lane / pieces) * kRows + (lane % pieces) * piece_rows;
+            if (t + lane / pieces >= u.tiles || j >= u.len) return (int)outside;
+            const int page = j / p.page_size;
+            const int64_t at = p.table[u.w.b * p.table_stride + page];
+            if (at < 0 || at >= p.num_pages) {
+                if (p.errors) atomicOr(p.errors, DEV_ERR_PAGE);
+                return (int)outside;
+            }
+            return (int)(at * p.page_size + (j - page * p.page_size));
+        };
+        int rows = look_up(0), later = look_up(batch);
+        for (int t = 0; t < u.tiles; ++t, ++ts) {
+            const int in = t % batch;
+            if (in == 0 && t > 0) {
+                rows = later;
+                later = look_up(t + batch);
+            }
+            const int row = __shfl_sync(0xffffffffu, rows, in * pieces + (lane & (pieces - 1)));
+            bool ok = true;
+            if (nb >= C::NB) ok = wait(&mi.empty_b[nb % C::NB], (nb / C::NB - 1) & 1, abort);
+            if (!__all_sync(0xffffffffu, ok)) goto gave_up;
+            uint64_t *bar = &mi.full_b[nb % C::NB];
+            unsigned char *dst = sm + C::B + (nb % C::NB) * kPanel;
+            if (lane == 0) mbar_arrive_expect_tx(bar, kPanel);
+            __syncwarp();
+            if (lane < pieces) tma_load_3d(dst + lane * piece_rows * 128, &tm, bar, 0, row, 8);
+            ++nb;
+            for (int i = 0; i < 4; ++i, ++na) {
+                const int slot = na % C::NA;
+                if (na >= C::NA) ok = wait(&mi.empty_a[slot], (na / C::NA - 1) & 1, abort);
+                if (!__all_sync(0xffffffffu, ok)) goto gave_up;
+                bar = &mi.full_a[slot];
+                dst = sm + C::A + slot * kPair;
+                if (lane == 0) mbar_arrive_expect_tx(bar, kPair);
+                __syncwarp();
+                if (lane < pieces) {
+                    tma_load_3d(dst + lane * piece_rows * 128, &tm, bar, 0, row, 2 * i);
+                    tma_load_3d(dst + kPanel + lane * piece_rows * 128, &tm, bar, 0, row, 2 * i + 1);
+                }
+            }
+        }
+    }
+    return;
+gave_up:  // the copies in flight land before the CTA goes
+    if (lane == 0) {
+        for (int k = max(0, nb - C::NB); k < nb; ++k) mbar_wait_ns(&mi.full_b[k % C::NB], (k / C::NB) & 1, kWait);
+        for (int k = max(0, na - C::NA); k < na; ++k) mbar_wait_ns(&mi.full_a[k % C::NA], (k / C::NA) & 1, kWait);
+    }
+}
+
+template <int NH>
+__device__ __forceinline__ void mma_role(uint32_t sb, Misc<NH> &mi, Units u, uint32_t tmem)
+{
+    using C = Cfg<NH>;
+    constexpr uint32_t id_s = idesc_bf16(64, NH, false, false), id_o = idesc_bf16(128, NH, true, false);
+    volatile int *abort = &mi.abort;
+    int ts = 0, units = 0;
+    // O^T of tile t (the running count), the first of its unit or not, the last or not
+    auto products = [&](int t, bool first, bool last, int unit) -> bool {
+        if (!wait(&mi.p_full[t % C::NP], (t / C::NP) & 1, abort)) return false;
+        if (first && unit > 0 && !wait(&mi.o_empty, (unit - 1) & 1, abort)) return false;
+        tc_fence_after_sync();
+        const uint32_t pb = sb + C::P + (t % C::NP) * (NH * 128);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const int slot = (4 * t + i) % C::NA;
+            const uint32_t a = sb + C::A + slot * kPair;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_bf16(tmem + i * NH, sdesc(a + k * 2048, kPanel, 1024, kSw128B), kdesc(pb + k * 32), id_o,
+                         !first || k > 0);
+            mma_commit(&mi.empty_a[slot]);
+        }
+        mma_commit(&mi.p_empty[t % C::NP]);
+        if (last) mma_commit(&mi.o_full);
+        return true;
+    };
+    bool pending = false, pend_first = false;
+    while (u.next()) {
+        // a new unit: finish the one before, then wait for the queries
+        if (pending && !products(ts - 1, pend_first, true, units - 1)) return;
+        pending = false;
+        if (!wait(&mi.q_full, units & 1, abort)) return;
+        ++units;
+        for (int t = 0; t < u.tiles; ++t, ++ts) {
+            if (ts >= 2 && !wait(&mi.s_empty[ts & 1], (ts / 2 - 1) & 1, abort)) return;
+            if (!wait(&mi.full_b[ts % C::NB], (ts / C::NB) & 1, abort)) return;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + C::SCOL + (ts & 1) * NH;
+            const uint32_t b = sb + C::B + (ts % C::NB) * kPanel;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_bf16(d, kdesc(b + k * 32), kdesc(sb + C::Q + 8 * NH * 128 + k * 32), id_s, k > 0);
+            mma_commit(&mi.empty_b[ts % C::NB]);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const int na = 4 * ts + i, slot = na % C::NA;
+                if (!wait(&mi.full_a[slot], (na / C::NA) & 1, abort)) return;
+                const uint32_t a = sb + C::A + slot * kPair;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_bf16(d, kdesc(a + (k >> 2) * kPanel + (k & 3) * 32),
+                             kdesc(sb + C::Q + (2 * i + (k >> 2)) * NH * 128 + (k & 3) * 32), id_s, 1);
+            }
+            mma_commit(&mi.s_full[ts & 1]);
+            if (t + 1 == u.tiles) mma_commit(&mi.q_empty);
+            if (pending && !products(ts - 1, pend_first, false, units - 1)) return;
+            pending = true;
+            pend_first = t == 0;
+        }
+    }
+    if (pending) products(ts - 1, pend_first, true, units - 1);
+}
+
+// Queries of a unit's heads into shared memory (K-major, swizzled); 64 threads.
+template <int NH>
+__device__ __forceinline__ void query_role(unsigned char *sm, Misc<NH> &mi, const LatentDecode &p, Units u, int id)
+{
+    using C = Cfg<NH>;
+    volatile int *abort = &mi.abort;
+    int units = 0;
+    while (u.next()) {
+        if (units > 0 && !wait(&mi.q_empty, (units - 1) & 1, abort)) return;
+        const int h0 = u.w.hg * NH;
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + u.w.b * p.q_bs;
+#pragma unroll 6
+        for (int e = id; e < NH * 72; e += 64) {
+            const int h = e / 72, c = e - h * 72;  // 8 channels
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (h0 + h < p.heads) x = *reinterpret_cast<const uint4 *>(q + (h0 + h) * p.q_hs + 8 * c);
+            *reinterpret_cast<uint4 *>(sm + C::Q + tc::km16(h, 8 * c, NH)) = x;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&mi.q_full);
+        ++units;
+    }
+}
+
+template <int NH>
+__device__ __forceinline__ void softmax_role(unsigned char *sm, Misc<NH> &mi, const LatentDecode &p, Units u,
+                                             uint32_t tmem, int tid)
+{
+    using C = Cfg<NH>;
+    constexpr int N = NH / 2, PER = N / 16 ? N / 16 : 1;
+    volatile int *abort = &mi.abort;
+    const int warp = tid >> 5, lane = tid & 31, side = lane >> 4, row = 16 * warp + (lane & 15);
+    const uint32_t quarter = (uint32_t)(warp * 32) << 16;
+    int ts = 0, units = 0;
+    bool bad = false;  // a wait gave up: the next barrier takes all four warps out together
+    while (u.next()) {
+        float m[N], l[N];  // of columns side * N + i: the held maximum (log2 units), this row's share of the sum
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+        for (int t = 0; t < u.tiles; ++t, ++ts) {
+            float s[N], r[N];
+            bad |= !wait(&mi.s_full[ts & 1], (ts / 2) & 1, abort);
+            tc_fence_after_sync();
+            load_scores<N>(tmem + C::SCOL + (ts & 1) * NH + quarter, s);
+            tmem_ld_wait();
+            tc_fence_before_sync();
+            mbar_arrive(&mi.s_empty[ts & 1]);
+            const int left = u.len - (u.tile0 + t) * kRows;  // rows of the tile that count
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i] = s[i] = row < left ? s[i] * p.scale_log2 : -INFINITY;
+            const int at = side * N + half_warp_reduce<N, true>(r, lane);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mi.red[ts & 1][warp][at + i] = r[i];
+            if (bar_sync_or(1, 128, bad)) return;
+            bool rise = false;
+            float top[N];
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                float4 a = *reinterpret_cast<const float4 *>(&mi.red[ts & 1][0][side * N + i]);
+#pragma unroll
+                for (int w = 1; w < 4; ++w) {
+                    const float4 b = *reinterpret_cast<const float4 *>(&mi.red[ts & 1][w][side * N + i]);
+                    a = make_float4(fmaxf(a.x, b.x), fmaxf(a.y, b.y), fmaxf(a.z, b.z), fmaxf(a.w, b.w));
+                }
+                top[i] = a.x; top[i + 1] = a.y; top[i + 2] = a.z; top[i + 3] = a.w;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) rise |= top[i] > m[i] + kSlack;
+            // the same in all four warps (each has both sides): all see the same maxima
+            if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float mn = fmaxf(m[i], top[i]);
+                    const float f = mn == m[i] ? 1.f : tc::exp2_approx(m[i] - mn);
+                    m[i] = mn;
+                    l[i] *= f;
+                    if (warp == 0 && (lane & 15) == 0) mi.fac[side * N + i] = f;
+                }
+                if (t > 0) {  // what O^T holds follows
+                    bad |= !wait(&mi.p_empty[(ts - 1) % C::NP], ((ts - 1) / C::NP) & 1, abort);
+                    if (bar_sync_or(1, 128, bad)) return;
+                    tc_fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < 4 * NH; c += 16) {
+                        float x[16];
+                        tmem_ld16(tmem + quarter + c, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] *= mi.fac[(c & (NH - 1)) + i];
+                        tmem_st16(tmem + quarter + c, x);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    if (bar_sync_or(1, 128, bad)) return;  // the factors are read before the next rise
+                }
+            }
+            if (ts >= C::NP) bad |= !wait(&mi.p_empty[ts % C::NP], (ts / C::NP - 1) & 1, abort);
+            unsigned char *pb = sm + C::P + (ts % C::NP) * (NH * 128);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float e = tc::exp2_approx(s[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+                l[i] += e;
+                // bf16: the product's operands share one type, and V is bf16
+                tc::store_bf16(pb + tc::km16(side * N + i, row, NH), e);
+            }
+            if (left < kRows) {  // rows past the end may hold anything: their weight is 0, so their values must be finite
+                for (int e = tid; e < (kRows - left) * 64; e += 128) {
+                    const int rr = left + (e >> 6), c = e & 63;  // 16-byte piece c of the row's 8 panels
+                    const int slot = (4 * ts + (c >> 4)) % C::NA;
+                    *reinterpret_cast<uint4 *>(sm + C::A + slot * kPair + ((c >> 3) & 1) * kPanel + rr * 128 +
+                                               (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&mi.p_full[ts % C::NP]);
+        }
+        // the unit's end: sums over the rows, then O^T out
+        float r[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = l[i];
+        const int at = side * N + half_warp_reduce<N, false>(r, lane);
+        bad |= !wait(&mi.o_full, units & 1, abort);
+        ++units;
+        if (bar_sync_or(1, 128, bad)) return;  // every read of the last maxima is done
+#pragma unroll
+        for (int i = 0; i < PER; ++i) mi.red[0][warp][at + i] = r[i];
+        if (warp == 0 && (lane & 15) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) mi.red[1][0][side * N + i] = m[i];
+        if (bar_sync_or(1, 128, bad)) return;
+        const int h0 = u.w.hg * NH, hs = min(NH, p.heads - h0);
+        const bool whole = u.tiles == u.n;
+        const int slot = u.first ? 2 * u.w.cta : 2 * u.w.cta + 1;
+        if (tid < NH) {
+            const float sum = (mi.red[0][0][tid] + mi.red[0][1][tid]) + (mi.red[0][2][tid] + mi.red[0][3][tid]);
+            const float mx = mi.red[1][0][tid];
+            mi.fac[tid] = sum == 0.f ? 0.f : 1.f / sum;
+            if (whole) {
+                if (p.lse && tid < hs) p.lse[(int64_t)u.w.b * p.heads + h0 + tid] = mx * kLn2 + logf(sum);
+            } else {
+                float *ml = latent_ml(p.workspace) + ((size_t)slot * NH + tid) * 2;
+                ml[0] = mx;
+                ml[1] = sum;
+            }
+        }
+        if (bar_sync_or(1, 128, bad)) return;
+        tc_fence_after_sync();
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((int64_t)u.w.b * p.heads + h0) * kLatR + tid;
+        float *part = latent_part(p.workspace, NH) + (size_t)slot * NH * kLatR + tid;
+#pragma unroll 1
+        for (int c = 0; c < 4 * NH; c += 16) {
+            float x[16];
+            tmem_ld16(tmem + quarter + c, x);
+            tmem_ld_wait();
+            const int i = c / NH, hb = c & (NH - 1);  // channels 128 i + tid of heads hb ...
+            if (whole) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (hb + k < hs) store_io(o + (size_t)(hb + k) * kLatR + 128 * i, x[k] * mi.fac[hb + k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (hb + k < hs) part[(size_t)(hb + k) * kLatR + 128 * i] = x[k];
+            }
+        }
+        tc_fence_before_sync();
+        mbar_arrive(&mi.o_empty);
+        if (bar_sync_or(1, 128, bad)) return;  // fac and red are free again
+    }
+}
+
+template <int NH>
+__global__ void __launch_bounds__(kT, 1)
+latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMap tm, int piece_rows)
+{
+    using C = Cfg<NH>;
+    static_assert(C::MISC + sizeof(Misc<NH>) <= kSmemMax, "shared memory");
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Misc<NH> &mi = *reinterpret_cast<Misc<NH> *>(sm + C::MISC);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_u32(sm) & 1023u) {  // the swizzled panels need it; never seen
+        if (tid == 0 && p.errors) atomicOr(p.errors, DEV_ERR_TIMEOUT);
+        return;
+    }
+    if (tid == 0) {
+        prefetch_tmap(&tm);
+        for (int i = 0; i < C::NA; ++i) {
+            mbar_init(&mi.full_a[i], 1);
+            mbar_init(&mi.empty_a[i], 1);
+        }
+        for (int i = 0; i < C::NB; ++i) {
+            mbar_init(&mi.full_b[i], 1);
+            mbar_init(&mi.empty_b[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&mi.s_full[i], 1);
+            mbar_init(&mi.s_empty[i], 128);
+            mbar_init(&mi.p_full[i], 128);
+            mbar_init(&mi.p_empty[i], 1);
+        }
+        mbar_init(&mi.q_full, 64);
+        mbar_init(&mi.q_empty, 1);
+        mbar_init(&mi.o_full, 1);
+        mbar_init(&mi.o_empty, 128);
+        mbar_init(&mi.drained, 1);
+        fence_mbar_init();
+        mi.abort = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(&mi.tmem, C::COLS);
+        tmem_relinquish();
+    }
+    const LatentWalk w = latent_walk<kT, __nv_bfloat16>(
+        p.lens, p.batch, (int64_t)p.table_width * p.page_size, kRows, (p.heads + NH - 1) / NH, p.heads,
+        static_cast<__nv_bfloat16 *>(p.o), p.lse, p.errors, mi.scan);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = mi.tmem;
+    if (tid == 0) {
+        bool ignore = false;
+        const int len = w.cta < w.ctas ? latent_len(p.lens, w.b, (int64_t)p.table_width * p.page_size, ignore) : 0;
+        latent_record_join(w, (len + kRows - 1) / kRows, NH, p.workspace);
+    }
+    __syncwarp();
+    if (w.cta < w.ctas) {
+        const Units u(p, w);
+        if (warp == 0) copy_role<NH>(sm, mi, p, u, tm, piece_rows, lane);
+        else if (warp == 1) {
+            if (lane == 0) {
+                mma_role<NH>(smem_u32(sm), mi, u, tmem);
+                if (*(volatile int *)&mi.abort) {  // nothing in flight when tensor memory is given back
+                    mma_commit(&mi.drained);
+                    mbar_wait_ns(&mi.drained, 0, kWait);
+                }
+            }
+            __syncwarp();
+        } else if (warp < 4) query_role<NH>(sm, mi, p, u, tid - 64);
+        else softmax_role<NH>(sm, mi, p, u, tmem, tid - 128);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    pdl_launch_dependents();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::COLS);
+    }
+    if (tid == 0 && mi.abort && p.errors) atomicOr(p.errors, DEV_ERR_TIMEOUT);
+}
+
+template <int NH>
+cudaError_t launch(const LatentDecode &p, int grid)
+{
+    tc::EncodeTiledFn enc = tc::encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    static int configured = -1;
+    cudaError_t err = tc::allow_smem(latent_decode_tc_kernel<NH>, kSmemMax, &configured);
+    if (err != cudaSuccess) return err;
+    // the cache as [channel panel][row][64 channels]; a copy is one panel of the rows that tile and
+    // page have in common
+    int piece = 64;
+    while (p.page_size % piece) piece /= 2;
+    const int64_t rows = p.num_pages * p.page_size;
+    CUtensorMap tm;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)(rows > 0 ? rows : 1), 9};
+    const cuuint64_t strides[2] = {kLatC * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)piece, 1}, es[3] = {1, 1, 1};
+    // (without pages every copy starts past the one row that is declared)
+    void *base = rows > 0 ? const_cast<void *>(p.cache) : static_cast<void *>(p.workspace);
+    if (enc(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    latent_decode_tc_kernel<NH><<<grid, kT, kSmemMax, p.stream>>>(p, tm, piece);
+    err = cudaGetLastError();
+    return err != cudaSuccess ? err : launch_latent_join(p, NH, grid);
+}
+
+// Heads per tile: the smallest of 16, 32 and 64 that holds them all, else tiles of 64 (each reads
+// the cache again, from L2).
+int head_tile(int heads) { return heads <= 16 ? 16 : (heads <= 32 ? 32 : 64); }
+
+}  // namespace
+
+size_t latent_decode_tc_ws_bytes(int heads) { return latent_ws_bytes(head_tile(heads), 152); }
+
+cudaError_t launch_latent_decode_tc(const LatentDecode &p)
+{
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    const int nh = head_tile(p.heads);
+    // no more CTAs than there can be tiles
+    const int64_t per_seq = ((int64_t)p.table_width * p.page_size + kRows - 1) / kRows;
+    const int64_t most = per_seq * p.batch * ((p.heads + nh - 1) / nh);
+    int grid = sms < 152 ? sms : 152;
+    if (most < grid) grid = most > 0 ? (int)most : 1;
+    return nh == 16 ? launch<16>(p, grid) : nh == 32 ? launch<32>(p, grid) : launch<64>(p, grid);
+}
+
+}  // namespace kda
