@@ -615,7 +615,8 @@ kda_status_t kda_latent_decode(const void *q, int64_t q_batch_stride, int64_t q_
  *  q        [q_tokens, num_heads, d_nope + d_pe], token and head strides
  *  k_nope   [k_tokens, num_heads, d_nope], v [k_tokens, num_heads, d_v], token and head
  *           strides (parts of one up-projection's rows, for instance); k_pe
- *           [k_tokens, d_pe], row stride, shared by the heads
+ *           [k_tokens, d_pe], row stride, shared by the heads.  A head stride of 0 shares
+ *           the rows among the heads; token strides are not 0
  *  cu_q, cu_k  [num_seqs + 1] int32 device prefix sums ending at q_tokens and k_tokens.
  *           cu_k NULL: cu_q (k_tokens == q_tokens); both NULL: one sequence.  A malformed
  *           array is reported (KDA_DEVICE_ERR_SEQLENS) and held to the buffers; the rows

@@ -68,6 +68,7 @@ kda_status_t check_device();  // kda_api.cu
 cudaError_t launch_latent_append(const LatentAppend &p);
 cudaError_t launch_latent_decode_simt(const LatentDecode &p);
 cudaError_t launch_latent_prefill_simt(const LatentPrefill &p);
+cudaError_t launch_latent_prefill_tc(const LatentPrefill &p);  // bf16
 cudaError_t launch_latent_decode_tc(const LatentDecode &p);  // bf16
 size_t latent_decode_simt_ws_bytes();
 size_t latent_decode_tc_ws_bytes(int heads);
@@ -110,12 +111,12 @@ cudaError_t launch_latent_join(const LatentDecode &p, int head_tile, int grid);
 #ifdef __CUDACC__
 // ---------------------------------------------------------------- expanded prefill: query tiles
 // A tile of one sequence's queries: rows from query q0 (global), the sequence's keys from k0
-// (global), how many of them the tile's last row sees, and the last key (counted from k0) that its
-// first row sees when causal.  rows 0: no tile has this number.
+// (global) and their count, how many of them the tile's last row sees, and the last key (counted
+// from k0) that its first row sees when causal.  rows 0: no tile has this number.
 struct LatentTile {
     int64_t q0, k0;
     int rows;
-    int64_t keys, off;
+    int64_t klen, keys, off;
 };
 
 // Sequence n's tiles are numbered from cu_q[n] / m + n, which increases with n and leaves room for
@@ -143,8 +144,8 @@ __device__ __forceinline__ LatentTile latent_tile(const LatentPrefill &p, int ti
     t.k0 = k0;
     t.rows = (int)max((int64_t)0, min((int64_t)m, q1 - first));
     t.off = (first - q0) + (k1 - k0) - (q1 - q0);
-    t.keys = k1 - k0;
-    if (p.causal) t.keys = max((int64_t)0, min(t.keys, t.off + t.rows));
+    t.klen = k1 - k0;
+    t.keys = p.causal ? max((int64_t)0, min(t.klen, t.off + t.rows)) : t.klen;
     return t;
 }
 

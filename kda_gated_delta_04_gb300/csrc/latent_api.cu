@@ -136,7 +136,8 @@ kda_status_t kda_latent_prefill(const void *q, int64_t q_token_stride, int64_t q
         return KDA_ERR_INVALID_ARG;
     if (!stride_ok(q_token_stride, es) || !stride_ok(q_head_stride, es) || !stride_ok(k_token_stride, es) ||
         !stride_ok(k_head_stride, es) || !stride_ok(k_pe_stride, es) || !stride_ok(v_token_stride, es) ||
-        !stride_ok(v_head_stride, es))
+        !stride_ok(v_head_stride, es) || (q_tokens > 1 && q_token_stride == 0) ||
+        (k_tokens > 1 && (k_token_stride == 0 || k_pe_stride == 0 || v_token_stride == 0)))
         return KDA_ERR_INVALID_ARG;
     const kda_status_t st = kda::check_device();
     if (st != KDA_OK) return st;
@@ -148,7 +149,8 @@ kda_status_t kda_latent_prefill(const void *q, int64_t q_token_stride, int64_t q
     p.q_tokens = q_tokens; p.k_tokens = k_tokens; p.heads = num_heads; p.scale_log2 = scale * kda::kLatLog2e;
     p.causal = !(flags & KDA_LATENT_FULL); p.o = o; p.lse = lse; p.dtype = dtype;
     p.errors = device_errors; p.stream = static_cast<cudaStream_t>(stream);
-    return kda::launch_latent_prefill_simt(p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t err = dtype == KDA_DTYPE_BF16 ? kda::launch_latent_prefill_tc(p) : kda::launch_latent_prefill_simt(p);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -164,7 +164,7 @@ cudaError_t launch_simt(const LatentPrefill &p)
 
 cudaError_t launch_latent_prefill_simt(const LatentPrefill &p)
 {
-    return p.dtype == KDA_DTYPE_BF16 ? launch_simt<__nv_bfloat16>(p) : launch_simt<float>(p);
+    return launch_simt<float>(p);
 }
 
 }  // namespace kda
