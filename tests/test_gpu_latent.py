@@ -382,6 +382,21 @@ def test_prefill_on_another_stream_and_in_a_graph():
     ref.check(o, lse, want, "graph")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.07, 1e-3, 1.5])
+def test_other_scales(dtype, scale):
+    """A scale of 0 (the mean of the seen values), a negative one, a tiny and a large one."""
+    g = gen(45)
+    dt = DT[dtype]
+    q, kn, kp, v, cu, _ = prefill_inputs(g, 2, [130, 31], [130, 31], dt, kscale=0.3)
+    ref.check(*kda.latent_prefill(q, kn, kp, v, scale, cu), ref.prefill(q, kn, kp, v, scale, [130, 31], [130, 31], True),
+              "prefill")
+    cache, table = paged(g, [130, 31], 16, dt, scale=0.3)
+    qd = normal(g, 2, 16, 576, dtype=dt)
+    o, lse = kda.latent_decode(qd, cache, table, torch.tensor([130, 31], dtype=torch.int32, device="cuda"), scale)
+    ref.check(o, lse, ref.decode(qd, cache, table, [130, 31], scale), "decode")
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_the_two_forms_agree(dtype):
