@@ -6,18 +6,21 @@
 // A sequence of lq queries and lk keys is aligned at its end: query i sees keys j <= i + lk - lq
 // (causal) or all.  Bound by the tensor cores: 640 FLOP per (query, key, head) against a few bytes.
 //
-// One CTA per SM holds 256 queries of one head as two tiles of 128 and passes over the keys in
-// tiles of 128.  Both products have M = 128 queries in the 128 lanes of tensor memory:
+// A pair of CTAs (a cluster of two, one CTA per SM) holds 512 queries of one head as two tiles of 256
+// and passes over the keys in tiles of 128.  A matrix instruction spans the pair (M = 256): each CTA
+// holds its 128 queries of a tile, half of K's rows and half of V's columns, so that a key tile takes
+// 40 KB a CTA instead of 80, and an instruction reads 6 KB of shared memory in its 64 cycles instead
+// of 8 (the limit).  One CTA alone left 4,600 cycles for what the tensor cores do in 2,560: its ring
+// held 1.6 key tiles, and the copies' writes competed with operand reads at the limit.
 //
-//   S [128 x 128] = Q [128 x 192] K^T          12 steps of K = 16, operands in shared memory
-//   O [128 x 128] += P [128 x 128] V            8 steps, P (bf16) in tensor memory over its S
+//   S [256 x 128] = Q [256 x 192] K^T          12 steps of K = 16, operands in shared memory
+//   O [256 x 128] += P [256 x 128] V            8 steps, P (bf16) in tensor memory over its S
 //
 // Tensor memory is full: two O, two S of 128 columns.  The two query tiles take turns: while one
 // tile's softmax runs (a warpgroup each, a thread per query, so that maximum and sum need no other
 // thread), the tensor cores run the other tile's products, O += P V of key tile j and S of j + 1.
-// K arrives in a ring of four 64-channel panels, each given back as soon as the second query tile
-// has read it, V in two buffers.  Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions;
-// 10 and 11 only make up the warpgroup whose registers the softmax takes over.
+// Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10 and 11 only
+// make up the warpgroup whose registers the softmax takes over.
 #include <math.h>
 
 #include "latent.cuh"
@@ -29,39 +32,52 @@ namespace {
 using namespace ptx;
 using tc::kdesc;
 
-constexpr int kT = 384, kM = 128, kN = 128;   // threads; queries and keys per tile
-constexpr uint32_t kPanel = 128 * 128;        // bytes: 128 rows x 64 channels
-constexpr int kNK = 4, kNV = 2;               // K panel slots, V buffers
+constexpr int kT = 384, kM = 128, kN = 128;   // threads; queries of a tile in one CTA; keys per tile
+constexpr int kPairM = 4 * kM;                // queries of a pair of CTAs
+constexpr uint32_t kPanelQ = 128 * 128;       // bytes: 128 queries x 64 channels
+constexpr uint32_t kPanelK = 64 * 128;        // half of a tile's keys x 64 channels
+constexpr uint32_t kTileK = 3 * kPanelK, kTileV = 128 * 128;  // a CTA's part of a K and a V tile
+constexpr int kStages = 3;                    // key tiles in shared memory
 constexpr int kAhead = 4;                     // key tiles brought into L2 before their copy
 constexpr uint32_t kOffQ = 0;                 // two tiles of three panels
-constexpr uint32_t kOffK = kOffQ + 6 * kPanel;
-constexpr uint32_t kOffV = kOffK + kNK * kPanel;
-constexpr uint32_t kOffMisc = kOffV + kNV * 2 * kPanel;
+constexpr uint32_t kOffK = kOffQ + 6 * kPanelQ;
+constexpr uint32_t kOffV = kOffK + kStages * kTileK;
+constexpr uint32_t kOffMisc = kOffV + kStages * kTileV;
 constexpr uint64_t kWait = tc::kWaitNs;
 constexpr float kSlack = 8.f;  // log2: how far scores may pass the held maximum before it is moved
 constexpr uint32_t kColO = 0, kColS = 256;    // + 128 x query tile
 
+// Barriers of the leading CTA only: q_full, k_full, v_full (bytes that both CTAs copy), p_full and
+// o_empty (a warp's arrival each, both CTAs).  The others each CTA has for itself; what the matrix
+// instructions signal arrives in both.
 struct Misc {
-    uint64_t q_full[2], k_full[kNK], k_empty[kNK], v_full[kNV], v_empty[kNV], s_full[2], p_full[2][2], o_full[2], drained;
+    uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], v_tail, drained;
     uint32_t tmem;
     int abort;
 };
 constexpr int kSmem = kOffMisc + (int)sizeof(Misc);
 static_assert(kSmem <= 232448, "shared memory");
 
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+// Waits for a phase; gives up after kWait ns or as soon as another role of the CTA has.  The same
+// answer on every lane of the (converged) warp.
+template <bool CLUSTER>
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > kWait) {
-            *abort = 1;
-            return false;
+    auto test = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    bool ok = test();
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+            for (int i = 0; i < 32 && !ok; ++i) ok = test();
+            if (ok || *abort) break;
+            if (globaltimer_ns() - t0 > kWait) {
+                *abort = 1;
+                break;
+            }
         }
     }
+    return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32])
@@ -104,162 +120,171 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// What one CTA works on, and how many key tiles each of its query tiles sees.
+// What a pair of CTAs works on, and how many key tiles each of its query tiles sees.
 struct Job {
-    LatentTile at;   // of all 256 queries
-    int64_t lk;      // the sequence's keys
+    LatentTile at;  // of all 512 queries
     int n0, n1, nmax;
+    bool tail;      // the last key tile reaches past the sequence's keys
     __device__ __forceinline__ int n(int i) const { return i ? n1 : n0; }
-    __device__ __forceinline__ int rows(int i) const { return max(0, min(kM, at.rows - kM * i)); }
-    __device__ __forceinline__ int64_t off(int i) const { return at.off + kM * i; }
+    // first of this CTA's rows of tile i, and their count
+    __device__ __forceinline__ int first(int i, int rank) const { return 2 * kM * i + kM * rank; }
+    __device__ __forceinline__ int rows(int i, int rank) const { return max(0, min(kM, at.rows - first(i, rank))); }
 };
 
 __device__ __forceinline__ Job make_job(const LatentPrefill &p, int tile)
 {
     Job j;
-    j.at = latent_tile(p, tile, 2 * kM);
-    j.lk = j.at.klen;
+    j.at = latent_tile(p, tile, kPairM);
     auto tiles = [&](int i) {
-        int64_t keys = j.lk;
-        if (p.causal) keys = max((int64_t)0, min(keys, j.off(i) + j.rows(i)));
-        return j.rows(i) > 0 ? (int)((keys + kN - 1) / kN) : 0;
+        const int rows = max(0, min(2 * kM, j.at.rows - 2 * kM * i));
+        int64_t keys = j.at.klen;
+        if (p.causal) keys = max((int64_t)0, min(keys, j.at.off + 2 * kM * i + rows));
+        return rows > 0 ? (int)((keys + kN - 1) / kN) : 0;
     };
     j.n0 = tiles(0);
     j.n1 = tiles(1);
     j.nmax = max(j.n0, j.n1);
+    j.tail = j.nmax > 0 && (int64_t)j.nmax * kN > j.at.klen;
     return j;
 }
 
+// One warp of each CTA.
 __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const Job &job, const CUtensorMap &tq,
                                           const CUtensorMap &tk, const CUtensorMap &tp, const CUtensorMap &tv, int h,
-                                          int kh, int vh)
+                                          int kh, int vh, int rank, int lane)
 {
     volatile int *abort = &mi.abort;
-    int nk = 0, nv = 0;
     const int k0 = (int)job.at.k0, q0 = (int)job.at.q0;
+    const bool lead = lane == 0, leader = rank == 0;
+    auto ahead = [&](int j) {  // this CTA's part of key tile j into L2
+        if (!lead || j >= job.nmax) return;
+        const int k = k0 + kN * j;
+        tma_prefetch_3d(&tk, 0, kh, k + 64 * rank);
+        tma_prefetch_3d(&tk, 64, kh, k + 64 * rank);
+        tma_prefetch_3d(&tp, 0, 0, k + 64 * rank);
+        tma_prefetch_3d(&tv, 64 * rank, vh, k);
+    };
     auto queries = [&](int i) {
-        if (job.n(i) == 0) return;
-        mbar_arrive_expect_tx(&mi.q_full[i], 3 * kPanel);
+        if (!lead || job.n(i) == 0) return;
+        if (leader) mbar_arrive_expect_tx(&mi.q_full[i], 2 * 3 * kPanelQ);
+        const uint32_t bar = map_to_rank(&mi.q_full[i], 0);
 #pragma unroll
         for (int c = 0; c < 3; ++c)
-            tma_load_3d(sm + kOffQ + (3 * i + c) * kPanel, &tq, &mi.q_full[i], 64 * c, h, q0 + kM * i);
-    };
-    auto ahead = [&](int j) {  // key tile j into L2
-        if (j >= job.nmax) return;
-        const int k = k0 + kN * j;
-        tma_prefetch_3d(&tk, 0, kh, k);
-        tma_prefetch_3d(&tk, 64, kh, k);
-        tma_prefetch_3d(&tp, 0, 0, k);
-        tma_prefetch_3d(&tv, 0, vh, k);
-        tma_prefetch_3d(&tv, 64, vh, k);
+            tma_load_3d_pair(sm + kOffQ + (3 * i + c) * kPanelQ, &tq, bar, 64 * c, h, q0 + job.first(i, rank));
     };
     queries(0);
-    bool ok = true;
     for (int j = 1; j < kAhead; ++j) ahead(j);
-    for (int j = 0; j < job.nmax && ok; ++j) {
+    int t = 0;
+    bool ok = true;
+    for (int j = 0; j < job.nmax; ++j, ++t) {
         ahead(j + kAhead);
-        for (int c = 0; c < 3 && ok; ++c) {
-            const int slot = nk % kNK;
-            if (nk >= kNK) ok = wait(&mi.k_empty[slot], (nk / kNK - 1) & 1, abort);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&mi.k_full[slot], kPanel);
-            unsigned char *dst = sm + kOffK + slot * kPanel;
-            if (c < 2) tma_load_3d(dst, &tk, &mi.k_full[slot], 64 * c, kh, k0 + kN * j);
-            else tma_load_3d(dst, &tp, &mi.k_full[slot], 0, 0, k0 + kN * j);
-            ++nk;
+        const int slot = t % kStages, k = k0 + kN * j;
+        if (t >= kStages && !(ok = all_wait<false>(&mi.k_empty[slot], (t / kStages - 1) & 1, abort))) break;
+        if (lead) {
+            if (leader) mbar_arrive_expect_tx(&mi.k_full[slot], 2 * kTileK);
+            const uint32_t bar = map_to_rank(&mi.k_full[slot], 0);
+            unsigned char *dst = sm + kOffK + slot * kTileK;
+            tma_load_3d_pair(dst, &tk, bar, 0, kh, k + 64 * rank);
+            tma_load_3d_pair(dst + kPanelK, &tk, bar, 64, kh, k + 64 * rank);
+            tma_load_3d_pair(dst + 2 * kPanelK, &tp, bar, 0, 0, k + 64 * rank);
         }
         if (j == 0) queries(1);
-        if (!ok) break;
-        const int slot = nv % kNV;
-        if (nv >= kNV) ok = wait(&mi.v_empty[slot], (nv / kNV - 1) & 1, abort);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&mi.v_full[slot], 2 * kPanel);
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            tma_load_3d(sm + kOffV + (2 * slot + c) * kPanel, &tv, &mi.v_full[slot], 64 * c, vh, k0 + kN * j);
-        ++nv;
+        if (t >= kStages && !(ok = all_wait<false>(&mi.v_empty[slot], (t / kStages - 1) & 1, abort))) break;
+        if (lead) {
+            unsigned char *dst = sm + kOffV + slot * kTileV;
+            if (job.tail && j == job.nmax - 1) {
+                // each CTA's softmax waits for this part itself (it clears the rows past the end) and
+                // answers for it with its weights
+                if (leader) mbar_arrive(&mi.v_full[slot]);
+                mbar_arrive_expect_tx(&mi.v_tail, kTileV);
+                tma_load_3d(dst, &tv, &mi.v_tail, 64 * rank, vh, k);
+            } else {
+                if (leader) mbar_arrive_expect_tx(&mi.v_full[slot], 2 * kTileV);
+                tma_load_3d_pair(dst, &tv, map_to_rank(&mi.v_full[slot], 0), 64 * rank, vh, k);
+            }
+        }
     }
-    if (!ok) {  // the copies in flight land before the CTA goes
+    if (!ok && lead && leader) {  // the copies in flight land before the pair goes (the other CTA stays for this one)
         for (int i = 0; i < 2; ++i)
             if (job.n(i)) mbar_wait_ns(&mi.q_full[i], 0, kWait);
-        for (int k = max(0, nk - kNK); k < nk; ++k) mbar_wait_ns(&mi.k_full[k % kNK], (k / kNK) & 1, kWait);
-        for (int k = max(0, nv - kNV); k < nv; ++k) mbar_wait_ns(&mi.v_full[k % kNV], (k / kNV) & 1, kWait);
+        for (int k = max(0, t - kStages); k < t; ++k) {
+            mbar_wait_ns(&mi.k_full[k % kStages], (k / kStages) & 1, kWait);
+            mbar_wait_ns(&mi.v_full[k % kStages], (k / kStages) & 1, kWait);
+        }
     }
 }
 
-// A whole warp's wait: the same answer on every lane.
-__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+// One warp of the leading CTA, in step.
+__device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, const Job &job, uint32_t tmem)
 {
-    return __all_sync(0xffffffffu, wait(bar, parity, abort));
-}
-
-// Executed by one whole warp in step.
-__device__ __forceinline__ void mma_role(uint32_t sb, Misc &mi, const Job &job, uint32_t tmem)
-{
-    constexpr uint32_t id_s = idesc_bf16(kM, kN, false, false), id_o = idesc_bf16(kM, 128, false, true);
+    constexpr uint32_t id_s = idesc_bf16(2 * kM, kN, false, false), id_o = idesc_bf16(2 * kM, 128, false, true);
     volatile int *abort = &mi.abort;
     const uint32_t lead = elect_lead();
     // the second query tile, where there is one, sees every key tile that the first sees
-    const bool two = job.n(1) > 0;
+    const bool two = job.n1 > 0;
     auto scores = [&](int i, int j) -> bool {  // S_i of key tile j
-        const uint32_t d = tmem + kColS + 128 * i;
-#pragma unroll 1
-        for (int c = 0; c < 3; ++c) {
-            const int nk = 3 * j + c, slot = nk % kNK;
-            if (!all_wait(&mi.k_full[slot], (nk / kNK) & 1, abort)) return false;
-            if (c == 0) tc_fence_after_sync();
-            const uint32_t a = sb + kOffQ + (3 * i + c) * kPanel, b = sb + kOffK + slot * kPanel;
+        const int slot = j % kStages;
+        if (!all_wait<true>(&mi.k_full[slot], (j / kStages) & 1, abort)) return false;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + kColS + 128 * i, a = sb + kOffQ + 3 * i * kPanelQ, b = sb + kOffK + slot * kTileK;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_bf16_lead(lead, d, kdesc(a + k * 32), kdesc(b + k * 32), id_s, c > 0 || k > 0);
-            if (i == (two ? 1 : 0)) mma_commit_lead(lead, &mi.k_empty[slot]);
-        }
-        mma_commit_lead(lead, &mi.s_full[i]);
+        for (int c = 0; c < 3; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_bf16_pair(lead, d, kdesc(a + c * kPanelQ + k * 32), kdesc(b + c * kPanelK + k * 32), id_s,
+                              c > 0 || k > 0);
+        mma_commit_pair(lead, &mi.s_full[i]);
+        if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.k_empty[slot]);
         return true;
     };
     auto values = [&](int i, int j) -> bool {  // O_i += P_i V of key tile j
-        const int slot = j % kNV;
-        if (!all_wait(&mi.v_full[slot], (j / kNV) & 1, abort)) return false;
-        const uint32_t d = tmem + kColO + 128 * i, a = tmem + kColS + 128 * i, b = sb + kOffV + 2 * slot * kPanel;
+        const int slot = j % kStages;
+        if (!all_wait<true>(&mi.v_full[slot], (j / kStages) & 1, abort)) return false;
+        const uint32_t d = tmem + kColO + 128 * i, a = tmem + kColS + 128 * i, b = sb + kOffV + slot * kTileV;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if ((k & 3) == 0) {
-                if (!all_wait(&mi.p_full[i][k >> 2], j & 1, abort)) return false;
+                if (!all_wait<true>(&mi.p_full[i][k >> 2], j & 1, abort)) return false;
                 tc_fence_after_sync();
             }
-            mma_tmem_a_lead(lead, d, a + 8 * k, sdesc(b + k * 2048, kPanel, 1024, kSw128B), id_o, j > 0 || k > 0);
+            mma_tmem_a_pair(lead, d, a + 8 * k, sdesc(b + k * 2048, kTileV, 1024, kSw128B), id_o, j > 0 || k > 0);
         }
-        if (i == (two ? 1 : 0)) mma_commit_lead(lead, &mi.v_empty[slot]);
-        if (j + 1 == job.n(i)) mma_commit_lead(lead, &mi.o_full[i]);
+        if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.v_empty[slot]);
+        if (j + 1 == job.n(i)) mma_commit_pair(lead, &mi.o_full[i]);
         return true;
     };
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         if (job.n(i) == 0) continue;
-        if (!all_wait(&mi.q_full[i], 0, abort)) return;
-        if (!scores(i, 0)) return;
+        if (!all_wait<true>(&mi.q_full[i], 0, abort) || !scores(i, 0)) return false;
     }
 #pragma unroll 1
     for (int j = 0; j < job.nmax; ++j)
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             if (j >= job.n(i)) continue;
-            if (!values(i, j)) return;
-            if (j + 1 < job.n(i) && !scores(i, j + 1)) return;
+            if (!values(i, j)) return false;
+            if (j + 1 < job.n(i) && !scores(i, j + 1)) return false;
         }
+    return true;
 }
 
+// A warpgroup of each CTA per query tile, a thread per query.
 __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const LatentPrefill &p, const Job &job,
-                                             uint32_t tmem, int i, int h)
+                                             uint32_t tmem, int i, int h, int rank)
 {
     volatile int *abort = &mi.abort;
-    const int row = threadIdx.x & 127;
+    const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t quarter = (uint32_t)((row >> 5) * 32) << 16;
     const uint32_t ts = tmem + kColS + 128 * i + quarter, to = tmem + kColO + 128 * i + quarter;
-    const int64_t last = p.causal ? min(job.off(i) + row, job.lk - 1) : job.lk - 1;  // last key this query sees
+    const uint32_t full[2] = {map_to_rank(&mi.p_full[i][0], 0), map_to_rank(&mi.p_full[i][1], 0)};
+    // last key this query sees
+    const int64_t last = p.causal ? min(job.at.off + job.first(i, rank) + row, job.at.klen - 1) : job.at.klen - 1;
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    const int n = job.n(i);
     float m = -INFINITY, l = 0.f;  // held maximum (log2 units) and the sum of the weights
-    for (int j = 0; j < job.n(i); ++j) {
-        if (!__all_sync(0xffffffffu, wait(&mi.s_full[i], j & 1, abort))) return;
+    for (int j = 0; j < n; ++j) {
+        if (!all_wait<false>(&mi.s_full[i], j & 1, abort)) return;
         tc_fence_after_sync();
         float s[128];
 #pragma unroll
@@ -280,7 +305,7 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
         // the maximum is moved only where a score passes it by kSlack: weights are below 2^kSlack, and
         // the precision of fp32 and bf16 does not depend on that
         const bool rise = mx > m + kSlack;
-        const int64_t left = job.lk - (int64_t)j * kN;
+        const int64_t left = job.at.klen - (int64_t)j * kN;
         if (__any_sync(0xffffffffu, rise) || left < kN) {
             float f = 1.f;
             if (rise) {
@@ -303,14 +328,12 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
             // keys past the sequence's end are other sequences' rows: their weight is 0, so their values
             // must be finite
             if (left < kN) {
-                const int slot = j % kNV;
-                if (!__all_sync(0xffffffffu, wait(&mi.v_full[slot], (j / kNV) & 1, abort))) return;
-                for (int e = row; e < (kN - (int)left) * 16; e += 128) {
-                    const int r = (int)left + (e >> 4), c = e & 15;
-                    *reinterpret_cast<uint4 *>(sm + kOffV + (2 * slot + (c >> 3)) * kPanel + r * 128 + (c & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
+                if (!all_wait<false>(&mi.v_tail, 0, abort)) return;
+                for (int e = row; e < (kN - (int)left) * 8; e += 128)
+                    *reinterpret_cast<uint4 *>(sm + kOffV + (j % kStages) * kTileV + ((int)left + (e >> 3)) * 128 +
+                                               (e & 7) * 16) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
+                fence_cluster();
             }
         }
         const float base = m == -INFINITY ? 0.f : -m;
@@ -331,7 +354,8 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
             if (c & 1) {  // the product starts on the first half of the keys
                 tmem_st_wait();
                 tc_fence_before_sync();
-                mbar_arrive(&mi.p_full[i][c >> 1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(full[c >> 1]);
             }
         }
         float2 sum[4] = {};
@@ -340,38 +364,29 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
         const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += all.x + all.y;
     }
-    // O's rows out, through this warp's part of the query tile's memory so that a row is stored whole
-    const int lane = row & 31, warp0 = row & ~31;
-    const int64_t q = job.at.q0 + kM * i;
-    if (p.lse && row < job.rows(i)) p.lse[(q + row) * p.heads + h] = m * kLn2 + logf(l);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    unsigned char *stage = sm + kOffQ + 3 * i * kPanel + warp0 * 256;
-    if (job.n(i) > 0) {
-        if (!__all_sync(0xffffffffu, wait(&mi.o_full[i], 0, abort))) return;
+    if (n > 0) {
+        if (!all_wait<false>(&mi.o_full[i], 0, abort)) return;
         tc_fence_after_sync();
     }
+    const bool mine = row < job.rows(i, rank);
+    const int64_t q = job.at.q0 + job.first(i, rank) + row;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + (q * p.heads + h) * kLatN;
+    if (mine && p.lse) p.lse[q * p.heads + h] = m * kLn2 + logf(l);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        float x[16];
-        if (job.n(i) > 0) {
-            tmem_ld16(to + 16 * c, x);
+    for (int c = 0; c < 4; ++c) {
+        float x[32];
+        if (n > 0) {
+            tmem_ld32(to + 32 * c, x);
             tmem_ld_wait();
         }
-        float y[2][8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) y[k >> 3][k & 7] = job.n(i) > 0 ? x[k] * inv : 0.f;
+        for (int k = 0; k < 32; k += 8) {
+            float y[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<uint4 *>(stage + lane * 256 + (((2 * c + k) ^ (lane & 15)) << 4)) = tc::pack_bf16x8(y[k]);
-    }
-    __syncwarp();
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + (q * p.heads + h) * kLatN;
-#pragma unroll 4
-    for (int r = lane >> 4; r < 32; r += 2) {
-        const int c = lane & 15;
-        const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 256 + ((c ^ (r & 15)) << 4));
-        if (warp0 + r < job.rows(i))
-            *reinterpret_cast<uint4 *>(o + (int64_t)(warp0 + r) * p.heads * kLatN + 8 * c) = x;
+            for (int u = 0; u < 8; ++u) y[u] = n > 0 ? x[k + u] * inv : 0.f;
+            if (mine) *reinterpret_cast<uint4 *>(o + 32 * c + k) = tc::pack_bf16x8(y);
+        }
     }
 }
 
@@ -383,79 +398,78 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     extern __shared__ __align__(1024) unsigned char sm[];
     Misc &mi = *reinterpret_cast<Misc *>(sm + kOffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     // heads innermost, the tiles with the most keys first
-    const int h = blockIdx.x % p.heads, tile = (int)(gridDim.x / p.heads - 1 - blockIdx.x / p.heads);
+    const int h = pair % p.heads, tile = pairs / p.heads - 1 - pair / p.heads;
     const Job job = make_job(p, tile);
     if (blockIdx.x == 0) {
         latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
         latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);
     }
-    if (job.at.rows <= 0) return;
-    if (smem_u32(sm) & 1023u) {  // the swizzled panels need it; never seen
+    if (job.at.rows <= 0) return;  // both CTAs of the pair
+    if (smem_u32(sm) & 1023u) {    // the swizzled panels need it; never seen
         if (tid == 0 && p.errors) atomicOr(p.errors, DEV_ERR_TIMEOUT);
         return;
     }
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&mi.q_full[i], 1);
+            mbar_init(&mi.q_empty[i], 1);
             mbar_init(&mi.s_full[i], 1);
-            mbar_init(&mi.p_full[i][0], 128);
-            mbar_init(&mi.p_full[i][1], 128);
+            mbar_init(&mi.p_full[i][0], 8);
+            mbar_init(&mi.p_full[i][1], 8);
             mbar_init(&mi.o_full[i], 1);
+            mbar_init(&mi.o_empty[i], 8);
         }
-        for (int i = 0; i < kNK; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&mi.k_full[i], 1);
             mbar_init(&mi.k_empty[i], 1);
-        }
-        for (int i = 0; i < kNV; ++i) {
             mbar_init(&mi.v_full[i], 1);
             mbar_init(&mi.v_empty[i], 1);
         }
+        mbar_init(&mi.v_tail, 1);
         mbar_init(&mi.drained, 1);
         fence_mbar_init();
         mi.abort = 0;
     }
-    if (warp == 9) {
-        tmem_alloc(&mi.tmem, 512);
-        tmem_relinquish();
-    }
+    if (warp == 9) tmem_alloc_pair(&mi.tmem, 512);
     tc_fence_before_sync();
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers are ready
     tc_fence_after_sync();
     const uint32_t tmem = mi.tmem;
     // registers: 384 x 168 at launch; 256 x 216 + 128 x 64 now
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int i = warp >> 2;
-        if (job.rows(i) > 0) softmax_role(sm, mi, p, job, tmem, i, h);
+        softmax_role(sm, mi, p, job, tmem, warp >> 2, h, rank);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 8) {
-            if (lane == 0) copy_role(sm, mi, job, tq, tk, tp, tv, h * q_step, h * k_step, h * v_step);
-        } else if (warp == 9) {
+            copy_role(sm, mi, job, tq, tk, tp, tv, h * q_step, h * k_step, h * v_step, rank, lane);
+        } else if (warp == 9 && rank == 0) {
             // (the reduction's result is uniform to the compiler, the loaded word is not)
-            mma_role(smem_u32(sm), mi, job, __reduce_or_sync(0xffffffffu, tmem));
-            __syncwarp();
-            if (lane == 0 && *(volatile int *)&mi.abort) {  // nothing in flight when tensor memory is given back
-                mma_commit(&mi.drained);
-                mbar_wait_ns(&mi.drained, 0, kWait);
+            if (!mma_role(smem_u32(sm), mi, job, __reduce_or_sync(0xffffffffu, tmem))) {
+                // nothing in flight when tensor memory is given back
+                mma_commit_pair(lane == 0, &mi.drained);
+                all_wait<false>(&mi.drained, 0, &mi.abort);
             }
         }
     }
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
+    cluster_sync();  // neither CTA goes while the other's instructions use its memory
     if (warp == 9) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
     if (tid == 0 && mi.abort && p.errors) atomicOr(p.errors, DEV_ERR_TIMEOUT);
 }
 
-// [tokens][heads][channels] with any strides as a tensor of boxes of 128 tokens x 64 channels of one
-// head; `step` is the head coordinate's step: 0 where the heads share their rows.
+// [tokens][heads][channels] with any strides as a tensor of boxes of `box_rows` tokens x 64 channels of
+// one head; `step` is the head coordinate's step: 0 where the heads share their rows.
 bool make_map(CUtensorMap *m, const void *ptr, int channels, int64_t heads, int64_t hs, int64_t tokens, int64_t ts,
-              int *step)
+              int box_rows, int *step)
 {
     tc::EncodeTiledFn enc = tc::encode_fn();
     if (!enc) return false;
@@ -467,7 +481,7 @@ bool make_map(CUtensorMap *m, const void *ptr, int channels, int64_t heads, int6
     if (ts == 0) ts = channels;  // one token
     const cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)heads, (cuuint64_t)tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)hs * 2, (cuuint64_t)ts * 2};
-    const cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -477,7 +491,7 @@ bool make_map(CUtensorMap *m, const void *ptr, int channels, int64_t heads, int6
 
 cudaError_t launch_latent_prefill_tc(const LatentPrefill &p)
 {
-    const int64_t blocks = (p.q_tokens / (2 * kM) + p.num_seqs) * p.heads;
+    const int64_t blocks = 2 * (p.q_tokens / kPairM + p.num_seqs) * p.heads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     CUtensorMap tq, tk, tp, tv;
     int q_step = 0, k_step = 0, v_step = 0, one = 0;
@@ -485,16 +499,26 @@ cudaError_t launch_latent_prefill_tc(const LatentPrefill &p)
     const bool keys = p.k_tokens > 0;
     const void *kn = keys ? p.k_nope : p.q, *kp = keys ? p.k_pe : p.q, *v = keys ? p.v : p.q;
     const int64_t tokens = keys ? p.k_tokens : 1;
-    if (!make_map(&tq, p.q, kLatQK, p.heads, p.q_hs, p.q_tokens, p.q_ts, &q_step) ||
-        !make_map(&tk, kn, kLatN, p.heads, p.kn_hs, tokens, p.kn_ts, &k_step) ||
-        !make_map(&tp, kp, kLatP, 1, 0, tokens, p.kp_ts, &one) ||
-        !make_map(&tv, v, kLatN, p.heads, p.v_hs, tokens, p.v_ts, &v_step))
+    if (!make_map(&tq, p.q, kLatQK, p.heads, p.q_hs, p.q_tokens, p.q_ts, kM, &q_step) ||
+        !make_map(&tk, kn, kLatN, p.heads, p.kn_hs, tokens, p.kn_ts, 64, &k_step) ||
+        !make_map(&tp, kp, kLatP, 1, 0, tokens, p.kp_ts, 64, &one) ||
+        !make_map(&tv, v, kLatN, p.heads, p.v_hs, tokens, p.v_ts, kN, &v_step))
         return cudaErrorInvalidValue;
     static int configured = -1;
     const cudaError_t err = tc::allow_smem(latent_prefill_tc_kernel, kSmem, &configured);
     if (err != cudaSuccess) return err;
-    latent_prefill_tc_kernel<<<(unsigned)blocks, kT, kSmem, p.stream>>>(p, tq, tk, tp, tv, q_step, k_step, v_step);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kT);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = p.stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_prefill_tc_kernel, p, tq, tk, tp, tv, q_step, k_step, v_step);
 }
 
 }  // namespace kda
