@@ -114,47 +114,51 @@ cudaError_t launch_latent_join(const LatentDecode &p, int head_tile, int grid);
 // (global) and their count, how many of them the tile's last row sees, and the last key (counted
 // from k0) that its first row sees when causal.  rows 0: no tile has this number.
 struct LatentTile {
-    int64_t q0, k0;
-    int rows;
-    int64_t klen, keys, off;
+    int q0, k0, rows, klen, keys, off;
 };
+
+// Token range [t0, t1) of sequence n, held to the buffer (int: the token counts are below 2^31).
+__device__ __forceinline__ void latent_range(const int32_t *cu, int n, int total, int &t0, int &t1)
+{
+    int64_t a, b;
+    seq_range(cu, n, total, a, b);
+    t0 = (int)a;
+    t1 = (int)b;
+}
 
 // Sequence n's tiles are numbered from cu_q[n] / m + n, which increases with n and leaves room for
 // all of them, so that bisection finds a tile's sequence without a table.  A malformed cu_q or
 // cu_k is reported and held to the buffers.
 __device__ __forceinline__ LatentTile latent_tile(const LatentPrefill &p, int tile, int m)
 {
-    int n = 0;
+    int n = 0, q0, q1, k0, k1;
     if (p.cu_q) {
         int hi = p.num_seqs - 1;
         while (n < hi) {  // the last sequence whose first tile is not after `tile`
             const int mid = (n + hi + 1) >> 1;
-            int64_t t0, t1;
-            seq_range(p.cu_q, mid, p.q_tokens, t0, t1);
-            if (t0 / m + mid <= tile) n = mid;
+            latent_range(p.cu_q, mid, (int)p.q_tokens, q0, q1);
+            if (q0 / m + mid <= tile) n = mid;
             else hi = mid - 1;
         }
     }
+    latent_range(p.cu_q, n, (int)p.q_tokens, q0, q1);
+    latent_range(p.cu_k, n, (int)p.k_tokens, k0, k1);
     LatentTile t;
-    int64_t q0, q1, k0, k1;
-    seq_range(p.cu_q, n, p.q_tokens, q0, q1);
-    seq_range(p.cu_k, n, p.k_tokens, k0, k1);
-    const int64_t first = max(q0, q0 + (tile - (q0 / m + n)) * (int64_t)m);
-    t.q0 = first;
+    t.q0 = q0 + max(0, tile - (q0 / m + n)) * m;
     t.k0 = k0;
-    t.rows = (int)max((int64_t)0, min((int64_t)m, q1 - first));
-    t.off = (first - q0) + (k1 - k0) - (q1 - q0);
     t.klen = k1 - k0;
-    t.keys = p.causal ? max((int64_t)0, min(t.klen, t.off + t.rows)) : t.klen;
+    t.rows = max(0, min(m, q1 - t.q0));
+    t.off = (t.q0 - q0) + t.klen - (q1 - q0);
+    t.keys = p.causal ? max(0, min(t.klen, t.off + t.rows)) : t.klen;
     return t;
 }
 
-// Reports a cu array that is not a prefix sum ending at `total`: every thread of one CTA calls it.
+// Reports a cu array that is not a prefix sum ending at `total`: the lanes of one warp call it.
 __device__ __forceinline__ void latent_check_cu(const int32_t *cu, int num_seqs, int64_t total, uint32_t *errors)
 {
     if (!cu || !errors) return;
-    bool bad = threadIdx.x == 0 && (cu[0] != 0 || cu[num_seqs] != total);
-    for (int n = threadIdx.x; n < num_seqs; n += blockDim.x) bad |= cu[n + 1] < cu[n];
+    bool bad = cu[0] != 0 || cu[num_seqs] != total;
+    for (int n = threadIdx.x & 31; n < num_seqs; n += 32) bad |= cu[n + 1] < cu[n];
     if (bad) atomicOr(errors, DEV_ERR_SEQLENS);
 }
 

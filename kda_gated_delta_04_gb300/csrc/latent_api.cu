@@ -11,6 +11,9 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // A stride in elements: not negative and a whole number of 16-byte pieces.
 bool stride_ok(int64_t s, size_t es) { return s >= 0 && s <= (int64_t)1 << 40 && (size_t)s * es % 16 == 0; }
 
+// Packed tokens are counted in int32, rounded up to tiles.
+constexpr int64_t kMaxTokens = INT32_MAX - 4096;
+
 size_t elem_size(kda_dtype_t dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
 
 bool dtype_ok(kda_dtype_t dtype) { return dtype == KDA_DTYPE_BF16 || dtype == KDA_DTYPE_F32; }
@@ -127,7 +130,7 @@ kda_status_t kda_latent_prefill(const void *q, int64_t q_token_stride, int64_t q
     if (num_seqs == 0 && (q_tokens != 0 || k_tokens != 0)) return KDA_ERR_INVALID_ARG;
     if (!cu_q && (cu_k || (num_seqs != 1 && num_seqs != 0))) return KDA_ERR_INVALID_ARG;
     if (cu_q && !cu_k && q_tokens != k_tokens) return KDA_ERR_INVALID_ARG;
-    if (num_seqs > 65535 || num_heads > 65535 || q_tokens > INT32_MAX || k_tokens > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || num_heads > 65535 || q_tokens > kMaxTokens || k_tokens > kMaxTokens) return KDA_ERR_UNSUPPORTED;
     if (q_tokens == 0) return KDA_OK;
     const size_t es = elem_size(dtype);
     if (!q || !o || (k_tokens > 0 && (!k_nope || !k_pe || !v))) return KDA_ERR_INVALID_ARG;

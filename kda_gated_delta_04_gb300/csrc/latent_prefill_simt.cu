@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
     // with room for every tile, found by bisection.  Late tiles (most keys) run first.
     const int tile = (int)(gridDim.x - 1 - blockIdx.x);
     const LatentTile at = latent_tile(p, tile, kM);
-    if (tile == 0 && h == 0) {
+    if (tile == 0 && h == 0 && tid < 32) {
         latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
         latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);
     }
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
     for (int e = tid; e < kM * (kLatQK / 4); e += kT) {
         const int r = e / (kLatQK / 4), c = 4 * (e - r * (kLatQK / 4));
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < at.rows) x = load4_io(static_cast<const IO *>(p.q) + (at.q0 + r) * p.q_ts + h * p.q_hs + c);
+        if (r < at.rows) x = load4_io(static_cast<const IO *>(p.q) + (int64_t)(at.q0 + r) * p.q_ts + h * p.q_hs + c);
         *reinterpret_cast<float4 *>(&sm.q[r][c]) = x;
     }
     float m[4], l[4], acc[4][8];
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[i][c] = 0.f;
     }
-    for (int64_t j0 = 0; j0 < at.keys; j0 += kN) {
+    for (int j0 = 0; j0 < at.keys; j0 += kN) {
         __syncthreads();
         for (int e = tid; e < kN * (kLatQK / 4); e += kT) {
             const int r = e / (kLatQK / 4), c = 4 * (e - r * (kLatQK / 4));
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
             const int r = e / (kLatN / 4), c = 4 * (e - r * (kLatN / 4));
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (j0 + r < at.keys)
-                x = load4_io(static_cast<const IO *>(p.v) + (at.k0 + j0 + r) * p.v_ts + h * p.v_hs + c);
+                x = load4_io(static_cast<const IO *>(p.v) + (int64_t)(at.k0 + j0 + r) * p.v_ts + h * p.v_hs + c);
             *reinterpret_cast<float4 *>(&sm.v[r][c]) = x;
         }
         __syncthreads();
@@ -91,11 +91,11 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t last = p.causal ? at.off + 4 * ty + i : at.keys - 1;  // last key this query sees
+            const int last = p.causal ? at.off + 4 * ty + i : at.keys - 1;  // last key this query sees
             float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t key = j0 + tx + 16 * j;
+                const int key = j0 + tx + 16 * j;
                 s[i][j] = key <= last && key < at.keys ? s[i][j] * p.scale_log2 : -INFINITY;
                 mx = fmaxf(mx, s[i][j]);
             }
@@ -142,10 +142,10 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
         const float lo[4] = {acc[i][0] * inv, acc[i][1] * inv, acc[i][2] * inv, acc[i][3] * inv};
         const float hi[4] = {acc[i][4] * inv, acc[i][5] * inv, acc[i][6] * inv, acc[i][7] * inv};
-        IO *o = static_cast<IO *>(p.o) + ((at.q0 + r) * p.heads + h) * kLatN + 4 * tx;
+        IO *o = static_cast<IO *>(p.o) + ((int64_t)(at.q0 + r) * p.heads + h) * kLatN + 4 * tx;
         store_io4(o, lo);
         store_io4(o + 64, hi);
-        if (p.lse && tx == 0) p.lse[(at.q0 + r) * p.heads + h] = m[i] * kLn2 + logf(l[i]);
+        if (p.lse && tx == 0) p.lse[(int64_t)(at.q0 + r) * p.heads + h] = m[i] * kLn2 + logf(l[i]);
     }
 }
 

@@ -47,12 +47,14 @@ constexpr uint64_t kWait = tc::kWaitNs;
 constexpr float kSlack = 8.f;  // log2: how far scores may pass the held maximum before it is moved
 constexpr uint32_t kColO = 0, kColS = 256;    // + 128 x query tile
 
-// Barriers of the leading CTA only: q_full, k_full, v_full (bytes that both CTAs copy), p_full and
-// o_empty (a warp's arrival each, both CTAs).  The others each CTA has for itself; what the matrix
+// Barriers of the leading CTA only: q_full, k_full, v_full (bytes that both CTAs copy), p_full,
+// o_empty and next_empty (a warp's arrival each, both CTAs).  The others each CTA has for itself; what the matrix
 // instructions signal arrives in both.
 struct Misc {
     uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], v_tail, drained;
+    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], v_tail[kStages], drained;
+    uint64_t next_full, next_empty;  // the next job's number: each CTA; all readers, in the leading CTA
+    alignas(16) uint4 next;
     uint32_t tmem;
     int abort;
 };
@@ -123,6 +125,7 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 // What a pair of CTAs works on, and how many key tiles each of its query tiles sees.
 struct Job {
     LatentTile at;  // of all 512 queries
+    int h;          // head
     int n0, n1, nmax;
     bool tail;      // the last key tile reaches past the sequence's keys
     __device__ __forceinline__ int n(int i) const { return i ? n1 : n0; }
@@ -131,165 +134,233 @@ struct Job {
     __device__ __forceinline__ int rows(int i, int rank) const { return max(0, min(kM, at.rows - first(i, rank))); }
 };
 
-__device__ __forceinline__ Job make_job(const LatentPrefill &p, int tile)
+// The job of cluster `pair` of the grid: heads innermost, the tiles with the most keys first.
+__device__ __forceinline__ Job make_job(const LatentPrefill &p, int pair)
 {
+    const int pairs = gridDim.x >> 1;
     Job j;
-    j.at = latent_tile(p, tile, kPairM);
+    j.h = pair % p.heads;
+    j.at = latent_tile(p, pairs / p.heads - 1 - pair / p.heads, kPairM);
     auto tiles = [&](int i) {
         const int rows = max(0, min(2 * kM, j.at.rows - 2 * kM * i));
-        int64_t keys = j.at.klen;
-        if (p.causal) keys = max((int64_t)0, min(keys, j.at.off + 2 * kM * i + rows));
-        return rows > 0 ? (int)((keys + kN - 1) / kN) : 0;
+        int keys = j.at.klen;
+        if (p.causal) keys = max(0, min(keys, j.at.off + 2 * kM * i + rows));
+        return rows > 0 ? (keys + kN - 1) / kN : 0;
     };
     j.n0 = tiles(0);
     j.n1 = tiles(1);
     j.nmax = max(j.n0, j.n1);
-    j.tail = j.nmax > 0 && (int64_t)j.nmax * kN > j.at.klen;
+    j.tail = j.nmax > 0 && j.nmax * kN > j.at.klen;
     return j;
 }
 
+// The jobs of this pair as every role walks them: its own cluster's, then those of clusters that were
+// still waiting to be launched.  The next one is asked for when the last copy of the present one has
+// been issued (copy_role): early enough for the answer to be there, and no sooner, so that the last
+// jobs go to the pairs that are done first.  Every warp of a role calls next in step.
+struct Jobs {
+    Misc &mi;
+    int at, count;
+    __device__ __forceinline__ Jobs(Misc &m) : mi(m), at((int)(blockIdx.x >> 1)), count(0) {}
+    __device__ __forceinline__ bool next(int lane)
+    {
+        if (!all_wait<false>(&mi.next_full, count & 1, &mi.abort)) return false;
+        at = cluster_taken(&mi.next) >> 1;  // (-1 stays -1)
+        fence_proxy_async_smem();           // read before it is written again
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(&mi.next_empty, 0));
+        ++count;
+        return at >= 0;
+    }
+};
+constexpr int kJobReaders = 2 * (8 + 1 + 1);  // warps of both CTAs: softmax, copies, matrix instructions
+
 // One warp of each CTA.
-__device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const Job &job, const CUtensorMap &tq,
-                                          const CUtensorMap &tk, const CUtensorMap &tp, const CUtensorMap &tv, int h,
-                                          int kh, int vh, int rank, int lane)
+__device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const LatentPrefill &p, const CUtensorMap &tq,
+                                          const CUtensorMap &tk, const CUtensorMap &tp, const CUtensorMap &tv,
+                                          int q_step, int k_step, int v_step, int rank, int lane)
 {
     volatile int *abort = &mi.abort;
-    const int k0 = (int)job.at.k0, q0 = (int)job.at.q0;
     const bool lead = lane == 0, leader = rank == 0;
-    auto ahead = [&](int j) {  // this CTA's part of key tile j into L2
-        if (!lead || j >= job.nmax) return;
-        const int k = k0 + kN * j;
-        tma_prefetch_3d(&tk, 0, kh, k + 64 * rank);
-        tma_prefetch_3d(&tk, 64, kh, k + 64 * rank);
-        tma_prefetch_3d(&tp, 0, 0, k + 64 * rank);
-        tma_prefetch_3d(&tv, 64 * rank, vh, k);
-    };
-    auto queries = [&](int i) {
-        if (!lead || job.n(i) == 0) return;
-        if (leader) mbar_arrive_expect_tx(&mi.q_full[i], 2 * 3 * kPanelQ);
-        const uint32_t bar = map_to_rank(&mi.q_full[i], 0);
-#pragma unroll
-        for (int c = 0; c < 3; ++c)
-            tma_load_3d_pair(sm + kOffQ + (3 * i + c) * kPanelQ, &tq, bar, 64 * c, h, q0 + job.first(i, rank));
-    };
-    queries(0);
-    for (int j = 1; j < kAhead; ++j) ahead(j);
-    int t = 0;
+    int t = 0, nq0 = 0, nq1 = 0;  // key tiles and queries copied so far
     bool ok = true;
-    for (int j = 0; j < job.nmax; ++j, ++t) {
-        ahead(j + kAhead);
-        const int slot = t % kStages, k = k0 + kN * j;
-        if (t >= kStages && !(ok = all_wait<false>(&mi.k_empty[slot], (t / kStages - 1) & 1, abort))) break;
-        if (lead) {
-            if (leader) mbar_arrive_expect_tx(&mi.k_full[slot], 2 * kTileK);
-            const uint32_t bar = map_to_rank(&mi.k_full[slot], 0);
-            unsigned char *dst = sm + kOffK + slot * kTileK;
-            tma_load_3d_pair(dst, &tk, bar, 0, kh, k + 64 * rank);
-            tma_load_3d_pair(dst + kPanelK, &tk, bar, 64, kh, k + 64 * rank);
-            tma_load_3d_pair(dst + 2 * kPanelK, &tp, bar, 0, 0, k + 64 * rank);
-        }
-        if (j == 0) queries(1);
-        if (t >= kStages && !(ok = all_wait<false>(&mi.v_empty[slot], (t / kStages - 1) & 1, abort))) break;
-        if (lead) {
-            unsigned char *dst = sm + kOffV + slot * kTileV;
-            if (job.tail && j == job.nmax - 1) {
-                // each CTA's softmax waits for this part itself (it clears the rows past the end) and
-                // answers for it with its weights
-                if (leader) mbar_arrive(&mi.v_full[slot]);
-                mbar_arrive_expect_tx(&mi.v_tail, kTileV);
-                tma_load_3d(dst, &tv, &mi.v_tail, 64 * rank, vh, k);
-            } else {
-                if (leader) mbar_arrive_expect_tx(&mi.v_full[slot], 2 * kTileV);
-                tma_load_3d_pair(dst, &tv, map_to_rank(&mi.v_full[slot], 0), 64 * rank, vh, k);
+    Jobs jobs(mi);
+    do {
+        const Job job = make_job(p, jobs.at);
+        const int k0 = job.at.k0, q0 = job.at.q0, h = job.h * q_step, kh = job.h * k_step, vh = job.h * v_step;
+        auto ahead = [&](int j) {  // this CTA's part of key tile j into L2
+            if (!lead || j >= job.nmax) return;
+            const int k = k0 + kN * j;
+            tma_prefetch_3d(&tk, 0, kh, k + 64 * rank);
+            tma_prefetch_3d(&tk, 64, kh, k + 64 * rank);
+            tma_prefetch_3d(&tp, 0, 0, k + 64 * rank);
+            tma_prefetch_3d(&tv, 64 * rank, vh, k);
+        };
+        auto queries = [&](int i, int &nq) -> bool {
+            if (job.n(i) == 0) return true;
+            if (nq > 0 && !all_wait<false>(&mi.q_empty[i], (nq - 1) & 1, abort)) return false;
+            if (lead) {
+                if (leader) mbar_arrive_expect_tx(&mi.q_full[i], 2 * 3 * kPanelQ);
+                const uint32_t bar = map_to_rank(&mi.q_full[i], 0);
+#pragma unroll
+                for (int c = 0; c < 3; ++c)
+                    tma_load_3d_pair(sm + kOffQ + (3 * i + c) * kPanelQ, &tq, bar, 64 * c, h, q0 + job.first(i, rank));
+            }
+            ++nq;
+            return true;
+        };
+        for (int j = 0; j < kAhead; ++j) ahead(j);
+        if (!(ok = queries(0, nq0))) break;
+        if (job.nmax == 0 && !(ok = queries(1, nq1))) break;
+        for (int j = 0; j < job.nmax; ++j, ++t) {
+            ahead(j + kAhead);
+            const int slot = t % kStages, k = k0 + kN * j;
+            if (t >= kStages && !(ok = all_wait<false>(&mi.k_empty[slot], (t / kStages - 1) & 1, abort))) break;
+            if (lead) {
+                if (leader) mbar_arrive_expect_tx(&mi.k_full[slot], 2 * kTileK);
+                const uint32_t bar = map_to_rank(&mi.k_full[slot], 0);
+                unsigned char *dst = sm + kOffK + slot * kTileK;
+                tma_load_3d_pair(dst, &tk, bar, 0, kh, k + 64 * rank);
+                tma_load_3d_pair(dst + kPanelK, &tk, bar, 64, kh, k + 64 * rank);
+                tma_load_3d_pair(dst + 2 * kPanelK, &tp, bar, 0, 0, k + 64 * rank);
+            }
+            if (j == 0 && !(ok = queries(1, nq1))) break;
+            if (t >= kStages && !(ok = all_wait<false>(&mi.v_empty[slot], (t / kStages - 1) & 1, abort))) break;
+            if (lead) {
+                unsigned char *dst = sm + kOffV + slot * kTileV;
+                if (job.tail && j == job.nmax - 1) {
+                    // each CTA's softmax waits for this part itself (it clears the rows past the end) and
+                    // answers for it with its weights
+                    if (leader) mbar_arrive(&mi.v_full[slot]);
+                    mbar_arrive_expect_tx(&mi.v_tail[slot], kTileV);
+                    tma_load_3d(dst, &tv, &mi.v_tail[slot], 64 * rank, vh, k);
+                } else {
+                    if (leader) mbar_arrive_expect_tx(&mi.v_full[slot], 2 * kTileV);
+                    tma_load_3d_pair(dst, &tv, map_to_rank(&mi.v_full[slot], 0), 64 * rank, vh, k);
+                }
             }
         }
-    }
-    if (!ok && lead && leader) {  // the copies in flight land before the pair goes (the other CTA stays for this one)
-        for (int i = 0; i < 2; ++i)
-            if (job.n(i)) mbar_wait_ns(&mi.q_full[i], 0, kWait);
-        for (int k = max(0, t - kStages); k < t; ++k) {
-            mbar_wait_ns(&mi.k_full[k % kStages], (k / kStages) & 1, kWait);
-            mbar_wait_ns(&mi.v_full[k % kStages], (k / kStages) & 1, kWait);
+        if (!ok) break;
+        if (lead) mbar_arrive_expect_tx(&mi.next_full, 16);
+        if (leader) {
+            if (jobs.count > 0 && !(ok = all_wait<true>(&mi.next_empty, (jobs.count - 1) & 1, abort))) break;
+            if (lead) cluster_take(&mi.next, &mi.next_full);
         }
+        __syncwarp();
+    } while (jobs.next(lane));
+    if (*abort && lead) {  // the copies in flight land before the pair goes (the other CTA stays for this one)
+        if (leader) {
+            if (nq0) mbar_wait_ns(&mi.q_full[0], (nq0 - 1) & 1, kWait);
+            if (nq1) mbar_wait_ns(&mi.q_full[1], (nq1 - 1) & 1, kWait);
+            for (int k = max(0, t - kStages); k < t; ++k) {
+                mbar_wait_ns(&mi.k_full[k % kStages], (k / kStages) & 1, kWait);
+                mbar_wait_ns(&mi.v_full[k % kStages], (k / kStages) & 1, kWait);
+            }
+        }
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000) {}  // the tail's copies and an answer on its way: 1 ms
     }
 }
 
 // One warp of the leading CTA, in step.
-__device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, const Job &job, uint32_t tmem)
+__device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, const LatentPrefill &p, uint32_t tmem, int lane)
 {
     constexpr uint32_t id_s = idesc_bf16(2 * kM, kN, false, false), id_o = idesc_bf16(2 * kM, 128, false, true);
     volatile int *abort = &mi.abort;
     const uint32_t lead = elect_lead();
-    // the second query tile, where there is one, sees every key tile that the first sees
-    const bool two = job.n1 > 0;
-    auto scores = [&](int i, int j) -> bool {  // S_i of key tile j
-        const int slot = j % kStages;
-        if (!all_wait<true>(&mi.k_full[slot], (j / kStages) & 1, abort)) return false;
-        tc_fence_after_sync();
-        const uint32_t d = tmem + kColS + 128 * i, a = sb + kOffQ + 3 * i * kPanelQ, b = sb + kOffK + slot * kTileK;
+    int t0 = 0;                  // key tiles of the jobs before
+    int np0 = 0, np1 = 0;        // products O += P V of each query tile so far
+    int nj0 = 0, nj1 = 0;        // jobs of each query tile so far
+    Jobs jobs(mi);
+    do {
+        const Job job = make_job(p, jobs.at);
+        // the second query tile, where there is one, sees every key tile that the first sees
+        const bool two = job.n1 > 0;
+        auto scores = [&](int i, int j) -> bool {  // S_i of key tile j
+            const int t = t0 + j, slot = t % kStages;
+            if (!all_wait<true>(&mi.k_full[slot], (t / kStages) & 1, abort)) return false;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + kColS + 128 * i, a = sb + kOffQ + 3 * i * kPanelQ, b = sb + kOffK + slot * kTileK;
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
+            for (int c = 0; c < 3; ++c)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_bf16_pair(lead, d, kdesc(a + c * kPanelQ + k * 32), kdesc(b + c * kPanelK + k * 32), id_s,
-                              c > 0 || k > 0);
-        mma_commit_pair(lead, &mi.s_full[i]);
-        if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.k_empty[slot]);
-        return true;
-    };
-    auto values = [&](int i, int j) -> bool {  // O_i += P_i V of key tile j
-        const int slot = j % kStages;
-        if (!all_wait<true>(&mi.v_full[slot], (j / kStages) & 1, abort)) return false;
-        const uint32_t d = tmem + kColO + 128 * i, a = tmem + kColS + 128 * i, b = sb + kOffV + slot * kTileV;
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16_pair(lead, d, kdesc(a + c * kPanelQ + k * 32), kdesc(b + c * kPanelK + k * 32), id_s,
+                                  c > 0 || k > 0);
+            mma_commit_pair(lead, &mi.s_full[i]);
+            if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.k_empty[slot]);
+            if (j + 1 == job.n(i)) mma_commit_pair(lead, &mi.q_empty[i]);
+            return true;
+        };
+        auto values = [&](int i, int j, int &np, int nj) -> bool {  // O_i += P_i V of key tile j
+            const int t = t0 + j, slot = t % kStages;
+            if (!all_wait<true>(&mi.v_full[slot], (t / kStages) & 1, abort)) return false;
+            if (j == 0 && nj > 0 && !all_wait<true>(&mi.o_empty[i], (nj - 1) & 1, abort)) return false;
+            const uint32_t d = tmem + kColO + 128 * i, a = tmem + kColS + 128 * i, b = sb + kOffV + slot * kTileV;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if ((k & 3) == 0) {
-                if (!all_wait<true>(&mi.p_full[i][k >> 2], j & 1, abort)) return false;
-                tc_fence_after_sync();
+            for (int k = 0; k < 8; ++k) {
+                if ((k & 3) == 0) {
+                    if (!all_wait<true>(&mi.p_full[i][k >> 2], np & 1, abort)) return false;
+                    tc_fence_after_sync();
+                }
+                mma_tmem_a_pair(lead, d, a + 8 * k, sdesc(b + k * 2048, kTileV, 1024, kSw128B), id_o, j > 0 || k > 0);
             }
-            mma_tmem_a_pair(lead, d, a + 8 * k, sdesc(b + k * 2048, kTileV, 1024, kSw128B), id_o, j > 0 || k > 0);
+            ++np;
+            if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.v_empty[slot]);
+            if (j + 1 == job.n(i)) mma_commit_pair(lead, &mi.o_full[i]);
+            return true;
+        };
+        if (job.n0 > 0 && (!all_wait<true>(&mi.q_full[0], nj0 & 1, abort) || !scores(0, 0))) return false;
+        if (job.n1 > 0 && (!all_wait<true>(&mi.q_full[1], nj1 & 1, abort) || !scores(1, 0))) return false;
+#pragma unroll 1
+        for (int j = 0; j < job.nmax; ++j) {
+            if (j < job.n0) {
+                if (!values(0, j, np0, nj0)) return false;
+                if (j + 1 < job.n0 && !scores(0, j + 1)) return false;
+            }
+            if (j < job.n1) {
+                if (!values(1, j, np1, nj1)) return false;
+                if (j + 1 < job.n1 && !scores(1, j + 1)) return false;
+            }
         }
-        if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.v_empty[slot]);
-        if (j + 1 == job.n(i)) mma_commit_pair(lead, &mi.o_full[i]);
-        return true;
-    };
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        if (job.n(i) == 0) continue;
-        if (!all_wait<true>(&mi.q_full[i], 0, abort) || !scores(i, 0)) return false;
-    }
-#pragma unroll 1
-    for (int j = 0; j < job.nmax; ++j)
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-            if (j >= job.n(i)) continue;
-            if (!values(i, j)) return false;
-            if (j + 1 < job.n(i) && !scores(i, j + 1)) return false;
-        }
-    return true;
+        t0 += job.nmax;
+        nj0 += job.n0 > 0;
+        nj1 += job.n1 > 0;
+    } while (jobs.next(lane));
+    return !*abort;
 }
 
 // A warpgroup of each CTA per query tile, a thread per query.
-__device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const LatentPrefill &p, const Job &job,
-                                             uint32_t tmem, int i, int h, int rank)
+__device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const LatentPrefill &p, uint32_t tmem, int i,
+                                             int rank)
 {
     volatile int *abort = &mi.abort;
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t quarter = (uint32_t)((row >> 5) * 32) << 16;
     const uint32_t ts = tmem + kColS + 128 * i + quarter, to = tmem + kColO + 128 * i + quarter;
     const uint32_t full[2] = {map_to_rank(&mi.p_full[i][0], 0), map_to_rank(&mi.p_full[i][1], 0)};
-    // last key this query sees
-    const int64_t last = p.causal ? min(job.at.off + job.first(i, rank) + row, job.at.klen - 1) : job.at.klen - 1;
+    const uint32_t o_empty = map_to_rank(&mi.o_empty[i], 0);
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    int ns = 0, nj = 0, t0 = 0;  // score tiles and jobs of this query tile, key tiles so far
+    uint32_t tails = 0;          // parity of the tails so far in each V buffer
+    Jobs jobs(mi);
+    do {
+    const Job job = make_job(p, jobs.at);
+    const int klen = job.at.klen;
+    // last key this query sees
+    const int last = p.causal ? min(job.at.off + job.first(i, rank) + row, klen - 1) : klen - 1;
     const int n = job.n(i);
+    // this query's row of the output, or none
+    const int64_t out =
+        row < job.rows(i, rank) ? (int64_t)(job.at.q0 + job.first(i, rank) + row) * p.heads + job.h : -1;
     float m = -INFINITY, l = 0.f;  // held maximum (log2 units) and the sum of the weights
-    for (int j = 0; j < n; ++j) {
-        if (!all_wait<false>(&mi.s_full[i], j & 1, abort)) return;
+    for (int j = 0; j < n; ++j, ++ns) {
+        if (!all_wait<false>(&mi.s_full[i], ns & 1, abort)) return;
         tc_fence_after_sync();
         float s[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
-        const int seen = (int)max((int64_t)-1, min((int64_t)kN, last - (int64_t)j * kN));  // columns 0 .. seen
+        const int seen = max(-1, min(kN, last - j * kN));  // columns 0 .. seen
         const bool special = __any_sync(0xffffffffu, seen < kN - 1) || p.scale_log2 <= 0.f;
         tmem_ld_wait();
         // one branch for all that is rare: the rest is straight code that the scheduler can interleave
@@ -305,7 +376,7 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
         // the maximum is moved only where a score passes it by kSlack: weights are below 2^kSlack, and
         // the precision of fp32 and bf16 does not depend on that
         const bool rise = mx > m + kSlack;
-        const int64_t left = job.at.klen - (int64_t)j * kN;
+        const int left = klen - j * kN;
         if (__any_sync(0xffffffffu, rise) || left < kN) {
             float f = 1.f;
             if (rise) {
@@ -328,9 +399,10 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
             // keys past the sequence's end are other sequences' rows: their weight is 0, so their values
             // must be finite
             if (left < kN) {
-                if (!all_wait<false>(&mi.v_tail, 0, abort)) return;
-                for (int e = row; e < (kN - (int)left) * 8; e += 128)
-                    *reinterpret_cast<uint4 *>(sm + kOffV + (j % kStages) * kTileV + ((int)left + (e >> 3)) * 128 +
+                const int slot = (t0 + j) % kStages;
+                if (!all_wait<false>(&mi.v_tail[slot], (tails >> slot) & 1, abort)) return;
+                for (int e = row; e < (kN - left) * 8; e += 128)
+                    *reinterpret_cast<uint4 *>(sm + kOffV + slot * kTileV + (left + (e >> 3)) * 128 +
                                                (e & 7) * 16) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 fence_cluster();
@@ -365,29 +437,36 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
         l += all.x + all.y;
     }
     if (n > 0) {
-        if (!all_wait<false>(&mi.o_full[i], 0, abort)) return;
+        if (!all_wait<false>(&mi.o_full[i], nj & 1, abort)) return;
         tc_fence_after_sync();
+        ++nj;
     }
-    const bool mine = row < job.rows(i, rank);
-    const int64_t q = job.at.q0 + job.first(i, rank) + row;
+    if (job.tail) tails ^= 1u << ((t0 + job.nmax - 1) % kStages);
+    t0 += job.nmax;
+    if (out >= 0 && p.lse) p.lse[out] = m * kLn2 + logf(l);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + (q * p.heads + h) * kLatN;
-    if (mine && p.lse) p.lse[q * p.heads + h] = m * kLn2 + logf(l);
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + out * kLatN;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         float x[32];
         if (n > 0) {
             tmem_ld32(to + 32 * c, x);
             tmem_ld_wait();
+            if (c == 3) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(o_empty);  // the next job's products may start
+            }
         }
 #pragma unroll
         for (int k = 0; k < 32; k += 8) {
             float y[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) y[u] = n > 0 ? x[k + u] * inv : 0.f;
-            if (mine) *reinterpret_cast<uint4 *>(o + 32 * c + k) = tc::pack_bf16x8(y);
+            if (out >= 0) *reinterpret_cast<uint4 *>(o + 32 * c + k) = tc::pack_bf16x8(y);
         }
     }
+    } while (jobs.next(lane));
 }
 
 __global__ void __launch_bounds__(kT, 1)
@@ -398,15 +477,7 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     extern __shared__ __align__(1024) unsigned char sm[];
     Misc &mi = *reinterpret_cast<Misc *>(sm + kOffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    // heads innermost, the tiles with the most keys first
-    const int h = pair % p.heads, tile = pairs / p.heads - 1 - pair / p.heads;
-    const Job job = make_job(p, tile);
-    if (blockIdx.x == 0) {
-        latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
-        latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);
-    }
-    if (job.at.rows <= 0) return;  // both CTAs of the pair
+    const int rank = (int)cluster_rank();
     if (smem_u32(sm) & 1023u) {    // the swizzled panels need it; never seen
         if (tid == 0 && p.errors) atomicOr(p.errors, DEV_ERR_TIMEOUT);
         return;
@@ -426,8 +497,10 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
             mbar_init(&mi.k_empty[i], 1);
             mbar_init(&mi.v_full[i], 1);
             mbar_init(&mi.v_empty[i], 1);
+            mbar_init(&mi.v_tail[i], 1);
         }
-        mbar_init(&mi.v_tail, 1);
+        mbar_init(&mi.next_full, 1);
+        mbar_init(&mi.next_empty, kJobReaders);
         mbar_init(&mi.drained, 1);
         fence_mbar_init();
         mi.abort = 0;
@@ -441,18 +514,24 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     // registers: 384 x 168 at launch; 256 x 216 + 128 x 64 now
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        softmax_role(sm, mi, p, job, tmem, warp >> 2, h, rank);
+        softmax_role(sm, mi, p, tmem, warp >> 2, rank);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 8) {
-            copy_role(sm, mi, job, tq, tk, tp, tv, h * q_step, h * k_step, h * v_step, rank, lane);
+            copy_role(sm, mi, p, tq, tk, tp, tv, q_step, k_step, v_step, rank, lane);
         } else if (warp == 9 && rank == 0) {
             // (the reduction's result is uniform to the compiler, the loaded word is not)
-            if (!mma_role(smem_u32(sm), mi, job, __reduce_or_sync(0xffffffffu, tmem))) {
+            if (!mma_role(smem_u32(sm), mi, p, __reduce_or_sync(0xffffffffu, tmem), lane)) {
                 // nothing in flight when tensor memory is given back
                 mma_commit_pair(lane == 0, &mi.drained);
-                all_wait<false>(&mi.drained, 0, &mi.abort);
+                if (lane == 0) mbar_wait_ns(&mi.drained, 0, kWait);
             }
+        } else if (warp == 9) {  // the other CTA's reads the jobs along: the count of readers is one for all
+            Jobs jobs(mi);
+            while (jobs.next(lane)) {}
+        } else if (warp == 10 && blockIdx.x == 0) {
+            latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
+            latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);
         }
     }
     __syncwarp();
@@ -491,7 +570,9 @@ bool make_map(CUtensorMap *m, const void *ptr, int channels, int64_t heads, int6
 
 cudaError_t launch_latent_prefill_tc(const LatentPrefill &p)
 {
-    const int64_t blocks = 2 * (p.q_tokens / kPairM + p.num_seqs) * p.heads;
+    // one sequence: its tiles; more: as latent_tile numbers them (numbers without a tile are passed over)
+    const int64_t tiles = p.num_seqs == 1 ? (p.q_tokens + kPairM - 1) / kPairM : p.q_tokens / kPairM + p.num_seqs;
+    const int64_t blocks = 2 * tiles * p.heads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     CUtensorMap tq, tk, tp, tv;
     int q_step = 0, k_step = 0, v_step = 0, one = 0;

@@ -570,6 +570,35 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t lead, uint64_t *bar)
         : "memory");
 }
 
+// ------------------------------------------------------------------ taking over pending clusters
+// Ask for a cluster of this grid that has not been launched yet, to run its work here instead: the
+// answer (16 bytes) is written to `slot` in every CTA of this cluster, 16 bytes counted on `bar` of
+// each.  Not to be called again once an answer was negative.
+__device__ __forceinline__ void cluster_take(void *slot, uint64_t *bar)
+{
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128"
+        " [%0], [%1];" ::"r"(smem_u32(slot)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The first CTA's index (x) of the cluster taken over, or -1: there was none left.
+__device__ __forceinline__ int cluster_taken(const void *slot)
+{
+    uint32_t ok, x = 0;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(slot))
+        : "memory");
+    return ok ? (int)x : -1;
+}
+
 // ------------------------------------------------------------------ tf32
 // Round an fp32 value to tf32 (10 explicit mantissa bits, nearest, ties away).
 __device__ __forceinline__ float to_tf32(float x)
