@@ -576,7 +576,8 @@ kda_status_t kda_latent_append(const void *latent, int64_t latent_stride, const 
  * A sequence of length 0 gives o = 0, lse = -inf.  What cache rows past a sequence's
  * end hold, NaN included, does not matter.
  *
- *  q           [batch, num_heads, d_latent + d_pe], batch and head strides
+ *  q           [batch, num_heads, d_latent + d_pe], batch and head strides (a batch
+ *              stride of 0 shares the queries among the sequences)
  *  cache       [num_pages, page_size, d_latent + d_pe] contiguous; page_size a positive
  *              multiple of 8
  *  page_table  [batch, max_pages] int32 device, row stride page_table_stride; position j of

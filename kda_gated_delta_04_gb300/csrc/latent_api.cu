@@ -99,7 +99,8 @@ kda_status_t kda_latent_decode(const void *q, int64_t q_batch_stride, int64_t q_
     if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
         !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(device_errors, 4))
         return KDA_ERR_INVALID_ARG;
-    if (!stride_ok(q_batch_stride, es) || !stride_ok(q_head_stride, es)) return KDA_ERR_INVALID_ARG;
+    if (!stride_ok(q_batch_stride, es) || !stride_ok(q_head_stride, es) || (num_heads > 1 && q_head_stride == 0))
+        return KDA_ERR_INVALID_ARG;
     if (workspace_bytes < workspace_bytes_of(num_heads, dtype)) return KDA_ERR_INVALID_ARG;
     const kda_status_t st = kda::check_device();
     if (st != KDA_OK) return st;

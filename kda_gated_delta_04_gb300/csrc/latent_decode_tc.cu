@@ -14,8 +14,8 @@
 // tile's cost is reading it from shared memory twice, below the time HBM takes to deliver it.  O^T
 // stays in tensor memory for the whole of a sequence (4 H columns), the two S^T buffers beside it.
 //
-// One CTA per SM, 256 threads: warp 0 copies (TMA), warp 1 issues the matrix instructions, warps 2
-// and 3 bring a sequence's queries in, warps 4 to 7 do the softmax.  The cache rows arrive as 64-row
+// One CTA per SM, 256 threads: warp 0 copies cache rows (TMA), warps 1 and 2 issue the two products,
+// warp 3 copies a sequence's queries, warps 4 to 7 do the softmax.  The cache rows arrive as 64-row
 // panels of 64 channels in rings of pieces: the position channels (read by S^T only, freed early)
 // in one, pairs of latent panels (read by both products) in the other.  S^T of tile t + 1 is issued
 // before O^T of tile t, so the softmax of one tile runs beside the products of its neighbours, and
@@ -79,6 +79,12 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
             return false;
         }
     }
+}
+
+// A whole warp's wait: the same answer on every lane.
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    return __all_sync(0xffffffffu, wait(bar, parity, abort));
 }
 
 // The units of this CTA, in order, as each role walks them.
@@ -228,92 +234,99 @@ gave_up:  // the copies in flight land before the CTA goes
     }
 }
 
+// S^T of every tile; one warp, in step.
 template <int NH>
-__device__ __forceinline__ void mma_role(uint32_t sb, Misc<NH> &mi, Units u, uint32_t tmem)
+__device__ __forceinline__ bool score_role(uint32_t sb, Misc<NH> &mi, Units u, uint32_t tmem)
 {
     using C = Cfg<NH>;
-    constexpr uint32_t id_s = idesc_bf16(64, NH, false, false), id_o = idesc_bf16(128, NH, true, false);
+    constexpr uint32_t id = idesc_bf16(64, NH, false, false);
     volatile int *abort = &mi.abort;
+    const uint32_t lead = elect_lead();
     int ts = 0, units = 0;
-    // O^T of tile t (the running count), the first of its unit or not, the last or not
-    auto products = [&](int t, bool first, bool last, int unit) -> bool {
-        if (!wait(&mi.p_full[t % C::NP], (t / C::NP) & 1, abort)) return false;
-        if (first && unit > 0 && !wait(&mi.o_empty, (unit - 1) & 1, abort)) return false;
-        tc_fence_after_sync();
-        const uint32_t pb = sb + C::P + (t % C::NP) * (NH * 128);
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const int slot = (4 * t + i) % C::NA;
-            const uint32_t a = sb + C::A + slot * kPair;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_bf16(tmem + i * NH, sdesc(a + k * 2048, kPanel, 1024, kSw128B), kdesc(pb + k * 32), id_o,
-                         !first || k > 0);
-            mma_commit(&mi.empty_a[slot]);
-        }
-        mma_commit(&mi.p_empty[t % C::NP]);
-        if (last) mma_commit(&mi.o_full);
-        return true;
-    };
-    bool pending = false, pend_first = false;
     while (u.next()) {
-        // a new unit: finish the one before, then wait for the queries
-        if (pending && !products(ts - 1, pend_first, true, units - 1)) return;
-        pending = false;
-        if (!wait(&mi.q_full, units & 1, abort)) return;
+        if (!all_wait(&mi.q_full, units & 1, abort)) return false;
         ++units;
         for (int t = 0; t < u.tiles; ++t, ++ts) {
-            if (ts >= 2 && !wait(&mi.s_empty[ts & 1], (ts / 2 - 1) & 1, abort)) return;
-            if (!wait(&mi.full_b[ts % C::NB], (ts / C::NB) & 1, abort)) return;
+            if (ts >= 2 && !all_wait(&mi.s_empty[ts & 1], (ts / 2 - 1) & 1, abort)) return false;
+            if (!all_wait(&mi.full_b[ts % C::NB], (ts / C::NB) & 1, abort)) return false;
             tc_fence_after_sync();
             const uint32_t d = tmem + C::SCOL + (ts & 1) * NH;
             const uint32_t b = sb + C::B + (ts % C::NB) * kPanel;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                mma_bf16(d, kdesc(b + k * 32), kdesc(sb + C::Q + 8 * NH * 128 + k * 32), id_s, k > 0);
-            mma_commit(&mi.empty_b[ts % C::NB]);
+                mma_bf16_lead(lead, d, kdesc(b + k * 32), kdesc(sb + C::Q + 8 * NH * 128 + k * 32), id, k > 0);
+            mma_commit_lead(lead, &mi.empty_b[ts % C::NB]);
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 const int na = 4 * ts + i, slot = na % C::NA;
-                if (!wait(&mi.full_a[slot], (na / C::NA) & 1, abort)) return;
+                if (!all_wait(&mi.full_a[slot], (na / C::NA) & 1, abort)) return false;
                 const uint32_t a = sb + C::A + slot * kPair;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    mma_bf16(d, kdesc(a + (k >> 2) * kPanel + (k & 3) * 32),
-                             kdesc(sb + C::Q + (2 * i + (k >> 2)) * NH * 128 + (k & 3) * 32), id_s, 1);
+                    mma_bf16_lead(lead, d, kdesc(a + (k >> 2) * kPanel + (k & 3) * 32),
+                                  kdesc(sb + C::Q + (2 * i + (k >> 2)) * NH * 128 + (k & 3) * 32), id, 1);
             }
-            mma_commit(&mi.s_full[ts & 1]);
-            if (t + 1 == u.tiles) mma_commit(&mi.q_empty);
-            if (pending && !products(ts - 1, pend_first, false, units - 1)) return;
-            pending = true;
-            pend_first = t == 0;
+            mma_commit_lead(lead, &mi.s_full[ts & 1]);
+            if (t + 1 == u.tiles) mma_commit_lead(lead, &mi.q_empty);
         }
     }
-    if (pending) products(ts - 1, pend_first, true, units - 1);
+    return true;
 }
 
-// Queries of a unit's heads into shared memory (K-major, swizzled); 64 threads.
+// O^T += C^T P^T of every tile; one warp, in step.  Its own warp, so that the waits of one product
+// (about 100 cycles each, ready or not) pass while the other's instructions run.
 template <int NH>
-__device__ __forceinline__ void query_role(unsigned char *sm, Misc<NH> &mi, const LatentDecode &p, Units u, int id)
+__device__ __forceinline__ bool value_role(uint32_t sb, Misc<NH> &mi, Units u, uint32_t tmem)
+{
+    using C = Cfg<NH>;
+    constexpr uint32_t id = idesc_bf16(128, NH, true, false);
+    volatile int *abort = &mi.abort;
+    const uint32_t lead = elect_lead();
+    int ts = 0, units = 0;
+    while (u.next()) {
+        if (units > 0 && !all_wait(&mi.o_empty, (units - 1) & 1, abort)) return false;
+        ++units;
+        for (int t = 0; t < u.tiles; ++t, ++ts) {
+            if (!all_wait(&mi.p_full[ts % C::NP], (ts / C::NP) & 1, abort)) return false;
+            tc_fence_after_sync();
+            const uint32_t pb = sb + C::P + (ts % C::NP) * (NH * 128);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const int slot = (4 * ts + i) % C::NA;
+                const uint32_t a = sb + C::A + slot * kPair;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16_lead(lead, tmem + i * NH, sdesc(a + k * 2048, kPanel, 1024, kSw128B), kdesc(pb + k * 32), id,
+                                  t > 0 || k > 0);
+                mma_commit_lead(lead, &mi.empty_a[slot]);
+            }
+            mma_commit_lead(lead, &mi.p_empty[ts % C::NP]);
+            if (t + 1 == u.tiles) mma_commit_lead(lead, &mi.o_full);
+        }
+    }
+    return true;
+}
+
+// The queries of each unit (TMA); one warp, so that the cache rows' copies never wait for it.
+template <int NH>
+__device__ __forceinline__ void query_role(unsigned char *sm, Misc<NH> &mi, const LatentDecode &p, Units u,
+                                           const CUtensorMap &tq, int b_step, int h_step, int lane)
 {
     using C = Cfg<NH>;
     volatile int *abort = &mi.abort;
     int units = 0;
-    while (u.next()) {
-        if (units > 0 && !wait(&mi.q_empty, (units - 1) & 1, abort)) return;
-        const int h0 = u.w.hg * NH;
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + u.w.b * p.q_bs;
-#pragma unroll 6
-        for (int e = id; e < NH * 72; e += 64) {
-            const int h = e / 72, c = e - h * 72;  // 8 channels
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (h0 + h < p.heads) x = *reinterpret_cast<const uint4 *>(q + (h0 + h) * p.q_hs + 8 * c);
-            *reinterpret_cast<uint4 *>(sm + C::Q + tc::km16(h, 8 * c, NH)) = x;
+    bool ok = true;
+    while (ok && u.next()) {
+        if (units > 0 && !(ok = all_wait(&mi.q_empty, (units - 1) & 1, abort))) break;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&mi.q_full, 9 * NH * 128);
+#pragma unroll
+            for (int c = 0; c < 9; ++c)
+                tma_load_3d(sm + C::Q + c * NH * 128, &tq, &mi.q_full, 64 * c, u.w.hg * NH * h_step, u.w.b * b_step);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(&mi.q_full);
         ++units;
     }
+    if (!ok && units > 0 && lane == 0) mbar_wait_ns(&mi.q_full, (units - 1) & 1, kWait);
 }
 
 template <int NH>
@@ -468,7 +481,8 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc<NH> &mi, co
 
 template <int NH>
 __global__ void __launch_bounds__(kT, 1)
-latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMap tm, int piece_rows)
+latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMap tm,
+                        const __grid_constant__ CUtensorMap tq, int piece_rows, int b_step, int h_step)
 {
     using C = Cfg<NH>;
     static_assert(C::MISC + sizeof(Misc<NH>) <= kSmemMax, "shared memory");
@@ -495,11 +509,11 @@ latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMa
             mbar_init(&mi.p_full[i], 128);
             mbar_init(&mi.p_empty[i], 1);
         }
-        mbar_init(&mi.q_full, 64);
+        mbar_init(&mi.q_full, 1);
         mbar_init(&mi.q_empty, 1);
         mbar_init(&mi.o_full, 1);
         mbar_init(&mi.o_empty, 128);
-        mbar_init(&mi.drained, 1);
+        mbar_init(&mi.drained, 2);
         fence_mbar_init();
         mi.abort = 0;
     }
@@ -523,16 +537,15 @@ latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMa
     if (w.cta < w.ctas) {
         const Units u(p, w);
         if (warp == 0) copy_role<NH>(sm, mi, p, u, tm, piece_rows, lane);
-        else if (warp == 1) {
-            if (lane == 0) {
-                mma_role<NH>(smem_u32(sm), mi, u, tmem);
-                if (*(volatile int *)&mi.abort) {  // nothing in flight when tensor memory is given back
-                    mma_commit(&mi.drained);
-                    mbar_wait_ns(&mi.drained, 0, kWait);
-                }
+        else if (warp < 3) {
+            // (the reduction's result is uniform to the compiler, the loaded word is not)
+            const uint32_t t = __reduce_or_sync(0xffffffffu, tmem);
+            if (!(warp == 1 ? score_role<NH>(smem_u32(sm), mi, u, t) : value_role<NH>(smem_u32(sm), mi, u, t))) {
+                // nothing in flight when tensor memory is given back
+                mma_commit_lead(lane == 0, &mi.drained);
+                if (lane == 0) mbar_wait_ns(&mi.drained, 0, kWait);
             }
-            __syncwarp();
-        } else if (warp < 4) query_role<NH>(sm, mi, p, u, tid - 64);
+        } else if (warp == 3) query_role<NH>(sm, mi, p, u, tq, b_step, h_step, lane);
         else softmax_role<NH>(sm, mi, p, u, tmem, tid - 128);
     }
     tc_fence_before_sync();
@@ -568,7 +581,17 @@ cudaError_t launch(const LatentDecode &p, int grid)
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    latent_decode_tc_kernel<NH><<<grid, kT, kSmemMax, p.stream>>>(p, tm, piece);
+    // the queries as [batch][heads][channels]; a step of 0 where heads or sequences share their rows
+    const int h_step = p.q_hs ? 1 : 0, b_step = p.q_bs ? 1 : 0;
+    CUtensorMap tq;
+    const cuuint64_t qdims[3] = {kLatC, (cuuint64_t)(h_step ? p.heads : 1), (cuuint64_t)(b_step ? p.batch : 1)};
+    const cuuint64_t qstrides[2] = {(cuuint64_t)(h_step ? p.q_hs : kLatC) * 2, (cuuint64_t)(b_step ? p.q_bs : kLatC) * 2};
+    const cuuint32_t qbox[3] = {64, NH, 1};
+    if (enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p.q), qdims, qstrides, qbox, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    latent_decode_tc_kernel<NH><<<grid, kT, kSmemMax, p.stream>>>(p, tm, tq, piece, b_step, h_step);
     err = cudaGetLastError();
     return err != cudaSuccess ? err : launch_latent_join(p, NH, grid);
 }

@@ -55,7 +55,7 @@ def decode_args(**over):
     (dict(o=None), INVALID), (dict(workspace=None), INVALID), (dict(q=FAKE + 8), INVALID), (dict(cache=FAKE + 8), INVALID),
     (dict(page_table=FAKE + 2), INVALID), (dict(seq_lens=FAKE + 2), INVALID), (dict(o=FAKE + 8), INVALID),
     (dict(lse=FAKE + 2), INVALID), (dict(workspace=FAKE + 128), INVALID), (dict(workspace_bytes=100), INVALID),
-    (dict(q_head_stride=577), INVALID), (dict(q_batch_stride=-8), INVALID), (dict(page_table_stride=-1), INVALID),
+    (dict(q_head_stride=577), INVALID), (dict(q_head_stride=0), INVALID), (dict(q_batch_stride=-8), INVALID), (dict(page_table_stride=-1), INVALID),
     (dict(batch=-1), INVALID), (dict(num_heads=0), INVALID), (dict(page_size=0), INVALID), (dict(num_pages=-1), INVALID),
     (dict(max_pages=-1), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(dtype=5), INVALID), (dict(d_latent=0), INVALID),
