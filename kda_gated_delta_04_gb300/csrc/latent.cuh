@@ -80,13 +80,14 @@ size_t latent_decode_tc_ws_bytes(int heads);
 // [c W / G', (c + 1) W / G'): every CTA reads the same number of cache rows whatever the lengths,
 // and the host needs to know no length.  A unit cut by a CTA boundary leaves partial results
 // (the running maximum and sum, and the unnormalised output, fp32): slot 2c for the first unit
-// of CTA c, 2c + 1 for its last.  The CTA after a unit's first boundary records where the unit's
-// parts lie, and the combine kernel joins them in the order of the cache rows.
+// of CTA c, 2c + 1 for its last.  Records tell the joining kernel which CTAs hold a unit's parts, to
+// be joined in the order of the cache rows: one record per unit where there are no more units than
+// CTAs (few joins, of many parts), else one per CTA boundary (at its first boundary inside a unit).
 constexpr int kLatMaxGrid = 320;  // bound on the decode grid (two CTAs on each of 152 SMs, rounded up)
 constexpr int kLatHeadTile = 64;  // most heads in one tile
 
-struct LatentJoin {  // at the head of the workspace, one per CTA
-    int b, h0;            // sequence and first head; b < 0: nothing to join at this boundary
+struct LatentJoin {  // at the head of the workspace
+    int b, h0;            // sequence and first head; b < 0: nothing to join
     int c_first, c_last;  // CTAs that hold parts
     int first_slot;       // slot of the first part; the others' are 2 c
     int pad[3];
@@ -107,6 +108,11 @@ inline size_t latent_ws_bytes(int head_tile, int grid)
 }
 // Joins the parts of the split units; `head_tile` heads per slot.
 cudaError_t launch_latent_join(const LatentDecode &p, int head_tile, int grid);
+// Whether records are per unit (see above).
+__host__ __device__ inline bool latent_join_by_unit(int batch, int heads, int head_tile, int grid)
+{
+    return (int64_t)batch * ((heads + head_tile - 1) / head_tile) <= grid;
+}
 
 #ifdef __CUDACC__
 // ---------------------------------------------------------------- expanded prefill: query tiles
@@ -182,14 +188,20 @@ struct LatentWalk {
     __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
 };
 
-// Called by all NT threads of the CTA (contains barriers); s_scan: NT + 4 int64 of shared memory.
-// The first CTAs also clear the outputs of the sequences without cache rows.
+// Called by all NT threads of the CTA (contains barriers); s_scan: NT / 32 + 2 int64 of shared memory.
+// The CTAs also clear the outputs of the sequences without cache rows, and write the records that say
+// that there is nothing to join.
 template <int NT, typename IO>
-__device__ __forceinline__ LatentWalk latent_walk(const int32_t *lens, int batch, int64_t capacity, int tile_rows,
-                                                  int head_groups, int heads, IO *o, float *lse, uint32_t *errors,
-                                                  int64_t *s_scan)
+__device__ __forceinline__ LatentWalk latent_walk(const LatentDecode &p, int tile_rows, int head_tile, int64_t *s_scan)
 {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, batch = p.batch, heads = p.heads, head_groups = (heads + head_tile - 1) / head_tile;
+    const int64_t capacity = (int64_t)p.table_width * p.page_size;
+    const int32_t *lens = p.lens;
+    uint32_t *errors = p.errors;
+    IO *o = static_cast<IO *>(p.o);
+    float *lse = p.lse;
+    LatentJoin *records = reinterpret_cast<LatentJoin *>(p.workspace);
+    const bool by_unit = latent_join_by_unit(batch, heads, head_tile, gridDim.x);
     const int chunk = (batch + NT - 1) / NT;
     const int lo = min(tid * chunk, batch), hi = min(lo + chunk, batch);
     bool bad = false;
@@ -246,27 +258,39 @@ __device__ __forceinline__ LatentWalk latent_walk(const int32_t *lens, int batch
         for (int64_t e = tid; e < (int64_t)heads * kLatR; e += NT) store_io(o + (size_t)b * heads * kLatR + e, 0.f);
         if (lse)
             for (int h = tid; h < heads; h += NT) lse[(size_t)b * heads + h] = -INFINITY;
+        if (by_unit)
+            for (int g = tid; g < head_groups; g += NT) records[g * batch + b].b = -1;
     }
+    if (!by_unit && tid == 0 && !(k.cta < k.ctas && k.tile > 0)) records[blockIdx.x].b = -1;
     return k;
 }
 
-// This CTA's record for the combine kernel: one thread, once, with the walk at its start.
-// n0: tiles of the first unit.
-__device__ __forceinline__ void latent_record_join(const LatentWalk &k, int n0, int head_tile, char *ws)
+// One thread, for each of this CTA's units: the record for the joining kernel, where it is this CTA's
+// to write.  k: the walk at the unit (k.tile its first tile here), n: the unit's tiles, tiles: those of
+// this CTA.
+__device__ __forceinline__ void latent_record_join(const LatentDecode &p, const LatentWalk &k, int64_t g, int tile0, int n,
+                                                   int tiles, bool first, int head_tile)
 {
-    LatentJoin j = {-1, 0, 0, 0, 0, {0, 0, 0}};
-    if (k.cta < k.ctas && k.tile > 0) {
-        const int64_t a = k.g - k.tile;
-        const int cf = k.cta_of(a);
-        if (cf == k.cta - 1) {
-            j.b = k.b;
-            j.h0 = k.hg * head_tile;
-            j.c_first = cf;
-            j.c_last = k.cta_of(a + n0 - 1);
-            j.first_slot = k.start_of(cf) >= a ? 2 * cf : 2 * cf + 1;
-        }
+    const bool by_unit = latent_join_by_unit(p.batch, p.heads, head_tile, gridDim.x);
+    LatentJoin *r = reinterpret_cast<LatentJoin *>(p.workspace);
+    if (by_unit) {
+        if (tile0 > 0) return;  // written by the CTA of the unit's first tile
+        r += k.hg * p.batch + k.b;
+    } else {
+        if (!first || tile0 == 0) return;  // (latent_walk wrote that there is nothing)
+        r += blockIdx.x;
     }
-    reinterpret_cast<LatentJoin *>(ws)[blockIdx.x] = j;
+    const int64_t a = g - tile0;  // the unit's first tile in the list
+    const int cf = by_unit ? k.cta : k.cta_of(a);
+    LatentJoin j = {-1, 0, 0, 0, 0, {0, 0, 0}};
+    if (by_unit ? tiles < n : cf == k.cta - 1) {
+        j.b = k.b;
+        j.h0 = k.hg * head_tile;
+        j.c_first = cf;
+        j.c_last = k.cta_of(a + n - 1);
+        j.first_slot = k.start_of(cf) >= a ? 2 * cf : 2 * cf + 1;
+    }
+    *r = j;
 }
 #endif
 

@@ -42,13 +42,8 @@ __global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentD
     Smem &sm = *reinterpret_cast<Smem *>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t capacity = (int64_t)p.table_width * p.page_size;
-    const int groups = (p.heads + kHeads - 1) / kHeads;
-    LatentWalk w = latent_walk<kT, IO>(p.lens, p.batch, capacity, kRows, groups, p.heads, static_cast<IO *>(p.o),
-                                       p.lse, p.errors, sm.scan);
-    if (w.cta >= w.ctas) {
-        if (tid == 0) latent_record_join(w, 0, kHeads, p.workspace);
-        return;
-    }
+    LatentWalk w = latent_walk<kT, IO>(p, kRows, kHeads, sm.scan);
+    if (w.cta >= w.ctas) return;
     const IO *cache = static_cast<const IO *>(p.cache);
     bool first_unit = true;
     while (w.g < w.g_end) {
@@ -59,8 +54,8 @@ __global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentD
             if (++w.b == p.batch) { w.b = 0; ++w.hg; }
             continue;
         }
-        if (first_unit && tid == 0) latent_record_join(w, n, kHeads, p.workspace);
         const int tile0 = w.tile, tiles = (int)min((int64_t)(n - tile0), w.g_end - w.g);
+        if (tid == 0) latent_record_join(p, w, w.g, tile0, n, tiles, first_unit, kHeads);
         const int h0 = w.hg * kHeads, hs = min(kHeads, p.heads - h0);
         __syncthreads();  // the previous unit's reads of q
         for (int e = tid; e < kHeads * kLatC; e += kT) {
@@ -174,55 +169,106 @@ __global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentD
     }
 }
 
-// Joins one split unit's parts for one head: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
-// over the parts in the order of the cache rows.  One CTA per (CTA boundary, head); most
-// boundaries of a large batch have nothing to join and return at once.
-template <typename IO>
-__global__ void __launch_bounds__(128)
+// Joins one split unit's parts for one head: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  One
+// CTA per (record, head), 128 threads with a float4 of the output each for every one of GROUPS groups
+// of parts (i mod GROUPS; a fixed order, so the same bits on every call).  Bound by the latency of its
+// loads: the first parts are asked for beside the maxima.  One group where there are many records (most
+// say at once that there is nothing to join, the others have few parts), four where there are few
+// (long sequences, dozens of parts): two sequences of 131k rows, 32 heads, 76 parts each: 15 us with
+// one group, 5 with four.
+template <typename IO, int GROUPS>
+__global__ void __launch_bounds__(128 * GROUPS)
 latent_join_kernel(const char *ws, int head_tile, int heads, IO *o, float *lse)
 {
+    constexpr int kAsk = 4;  // parts asked for at a time
     __shared__ float s_w[kLatMaxGrid];
-    __shared__ float s_red[4];
+    __shared__ float s_red[4 * GROUPS];
+    __shared__ float4 s_o[GROUPS > 1 ? GROUPS - 1 : 1][128];
     pdl_wait();  // launched early behind the kernel that wrote the parts
     const LatentJoin j = reinterpret_cast<const LatentJoin *>(ws)[blockIdx.x];
-    const int hl = blockIdx.y, h = j.h0 + hl, tid = threadIdx.x;
+    const int hl = blockIdx.y, h = j.h0 + hl, tid = threadIdx.x, quad = tid & 127, group = tid >> 7;
     if (j.b < 0 || h >= heads) return;
     const int parts = j.c_last - j.c_first + 1;
     auto slot = [&](int i) { return i == 0 ? j.first_slot : 2 * (j.c_first + i); };
     const float *ml = latent_ml(const_cast<char *>(ws));
-    const float *part = latent_part(const_cast<char *>(ws), head_tile);
+    const float *part = latent_part(const_cast<char *>(ws), head_tile) + (size_t)hl * kLatR + 4 * quad;
+    auto load = [&](int i) {
+        return i < parts ? *reinterpret_cast<const float4 *>(part + (size_t)slot(i) * head_tile * kLatR)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 x[kAsk];
+#pragma unroll
+    for (int u = 0; u < kAsk; ++u) x[u] = load(group + u * GROUPS);
     float mx = -INFINITY;
-    for (int i = tid; i < parts; i += 128) mx = fmaxf(mx, ml[((size_t)slot(i) * head_tile + hl) * 2]);
+    for (int i = tid; i < parts; i += 128 * GROUPS) mx = fmaxf(mx, ml[((size_t)slot(i) * head_tile + hl) * 2]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     if ((tid & 31) == 0) s_red[tid >> 5] = mx;
     __syncthreads();
-    mx = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+#pragma unroll
+    for (int w = 0; w < 4 * GROUPS; ++w) mx = fmaxf(mx, s_red[w]);
     const float base = mx == -INFINITY ? 0.f : mx;
     __syncthreads();
     float l = 0.f;
-    for (int i = tid; i < parts; i += 128) {
-        const float *x = ml + ((size_t)slot(i) * head_tile + hl) * 2;
-        const float f = exp2f(x[0] - base);
+    for (int i = tid; i < parts; i += 128 * GROUPS) {
+        const float2 y = *reinterpret_cast<const float2 *>(ml + ((size_t)slot(i) * head_tile + hl) * 2);
+        const float f = exp2f(y.x - base);
         s_w[i] = f;
-        l += f * x[1];
+        l += f * y.y;
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     if ((tid & 31) == 0) s_red[tid >> 5] = l;
     __syncthreads();
-    l = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4 * GROUPS; ++w) l += s_red[w];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const float4 x = *reinterpret_cast<const float4 *>(part + ((size_t)slot(i) * head_tile + hl) * kLatR + 4 * tid);
-        const float f = s_w[i];
-        acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
+    for (int i = group; i < parts; i += kAsk * GROUPS) {
+        float4 y[kAsk];
+#pragma unroll
+        for (int u = 0; u < kAsk; ++u) y[u] = load(i + (kAsk + u) * GROUPS);
+#pragma unroll
+        for (int u = 0; u < kAsk; ++u) {
+            const float f = i + u * GROUPS < parts ? s_w[i + u * GROUPS] : 0.f;
+            acc.x += f * x[u].x; acc.y += f * x[u].y; acc.z += f * x[u].z; acc.w += f * x[u].w;
+            x[u] = y[u];
+        }
+    }
+    if (GROUPS > 1) {
+        if (group > 0) s_o[group - 1][quad] = acc;
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 0; g < GROUPS - 1; ++g) {
+            const float4 y = s_o[g][quad];
+            acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float out[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-    store_io4(o + ((int64_t)j.b * heads + h) * kLatR + 4 * tid, out);
+    store_io4(o + ((int64_t)j.b * heads + h) * kLatR + 4 * quad, out);
     if (lse && tid == 0) lse[(int64_t)j.b * heads + h] = mx * kLn2 + logf(l);
+}
+
+template <typename IO>
+cudaError_t launch_join(const LatentDecode &p, int head_tile, int grid)
+{
+    const int units = p.batch * ((p.heads + head_tile - 1) / head_tile);
+    const int records = latent_join_by_unit(p.batch, p.heads, head_tile, grid) ? units : grid;
+    const int heads = p.heads < head_tile ? p.heads : head_tile;
+    const bool few = records * heads <= 4 * 152;  // one wave of 512 threads a CTA
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)records, (unsigned)heads);
+    cfg.blockDim = dim3(few ? 512 : 128);
+    cfg.stream = p.stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, few ? latent_join_kernel<IO, 4> : latent_join_kernel<IO, 1>,
+                              (const char *)p.workspace, head_tile, p.heads, static_cast<IO *>(p.o), p.lse);
 }
 
 int sm_count()
@@ -252,20 +298,8 @@ cudaError_t launch_simt(const LatentDecode &p)
 
 cudaError_t launch_latent_join(const LatentDecode &p, int head_tile, int grid)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.heads < head_tile ? p.heads : head_tile));
-    cfg.blockDim = dim3(128);
-    cfg.stream = p.stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    if (p.dtype == KDA_DTYPE_BF16)
-        return cudaLaunchKernelEx(&cfg, latent_join_kernel<__nv_bfloat16>, (const char *)p.workspace, head_tile, p.heads,
-                                  static_cast<__nv_bfloat16 *>(p.o), p.lse);
-    return cudaLaunchKernelEx(&cfg, latent_join_kernel<float>, (const char *)p.workspace, head_tile, p.heads,
-                              static_cast<float *>(p.o), p.lse);
+    return p.dtype == KDA_DTYPE_BF16 ? launch_join<__nv_bfloat16>(p, head_tile, grid)
+                                     : launch_join<float>(p, head_tile, grid);
 }
 
 size_t latent_decode_simt_ws_bytes() { return latent_ws_bytes(kHeads, kLatMaxGrid); }

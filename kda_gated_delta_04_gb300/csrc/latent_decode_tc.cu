@@ -341,6 +341,7 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc<NH> &mi, co
     int ts = 0, units = 0;
     bool bad = false;  // a wait gave up: the next barrier takes all four warps out together
     while (u.next()) {
+        if (tid == 0) latent_record_join(p, u.w, u.w.g - u.tiles, u.tile0, u.n, u.tiles, u.first, NH);
         float m[N], l[N];  // of columns side * N + i: the held maximum (log2 units), this row's share of the sum
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -521,19 +522,12 @@ latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMa
         tmem_alloc(&mi.tmem, C::COLS);
         tmem_relinquish();
     }
-    const LatentWalk w = latent_walk<kT, __nv_bfloat16>(
-        p.lens, p.batch, (int64_t)p.table_width * p.page_size, kRows, (p.heads + NH - 1) / NH, p.heads,
-        static_cast<__nv_bfloat16 *>(p.o), p.lse, p.errors, mi.scan);
+    const LatentWalk w = latent_walk<kT, __nv_bfloat16>(p, kRows, NH, mi.scan);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = mi.tmem;
-    if (tid == 0) {
-        bool ignore = false;
-        const int len = w.cta < w.ctas ? latent_len(p.lens, w.b, (int64_t)p.table_width * p.page_size, ignore) : 0;
-        latent_record_join(w, (len + kRows - 1) / kRows, NH, p.workspace);
-    }
-    __syncwarp();
+    pdl_launch_dependents();
     if (w.cta < w.ctas) {
         const Units u(p, w);
         if (warp == 0) copy_role<NH>(sm, mi, p, u, tm, piece_rows, lane);
@@ -550,7 +544,6 @@ latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMa
     }
     tc_fence_before_sync();
     __syncthreads();
-    pdl_launch_dependents();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, C::COLS);

@@ -517,46 +517,70 @@ def decode_step(q, k, v, log_alpha, beta, state, *, o=None, stream=None, qk_l2no
 
 
 # ------------------------------------------------------------------ latent attention
-def _rows(t, name, shape, like):
-    """Address of a CUDA tensor of `like`'s type and device whose last dimension is contiguous
-    (the others may be strided); shape entries of None are not checked."""
-    if not hasattr(t, "is_cuda") or not t.is_cuda:
+# These calls are made once per layer and generated token, where the host's time counts: a tensor
+# that is as it should be is checked with a handful of comparisons, and only one that is not is
+# looked at again for the message.
+def _refuse(t, name, dtype, dev, shape):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple('*' if n is None else n for n in shape)}, "
-                         f"got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t.data_ptr()
-
-
-def _step(t, dim):
-    """Stride of a dimension; 0 where there is one entry only (torch's is then arbitrary)."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
-
-
-def _flat(t, name, dtype, shape, like):
-    """Address of a contiguous CUDA tensor of a given type and shape on `like`'s device, or None."""
-    if t is None:
-        return None
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return _ptr(t, name, dtype)
+    raise ValueError(f"{name} must be contiguous{' in its last dimension' if t.stride(-1) != 1 else ''}")
 
 
-def _empty(shape, dtype, device, stream):
+def _rows(t, name, dtype, dev, shape):
+    """Address and leading strides (0 where there is one entry only) of a CUDA tensor whose last
+    dimension is contiguous."""
+    try:
+        st = t.stride()
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and (st[-1] == 1 or shape[-1] == 1):
+            if len(shape) == 3:
+                return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
+            return t.data_ptr(), st[0] if shape[0] > 1 else 0
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, dev, shape)
+
+
+def _flat(t, name, dtype, dev, shape):
+    """Address of a contiguous CUDA tensor."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, dev, shape)
+
+
+def _latent_like(t, name, dims):
+    """Type code, type and device index that every other tensor of the call shares with t."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    dt = t.dtype
+    return KDA_DTYPE_BF16 if dt is torch.bfloat16 else _dtype_code(t), dt, t.get_device()
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream
+
+
+def _empty(shape, dtype, dev, stream):
     """torch.empty, owned by the stream that will use it."""
     torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def latent_append(latent, k_pe, cache, slots, *, norm_weight=None, norm_eps=1e-6, cos_sin=None, positions=None,
@@ -571,36 +595,38 @@ def latent_append(latent, k_pe, cache, slots, *, norm_weight=None, norm_eps=1e-6
     again.  Rows may be strided; all are bf16 or all fp32.  interleaved: the rotated pairs are
     (2i, 2i + 1) instead of (i, i + 32).  errors: int32 [1] that collects KDA_DEVICE_ERR_* bits."""
     torch = _torch()
-    T = latent.shape[0]
-    dt = _dtype_code(latent)
-    i32 = torch.int32
-    if not cache.is_contiguous():
-        raise ValueError("cache must be contiguous")
     if (cos_sin is None) != (positions is None):
         raise ValueError("cos_sin and positions go together")
-    H = qt = qh = ot = oh = lo = ko = 0
-    q = qo = lo_p = ko_p = None
-    if q_pe is not None:
-        H = q_pe.shape[1]
-        q_pe_out = q_pe if q_pe_out is None else q_pe_out
-        q, qo = _rows(q_pe, "q_pe", (T, None, 64), latent), _rows(q_pe_out, "q_pe_out", (T, H, 64), latent)
-        qt, qh = _step(q_pe, 0), _step(q_pe, 1)
-        ot, oh = _step(q_pe_out, 0), _step(q_pe_out, 1)
-    elif q_pe_out is not None:
+    if q_pe is None and q_pe_out is not None:
         raise ValueError("q_pe_out without q_pe")
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    code, dt, dev = _latent_like(latent, "latent", 2)
+    i32 = torch.int32
+    T = latent.shape[0]
+    x, xs = _rows(latent, "latent", dt, dev, (T, 512))
+    k, ks = _rows(k_pe, "k_pe", dt, dev, (T, 64))
+    H = qt = qh = ot = oh = lo_s = ko_s = num_positions = 0
+    q = qo = lo = ko = cs = pos = None
+    if q_pe is not None:
+        H = q_pe.shape[1] if q_pe.dim() == 3 else -1
+        q, qt, qh = _rows(q_pe, "q_pe", dt, dev, (T, H, 64))
+        qo, ot, oh = (q, qt, qh) if q_pe_out is None else _rows(q_pe_out, "q_pe_out", dt, dev, (T, H, 64))
     if latent_out is not None:
-        lo_p, lo = _rows(latent_out, "latent_out", (T, 512), latent), _step(latent_out, 0)
+        lo, lo_s = _rows(latent_out, "latent_out", dt, dev, (T, 512))
     if k_pe_out is not None:
-        ko_p, ko = _rows(k_pe_out, "k_pe_out", (T, 64), latent), _step(k_pe_out, 0)
-    st = kda_latent_append(
-        _rows(latent, "latent", (None, 512), latent), _step(latent, 0), _rows(k_pe, "k_pe", (T, 64), latent),
-        _step(k_pe, 0), _flat(norm_weight, "norm_weight", latent.dtype, (512,), latent), norm_eps,
-        None if cos_sin is None else _flat(cos_sin, "cos_sin", torch.float32, (cos_sin.shape[0], 64), latent),
-        0 if cos_sin is None else cos_sin.shape[0], _flat(positions, "positions", i32, (T,), latent),
-        q, qt, qh, qo, ot, oh, lo_p, lo, ko_p, ko, T, H, 512, 64, dt,
-        _rows(cache, "cache", (None, None, 576), latent), cache.shape[0] * cache.shape[1],
-        _flat(slots, "slots", i32, (T,), latent), _flat(errors, "errors", i32, (1,), latent),
-        _stream_handle(stream, latent.device), KDA_LATENT_INTERLEAVED if interleaved else 0)
+        ko, ko_s = _rows(k_pe_out, "k_pe_out", dt, dev, (T, 64))
+    if cos_sin is not None:
+        num_positions = cos_sin.shape[0]
+        cs = _flat(cos_sin, "cos_sin", torch.float32, dev, (num_positions, 64))
+        pos = _flat(positions, "positions", i32, dev, (T,))
+    pages, page = cache.shape[:2] if cache.dim() == 3 else (-1, -1)
+    st = (_lib or lib()).kda_latent_append(
+        x, xs, k, ks, None if norm_weight is None else _flat(norm_weight, "norm_weight", dt, dev, (512,)), norm_eps,
+        cs, num_positions, pos, q, qt, qh, qo, ot, oh, lo, lo_s, ko, ko_s, T, H, 512, 64, code,
+        _flat(cache, "cache", dt, dev, (pages, page, 576)), pages * page, _flat(slots, "slots", i32, dev, (T,)),
+        None if errors is None else _flat(errors, "errors", i32, dev, (1,)), _raw_stream(stream, dev),
+        KDA_LATENT_INTERLEAVED if interleaved else 0)
     if st != KDA_OK:
         raise KdaError(st, "kda_latent_append")
 
@@ -619,28 +645,24 @@ def latent_decode(q, cache, page_table, seq_lens, scale, *, o=None, lse=None, wo
     lse [B, H] fp32); a sequence of length 0 gives zeros and -inf.  bf16 or fp32.  The scratch
     buffer (latent_decode_workspace_for) may be kept by the caller; errors as latent_append."""
     torch = _torch()
+    code, dt, dev = _latent_like(q, "q", 3)
+    i32, f32 = torch.int32, torch.float32
     B, H = q.shape[:2]
-    dt = _dtype_code(q)
-    i32 = torch.int32
-    if not cache.is_contiguous():
-        raise ValueError("cache must be contiguous")
-    if page_table.dtype != i32 or not page_table.is_cuda or page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table must be an int32 CUDA tensor [{B}, *]")
-    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table's last dimension must be contiguous")
+    qp, qb, qh = _rows(q, "q", dt, dev, (B, H, 576))
+    pages, page = cache.shape[:2] if cache.dim() == 3 else (-1, -1)
+    width = page_table.shape[-1]
+    table, ts = _rows(page_table, "page_table", i32, dev, (B, width))
     if o is None:
-        o = _empty((B, H, 512), q.dtype, q.device, stream)
+        o = _empty((B, H, 512), dt, dev, stream)
     if lse is None:
-        lse = _empty((B, H), torch.float32, q.device, stream)
+        lse = _empty((B, H), f32, dev, stream)
     if workspace is None:
-        workspace = _empty((kda_latent_decode_workspace_size(H, dt),), torch.uint8, q.device, stream)
-    width = page_table.shape[1]
-    st = kda_latent_decode(
-        _rows(q, "q", (B, H, 576), q), _step(q, 0), _step(q, 1), _rows(cache, "cache", (None, None, 576), q),
-        cache.shape[0], cache.shape[1], page_table.data_ptr(), _step(page_table, 0), width, _flat(seq_lens, "seq_lens", i32, (B,), q), B, H, 512, 64, dt, scale,
-        _flat(o, "o", q.dtype, (B, H, 512), q), _flat(lse, "lse", torch.float32, (B, H), q),
-        _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _flat(errors, "errors", i32, (1,), q), _stream_handle(stream, q.device))
+        workspace = _empty((kda_latent_decode_workspace_size(H, code),), torch.uint8, dev, stream)
+    st = (_lib or lib()).kda_latent_decode(
+        qp, qb, qh, _flat(cache, "cache", dt, dev, (pages, page, 576)), pages, page, table, ts, width,
+        _flat(seq_lens, "seq_lens", i32, dev, (B,)), B, H, 512, 64, code, scale, _flat(o, "o", dt, dev, (B, H, 512)),
+        _flat(lse, "lse", f32, dev, (B, H)), _flat(workspace, "workspace", workspace.dtype, dev, workspace.shape),
+        workspace.nbytes, None if errors is None else _flat(errors, "errors", i32, dev, (1,)), _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_latent_decode")
     return o, lse
@@ -655,24 +677,28 @@ def latent_prefill(q, k_nope, k_pe, v, scale, cu_q=None, cu_k=None, *, causal=Tr
     positions.  causal=False: every query sees all keys of its sequence.  Returns (o [Tq, H, 128],
     lse [Tq, H] fp32); a query without keys gives zeros and -inf.  errors as latent_append."""
     torch = _torch()
-    Tq, H = q.shape[:2]
-    Tk = k_pe.shape[0]
-    dt = _dtype_code(q)
-    i32 = torch.int32
     if cu_q is None and cu_k is not None:
         raise ValueError("cu_k without cu_q")
-    N = 1 if cu_q is None else cu_q.numel() - 1
+    code, dt, dev = _latent_like(q, "q", 3)
+    i32, f32 = torch.int32, torch.float32
+    Tq, H = q.shape[:2]
+    Tk = k_pe.shape[0]
+    N = 1 if cu_q is None else cu_q.shape[0] - 1
+    qp, qt, qh = _rows(q, "q", dt, dev, (Tq, H, 192))
+    kn, kt, kh = _rows(k_nope, "k_nope", dt, dev, (Tk, H, 128))
+    kp, kps = _rows(k_pe, "k_pe", dt, dev, (Tk, 64))
+    vp, vt, vh = _rows(v, "v", dt, dev, (Tk, H, 128))
     if o is None:
-        o = _empty((Tq, H, 128), q.dtype, q.device, stream)
+        o = _empty((Tq, H, 128), dt, dev, stream)
     if lse is None:
-        lse = _empty((Tq, H), torch.float32, q.device, stream)
-    st = kda_latent_prefill(
-        _rows(q, "q", (Tq, H, 192), q), _step(q, 0), _step(q, 1), _rows(k_nope, "k_nope", (Tk, H, 128), q),
-        _step(k_nope, 0), _step(k_nope, 1), _rows(k_pe, "k_pe", (Tk, 64), q), _step(k_pe, 0),
-        _rows(v, "v", (Tk, H, 128), q), _step(v, 0), _step(v, 1), _flat(cu_q, "cu_q", i32, (N + 1,), q),
-        _flat(cu_k, "cu_k", i32, (N + 1,), q), N, Tq, Tk, H, 128, 64, 128, dt, scale,
-        _flat(o, "o", q.dtype, (Tq, H, 128), q), _flat(lse, "lse", torch.float32, (Tq, H), q),
-        _flat(errors, "errors", i32, (1,), q), _stream_handle(stream, q.device), 0 if causal else KDA_LATENT_FULL)
+        lse = _empty((Tq, H), f32, dev, stream)
+    st = (_lib or lib()).kda_latent_prefill(
+        qp, qt, qh, kn, kt, kh, kp, kps, vp, vt, vh,
+        None if cu_q is None else _flat(cu_q, "cu_q", i32, dev, (N + 1,)),
+        None if cu_k is None else _flat(cu_k, "cu_k", i32, dev, (N + 1,)), N, Tq, Tk, H, 128, 64, 128, code, scale,
+        _flat(o, "o", dt, dev, (Tq, H, 128)), _flat(lse, "lse", f32, dev, (Tq, H)),
+        None if errors is None else _flat(errors, "errors", i32, dev, (1,)), _raw_stream(stream, dev),
+        0 if causal else KDA_LATENT_FULL)
     if st != KDA_OK:
         raise KdaError(st, "kda_latent_prefill")
     return o, lse
