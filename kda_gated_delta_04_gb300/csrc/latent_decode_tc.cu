@@ -14,8 +14,9 @@
 // tile's cost is reading it from shared memory twice, below the time HBM takes to deliver it.  O^T
 // stays in tensor memory for the whole of a sequence (4 H columns), the two S^T buffers beside it.
 //
-// One CTA per SM, 256 threads: warp 0 copies cache rows (TMA), warps 1 and 2 issue the two products,
-// warp 3 copies a sequence's queries, warps 4 to 7 do the softmax.  The cache rows arrive as 64-row
+// One CTA per SM, 384 threads: warp 0 copies cache rows (TMA), warps 1 and 2 issue the two products,
+// warp 3 copies a sequence's queries, warps 4 to 11 do the softmax (a
+// warpgroup for each half of the heads).  The cache rows arrive as 64-row
 // panels of 64 channels in rings of pieces: the position channels (read by S^T only, freed early)
 // in one, pairs of latent panels (read by both products) in the other.  S^T of tile t + 1 is issued
 // before O^T of tile t, so the softmax of one tile runs beside the products of its neighbours, and
@@ -32,7 +33,8 @@ namespace {
 using namespace ptx;
 using tc::kdesc;
 
-constexpr int kT = 256;
+constexpr int kT = 384;
+constexpr int kSoft = 256;                // threads of the softmax: two warpgroups, half of the heads each
 constexpr int kRows = 64;                 // cache rows per tile
 constexpr uint32_t kPanel = kRows * 128;  // bytes of a panel: 64 rows x 64 channels
 constexpr uint32_t kPair = 2 * kPanel;
@@ -60,7 +62,7 @@ struct Misc {
     uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, q_empty, o_full, o_empty, drained;
     uint32_t tmem;
     int abort;
-    float red[2][4][NH];  // per warp: a tile's column maxima (by tile parity), at the end the sums
+    alignas(16) float red[2][4][NH];  // (read as float4) per warp: a tile's column maxima (by tile parity), at the end the sums
     float fac[NH];        // rescaling factors, at the end 1 / sum
     int64_t scan[kT / 32 + 2];
 };
@@ -160,16 +162,19 @@ __device__ __forceinline__ int half_warp_reduce(float (&r)[N], int lane)
 template <int N>
 __device__ __forceinline__ void load_scores(uint32_t t, float (&s)[N])
 {
-    if constexpr (N == 8) {
-        tmem_ld16x2_x8<8>(t, s);
-    } else if constexpr (N == 16) {
-        tmem_ld16x2_x16<16>(t, s);
-    } else {
-        static_assert(N == 32, "");
-        tmem_ld16x2_x16<32>(t, *reinterpret_cast<float(*)[16]>(&s[0]));
-        tmem_ld16x2_x16<32>(t + 16, *reinterpret_cast<float(*)[16]>(&s[16]));
-    }
+    if constexpr (N == 4) tmem_ld16x2_x4<4>(t, s);
+    else if constexpr (N == 8) tmem_ld16x2_x8<8>(t, s);
+    else tmem_ld16x2_x16<16>(t, s);
 }
+
+// 8 or 16 consecutive columns of a lane.
+__device__ __forceinline__ void load_cols(uint32_t t, float (&x)[8]) { tmem_ld8(t, x); }
+__device__ __forceinline__ void load_cols(uint32_t t, float (&x)[16]) { tmem_ld16(t, x); }
+__device__ __forceinline__ void store_cols(uint32_t t, const float (&x)[8])
+{
+    tmem_st8(t, *reinterpret_cast<const uint32_t(*)[8]>(&x));
+}
+__device__ __forceinline__ void store_cols(uint32_t t, const float (&x)[16]) { tmem_st16(t, x); }
 
 template <int NH>
 __device__ __forceinline__ void copy_role(unsigned char *sm, Misc<NH> &mi, const LatentDecode &p, Units u,
@@ -329,20 +334,30 @@ __device__ __forceinline__ void query_role(unsigned char *sm, Misc<NH> &mi, cons
     if (!ok && units > 0 && lane == 0) mbar_wait_ns(&mi.q_full, (units - 1) & 1, kWait);
 }
 
+// Softmax of half of the heads (`part`): one warpgroup.  A thread has one cache row of the tile and N
+// heads of it; a head's maximum is taken over 16 lanes and then four warps.
 template <int NH>
 __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc<NH> &mi, const LatentDecode &p, Units u,
-                                             uint32_t tmem, int tid)
+                                             uint32_t tmem, int part, int tid)
 {
     using C = Cfg<NH>;
-    constexpr int N = NH / 2, PER = N / 16 ? N / 16 : 1;
+    constexpr int N = NH / 4, HALF = NH / 2, CH = HALF < 16 ? HALF : 16;
     volatile int *abort = &mi.abort;
     const int warp = tid >> 5, lane = tid & 31, side = lane >> 4, row = 16 * warp + (lane & 15);
-    const uint32_t quarter = (uint32_t)(warp * 32) << 16;
+    const int head0 = part * HALF, mine = head0 + side * N;  // first head of the warpgroup, of this thread
+    const uint32_t quarter = (uint32_t)(warp * 32) << 16, bar = 1 + part;
     int ts = 0, units = 0;
     bool bad = false;  // a wait gave up: the next barrier takes all four warps out together
+    // every head column of O^T that this warpgroup has: 4 M tiles x HALF columns, CH at a time
+    auto columns = [&](auto &&f) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < HALF; c += CH) f(i, head0 + c);
+    };
     while (u.next()) {
-        if (tid == 0) latent_record_join(p, u.w, u.w.g - u.tiles, u.tile0, u.n, u.tiles, u.first, NH);
-        float m[N], l[N];  // of columns side * N + i: the held maximum (log2 units), this row's share of the sum
+        if (part == 0 && tid == 0) latent_record_join(p, u.w, u.w.g - u.tiles, u.tile0, u.n, u.tiles, u.first, NH);
+        float m[N], l[N];  // of heads mine + i: the held maximum (log2 units), this row's share of the sum
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             m[i] = -INFINITY;
@@ -351,33 +366,33 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc<NH> &mi, co
         for (int t = 0; t < u.tiles; ++t, ++ts) {
             float s[N], r[N];
             bad |= !wait(&mi.s_full[ts & 1], (ts / 2) & 1, abort);
+            __syncwarp();
             tc_fence_after_sync();
-            load_scores<N>(tmem + C::SCOL + (ts & 1) * NH + quarter, s);
+            load_scores<N>(tmem + C::SCOL + (ts & 1) * NH + head0 + quarter, s);
             tmem_ld_wait();
             tc_fence_before_sync();
             mbar_arrive(&mi.s_empty[ts & 1]);
             const int left = u.len - (u.tile0 + t) * kRows;  // rows of the tile that count
 #pragma unroll
             for (int i = 0; i < N; ++i) r[i] = s[i] = row < left ? s[i] * p.scale_log2 : -INFINITY;
-            const int at = side * N + half_warp_reduce<N, true>(r, lane);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) mi.red[ts & 1][warp][at + i] = r[i];
-            if (bar_sync_or(1, 128, bad)) return;
+            const int at = mine + half_warp_reduce<N, true>(r, lane);
+            mi.red[ts & 1][warp][at] = r[0];
+            if (bar_sync_or(bar, 128, bad)) return;
             bool rise = false;
             float top[N];
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
-                float4 a = *reinterpret_cast<const float4 *>(&mi.red[ts & 1][0][side * N + i]);
+                float4 a = *reinterpret_cast<const float4 *>(&mi.red[ts & 1][0][mine + i]);
 #pragma unroll
                 for (int w = 1; w < 4; ++w) {
-                    const float4 b = *reinterpret_cast<const float4 *>(&mi.red[ts & 1][w][side * N + i]);
+                    const float4 b = *reinterpret_cast<const float4 *>(&mi.red[ts & 1][w][mine + i]);
                     a = make_float4(fmaxf(a.x, b.x), fmaxf(a.y, b.y), fmaxf(a.z, b.z), fmaxf(a.w, b.w));
                 }
                 top[i] = a.x; top[i + 1] = a.y; top[i + 2] = a.z; top[i + 3] = a.w;
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) rise |= top[i] > m[i] + kSlack;
-            // the same in all four warps (each has both sides): all see the same maxima
+            // the same in the four warps (each has both sides): all see the same maxima
             if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
@@ -385,24 +400,23 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc<NH> &mi, co
                     const float f = mn == m[i] ? 1.f : tc::exp2_approx(m[i] - mn);
                     m[i] = mn;
                     l[i] *= f;
-                    if (warp == 0 && (lane & 15) == 0) mi.fac[side * N + i] = f;
+                    if (warp == 0 && (lane & 15) == 0) mi.fac[mine + i] = f;
                 }
                 if (t > 0) {  // what O^T holds follows
                     bad |= !wait(&mi.p_empty[(ts - 1) % C::NP], ((ts - 1) / C::NP) & 1, abort);
-                    if (bar_sync_or(1, 128, bad)) return;
+                    if (bar_sync_or(bar, 128, bad)) return;
                     tc_fence_after_sync();
-#pragma unroll 1
-                    for (int c = 0; c < 4 * NH; c += 16) {
-                        float x[16];
-                        tmem_ld16(tmem + quarter + c, x);
+                    columns([&](int i, int h) {
+                        float x[CH];
+                        load_cols(tmem + quarter + i * NH + h, x);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] *= mi.fac[(c & (NH - 1)) + i];
-                        tmem_st16(tmem + quarter + c, x);
-                    }
+                        for (int k = 0; k < CH; ++k) x[k] *= mi.fac[h + k];
+                        store_cols(tmem + quarter + i * NH + h, x);
+                    });
                     tmem_st_wait();
                     tc_fence_before_sync();
-                    if (bar_sync_or(1, 128, bad)) return;  // the factors are read before the next rise
+                    if (bar_sync_or(bar, 128, bad)) return;  // the factors are read before the next rise
                 }
             }
             if (ts >= C::NP) bad |= !wait(&mi.p_empty[ts % C::NP], (ts / C::NP - 1) & 1, abort);
@@ -412,10 +426,10 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc<NH> &mi, co
                 const float e = tc::exp2_approx(s[i] - (m[i] == -INFINITY ? 0.f : m[i]));
                 l[i] += e;
                 // bf16: the product's operands share one type, and V is bf16
-                tc::store_bf16(pb + tc::km16(side * N + i, row, NH), e);
+                tc::store_bf16(pb + tc::km16(mine + i, row, NH), e);
             }
             if (left < kRows) {  // rows past the end may hold anything: their weight is 0, so their values must be finite
-                for (int e = tid; e < (kRows - left) * 64; e += 128) {
+                for (int e = part * 128 + tid; e < (kRows - left) * 64; e += kSoft) {
                     const int rr = left + (e >> 6), c = e & 63;  // 16-byte piece c of the row's 8 panels
                     const int slot = (4 * ts + (c >> 4)) % C::NA;
                     *reinterpret_cast<uint4 *>(sm + C::A + slot * kPair + ((c >> 3) & 1) * kPanel + rr * 128 +
@@ -429,54 +443,52 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc<NH> &mi, co
         float r[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) r[i] = l[i];
-        const int at = side * N + half_warp_reduce<N, false>(r, lane);
+        const int at = mine + half_warp_reduce<N, false>(r, lane);
         bad |= !wait(&mi.o_full, units & 1, abort);
         ++units;
-        if (bar_sync_or(1, 128, bad)) return;  // every read of the last maxima is done
-#pragma unroll
-        for (int i = 0; i < PER; ++i) mi.red[0][warp][at + i] = r[i];
+        if (bar_sync_or(bar, 128, bad)) return;  // every read of the last maxima is done
+        mi.red[0][warp][at] = r[0];
         if (warp == 0 && (lane & 15) == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) mi.red[1][0][side * N + i] = m[i];
-        if (bar_sync_or(1, 128, bad)) return;
+            for (int i = 0; i < N; ++i) mi.red[1][0][mine + i] = m[i];
+        if (bar_sync_or(bar, 128, bad)) return;
         const int h0 = u.w.hg * NH, hs = min(NH, p.heads - h0);
         const bool whole = u.tiles == u.n;
         const int slot = u.first ? 2 * u.w.cta : 2 * u.w.cta + 1;
-        if (tid < NH) {
-            const float sum = (mi.red[0][0][tid] + mi.red[0][1][tid]) + (mi.red[0][2][tid] + mi.red[0][3][tid]);
-            const float mx = mi.red[1][0][tid];
-            mi.fac[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        if (tid < HALF) {
+            const int h = head0 + tid;
+            const float sum = (mi.red[0][0][h] + mi.red[0][1][h]) + (mi.red[0][2][h] + mi.red[0][3][h]);
+            const float mx = mi.red[1][0][h];
+            mi.fac[h] = sum == 0.f ? 0.f : 1.f / sum;
             if (whole) {
-                if (p.lse && tid < hs) p.lse[(int64_t)u.w.b * p.heads + h0 + tid] = mx * kLn2 + logf(sum);
+                if (p.lse && h < hs) p.lse[(int64_t)u.w.b * p.heads + h0 + h] = mx * kLn2 + logf(sum);
             } else {
-                float *ml = latent_ml(p.workspace) + ((size_t)slot * NH + tid) * 2;
+                float *ml = latent_ml(p.workspace) + ((size_t)slot * NH + h) * 2;
                 ml[0] = mx;
                 ml[1] = sum;
             }
         }
-        if (bar_sync_or(1, 128, bad)) return;
+        if (bar_sync_or(bar, 128, bad)) return;
         tc_fence_after_sync();
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((int64_t)u.w.b * p.heads + h0) * kLatR + tid;
-        float *part = latent_part(p.workspace, NH) + (size_t)slot * NH * kLatR + tid;
-#pragma unroll 1
-        for (int c = 0; c < 4 * NH; c += 16) {
-            float x[16];
-            tmem_ld16(tmem + quarter + c, x);
+        float *out = latent_part(p.workspace, NH) + (size_t)slot * NH * kLatR + tid;
+        columns([&](int i, int h) {  // channels 128 i + tid of heads h ...
+            float x[CH];
+            load_cols(tmem + quarter + i * NH + h, x);
             tmem_ld_wait();
-            const int i = c / NH, hb = c & (NH - 1);  // channels 128 i + tid of heads hb ...
             if (whole) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (hb + k < hs) store_io(o + (size_t)(hb + k) * kLatR + 128 * i, x[k] * mi.fac[hb + k]);
+                for (int k = 0; k < CH; ++k)
+                    if (h + k < hs) store_io(o + (size_t)(h + k) * kLatR + 128 * i, x[k] * mi.fac[h + k]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (hb + k < hs) part[(size_t)(hb + k) * kLatR + 128 * i] = x[k];
+                for (int k = 0; k < CH; ++k)
+                    if (h + k < hs) out[(size_t)(h + k) * kLatR + 128 * i] = x[k];
             }
-        }
+        });
         tc_fence_before_sync();
         mbar_arrive(&mi.o_empty);
-        if (bar_sync_or(1, 128, bad)) return;  // fac and red are free again
+        if (bar_sync_or(bar, 128, bad)) return;  // fac and red are free again
     }
 }
 
@@ -496,6 +508,7 @@ latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMa
     }
     if (tid == 0) {
         prefetch_tmap(&tm);
+        prefetch_tmap(&tq);
         for (int i = 0; i < C::NA; ++i) {
             mbar_init(&mi.full_a[i], 1);
             mbar_init(&mi.empty_a[i], 1);
@@ -506,14 +519,14 @@ latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMa
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&mi.s_full[i], 1);
-            mbar_init(&mi.s_empty[i], 128);
-            mbar_init(&mi.p_full[i], 128);
+            mbar_init(&mi.s_empty[i], kSoft);
+            mbar_init(&mi.p_full[i], kSoft);
             mbar_init(&mi.p_empty[i], 1);
         }
         mbar_init(&mi.q_full, 1);
         mbar_init(&mi.q_empty, 1);
         mbar_init(&mi.o_full, 1);
-        mbar_init(&mi.o_empty, 128);
+        mbar_init(&mi.o_empty, kSoft);
         mbar_init(&mi.drained, 2);
         fence_mbar_init();
         mi.abort = 0;
@@ -540,7 +553,7 @@ latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMa
                 if (lane == 0) mbar_wait_ns(&mi.drained, 0, kWait);
             }
         } else if (warp == 3) query_role<NH>(sm, mi, p, u, tq, b_step, h_step, lane);
-        else softmax_role<NH>(sm, mi, p, u, tmem, tid - 128);
+        else softmax_role<NH>(sm, mi, p, u, tmem, (warp - 4) >> 2, (tid - 128) & 127);
     }
     tc_fence_before_sync();
     __syncthreads();
