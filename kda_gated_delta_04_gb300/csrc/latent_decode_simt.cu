@@ -14,7 +14,7 @@
 namespace kda {
 namespace {
 
-using ptx::pdl_wait;
+using namespace ptx;
 
 constexpr int kT = 256;        // threads
 constexpr int kRows = 32;      // cache rows per tile, one per lane
@@ -25,6 +25,7 @@ constexpr int kSpan = kLatC / 8;  // channels of one warp in the score product
 struct Smem {
     float q[kHeads][kLatC];
     float k[kRows][kLdK];
+    const float *row[2][kRows];  // where the tile's rows lie (null: zeros), by tile parity
     float red[8][kHeads][kRows];
     float p[kRows][kHeads];
     float alpha[kHeads];
@@ -35,16 +36,16 @@ struct Smem {
 // Two CTAs on an SM overlap one's loads with the other's products.  Scores: warp w multiplies
 // channels [72 w, 72 w + 72) for the tile's 32 rows (a lane each) and 8 heads, then the eight
 // partial products are summed.  Output: a thread owns two of the 512 channels for 8 heads.
-template <typename IO>
 __global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentDecode p)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t capacity = (int64_t)p.table_width * p.page_size;
-    LatentWalk w = latent_walk<kT, IO>(p, kRows, kHeads, sm.scan);
+    LatentWalk w = latent_walk<kT, float>(p, kRows, kHeads, sm.scan);
+    pdl_launch_dependents();
     if (w.cta >= w.ctas) return;
-    const IO *cache = static_cast<const IO *>(p.cache);
+    const float *cache = static_cast<const float *>(p.cache);
     bool first_unit = true;
     while (w.g < w.g_end) {
         bool ignore = false;
@@ -57,10 +58,24 @@ __global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentD
         const int tile0 = w.tile, tiles = (int)min((int64_t)(n - tile0), w.g_end - w.g);
         if (tid == 0) latent_record_join(p, w, w.g, tile0, n, tiles, first_unit, kHeads);
         const int h0 = w.hg * kHeads, hs = min(kHeads, p.heads - h0);
-        __syncthreads();  // the previous unit's reads of q
-        for (int e = tid; e < kHeads * kLatC; e += kT) {
-            const int h = e / kLatC, c = e - h * kLatC;
-            sm.q[h][c] = h < hs ? load_io(static_cast<const IO *>(p.q) + w.b * p.q_bs + (h0 + h) * p.q_hs + c) : 0.f;
+        // the row pointers of tile t: one warp looks the pages up
+        auto look_up = [&](int t) {
+            const int j = t * kRows + lane;
+            const float *at = nullptr;  // rows past the end count nothing, whatever they hold
+            if (j < len) {
+                const int page = j / p.page_size;
+                const int64_t x = p.table[w.b * p.table_stride + page];
+                if (x >= 0 && x < p.num_pages) at = cache + (x * p.page_size + (j - page * p.page_size)) * kLatC;
+                else if (p.errors) atomicOr(p.errors, DEV_ERR_PAGE);
+            }
+            sm.row[t & 1][lane] = at;
+        };
+        __syncthreads();  // the previous unit's reads of q, k and the row pointers
+        if (warp == 0) look_up(tile0);
+        for (int e = tid; e < kHeads * (kLatC / 4); e += kT) {
+            const int h = e / (kLatC / 4), c = 4 * (e - h * (kLatC / 4));
+            cp_async16(&sm.q[h][c],
+                       static_cast<const float *>(p.q) + w.b * p.q_bs + (h0 + (h < hs ? h : 0)) * p.q_hs + c, h < hs);
         }
         float m = -INFINITY, l = 0.f;  // of head `warp`, the same on every lane (l: this lane's rows)
         float acc[kHeads][2];
@@ -68,20 +83,20 @@ __global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentD
         for (int h = 0; h < kHeads; ++h) acc[h][0] = acc[h][1] = 0.f;
         for (int t = tile0; t < tile0 + tiles; ++t) {
             const int j0 = t * kRows, rows = min(kRows, len - j0);
-            __syncthreads();  // the previous tile's reads of k and p
-            for (int e = tid; e < kRows * (kLatC / 4); e += kT) {
-                const int r = e / (kLatC / 4), c = 4 * (e - r * (kLatC / 4));
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);  // rows past the end count nothing, whatever they hold
-                if (r < rows) {
-                    const int j = j0 + r, page = j / p.page_size;
-                    const int64_t at = p.table[w.b * p.table_stride + page];
-                    if (at >= 0 && at < p.num_pages)
-                        x = load4_io(cache + (at * p.page_size + (j - page * p.page_size)) * kLatC + c);
-                    else if (c == 0 && p.errors)
-                        atomicOr(p.errors, DEV_ERR_PAGE);
+            __syncthreads();  // the previous tile's reads of k and p; this one's row pointers are there
+            // a warp has four rows: 576 channels are 4.5 copies of 16 bytes a lane
+#pragma unroll
+            for (int r = 4 * warp; r < 4 * warp + 4; ++r) {
+                const float *at = sm.row[t & 1][r];
+#pragma unroll
+                for (int u = 0; u < 5; ++u) {
+                    const int c = 4 * (lane + 32 * u);
+                    if (c < kLatC) cp_async16(&sm.k[r][c], at ? at + c : cache, at != nullptr);
                 }
-                *reinterpret_cast<float4 *>(&sm.k[r][c]) = x;
             }
+            cp_async_commit();
+            if (warp == 0 && t + 1 < tile0 + tiles) look_up(t + 1);
+            cp_async_wait<0>();
             __syncthreads();
             float s[kHeads];
 #pragma unroll
@@ -144,9 +159,8 @@ __global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentD
             for (int h = 0; h < kHeads; ++h) {
                 if (h >= hs) break;
                 const float inv = sm.ml[h][1] == 0.f ? 0.f : 1.f / sm.ml[h][1];
-                IO *o = static_cast<IO *>(p.o) + ((int64_t)w.b * p.heads + h0 + h) * kLatR + 2 * tid;
-                store_io(o, acc[h][0] * inv);
-                store_io(o + 1, acc[h][1] * inv);
+                float *o = static_cast<float *>(p.o) + ((int64_t)w.b * p.heads + h0 + h) * kLatR + 2 * tid;
+                *reinterpret_cast<float2 *>(o) = make_float2(acc[h][0] * inv, acc[h][1] * inv);
             }
             if (p.lse && tid < hs)
                 p.lse[(int64_t)w.b * p.heads + h0 + tid] = sm.ml[tid][0] * kLn2 + logf(sm.ml[tid][1]);
@@ -280,20 +294,6 @@ int sm_count()
     return n;
 }
 
-template <typename IO>
-cudaError_t launch_simt(const LatentDecode &p)
-{
-    const cudaError_t err = cudaFuncSetAttribute(latent_decode_simt_kernel<IO>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-    if (err != cudaSuccess) return err;
-    const int sms = sm_count();
-    if (sms <= 0) return cudaErrorInvalidDevice;
-    const int grid = 2 * sms < kLatMaxGrid ? 2 * sms : kLatMaxGrid;
-    latent_decode_simt_kernel<IO><<<grid, kT, sizeof(Smem), p.stream>>>(p);
-    const cudaError_t launched = cudaGetLastError();
-    return launched != cudaSuccess ? launched : launch_latent_join(p, kHeads, grid);
-}
-
 }  // namespace
 
 cudaError_t launch_latent_join(const LatentDecode &p, int head_tile, int grid)
@@ -306,7 +306,18 @@ size_t latent_decode_simt_ws_bytes() { return latent_ws_bytes(kHeads, kLatMaxGri
 
 cudaError_t launch_latent_decode_simt(const LatentDecode &p)
 {
-    return launch_simt<float>(p);
+    const cudaError_t err = cudaFuncSetAttribute(latent_decode_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)sizeof(Smem));
+    if (err != cudaSuccess) return err;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int64_t per_seq = ((int64_t)p.table_width * p.page_size + kRows - 1) / kRows;
+    const int64_t most = per_seq * p.batch * ((p.heads + kHeads - 1) / kHeads);  // no more CTAs than there can be tiles
+    int grid = 2 * sms < kLatMaxGrid ? 2 * sms : kLatMaxGrid;
+    if (most < grid) grid = most > 0 ? (int)most : 1;
+    latent_decode_simt_kernel<<<grid, kT, sizeof(Smem), p.stream>>>(p);
+    const cudaError_t launched = cudaGetLastError();
+    return launched != cudaSuccess ? launched : launch_latent_join(p, kHeads, grid);
 }
 
 }  // namespace kda

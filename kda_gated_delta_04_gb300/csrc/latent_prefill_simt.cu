@@ -4,14 +4,23 @@
 //   s_ij = scale q_i . [k_nope_j, k_pe_j],  o_i = sum_j softmax_j(s_i) v_j
 //
 // A sequence of lq queries and lk keys is aligned at its end: query i sees keys j <= i + lk - lq
-// (causal) or all.  One CTA holds 64 queries of one head and passes over the keys in tiles of 64
-// with a running maximum and sum per query (base 2).
+// (causal) or all.  64 queries of one head pass over the keys in tiles of 64 with a running maximum and
+// sum per query (base 2).  Bound by the fp32 rate: 128 products a cycle and SM, 10,240 cycles a tile.
+// K and V have one buffer each: K of the next tile is copied (cp.async) while the softmax and the value
+// product run, V while the scores do.
+//
+// With fewer query tiles than SMs a cluster of four CTAs shares a query tile, each taking every fourth
+// key tile, and the four results are joined through distributed shared memory (1,027 tokens, 4 heads:
+// XXX us; one CTA a tile: 216).
 #include <math.h>
 
 #include "latent.cuh"
+#include "sm100_ptx.cuh"
 
 namespace kda {
 namespace {
+
+using namespace ptx;
 
 constexpr int kT = 256, kM = 64, kN = 64;  // threads, queries and keys per tile
 constexpr int kLdQ = kLatQK + 4, kLdV = kLatN, kLdS = kN + 4;  // row strides (floats)
@@ -19,34 +28,77 @@ constexpr int kLdQ = kLatQK + 4, kLdV = kLatN, kLdS = kN + 4;  // row strides (f
 struct Smem {
     float q[kM][kLdQ];
     float k[kN][kLdQ];
-    float v[kN][kLdV];
-    float p[kM][kLdS];
+    union {
+        struct {
+            float v[kN][kLdV];
+            float p[kM][kLdS];
+        };
+        float o[kM][kLatN];  // a CTA's unnormalised output, for the join
+    };
+    float m[kM], l[kM];
 };
 
+// A float of this CTA's shared memory as CTA `rank` of the cluster has it.
+__device__ __forceinline__ float4 peer_load4(const float *p, uint32_t rank)
+{
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(map_to_rank(p, rank)));
+    return x;
+}
+__device__ __forceinline__ float peer_load(const float *p, uint32_t rank)
+{
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_to_rank(p, rank)));
+    return x;
+}
+
 // Threads are 16 x 16: thread (ty, tx) has queries 4 ty .. 4 ty + 3, and keys tx + 16 j or output
-// channels 4 tx + 64 j.  The 16 threads of a query row are half a warp.
-template <typename IO>
+// channels 4 tx + 64 j.  The 16 threads of a query row are half a warp.  CS: CTAs per query tile.
+template <int CS>
 __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const LatentPrefill p)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     Smem &sm = *reinterpret_cast<Smem *>(raw);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int h = blockIdx.y;
-    // Query tiles are numbered so that sequence n's start at cu_q[n] / 64 + n: increasing in n,
-    // with room for every tile, found by bisection.  Late tiles (most keys) run first.
-    const int tile = (int)(gridDim.x - 1 - blockIdx.x);
+    const int rank = CS > 1 ? (int)cluster_rank() : 0, unit = blockIdx.x / CS;
+    const int h = unit % p.heads;
+    // the tiles with the most keys first
+    const int tile = (int)(gridDim.x / CS / p.heads) - 1 - unit / p.heads;
     const LatentTile at = latent_tile(p, tile, kM);
-    if (tile == 0 && h == 0 && tid < 32) {
+    if (blockIdx.x == 0 && tid < 32) {
         latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
         latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);
     }
-    if (at.rows <= 0) return;
+    if (at.rows <= 0) return;  // every CTA of the cluster
+    const float *q = static_cast<const float *>(p.q) + h * p.q_hs, *kn = static_cast<const float *>(p.k_nope) + h * p.kn_hs;
+    const float *kp = static_cast<const float *>(p.k_pe), *v = static_cast<const float *>(p.v) + h * p.v_hs;
+    auto copy_k = [&](int j0) {
+        for (int e = tid; e < kN * (kLatQK / 4); e += kT) {
+            const int r = e / (kLatQK / 4), c = 4 * (e - r * (kLatQK / 4));
+            const bool ok = j0 + r < at.keys;
+            const int64_t j = ok ? at.k0 + j0 + r : 0;
+            cp_async16(&sm.k[r][c], c < kLatN ? kn + j * p.kn_ts + c : kp + j * p.kp_ts + (c - kLatN), ok);
+        }
+        cp_async_commit();
+    };
+    auto copy_v = [&](int j0) {
+        for (int e = tid; e < kN * (kLatN / 4); e += kT) {
+            const int r = e / (kLatN / 4), c = 4 * (e - r * (kLatN / 4));
+            const bool ok = j0 + r < at.keys;
+            cp_async16(&sm.v[r][c], v + (ok ? at.k0 + j0 + r : 0) * (int64_t)p.v_ts + c, ok);
+        }
+        cp_async_commit();
+    };
+    const int first = rank * kN, step = CS * kN;
     for (int e = tid; e < kM * (kLatQK / 4); e += kT) {
         const int r = e / (kLatQK / 4), c = 4 * (e - r * (kLatQK / 4));
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < at.rows) x = load4_io(static_cast<const IO *>(p.q) + (int64_t)(at.q0 + r) * p.q_ts + h * p.q_hs + c);
-        *reinterpret_cast<float4 *>(&sm.q[r][c]) = x;
+        const bool ok = r < at.rows;
+        cp_async16(&sm.q[r][c], q + (at.q0 + (ok ? r : 0)) * (int64_t)p.q_ts + c, ok);
     }
+    copy_k(first);
+    copy_v(first);
     float m[4], l[4], acc[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -55,25 +107,8 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[i][c] = 0.f;
     }
-    for (int j0 = 0; j0 < at.keys; j0 += kN) {
-        __syncthreads();
-        for (int e = tid; e < kN * (kLatQK / 4); e += kT) {
-            const int r = e / (kLatQK / 4), c = 4 * (e - r * (kLatQK / 4));
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j0 + r < at.keys) {
-                const int64_t j = at.k0 + j0 + r;
-                x = c < kLatN ? load4_io(static_cast<const IO *>(p.k_nope) + j * p.kn_ts + h * p.kn_hs + c)
-                              : load4_io(static_cast<const IO *>(p.k_pe) + j * p.kp_ts + (c - kLatN));
-            }
-            *reinterpret_cast<float4 *>(&sm.k[r][c]) = x;
-        }
-        for (int e = tid; e < kN * (kLatN / 4); e += kT) {
-            const int r = e / (kLatN / 4), c = 4 * (e - r * (kLatN / 4));
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j0 + r < at.keys)
-                x = load4_io(static_cast<const IO *>(p.v) + (int64_t)(at.k0 + j0 + r) * p.v_ts + h * p.v_hs + c);
-            *reinterpret_cast<float4 *>(&sm.v[r][c]) = x;
-        }
+    for (int j0 = first; j0 < at.keys; j0 += step) {
+        cp_async_wait<1>();  // K (V may still be on its way)
         __syncthreads();
         float s[4][4] = {};
 #pragma unroll 4
@@ -89,6 +124,8 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
                 for (int j = 0; j < 4; ++j)
                     s[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
         }
+        __syncthreads();  // K is read
+        copy_k(j0 + step);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int last = p.causal ? at.off + 4 * ty + i : at.keys - 1;  // last key this query sees
@@ -114,7 +151,8 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
                 sm.p[4 * ty + i][tx + 16 * j] = e;
             }
         }
-        __syncwarp();  // a query row's weights are written and read by the same half warp
+        cp_async_wait<1>();  // V (the next K may still be on its way)
+        __syncthreads();
 #pragma unroll 4
         for (int r = 0; r < kN; r += 4) {
             float4 w[4];
@@ -132,39 +170,100 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
                 }
             }
         }
+        __syncthreads();  // V is read
+        copy_v(j0 + step);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int d = 8; d; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+    }
+    cp_async_wait<0>();
+    if constexpr (CS > 1) {
+        // every CTA's part where the others can read it, then each writes a share of the rows
+        __syncthreads();  // o lies over v and p
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i;
+            *reinterpret_cast<float4 *>(&sm.o[r][4 * tx]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            *reinterpret_cast<float4 *>(&sm.o[r][64 + 4 * tx]) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+            if (tx == 0) {
+                sm.m[r] = m[i];
+                sm.l[r] = l[i];
+            }
+        }
+        cluster_sync();
+        constexpr int kShare = kM / CS;
+        for (int e = tid; e < kShare * (kLatN / 4); e += kT) {
+            const int r = rank * kShare + e / (kLatN / 4), c = 4 * (e % (kLatN / 4));
+            float pm[CS], top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < CS; ++u) {
+                pm[u] = peer_load(&sm.m[r], u);
+                top = fmaxf(top, pm[u]);
+            }
+            const float base = top == -INFINITY ? 0.f : top;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < CS; ++u) {
+                const float f = exp2f(pm[u] - base);
+                const float4 y = peer_load4(&sm.o[r][c], u);
+                sum += f * peer_load(&sm.l[r], u);
+                x.x += f * y.x; x.y += f * y.y; x.z += f * y.z; x.w += f * y.w;
+            }
+            if (r >= at.rows) continue;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t row = (int64_t)(at.q0 + r) * p.heads + h;
+            store4_io(static_cast<float *>(p.o) + row * kLatN + c, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+            if (p.lse && c == 0) p.lse[row] = top * kLn2 + logf(sum);
+        }
+        cluster_sync();  // no CTA goes while another reads its part
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
         if (r >= at.rows) continue;
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
         const float lo[4] = {acc[i][0] * inv, acc[i][1] * inv, acc[i][2] * inv, acc[i][3] * inv};
         const float hi[4] = {acc[i][4] * inv, acc[i][5] * inv, acc[i][6] * inv, acc[i][7] * inv};
-        IO *o = static_cast<IO *>(p.o) + ((int64_t)(at.q0 + r) * p.heads + h) * kLatN + 4 * tx;
+        const int64_t row = (int64_t)(at.q0 + r) * p.heads + h;
+        float *o = static_cast<float *>(p.o) + row * kLatN + 4 * tx;
         store_io4(o, lo);
         store_io4(o + 64, hi);
-        if (p.lse && tx == 0) p.lse[(int64_t)(at.q0 + r) * p.heads + h] = m[i] * kLn2 + logf(l[i]);
+        if (p.lse && tx == 0) p.lse[row] = m[i] * kLn2 + logf(l[i]);
     }
 }
 
-template <typename IO>
-cudaError_t launch_simt(const LatentPrefill &p)
+template <int CS>
+cudaError_t launch(const LatentPrefill &p, int64_t units)
 {
-    const cudaError_t err = cudaFuncSetAttribute(latent_prefill_simt_kernel<IO>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    cudaError_t err = cudaFuncSetAttribute(latent_prefill_simt_kernel<CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)sizeof(Smem));
     if (err != cudaSuccess) return err;
-    const dim3 grid((unsigned)(p.q_tokens / kM + p.num_seqs), (unsigned)p.heads);
-    latent_prefill_simt_kernel<IO><<<grid, kT, sizeof(Smem), p.stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * CS));
+    cfg.blockDim = dim3(kT);
+    cfg.dynamicSmemBytes = sizeof(Smem);
+    cfg.stream = p.stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = CS;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_prefill_simt_kernel<CS>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_prefill_simt(const LatentPrefill &p)
 {
-    return launch_simt<float>(p);
+    const int64_t tiles = p.num_seqs == 1 ? (p.q_tokens + kM - 1) / kM : p.q_tokens / kM + p.num_seqs;
+    const int64_t units = tiles * p.heads;
+    if (4 * units > 0x7fffffff) return cudaErrorInvalidValue;
+    // four CTAs a tile up to two tiles an SM: the longest tile then no longer sets the time
+    return units <= 2 * 152 ? launch<4>(p, units) : launch<1>(p, units);
 }
 
 }  // namespace kda

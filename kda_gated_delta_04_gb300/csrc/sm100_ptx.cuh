@@ -210,6 +210,21 @@ __device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int32_t x, int
                  : "memory");
 }
 
+// 16 bytes global -> shared by the thread's own asynchronous copy (zeros where `ok` is false; the
+// source is then not read).
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most N of the thread's committed groups are unfinished.
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Global-memory flags between CTAs of one grid: a release store after the data it
 // publishes, an acquire load before the data is read, and the proxy fence that orders
 // bulk-copy (async proxy) traffic on global memory with them.
