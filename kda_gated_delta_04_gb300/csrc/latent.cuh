@@ -133,18 +133,25 @@ __device__ __forceinline__ void latent_range(const int32_t *cu, int n, int total
 }
 
 // Sequence n's tiles are numbered from cu_q[n] / m + n, which increases with n and leaves room for
-// all of them, so that bisection finds a tile's sequence without a table.  A malformed cu_q or
-// cu_k is reported and held to the buffers.
-__device__ __forceinline__ LatentTile latent_tile(const LatentPrefill &p, int tile, int m)
+// all of them, so that a search finds a tile's sequence without a table: 32 candidates at a time, by a
+// whole warp (65,535 sequences: four rounds of one load).  A malformed cu_q or cu_k is reported and held
+// to the buffers.
+__device__ __forceinline__ LatentTile latent_tile(const LatentPrefill &p, int tile, int m, int lane)
 {
     int n = 0, q0, q1, k0, k1;
     if (p.cu_q) {
-        int hi = p.num_seqs - 1;
-        while (n < hi) {  // the last sequence whose first tile is not after `tile`
-            const int mid = (n + hi + 1) >> 1;
-            latent_range(p.cu_q, mid, (int)p.q_tokens, q0, q1);
-            if (q0 / m + mid <= tile) n = mid;
-            else hi = mid - 1;
+        int count = p.num_seqs;  // the last sequence whose first tile is not after `tile` is in [n, n + count)
+        while (count > 1) {
+            const int step = (count + 31) / 32, at = n + lane * step;
+            bool before = false;
+            if (lane * step < count) {
+                latent_range(p.cu_q, at, (int)p.q_tokens, q0, q1);
+                before = q0 / m + at <= tile;
+            }
+            const uint32_t set = __ballot_sync(0xffffffffu, before) | 1u;
+            const int k = 31 - __clz(set);
+            n += k * step;
+            count = min(step, count - k * step);
         }
     }
     latent_range(p.cu_q, n, (int)p.q_tokens, q0, q1);

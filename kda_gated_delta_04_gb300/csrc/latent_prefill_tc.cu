@@ -19,8 +19,8 @@
 // Tensor memory is full: two O, two S of 128 columns.  The two query tiles take turns: while one
 // tile's softmax runs (a warpgroup each, a thread per query, so that maximum and sum need no other
 // thread), the tensor cores run the other tile's products, O += P V of key tile j and S of j + 1.
-// Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10 and 11 only
-// make up the warpgroup whose registers the softmax takes over.
+// Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10 and 11 make up
+// the warpgroup whose registers the softmax takes over.
 #include <math.h>
 
 #include "latent.cuh"
@@ -47,14 +47,30 @@ constexpr uint64_t kWait = tc::kWaitNs;
 constexpr float kSlack = 8.f;  // log2: how far scores may pass the held maximum before it is moved
 constexpr uint32_t kColO = 0, kColS = 256;    // + 128 x query tile
 
+// What a pair of CTAs works on: queries [q0, q0 + rows) of one head against the keys of their sequence,
+// klen from k0; the first query sees the keys up to `off` when causal.  n0, n1: key tiles that the two
+// query tiles see (with the second tile there is, it sees every key tile that the first does).
+struct alignas(16) Job {
+    int q0, k0, rows, klen, off, n0, n1;
+    int h;  // head; -1: no job, the pair is done
+    __device__ __forceinline__ int n(int i) const { return i ? n1 : n0; }
+    __device__ __forceinline__ int nmax() const { return max(n0, n1); }
+    // the last key tile reaches past the sequence's keys
+    __device__ __forceinline__ bool tail() const { return nmax() > 0 && nmax() * kN > klen; }
+    // first of this CTA's rows of tile i
+    __device__ __forceinline__ static int first(int i, int rank) { return 2 * kM * i + kM * rank; }
+};
+
 // Barriers of the leading CTA only: q_full, k_full, v_full (bytes that both CTAs copy), p_full,
 // o_empty and next_empty (a warp's arrival each, both CTAs).  The others each CTA has for itself; what the matrix
 // instructions signal arrives in both.
 struct Misc {
     uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], v_tail[kStages], drained;
-    uint64_t next_full, next_empty;  // the next job's number: each CTA; all readers, in the leading CTA
+    uint64_t next_full, next_empty;  // the number of the next job: each CTA; both CTAs' copy warps, in the leading CTA
+    uint64_t job_full[2], job_empty[2];
     alignas(16) uint4 next;
+    alignas(16) Job job[2];          // the present job and the next, for this CTA's other warps
     uint32_t tmem;
     int abort;
 };
@@ -97,6 +113,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32])
         : "r"(taddr));
 }
 
+// 32 bytes to global memory: whole sectors (16-byte aligned; in one instruction where 32-byte aligned).
+__device__ __forceinline__ void store32(__nv_bfloat16 *p, const uint32_t (&w)[8])
+{
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // Pairs of fp32 in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -122,60 +151,52 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// What a pair of CTAs works on, and how many key tiles each of its query tiles sees.
-struct Job {
-    LatentTile at;  // of all 512 queries
-    int h;          // head
-    int n0, n1, nmax;
-    bool tail;      // the last key tile reaches past the sequence's keys
-    __device__ __forceinline__ int n(int i) const { return i ? n1 : n0; }
-    // first of this CTA's rows of tile i, and their count
-    __device__ __forceinline__ int first(int i, int rank) const { return 2 * kM * i + kM * rank; }
-    __device__ __forceinline__ int rows(int i, int rank) const { return max(0, min(kM, at.rows - first(i, rank))); }
-};
-
-// The job of cluster `pair` of the grid: heads innermost, the tiles with the most keys first.
-__device__ __forceinline__ Job make_job(const LatentPrefill &p, int pair)
+// The job of cluster `pair` of the grid: heads innermost, the tiles with the most keys first.  A whole warp.
+__device__ __forceinline__ Job make_job(const LatentPrefill &p, int pair, int lane)
 {
     const int pairs = gridDim.x >> 1;
+    const LatentTile at = latent_tile(p, pairs / p.heads - 1 - pair / p.heads, kPairM, lane);
     Job j;
     j.h = pair % p.heads;
-    j.at = latent_tile(p, pairs / p.heads - 1 - pair / p.heads, kPairM);
+    j.q0 = at.q0;
+    j.k0 = at.k0;
+    j.rows = at.rows;
+    j.klen = at.klen;
+    j.off = at.off;
     auto tiles = [&](int i) {
-        const int rows = max(0, min(2 * kM, j.at.rows - 2 * kM * i));
-        int keys = j.at.klen;
-        if (p.causal) keys = max(0, min(keys, j.at.off + 2 * kM * i + rows));
+        const int rows = max(0, min(2 * kM, j.rows - 2 * kM * i));
+        int keys = j.klen;
+        if (p.causal) keys = max(0, min(keys, j.off + 2 * kM * i + rows));
         return rows > 0 ? (keys + kN - 1) / kN : 0;
     };
     j.n0 = tiles(0);
     j.n1 = tiles(1);
-    j.nmax = max(j.n0, j.n1);
-    j.tail = j.nmax > 0 && j.nmax * kN > j.at.klen;
     return j;
 }
 
-// The jobs of this pair as every role walks them: its own cluster's, then those of clusters that were
-// still waiting to be launched.  The next one is asked for when the last copy of the present one has
-// been issued (copy_role): early enough for the answer to be there, and no sooner, so that the last
-// jobs go to the pairs that are done first.  Every warp of a role calls next in step.
+// The jobs of this pair as the other warps of a CTA read them from its copy warp, which writes them one
+// job ahead.  Every warp of a role calls take in step.
 struct Jobs {
     Misc &mi;
-    int at, count;
-    __device__ __forceinline__ Jobs(Misc &m) : mi(m), at((int)(blockIdx.x >> 1)), count(0) {}
-    __device__ __forceinline__ bool next(int lane)
+    int count;
+    __device__ __forceinline__ Jobs(Misc &m) : mi(m), count(0) {}
+    // false: there is none, or a wait gave up
+    __device__ __forceinline__ bool take(Job &job, int lane)
     {
-        if (!all_wait<false>(&mi.next_full, count & 1, &mi.abort)) return false;
-        at = cluster_taken(&mi.next) >> 1;  // (-1 stays -1)
-        fence_proxy_async_smem();           // read before it is written again
+        const int slot = count & 1;
+        if (!all_wait<false>(&mi.job_full[slot], (count >> 1) & 1, &mi.abort)) return false;
+        job = mi.job[slot];
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(&mi.next_empty, 0));
+        if (lane == 0) mbar_arrive(&mi.job_empty[slot]);
         ++count;
-        return at >= 0;
+        return job.h >= 0;
     }
 };
-constexpr int kJobReaders = 2 * (8 + 1 + 1);  // warps of both CTAs: softmax, copies, matrix instructions
 
-// One warp of each CTA.
+// One warp of each CTA: finds the jobs (its own cluster's, then those of clusters that were still
+// waiting to be launched) and copies their tiles.  The next one is asked for when the last copy of the
+// present one has been issued: early enough for the answer to be there, and no sooner, so that the last
+// jobs go to the pairs that are done first.
 __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const LatentPrefill &p, const CUtensorMap &tq,
                                           const CUtensorMap &tk, const CUtensorMap &tp, const CUtensorMap &tv,
                                           int q_step, int k_step, int v_step, int rank, int lane)
@@ -183,13 +204,23 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const Lat
     volatile int *abort = &mi.abort;
     const bool lead = lane == 0, leader = rank == 0;
     int t = 0, nq0 = 0, nq1 = 0;  // key tiles and queries copied so far
+    int at = blockIdx.x >> 1;
     bool ok = true;
-    Jobs jobs(mi);
-    do {
-        const Job job = make_job(p, jobs.at);
-        const int k0 = job.at.k0, q0 = job.at.q0, h = job.h * q_step, kh = job.h * k_step, vh = job.h * v_step;
+    for (int count = 0;; ++count) {
+        const int js = count & 1;
+        if (count >= 2 && !(ok = all_wait<false>(&mi.job_empty[js], (count / 2 - 1) & 1, abort))) break;
+        Job job;
+        job.h = -1;
+        if (at >= 0) job = make_job(p, at, lane);
+        if (lead) {
+            mi.job[js] = job;
+            mbar_arrive(&mi.job_full[js]);
+        }
+        if (at < 0) break;
+        const int k0 = job.k0, q0 = job.q0, h = job.h * q_step, kh = job.h * k_step, vh = job.h * v_step;
+        const int nmax = job.nmax();
         auto ahead = [&](int j) {  // this CTA's part of key tile j into L2
-            if (!lead || j >= job.nmax) return;
+            if (!lead || j >= nmax) return;
             const int k = k0 + kN * j;
             tma_prefetch_3d(&tk, 0, kh, k + 64 * rank);
             tma_prefetch_3d(&tk, 64, kh, k + 64 * rank);
@@ -209,10 +240,15 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const Lat
             ++nq;
             return true;
         };
+        if (lead) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (job.n(i) > 0)
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) tma_prefetch_3d(&tq, 64 * c, h, q0 + job.first(i, rank));
+        }
         for (int j = 0; j < kAhead; ++j) ahead(j);
-        if (!(ok = queries(0, nq0))) break;
-        if (job.nmax == 0 && !(ok = queries(1, nq1))) break;
-        for (int j = 0; j < job.nmax; ++j, ++t) {
+        for (int j = 0; j < nmax; ++j, ++t) {
             ahead(j + kAhead);
             const int slot = t % kStages, k = k0 + kN * j;
             if (t >= kStages && !(ok = all_wait<false>(&mi.k_empty[slot], (t / kStages - 1) & 1, abort))) break;
@@ -224,11 +260,11 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const Lat
                 tma_load_3d_pair(dst + kPanelK, &tk, bar, 64, kh, k + 64 * rank);
                 tma_load_3d_pair(dst + 2 * kPanelK, &tp, bar, 0, 0, k + 64 * rank);
             }
-            if (j == 0 && !(ok = queries(1, nq1))) break;
+            if (j == 0 && !(ok = queries(0, nq0) && queries(1, nq1))) break;
             if (t >= kStages && !(ok = all_wait<false>(&mi.v_empty[slot], (t / kStages - 1) & 1, abort))) break;
             if (lead) {
                 unsigned char *dst = sm + kOffV + slot * kTileV;
-                if (job.tail && j == job.nmax - 1) {
+                if (job.tail() && j == nmax - 1) {
                     // each CTA's softmax waits for this part itself (it clears the rows past the end) and
                     // answers for it with its weights
                     if (leader) mbar_arrive(&mi.v_full[slot]);
@@ -243,11 +279,16 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const Lat
         if (!ok) break;
         if (lead) mbar_arrive_expect_tx(&mi.next_full, 16);
         if (leader) {
-            if (jobs.count > 0 && !(ok = all_wait<true>(&mi.next_empty, (jobs.count - 1) & 1, abort))) break;
+            if (count > 0 && !(ok = all_wait<true>(&mi.next_empty, (count - 1) & 1, abort))) break;
             if (lead) cluster_take(&mi.next, &mi.next_full);
         }
         __syncwarp();
-    } while (jobs.next(lane));
+        if (!(ok = all_wait<false>(&mi.next_full, count & 1, abort))) break;
+        at = cluster_taken(&mi.next) >> 1;  // (-1 stays -1)
+        fence_proxy_async_smem();           // read before it is written again
+        __syncwarp();
+        if (lead) mbar_arrive_cluster(map_to_rank(&mi.next_empty, 0));
+    }
     if (*abort && lead) {  // the copies in flight land before the pair goes (the other CTA stays for this one)
         if (leader) {
             if (nq0) mbar_wait_ns(&mi.q_full[0], (nq0 - 1) & 1, kWait);
@@ -262,8 +303,10 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const Lat
     }
 }
 
-// One warp of the leading CTA, in step.
-__device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, const LatentPrefill &p, uint32_t tmem, int lane)
+// One warp of the leading CTA, in step: for each key tile and query tile in turn O += P V, then S of the
+// next key tile.  (A warp for each query tile: 6% slower; both tiles' softmax then run at the same time and
+// share the exponential units.)
+__device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, int lane)
 {
     constexpr uint32_t id_s = idesc_bf16(2 * kM, kN, false, false), id_o = idesc_bf16(2 * kM, 128, false, true);
     volatile int *abort = &mi.abort;
@@ -272,14 +315,13 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, const LatentPref
     int np0 = 0, np1 = 0;        // products O += P V of each query tile so far
     int nj0 = 0, nj1 = 0;        // jobs of each query tile so far
     Jobs jobs(mi);
-    do {
-        const Job job = make_job(p, jobs.at);
-        // the second query tile, where there is one, sees every key tile that the first sees
+    Job job;
+    while (jobs.take(job, lane)) {
+        const int nmax = job.nmax();
         const bool two = job.n1 > 0;
-        auto scores = [&](int i, int j) -> bool {  // S_i of key tile j
-            const int t = t0 + j, slot = t % kStages;
-            if (!all_wait<true>(&mi.k_full[slot], (t / kStages) & 1, abort)) return false;
-            tc_fence_after_sync();
+        auto k_ready = [&](int j) { return all_wait<true>(&mi.k_full[(t0 + j) % kStages], ((t0 + j) / kStages) & 1, abort); };
+        auto scores = [&](int i, int j) {  // S_i of key tile j
+            const int slot = (t0 + j) % kStages;
             const uint32_t d = tmem + kColS + 128 * i, a = sb + kOffQ + 3 * i * kPanelQ, b = sb + kOffK + slot * kTileK;
 #pragma unroll
             for (int c = 0; c < 3; ++c)
@@ -290,16 +332,16 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, const LatentPref
             mma_commit_pair(lead, &mi.s_full[i]);
             if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.k_empty[slot]);
             if (j + 1 == job.n(i)) mma_commit_pair(lead, &mi.q_empty[i]);
-            return true;
         };
-        auto values = [&](int i, int j, int &np, int nj) -> bool {  // O_i += P_i V of key tile j
+        auto step = [&](int i, int j, int &np, int nj) -> bool {  // O_i += P_i V of key tile j, S_i of the next
             const int t = t0 + j, slot = t % kStages;
-            if (!all_wait<true>(&mi.v_full[slot], (t / kStages) & 1, abort)) return false;
+            const bool more = j + 1 < job.n(i);
             if (j == 0 && nj > 0 && !all_wait<true>(&mi.o_empty[i], (nj - 1) & 1, abort)) return false;
             const uint32_t d = tmem + kColO + 128 * i, a = tmem + kColS + 128 * i, b = sb + kOffV + slot * kTileV;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                if ((k & 3) == 0) {
+                if (k == 0 && !all_wait<true>(&mi.v_full[slot], (t / kStages) & 1, abort)) return false;
+                if ((k & 3) == 0) {  // a half of the keys
                     if (!all_wait<true>(&mi.p_full[i][k >> 2], np & 1, abort)) return false;
                     tc_fence_after_sync();
                 }
@@ -307,26 +349,34 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, const LatentPref
             }
             ++np;
             if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.v_empty[slot]);
-            if (j + 1 == job.n(i)) mma_commit_pair(lead, &mi.o_full[i]);
+            if (!more) {
+                mma_commit_pair(lead, &mi.o_full[i]);
+                return true;
+            }
+            if (!k_ready(j + 1)) return false;
+            tc_fence_after_sync();
+            scores(i, j + 1);
             return true;
         };
-        if (job.n0 > 0 && (!all_wait<true>(&mi.q_full[0], nj0 & 1, abort) || !scores(0, 0))) return false;
-        if (job.n1 > 0 && (!all_wait<true>(&mi.q_full[1], nj1 & 1, abort) || !scores(1, 0))) return false;
-#pragma unroll 1
-        for (int j = 0; j < job.nmax; ++j) {
-            if (j < job.n0) {
-                if (!values(0, j, np0, nj0)) return false;
-                if (j + 1 < job.n0 && !scores(0, j + 1)) return false;
-            }
-            if (j < job.n1) {
-                if (!values(1, j, np1, nj1)) return false;
-                if (j + 1 < job.n1 && !scores(1, j + 1)) return false;
-            }
+        if (job.n0 > 0) {
+            if (!all_wait<true>(&mi.q_full[0], nj0 & 1, abort) || !k_ready(0)) return false;
+            tc_fence_after_sync();
+            scores(0, 0);
         }
-        t0 += job.nmax;
+        if (two) {
+            if (!all_wait<true>(&mi.q_full[1], nj1 & 1, abort) || !k_ready(0)) return false;
+            tc_fence_after_sync();
+            scores(1, 0);
+        }
+#pragma unroll 1
+        for (int j = 0; j < nmax; ++j) {
+            if (j < job.n0 && !step(0, j, np0, nj0)) return false;
+            if (j < job.n1 && !step(1, j, np1, nj1)) return false;
+        }
+        t0 += nmax;
         nj0 += job.n0 > 0;
-        nj1 += job.n1 > 0;
-    } while (jobs.next(lane));
+        nj1 += two;
+    }
     return !*abort;
 }
 
@@ -338,135 +388,132 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t quarter = (uint32_t)((row >> 5) * 32) << 16;
     const uint32_t ts = tmem + kColS + 128 * i + quarter, to = tmem + kColO + 128 * i + quarter;
-    const uint32_t full[2] = {map_to_rank(&mi.p_full[i][0], 0), map_to_rank(&mi.p_full[i][1], 0)};
-    const uint32_t o_empty = map_to_rank(&mi.o_empty[i], 0);
+    const uint32_t p_full = map_to_rank(&mi.p_full[i][0], 0), o_empty = map_to_rank(&mi.o_empty[i], 0);
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
     int ns = 0, nj = 0, t0 = 0;  // score tiles and jobs of this query tile, key tiles so far
     uint32_t tails = 0;          // parity of the tails so far in each V buffer
     Jobs jobs(mi);
-    do {
-    const Job job = make_job(p, jobs.at);
-    const int klen = job.at.klen;
-    // last key this query sees
-    const int last = p.causal ? min(job.at.off + job.first(i, rank) + row, klen - 1) : klen - 1;
-    const int n = job.n(i);
-    // this query's row of the output, or none
-    const int64_t out =
-        row < job.rows(i, rank) ? (int64_t)(job.at.q0 + job.first(i, rank) + row) * p.heads + job.h : -1;
-    float m = -INFINITY, l = 0.f;  // held maximum (log2 units) and the sum of the weights
-    for (int j = 0; j < n; ++j, ++ns) {
-        if (!all_wait<false>(&mi.s_full[i], ns & 1, abort)) return;
-        tc_fence_after_sync();
-        float s[128];
+    Job job;
+    while (jobs.take(job, lane)) {
+        const int klen = job.klen, n = job.n(i), first = job.first(i, rank) + row;
+        // last key this query sees
+        const int last = p.causal ? min(job.off + first, klen - 1) : klen - 1;
+        // this query's row of the output, or none
+        const int64_t out = first < job.rows ? (int64_t)(job.q0 + first) * p.heads + job.h : -1;
+        float m = -INFINITY, l = 0.f;  // held maximum (log2 units) and the sum of the weights
+        for (int j = 0; j < n; ++j, ++ns) {
+            if (!all_wait<false>(&mi.s_full[i], ns & 1, abort)) return;
+            tc_fence_after_sync();
+            float s[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
-        const int seen = max(-1, min(kN, last - j * kN));  // columns 0 .. seen
-        const bool special = __any_sync(0xffffffffu, seen < kN - 1) || p.scale_log2 <= 0.f;
-        tmem_ld_wait();
-        // one branch for all that is rare: the rest is straight code that the scheduler can interleave
-        if (special) {
-            const float sign = p.scale_log2 > 0.f ? 1.f : (p.scale_log2 < 0.f ? -1.f : 0.f);
+            for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
+            const int seen = max(-1, min(kN, last - j * kN));  // columns 0 .. seen
+            const bool special = __any_sync(0xffffffffu, seen < kN - 1) || p.scale_log2 <= 0.f;
+            tmem_ld_wait();
+            // one branch for all that is rare: the rest is straight code that the scheduler can interleave
+            if (special) {
+                const float sign = p.scale_log2 > 0.f ? 1.f : (p.scale_log2 < 0.f ? -1.f : 0.f);
 #pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = c <= seen ? s[c] * sign : -INFINITY;
-        }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 128; c += 2) top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], s[c], s[c + 1]);
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-        // the maximum is moved only where a score passes it by kSlack: weights are below 2^kSlack, and
-        // the precision of fp32 and bf16 does not depend on that
-        const bool rise = mx > m + kSlack;
-        const int left = klen - j * kN;
-        if (__any_sync(0xffffffffu, rise) || left < kN) {
-            float f = 1.f;
-            if (rise) {
-                f = tc::exp2_approx(m - mx);
-                m = mx;
-                l *= f;
+                for (int c = 0; c < 128; ++c) s[c] = c <= seen ? s[c] * sign : -INFINITY;
             }
-            // what O holds follows (its last product finished before this S did)
-            if (j > 0 && __any_sync(0xffffffffu, rise)) {
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 16) {
-                    float x[16];
-                    tmem_ld16(to + c, x);
-                    tmem_ld_wait();
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] *= f;
-                    tmem_st16(to + c, x);
+            for (int c = 0; c < 128; c += 2) top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], s[c], s[c + 1]);
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+            // the maximum is moved only where a score passes it by kSlack: weights are below 2^kSlack, and
+            // the precision of fp32 and bf16 does not depend on that
+            const bool rise = mx > m + kSlack;
+            const int left = klen - j * kN;
+            if (__any_sync(0xffffffffu, rise) || left < kN) {
+                float f = 1.f;
+                if (rise) {
+                    f = tc::exp2_approx(m - mx);
+                    m = mx;
+                    l *= f;
+                }
+                // what O holds follows (its last product finished before this S did)
+                if (j > 0 && __any_sync(0xffffffffu, rise)) {
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 16) {
+                        float x[16];
+                        tmem_ld16(to + c, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) x[k] *= f;
+                        tmem_st16(to + c, x);
+                    }
+                }
+                // keys past the sequence's end are other sequences' rows: their weight is 0, so their values
+                // must be finite
+                if (left < kN) {
+                    const int slot = (t0 + j) % kStages;
+                    if (!all_wait<false>(&mi.v_tail[slot], (tails >> slot) & 1, abort)) return;
+                    for (int e = row; e < (kN - left) * 8; e += 128)
+                        *reinterpret_cast<uint4 *>(sm + kOffV + slot * kTileV + (left + (e >> 3)) * 128 + (e & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    fence_cluster();
                 }
             }
-            // keys past the sequence's end are other sequences' rows: their weight is 0, so their values
-            // must be finite
-            if (left < kN) {
-                const int slot = (t0 + j) % kStages;
-                if (!all_wait<false>(&mi.v_tail[slot], (tails >> slot) & 1, abort)) return;
-                for (int e = row; e < (kN - left) * 8; e += 128)
-                    *reinterpret_cast<uint4 *>(sm + kOffV + slot * kTileV + (left + (e >> 3)) * 128 +
-                                               (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                fence_cluster();
+            const float base = m == -INFINITY ? 0.f : -m;
+            const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float w[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float2 &x = *reinterpret_cast<float2 *>(&s[32 * c + 2 * k]);
+                    x = fma2(x, scale2, base2);
+                    x.x = tc::exp2_approx(x.x);
+                    x.y = tc::exp2_approx(x.y);
+                    // bf16: the product's operands share one type, and V is bf16
+                    w[k] = __uint_as_float(tc::pack_bf16x2(x.x, x.y));
+                }
+                tmem_st16(ts + 16 * c, w);
+                if (c & 1) {  // the product starts on the first half of the keys
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(p_full + 8 * (c >> 1));
+                }
             }
+            float2 sum[4] = {};
+#pragma unroll
+            for (int k = 0; k < 64; ++k) sum[k & 3] = add2(sum[k & 3], *reinterpret_cast<float2 *>(&s[2 * k]));
+            const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += all.x + all.y;
         }
-        const float base = m == -INFINITY ? 0.f : -m;
-        const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
+        if (job.tail()) tails ^= 1u << ((t0 + job.nmax() - 1) % kStages);
+        t0 += job.nmax();
+        if (out >= 0 && p.lse) p.lse[out] = m * kLn2 + logf(l);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + out * kLatN;
+        if (n == 0) {
+            const uint32_t zero[8] = {};
+            if (out >= 0)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float w[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                float2 &x = *reinterpret_cast<float2 *>(&s[32 * c + 2 * k]);
-                x = fma2(x, scale2, base2);
-                x.x = tc::exp2_approx(x.x);
-                x.y = tc::exp2_approx(x.y);
-                // bf16: the product's operands share one type, and V is bf16
-                w[k] = __uint_as_float(tc::pack_bf16x2(x.x, x.y));
-            }
-            tmem_st16(ts + 16 * c, w);
-            if (c & 1) {  // the product starts on the first half of the keys
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(full[c >> 1]);
-            }
+                for (int k = 0; k < 128; k += 16) store32(o + k, zero);
+            continue;
         }
-        float2 sum[4] = {};
-#pragma unroll
-        for (int k = 0; k < 64; ++k) sum[k & 3] = add2(sum[k & 3], *reinterpret_cast<float2 *>(&s[2 * k]));
-        const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l += all.x + all.y;
-    }
-    if (n > 0) {
         if (!all_wait<false>(&mi.o_full[i], nj & 1, abort)) return;
         tc_fence_after_sync();
         ++nj;
-    }
-    if (job.tail) tails ^= 1u << ((t0 + job.nmax - 1) % kStages);
-    t0 += job.nmax;
-    if (out >= 0 && p.lse) p.lse[out] = m * kLn2 + logf(l);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + out * kLatN;
+        float x[128];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float x[32];
-        if (n > 0) {
-            tmem_ld32(to + 32 * c, x);
-            tmem_ld_wait();
-            if (c == 3) {
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(o_empty);  // the next job's products may start
-            }
-        }
+        for (int c = 0; c < 4; ++c) tmem_ld32(to + 32 * c, *reinterpret_cast<float(*)[32]>(&x[32 * c]));
+        tmem_ld_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(o_empty);  // the next job's products may start
+        if (out < 0) continue;
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-            float y[8];
+        for (int k = 0; k < 128; k += 16) {
+            uint32_t w[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) y[u] = n > 0 ? x[k + u] * inv : 0.f;
-            if (out >= 0) *reinterpret_cast<uint4 *>(o + 32 * c + k) = tc::pack_bf16x8(y);
+            for (int u = 0; u < 8; ++u) w[u] = tc::pack_bf16x2(x[k + 2 * u] * inv, x[k + 2 * u + 1] * inv);
+            store32(o + k, w);
         }
     }
-    } while (jobs.next(lane));
 }
 
 __global__ void __launch_bounds__(kT, 1)
@@ -489,6 +536,8 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
             mbar_init(&mi.s_full[i], 1);
             mbar_init(&mi.p_full[i][0], 8);
             mbar_init(&mi.p_full[i][1], 8);
+            mbar_init(&mi.job_full[i], 1);
+            mbar_init(&mi.job_empty[i], rank == 0 ? 9 : 8);  // warps: softmax, matrix instructions
             mbar_init(&mi.o_full[i], 1);
             mbar_init(&mi.o_empty[i], 8);
         }
@@ -499,9 +548,9 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
             mbar_init(&mi.v_empty[i], 1);
             mbar_init(&mi.v_tail[i], 1);
         }
-        mbar_init(&mi.next_full, 1);
-        mbar_init(&mi.next_empty, kJobReaders);
         mbar_init(&mi.drained, 1);
+        mbar_init(&mi.next_full, 1);
+        mbar_init(&mi.next_empty, 2);
         fence_mbar_init();
         mi.abort = 0;
     }
@@ -511,24 +560,21 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     cluster_sync();  // the other CTA's barriers are ready
     tc_fence_after_sync();
     const uint32_t tmem = mi.tmem;
-    // registers: 384 x 168 at launch; 256 x 216 + 128 x 64 now
+    // registers: 384 x 168 = 64,512 at launch; 256 x 232 + 128 x 40 = 64,512 now
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         softmax_role(sm, mi, p, tmem, warp >> 2, rank);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 8) {
             copy_role(sm, mi, p, tq, tk, tp, tv, q_step, k_step, v_step, rank, lane);
         } else if (warp == 9 && rank == 0) {
             // (the reduction's result is uniform to the compiler, the loaded word is not)
-            if (!mma_role(smem_u32(sm), mi, p, __reduce_or_sync(0xffffffffu, tmem), lane)) {
+            if (!mma_role(smem_u32(sm), mi, __reduce_or_sync(0xffffffffu, tmem), lane)) {
                 // nothing in flight when tensor memory is given back
                 mma_commit_pair(lane == 0, &mi.drained);
                 if (lane == 0) mbar_wait_ns(&mi.drained, 0, kWait);
             }
-        } else if (warp == 9) {  // the other CTA's reads the jobs along: the count of readers is one for all
-            Jobs jobs(mi);
-            while (jobs.next(lane)) {}
         } else if (warp == 10 && blockIdx.x == 0) {
             latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
             latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);
