@@ -7,16 +7,17 @@
 //
 // The pair i is (i, i + 32) or, interleaved, (2i, 2i + 1).  Sums and products are fp32, rounded
 // once when stored.  Bound by memory (T large) or by the latency of one dependent chain,
-// position -> table row -> store (T small).  A warp is one unit of work: either a token's latent
-// row and position key, or the position channels of eight of its query heads (32 lanes = 8 heads
-// x 4 quarters of the pairs, 8 pairs a lane: two 16-byte loads in bf16).  Small batches so spread
-// over 1 + H / 8 warps a token, and large ones keep 1 KB a warp in flight.
+// position -> table row -> store (T small).  A warp is one unit of work and one CTA: either a token's
+// latent row and position key, or the position channels of 16 of its query heads (32 lanes = 8 heads x 4
+// quarters of the pairs, two heads and 2 x 8 pairs a lane).  Small batches so spread over 1 + H / 16 CTAs a
+// token, and large ones keep up to 2 KB a warp in flight while warps come and go singly: 32,768 tokens of 32
+// heads 72 us (386 MB, 5.4 TB/s); CTAs of four warps 76, one head a lane 79, one warp and one head 88.
 #include "latent.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 1;
 
 // Eight consecutive elements as they lie in memory (16-byte aligned): what is neither normalised
 // nor rotated is stored again bit for bit.
@@ -108,6 +109,9 @@ __device__ __forceinline__ void rotate8(Raw8<IO> &rx, Raw8<IO> &ry, const float 
     narrow(y, ry);
 }
 
+constexpr int kRounds = 2;  // heads of a lane in a query unit
+constexpr int kUnitHeads = 8 * kRounds;
+
 // q_pe / q_pe_out, latent / latent_out and k_pe / k_pe_out may be the same rows: a lane reads
 // what it overwrites before it does.
 template <typename IO>
@@ -115,55 +119,62 @@ __global__ void __launch_bounds__(32 * kWarps)
 latent_append_kernel(const LatentAppend p)
 {
     const int lane = threadIdx.x & 31;
-    const int units = 1 + (p.q_pe_out ? (p.heads + 7) / 8 : 0);
+    const int units = 1 + (p.q_pe_out ? (p.heads + kUnitHeads - 1) / kUnitHeads : 0);
     const int64_t work = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (work >= (int64_t)p.tokens * units) return;
     const int t = (int)(work / units), unit = (int)(work - (int64_t)t * units);
     const int j = lane & 3;
-
-    // the loads that depend on nothing, before the chain position -> table row
-    Raw8<IO> x0, x1, kx = {}, ky = {};
     int lo, hi;
     quarter_at(j, p.interleaved, lo, hi);
-    const int head = (unit - 1) * 8 + (lane >> 2);
-    const bool has_head = unit > 0 && head < p.heads;
+    const int pos = p.cos_sin ? p.positions[t] : 0;
+
+    // the loads that depend on nothing, beside the chain position -> table row
+    Raw8<IO> x[kRounds], y[kRounds], x0, x1;
+    const int head = (unit - 1) * kUnitHeads + (lane >> 2);
+    int64_t slot = -1;
     if (unit == 0) {
+        slot = p.slots[t];
         const IO *row = static_cast<const IO *>(p.latent) + t * p.latent_stride;
         load8(row + 8 * lane, x0);
         load8(row + 256 + 8 * lane, x1);
         if (lane < 4) {
             const IO *kr = static_cast<const IO *>(p.k_pe) + t * p.k_pe_stride;
-            load8(kr + lo, kx);
-            load8(kr + hi, ky);
+            load8(kr + lo, x[0]);
+            load8(kr + hi, y[0]);
         }
-    } else if (has_head) {
-        const IO *qr = static_cast<const IO *>(p.q_pe) + t * p.q_ts + head * p.q_hs;
-        load8(qr + lo, kx);
-        load8(qr + hi, ky);
+    } else {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            if (head + 8 * r < p.heads) {
+                const IO *qr = static_cast<const IO *>(p.q_pe) + t * p.q_ts + (head + 8 * r) * p.q_hs;
+                load8(qr + lo, x[r]);
+                load8(qr + hi, y[r]);
+            }
     }
-    if (p.cos_sin) {
-        const int pos = p.positions[t];
-        if (pos < 0 || pos >= p.num_positions) {  // the token is left out
-            if (unit == 0 && lane == 0 && p.errors) atomicOr(p.errors, DEV_ERR_POSITION);
-            return;
-        }
-        if (unit > 0 ? has_head : lane < 4) {
-            const float *cs = p.cos_sin + (size_t)pos * kLatP + 8 * j;
-            Raw8<float> rc, rs;
-            load8(cs, rc);
-            load8(cs + kLatP / 2, rs);
-            float c[8], s[8];
-            widen(rc, c);
-            widen(rs, s);
-            rotate8(kx, ky, c, s, p.interleaved);
-        }
+    if (p.cos_sin && (pos < 0 || pos >= p.num_positions)) {  // the token is left out
+        if (unit == 0 && lane == 0 && p.errors) atomicOr(p.errors, DEV_ERR_POSITION);
+        return;
+    }
+    if (p.cos_sin && (unit > 0 || lane < 4)) {
+        const float *cs = p.cos_sin + (size_t)pos * kLatP + 8 * j;
+        Raw8<float> rc, rs;
+        load8(cs, rc);
+        load8(cs + kLatP / 2, rs);
+        float c[8], s[8];
+        widen(rc, c);
+        widen(rs, s);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            if (unit == 0 ? r == 0 : head + 8 * r < p.heads) rotate8(x[r], y[r], c, s, p.interleaved);
     }
     if (unit > 0) {
-        if (has_head) {
-            IO *qo = static_cast<IO *>(p.q_pe_out) + t * p.qo_ts + head * p.qo_hs;
-            store8(qo + lo, kx);
-            store8(qo + hi, ky);
-        }
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            if (head + 8 * r < p.heads) {
+                IO *qo = static_cast<IO *>(p.q_pe_out) + t * p.qo_ts + (head + 8 * r) * p.qo_hs;
+                store8(qo + lo, x[r]);
+                store8(qo + hi, y[r]);
+            }
         return;
     }
     if (p.norm_weight) {
@@ -197,10 +208,9 @@ latent_append_kernel(const LatentAppend p)
     }
     if (p.k_pe_out && lane < 4) {
         IO *out = static_cast<IO *>(p.k_pe_out) + t * p.ko_stride;
-        store8(out + lo, kx);
-        store8(out + hi, ky);
+        store8(out + lo, x[0]);
+        store8(out + hi, y[0]);
     }
-    const int64_t slot = p.slots[t];
     if (slot < 0 || slot >= p.num_slots) {  // -1: not cached
         if (slot != -1 && lane == 0 && p.errors) atomicOr(p.errors, DEV_ERR_SLOT);
         return;
@@ -209,8 +219,8 @@ latent_append_kernel(const LatentAppend p)
     store8(c + 8 * lane, x0);
     store8(c + 256 + 8 * lane, x1);
     if (lane < 4) {
-        store8(c + kLatR + lo, kx);
-        store8(c + kLatR + hi, ky);
+        store8(c + kLatR + lo, x[0]);
+        store8(c + kLatR + hi, y[0]);
     }
 }
 
@@ -218,7 +228,7 @@ latent_append_kernel(const LatentAppend p)
 
 cudaError_t launch_latent_append(const LatentAppend &p)
 {
-    const int64_t units = 1 + (p.q_pe_out ? (p.heads + 7) / 8 : 0);
+    const int64_t units = 1 + (p.q_pe_out ? (p.heads + kUnitHeads - 1) / kUnitHeads : 0);
     const int64_t blocks = (p.tokens * units + kWarps - 1) / kWarps;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;

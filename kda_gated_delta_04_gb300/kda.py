@@ -520,6 +520,15 @@ def decode_step(q, k, v, log_alpha, beta, state, *, o=None, stream=None, qk_l2no
 # These calls are made once per layer and generated token, where the host's time counts: a tensor
 # that is as it should be is checked with a handful of comparisons, and only one that is not is
 # looked at again for the message.
+_torch_module = None
+
+
+def _load_torch():
+    global _torch_module
+    _torch_module = _torch()
+    return _torch_module
+
+
 def _refuse(t, name, dtype, dev, shape):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -533,16 +542,25 @@ def _refuse(t, name, dtype, dev, shape):
     raise ValueError(f"{name} must be contiguous{' in its last dimension' if t.stride(-1) != 1 else ''}")
 
 
-def _rows(t, name, dtype, dev, shape):
-    """Address and leading strides (0 where there is one entry only) of a CUDA tensor whose last
-    dimension is contiguous."""
+def _rows3(t, name, dtype, dev, shape):
+    """Address and leading strides (0 where there is one entry only) of a CUDA tensor of three
+    dimensions whose last one is contiguous."""
     try:
-        st = t.stride()
-        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and (st[-1] == 1 or shape[-1] == 1):
-            if len(shape) == 3:
-                return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0
-            return t.data_ptr(), st[0] if shape[0] > 1 else 0
-    except AttributeError:
+        a, b, c = t.stride()
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and c == 1:
+            return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
+    except (AttributeError, ValueError):
+        pass
+    _refuse(t, name, dtype, dev, shape)
+
+
+def _rows2(t, name, dtype, dev, shape):
+    """The same of two dimensions."""
+    try:
+        a, c = t.stride()
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and (c == 1 or shape[1] <= 1):
+            return t.data_ptr(), a if shape[0] > 1 else 0
+    except (AttributeError, ValueError):
         pass
     _refuse(t, name, dtype, dev, shape)
 
@@ -559,7 +577,7 @@ def _flat(t, name, dtype, dev, shape):
 
 def _latent_like(t, name, dims):
     """Type code, type and device index that every other tensor of the call shares with t."""
-    torch = _torch()
+    torch = _torch_module or _load_torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != dims:
@@ -571,7 +589,7 @@ def _latent_like(t, name, dims):
 def _raw_stream(stream, dev):
     if stream is not None:
         return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream
+    return _torch_module._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream
 
 
 def _empty(shape, dtype, dev, stream):
@@ -594,7 +612,7 @@ def latent_append(latent, k_pe, cache, slots, *, norm_weight=None, norm_eps=1e-6
     latent_out [T, 512] and k_pe_out [T, 64] receive the normalised latent and the rotated key
     again.  Rows may be strided; all are bf16 or all fp32.  interleaved: the rotated pairs are
     (2i, 2i + 1) instead of (i, i + 32).  errors: int32 [1] that collects KDA_DEVICE_ERR_* bits."""
-    torch = _torch()
+    torch = _torch_module or _load_torch()
     if (cos_sin is None) != (positions is None):
         raise ValueError("cos_sin and positions go together")
     if q_pe is None and q_pe_out is not None:
@@ -604,18 +622,18 @@ def latent_append(latent, k_pe, cache, slots, *, norm_weight=None, norm_eps=1e-6
     code, dt, dev = _latent_like(latent, "latent", 2)
     i32 = torch.int32
     T = latent.shape[0]
-    x, xs = _rows(latent, "latent", dt, dev, (T, 512))
-    k, ks = _rows(k_pe, "k_pe", dt, dev, (T, 64))
+    x, xs = _rows2(latent, "latent", dt, dev, (T, 512))
+    k, ks = _rows2(k_pe, "k_pe", dt, dev, (T, 64))
     H = qt = qh = ot = oh = lo_s = ko_s = num_positions = 0
     q = qo = lo = ko = cs = pos = None
     if q_pe is not None:
         H = q_pe.shape[1] if q_pe.dim() == 3 else -1
-        q, qt, qh = _rows(q_pe, "q_pe", dt, dev, (T, H, 64))
-        qo, ot, oh = (q, qt, qh) if q_pe_out is None else _rows(q_pe_out, "q_pe_out", dt, dev, (T, H, 64))
+        q, qt, qh = _rows3(q_pe, "q_pe", dt, dev, (T, H, 64))
+        qo, ot, oh = (q, qt, qh) if q_pe_out is None else _rows3(q_pe_out, "q_pe_out", dt, dev, (T, H, 64))
     if latent_out is not None:
-        lo, lo_s = _rows(latent_out, "latent_out", dt, dev, (T, 512))
+        lo, lo_s = _rows2(latent_out, "latent_out", dt, dev, (T, 512))
     if k_pe_out is not None:
-        ko, ko_s = _rows(k_pe_out, "k_pe_out", dt, dev, (T, 64))
+        ko, ko_s = _rows2(k_pe_out, "k_pe_out", dt, dev, (T, 64))
     if cos_sin is not None:
         num_positions = cos_sin.shape[0]
         cs = _flat(cos_sin, "cos_sin", torch.float32, dev, (num_positions, 64))
@@ -644,14 +662,14 @@ def latent_decode(q, cache, page_table, seq_lens, scale, *, o=None, lse=None, wo
     [B, W] (rows may be strided), seq_lens int32 [B] on the device.  Returns (o [B, H, 512],
     lse [B, H] fp32); a sequence of length 0 gives zeros and -inf.  bf16 or fp32.  The scratch
     buffer (latent_decode_workspace_for) may be kept by the caller; errors as latent_append."""
-    torch = _torch()
+    torch = _torch_module or _load_torch()
     code, dt, dev = _latent_like(q, "q", 3)
     i32, f32 = torch.int32, torch.float32
     B, H = q.shape[:2]
-    qp, qb, qh = _rows(q, "q", dt, dev, (B, H, 576))
+    qp, qb, qh = _rows3(q, "q", dt, dev, (B, H, 576))
     pages, page = cache.shape[:2] if cache.dim() == 3 else (-1, -1)
     width = page_table.shape[-1]
-    table, ts = _rows(page_table, "page_table", i32, dev, (B, width))
+    table, ts = _rows2(page_table, "page_table", i32, dev, (B, width))
     if o is None:
         o = _empty((B, H, 512), dt, dev, stream)
     if lse is None:
@@ -676,7 +694,7 @@ def latent_prefill(q, k_nope, k_pe, v, scale, cu_q=None, cu_k=None, *, causal=Tr
     Causal, aligned at each sequence's end: with lk > lq keys the queries are the last lq
     positions.  causal=False: every query sees all keys of its sequence.  Returns (o [Tq, H, 128],
     lse [Tq, H] fp32); a query without keys gives zeros and -inf.  errors as latent_append."""
-    torch = _torch()
+    torch = _torch_module or _load_torch()
     if cu_q is None and cu_k is not None:
         raise ValueError("cu_k without cu_q")
     code, dt, dev = _latent_like(q, "q", 3)
@@ -684,10 +702,10 @@ def latent_prefill(q, k_nope, k_pe, v, scale, cu_q=None, cu_k=None, *, causal=Tr
     Tq, H = q.shape[:2]
     Tk = k_pe.shape[0]
     N = 1 if cu_q is None else cu_q.shape[0] - 1
-    qp, qt, qh = _rows(q, "q", dt, dev, (Tq, H, 192))
-    kn, kt, kh = _rows(k_nope, "k_nope", dt, dev, (Tk, H, 128))
-    kp, kps = _rows(k_pe, "k_pe", dt, dev, (Tk, 64))
-    vp, vt, vh = _rows(v, "v", dt, dev, (Tk, H, 128))
+    qp, qt, qh = _rows3(q, "q", dt, dev, (Tq, H, 192))
+    kn, kt, kh = _rows3(k_nope, "k_nope", dt, dev, (Tk, H, 128))
+    kp, kps = _rows2(k_pe, "k_pe", dt, dev, (Tk, 64))
+    vp, vt, vh = _rows3(v, "v", dt, dev, (Tk, H, 128))
     if o is None:
         o = _empty((Tq, H, 128), dt, dev, stream)
     if lse is None:
