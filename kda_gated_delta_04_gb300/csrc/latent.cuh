@@ -185,21 +185,32 @@ __device__ __forceinline__ int latent_len(const int32_t *lens, int b, int64_t ca
     return n < 0 ? 0 : (int)capacity;
 }
 
-// Position of a CTA in the tile list.
+// a / b for non-negative a and positive b; in 32 bits where both fit (a 64-bit division costs some 300
+// cycles, and these stand before the first copy).
+__device__ __forceinline__ int64_t latent_div(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
+// Position of a CTA in the tile list.  W = base G' + rem: CTA c starts at floor(c W / G'), so that with two
+// head groups CTA c and CTA c + G' / 2 read the same cache rows at the same time.
 struct LatentWalk {
     int64_t g, g_end;   // tile list range of this CTA
-    int64_t total;      // W
+    int64_t base;
+    int rem;
     int cta, ctas;      // c, G'
     int hg, b, tile;    // head group, sequence and tile of g
-    __device__ __forceinline__ int64_t start_of(int64_t c) const { return c * total / ctas; }
-    __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
+    int64_t total;      // W
+    __device__ __forceinline__ int64_t start_of(int c) const { return c * base + (uint32_t)(c * rem) / (uint32_t)ctas; }
+    __device__ __forceinline__ int cta_of(int64_t x) const { return (int)latent_div((x + 1) * ctas - 1, total); }
 };
 
-// Called by all NT threads of the CTA (contains barriers); s_scan: NT / 32 + 2 int64 of shared memory.
+// Called by all NT threads of the CTA (contains barriers); s_scan: NT / 32 + 2 ints of shared memory.
 // The CTAs also clear the outputs of the sequences without cache rows, and write the records that say
-// that there is nothing to join.
+// that there is nothing to join.  The tiles of all sequences are below 2^31 (the entry point sees to it).
 template <int NT, typename IO>
-__device__ __forceinline__ LatentWalk latent_walk(const LatentDecode &p, int tile_rows, int head_tile, int64_t *s_scan)
+__device__ __forceinline__ LatentWalk latent_walk(const LatentDecode &p, int tile_rows, int head_tile, int *s_scan)
 {
     const int tid = threadIdx.x, batch = p.batch, heads = p.heads, head_groups = (heads + head_tile - 1) / head_tile;
     const int64_t capacity = (int64_t)p.table_width * p.page_size;
@@ -212,40 +223,44 @@ __device__ __forceinline__ LatentWalk latent_walk(const LatentDecode &p, int til
     const int chunk = (batch + NT - 1) / NT;
     const int lo = min(tid * chunk, batch), hi = min(lo + chunk, batch);
     bool bad = false;
-    int64_t sum = 0;
+    int sum = 0;
     for (int b = lo; b < hi; ++b) sum += (latent_len(lens, b, capacity, bad) + tile_rows - 1) / tile_rows;
     if (bad && errors && blockIdx.x == 0) atomicOr(errors, DEV_ERR_SEQLENS);
-    int64_t inc = sum;  // inclusive scan: within the warp, then over the warps
+    int inc = sum;  // inclusive scan: within the warp, then over the warps
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, inc, m);
+        const int up = __shfl_up_sync(0xffffffffu, inc, m);
         if ((tid & 31) >= m) inc += up;
     }
     if ((tid & 31) == 31) s_scan[tid >> 5] = inc;
     __syncthreads();
-    int64_t before = 0, all = 0;
+    int before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
-        if (w < (tid >> 5)) before += s_scan[w];
-        all += s_scan[w];
+        const int x = s_scan[w];
+        before += w < (tid >> 5) ? x : 0;
+        all += x;
     }
-    const int64_t first = before + inc - sum;  // tiles before this thread's sequences
+    const int first = before + inc - sum;  // tiles before this thread's sequences
+    const int64_t total = (int64_t)all * head_groups;
     LatentWalk k;
-    k.total = all * head_groups;
     k.cta = blockIdx.x;
-    k.ctas = (int)min((int64_t)gridDim.x, k.total);
+    k.ctas = (int)min((int64_t)gridDim.x, total);
     k.hg = k.b = k.tile = 0;
-    k.g = k.g_end = 0;
+    k.g = k.g_end = k.base = k.rem = 0;
+    k.total = total;
     if (k.cta < k.ctas) {
+        k.base = latent_div(total, k.ctas);
+        k.rem = (int)(total - k.base * k.ctas);
         k.g = k.start_of(k.cta);
         k.g_end = k.start_of(k.cta + 1);
-        k.hg = (int)(k.g / all);
-        int64_t r = k.g - k.hg * all;
+        k.hg = (int)latent_div(k.g, all);
+        int r = (int)(k.g - (int64_t)k.hg * all);
         if (r >= first && r < first + sum) {
             r -= first;
             bool ignore = false;
             int b = lo;
-            for (; b < hi; ++b) {
+            for (; b < hi - 1; ++b) {
                 const int n = (latent_len(lens, b, capacity, ignore) + tile_rows - 1) / tile_rows;
                 if (r < n) break;
                 r -= n;
@@ -256,8 +271,8 @@ __device__ __forceinline__ LatentWalk latent_walk(const LatentDecode &p, int til
     }
     __syncthreads();
     if (k.cta < k.ctas) {
-        k.b = (int)s_scan[NT / 32];
-        k.tile = (int)s_scan[NT / 32 + 1];
+        k.b = s_scan[NT / 32];
+        k.tile = s_scan[NT / 32 + 1];
     }
     for (int b = blockIdx.x; b < batch; b += gridDim.x) {
         bool ignore = false;

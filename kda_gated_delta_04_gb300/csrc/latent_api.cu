@@ -89,8 +89,10 @@ kda_status_t kda_latent_decode(const void *q, int64_t q_batch_stride, int64_t q_
     if (batch < 0 || num_heads <= 0 || num_pages < 0 || page_size <= 0 || max_pages < 0 || page_table_stride < 0 ||
         !isfinite(scale))
         return KDA_ERR_INVALID_ARG;
-    // a cache row's index is a TMA coordinate; a unit count is an int
-    if (page_size % 8 != 0 || num_pages > INT32_MAX / page_size || num_heads > 65535 || batch > (1 << 24))
+    // a cache row's index is a TMA coordinate; the tiles of all sequences are counted in an int
+    if (page_size % 8 != 0 || num_pages > INT32_MAX / page_size || num_heads > 65535 ||
+        (int64_t)max_pages * page_size > INT32_MAX ||
+        (int64_t)batch * (((int64_t)max_pages * page_size + 31) / 32) > INT32_MAX || batch > (1 << 24))
         return KDA_ERR_UNSUPPORTED;
     if (batch == 0) return KDA_OK;
     const size_t es = elem_size(dtype);

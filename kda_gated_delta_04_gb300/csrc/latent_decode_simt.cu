@@ -30,7 +30,7 @@ struct Smem {
     float p[kRows][kHeads];
     float alpha[kHeads];
     float ml[kHeads][2];
-    int64_t scan[kT / 32 + 2];
+    int scan[kT / 32 + 2];
 };
 
 // Two CTAs on an SM overlap one's loads with the other's products.  Scores: warp w multiplies

@@ -64,7 +64,7 @@ struct Misc {
     int abort;
     alignas(16) float red[2][4][NH];  // (read as float4) per warp: a tile's column maxima (by tile parity), at the end the sums
     float fac[NH];        // rescaling factors, at the end 1 / sum
-    int64_t scan[kT / 32 + 2];
+    int scan[kT / 32 + 2];
 };
 
 // Waits for a phase; gives up after kWait ns or as soon as another role has.
@@ -188,23 +188,25 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc<NH> &mi, const
     volatile int *abort = &mi.abort;
     while (u.next()) {
         // row of the cache at which piece (lane % pieces) of tile (t + lane / pieces) starts
-        auto look_up = [&](int t) -> int {
-            const int j = (u.tile0 + t + lane / pieces) * kRows + (lane % pieces) * piece_rows;
-            if (t + lane / pieces >= u.tiles || j >= u.len) return (int)outside;
-            const int page = j / p.page_size;
-            const int64_t at = p.table[u.w.b * p.table_stride + page];
-            if (at < 0 || at >= p.num_pages) {
-                if (p.errors) atomicOr(p.errors, DEV_ERR_PAGE);
-                return (int)outside;
-            }
-            return (int)(at * p.page_size + (j - page * p.page_size));
+        auto entry = [&](int t, int &j) -> int {  // its page; -1: it is past the end
+            j = (u.tile0 + t + lane / pieces) * kRows + (lane % pieces) * piece_rows;
+            return t + lane / pieces < u.tiles && j < u.len ? p.table[u.w.b * p.table_stride + j / p.page_size] : -1;
         };
-        int rows = look_up(0), later = look_up(batch);
+        auto row_of = [&](int page, int j, bool asked) -> int {
+            if (page >= 0 && page < p.num_pages) return page * p.page_size + j % p.page_size;
+            if (asked && p.errors) atomicOr(p.errors, DEV_ERR_PAGE);
+            return (int)outside;
+        };
+        auto asked = [&](int t, int j) { return t + lane / pieces < u.tiles && j < u.len; };
+        int j0, j1;
+        const int page0 = entry(0, j0), page1 = entry(batch, j1);  // (both loads on their way)
+        int rows = row_of(page0, j0, asked(0, j0)), later = row_of(page1, j1, asked(batch, j1));
         for (int t = 0; t < u.tiles; ++t, ++ts) {
             const int in = t % batch;
             if (in == 0 && t > 0) {
                 rows = later;
-                later = look_up(t + batch);
+                const int page = entry(t + batch, j1);
+                later = row_of(page, j1, asked(t + batch, j1));
             }
             const int row = __shfl_sync(0xffffffffu, rows, in * pieces + (lane & (pieces - 1)));
             bool ok = true;
