@@ -9,7 +9,7 @@ namespace {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // A stride in elements: not negative and a whole number of 16-byte pieces.
-bool stride_ok(int64_t s, size_t es) { return s >= 0 && s <= (int64_t)1 << 40 && (size_t)s * es % 16 == 0; }
+bool stride_ok(int64_t s, size_t es) { return s >= 0 && s <= (int64_t)1 << 38 && (size_t)s * es % 16 == 0; }
 
 // Packed tokens are counted in int32, rounded up to tiles.
 constexpr int64_t kMaxTokens = INT32_MAX - 4096;

@@ -154,7 +154,8 @@ DECODE = [
     ("page_8", 2, 32, 8, [1000, 77]), ("heads_33", 2, 33, 64, [300, 5]), ("heads_64", 3, 64, 64, [64, 1, 700]),
     ("heads_128", 2, 128, 128, [1500, 129]), ("heads_100", 2, 100, 64, [100, 400]), ("long", 1, 32, 64, [20001]),
     ("many", 200, 16, 16, [(37 * i) % 300 for i in range(200)]), ("page_256", 2, 32, 256, [257, 1023]),
-    ("page_96", 2, 16, 96, [95, 1000]),
+    ("page_96", 2, 16, 96, [95, 1000]), ("a_thousand", 1000, 8, 8, [(53 * i) % 90 for i in range(1000)]),
+    ("many_parts", 24, 32, 64, [3000 + 17 * i for i in range(24)]), ("long_short", 6, 64, 16, [5000, 1, 0, 3, 4000, 64]),
 ]
 
 
@@ -363,6 +364,36 @@ def test_prefill_reports_malformed_offsets(dtype):
         assert err.item() == 1, bad
 
 
+def test_prefill_is_deterministic():
+    """The pairs of CTAs take work over as they get done, in another order on every call: the same bits."""
+    g = gen(46)
+    lens = [700, 3, 1300, 0, 513, 64, 256]
+    q, kn, kp, v, cu, _ = prefill_inputs(g, 16, lens, lens, torch.bfloat16)
+    a = [t.clone() for t in kda.latent_prefill(q, kn, kp, v, SCALE, cu)]
+    for _ in range(5):
+        b = kda.latent_prefill(q, kn, kp, v, SCALE, cu)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("heads", [1, 24])
+def test_prefill_many_sequences(heads):
+    """More sequences than one round of the tile search holds (32 x 32), with empty ones between."""
+    g = gen(47)
+    lens = [(7 * i) % 13 for i in range(1500)]
+    q, kn, kp, v, cu, _ = prefill_inputs(g, heads, lens, lens, torch.bfloat16)
+    o, lse = kda.latent_prefill(q, kn, kp, v, SCALE, cu)
+    ref.check(o, lse, ref.prefill(q, kn, kp, v, SCALE, lens, lens, True), "1500 sequences")
+
+
+def test_prefill_output_aligned_to_16_bytes_only():
+    g = gen(48)
+    q, kn, kp, v, cu, _ = prefill_inputs(g, 3, [300], [300], torch.bfloat16)
+    o = torch.empty(300 * 3 * 128 + 8, dtype=torch.bfloat16, device="cuda")[8:].view(300, 3, 128)
+    assert o.data_ptr() % 32 == 16
+    o, lse = kda.latent_prefill(q, kn, kp, v, SCALE, o=o)
+    ref.check(o, lse, ref.prefill(q, kn, kp, v, SCALE, [300], [300], True), "unaligned output")
+
+
 def test_prefill_on_another_stream_and_in_a_graph():
     g = gen(44)
     q, kn, kp, v, cu, _ = prefill_inputs(g, 4, [200, 100], [200, 100], torch.bfloat16)
@@ -425,3 +456,15 @@ def test_the_two_forms_agree(dtype):
     absorbed = torch.einsum("hr,hnr->hn", ol[0].double(), wv.double())
     u = ref.U[dt] if dtype == "bf16" else ref.U32 * 64
     assert (absorbed - o[-1].double()).abs().max() <= 8 * u * o[-1].double().abs().max()
+
+
+@pytest.mark.parametrize("dtype,bound", [("bf16", 0.05), ("f32", 1e-4)])
+def test_hybrid_example(dtype, bound):
+    """The example's block: KDA and latent attention from packed prompts to generated tokens.  The two
+    forms of the latent layer differ by the roundings of four matrix products and of the latent path
+    between them: up to a dozen roundings of 2^-8 (bf16) of values no larger than the largest output."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import hybrid_block
+    assert hybrid_block.run(dtype=DT[dtype]) <= bound
