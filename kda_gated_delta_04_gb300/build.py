@@ -3,6 +3,11 @@
 Each CUDA translation unit is compiled in its own nvcc process (in parallel),
 then linked into ``kda_gated_delta_04_gb300/libkda.so`` against the shared CUDA
 runtime, so the library shares the process's runtime with PyTorch.
+
+Beside it goes ``_latent_args.so`` (g++, against this interpreter's and the
+installed torch's headers): the latent calls' arguments from tensors to the C
+entry points without ctypes.  Where those headers are missing it is left out,
+and kda.py passes the same arguments through ctypes.
 """
 from __future__ import annotations
 
@@ -18,6 +23,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libkda.so")
+ARGS_SRC = os.path.join(PKG, "native", "latent_args.cpp")
+ARGS_PATH = os.path.join(PKG, "_latent_args.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,7 +41,7 @@ def _sources():
 
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(ROOT, "include", "kda.h"), os.path.abspath(__file__)]
+        os.path.join(ROOT, "include", "kda.h"), ARGS_SRC, os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
@@ -62,7 +69,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 1))) as ex:
+        args_obj = ex.submit(_compile_args)
         results = list(ex.map(compile_one, _sources()))
     if verbose or ptxas_info:
         for _, log in results:
@@ -74,7 +82,48 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_args(*args_obj.result())
     return LIB_PATH
+
+
+def _compile_args():
+    """The object file of latent_args.cpp and torch's library folder, or (None, why)."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        return None, "torch is not installed"
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    py = sysconfig.get_paths()["include"]
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    for need in (os.path.join(py, "Python.h"), os.path.join(inc, "torch", "csrc", "autograd", "python_variable.h")):
+        if not os.path.exists(need):
+            return None, f"{need} is missing"
+    obj = os.path.join(BUILD_DIR, "latent_args.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", py, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           "-c", ARGS_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {ARGS_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
+
+
+def _link_args(obj, where):
+    """_latent_args.so against the libkda.so that stands beside it."""
+    if os.path.exists(ARGS_PATH):
+        os.remove(ARGS_PATH)
+    if obj is None:
+        print(f"_latent_args left out ({where}): the latent calls go through ctypes", file=sys.stderr)
+        return
+    tmp = ARGS_PATH + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libkda.so", "-Wl,-rpath,$ORIGIN", "-L", where,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _latent_args failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, ARGS_PATH)
 
 
 if __name__ == "__main__":

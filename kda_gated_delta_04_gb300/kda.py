@@ -520,13 +520,30 @@ def decode_step(q, k, v, log_alpha, beta, state, *, o=None, stream=None, qk_l2no
 # These calls are made once per layer and generated token, where the host's time counts: a tensor
 # that is as it should be is checked with a handful of comparisons, and only one that is not is
 # looked at again for the message.
+# Where latent_args.cpp has been built (against the torch that runs), a call whose every argument is as
+# it should be goes through it; the checks here are then for naming what is not.
 _torch_module = None
+_native = None
 
 
 def _load_torch():
-    global _torch_module
-    _torch_module = _torch()
-    return _torch_module
+    """torch, and the native argument passing when it fits."""
+    global _torch_module, _native
+    torch = _torch()
+    path = os.path.join(PKG, "_latent_args.so")
+    if os.path.exists(path) and torch.cuda.is_available():
+        import importlib.machinery
+        import importlib.util
+        lib()
+        loader = importlib.machinery.ExtensionFileLoader("_latent_args", path)
+        try:
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_latent_args", loader))
+        except ImportError:  # built against another torch
+            module = None
+        if module is not None and module.torch_version == torch.__version__.split("+")[0]:
+            _native = module
+    _torch_module = torch
+    return torch
 
 
 def _refuse(t, name, dtype, dev, shape):
@@ -613,6 +630,13 @@ def latent_append(latent, k_pe, cache, slots, *, norm_weight=None, norm_eps=1e-6
     again.  Rows may be strided; all are bf16 or all fp32.  interleaved: the rotated pairs are
     (2i, 2i + 1) instead of (i, i + 32).  errors: int32 [1] that collects KDA_DEVICE_ERR_* bits."""
     torch = _torch_module or _load_torch()
+    if _native is not None:
+        st = _native.append(latent, k_pe, cache, slots, norm_weight, norm_eps, cos_sin, positions, interleaved, q_pe,
+                            q_pe_out, latent_out, k_pe_out, errors, None if stream is None else stream.cuda_stream)
+        if st == KDA_OK:
+            return
+        if st > 0:
+            raise KdaError(st, "kda_latent_append")
     if (cos_sin is None) != (positions is None):
         raise ValueError("cos_sin and positions go together")
     if q_pe is None and q_pe_out is not None:
@@ -663,6 +687,20 @@ def latent_decode(q, cache, page_table, seq_lens, scale, *, o=None, lse=None, wo
     lse [B, H] fp32); a sequence of length 0 gives zeros and -inf.  bf16 or fp32.  The scratch
     buffer (latent_decode_workspace_for) may be kept by the caller; errors as latent_append."""
     torch = _torch_module or _load_torch()
+    if o is None or lse is None or workspace is None:
+        code, dt, dev = _latent_like(q, "q", 3)
+        B, H = q.shape[:2]
+        o = _empty((B, H, 512), dt, dev, stream) if o is None else o
+        lse = _empty((B, H), torch.float32, dev, stream) if lse is None else lse
+        if workspace is None:
+            workspace = _empty((kda_latent_decode_workspace_size(H, code),), torch.uint8, dev, stream)
+    if _native is not None:
+        st = _native.decode(q, cache, page_table, seq_lens, scale, o, lse, workspace, errors,
+                            None if stream is None else stream.cuda_stream)
+        if st == KDA_OK:
+            return o, lse
+        if st > 0:
+            raise KdaError(st, "kda_latent_decode")
     code, dt, dev = _latent_like(q, "q", 3)
     i32, f32 = torch.int32, torch.float32
     B, H = q.shape[:2]
@@ -670,12 +708,6 @@ def latent_decode(q, cache, page_table, seq_lens, scale, *, o=None, lse=None, wo
     pages, page = cache.shape[:2] if cache.dim() == 3 else (-1, -1)
     width = page_table.shape[-1]
     table, ts = _rows2(page_table, "page_table", i32, dev, (B, width))
-    if o is None:
-        o = _empty((B, H, 512), dt, dev, stream)
-    if lse is None:
-        lse = _empty((B, H), f32, dev, stream)
-    if workspace is None:
-        workspace = _empty((kda_latent_decode_workspace_size(H, code),), torch.uint8, dev, stream)
     st = (_lib or lib()).kda_latent_decode(
         qp, qb, qh, _flat(cache, "cache", dt, dev, (pages, page, 576)), pages, page, table, ts, width,
         _flat(seq_lens, "seq_lens", i32, dev, (B,)), B, H, 512, 64, code, scale, _flat(o, "o", dt, dev, (B, H, 512)),
@@ -697,6 +729,17 @@ def latent_prefill(q, k_nope, k_pe, v, scale, cu_q=None, cu_k=None, *, causal=Tr
     torch = _torch_module or _load_torch()
     if cu_q is None and cu_k is not None:
         raise ValueError("cu_k without cu_q")
+    if o is None or lse is None:
+        _, dt, dev = _latent_like(q, "q", 3)
+        o = _empty((*q.shape[:2], 128), dt, dev, stream) if o is None else o
+        lse = _empty(tuple(q.shape[:2]), torch.float32, dev, stream) if lse is None else lse
+    if _native is not None:
+        st = _native.prefill(q, k_nope, k_pe, v, scale, cu_q, cu_k, causal, o, lse, errors,
+                             None if stream is None else stream.cuda_stream)
+        if st == KDA_OK:
+            return o, lse
+        if st > 0:
+            raise KdaError(st, "kda_latent_prefill")
     code, dt, dev = _latent_like(q, "q", 3)
     i32, f32 = torch.int32, torch.float32
     Tq, H = q.shape[:2]
@@ -706,10 +749,6 @@ def latent_prefill(q, k_nope, k_pe, v, scale, cu_q=None, cu_k=None, *, causal=Tr
     kn, kt, kh = _rows3(k_nope, "k_nope", dt, dev, (Tk, H, 128))
     kp, kps = _rows2(k_pe, "k_pe", dt, dev, (Tk, 64))
     vp, vt, vh = _rows3(v, "v", dt, dev, (Tk, H, 128))
-    if o is None:
-        o = _empty((Tq, H, 128), dt, dev, stream)
-    if lse is None:
-        lse = _empty((Tq, H), f32, dev, stream)
     st = (_lib or lib()).kda_latent_prefill(
         qp, qt, qh, kn, kt, kh, kp, kps, vp, vt, vh,
         None if cu_q is None else _flat(cu_q, "cu_q", i32, dev, (N + 1,)),
