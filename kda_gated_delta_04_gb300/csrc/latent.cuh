@@ -65,6 +65,28 @@ struct LatentPrefill {
 
 kda_status_t check_device();  // kda_api.cu
 
+// Launch of a kernel that waits (griddepcontrol.wait) before its first access to global memory: it may be
+// set up while the kernel before it on the stream ends.  cluster: CTAs per cluster (1: none).
+template <class... P, class... A>
+inline cudaError_t latent_launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                                 A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<A &&>(args)...);
+}
+
 cudaError_t launch_latent_append(const LatentAppend &p);
 cudaError_t launch_latent_decode_simt(const LatentDecode &p);
 cudaError_t launch_latent_prefill_simt(const LatentPrefill &p);

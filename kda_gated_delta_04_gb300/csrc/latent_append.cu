@@ -7,17 +7,19 @@
 //
 // The pair i is (i, i + 32) or, interleaved, (2i, 2i + 1).  Sums and products are fp32, rounded
 // once when stored.  Bound by memory (T large) or by the latency of one dependent chain,
-// position -> table row -> store (T small).  A warp is one unit of work and one CTA: either a token's
-// latent row and position key, or the position channels of 16 of its query heads (32 lanes = 8 heads x 4
-// quarters of the pairs, two heads and 2 x 8 pairs a lane).  Small batches so spread over 1 + H / 16 CTAs a
-// token, and large ones keep up to 2 KB a warp in flight while warps come and go singly: 32,768 tokens of 32
-// heads 72 us (386 MB, 5.4 TB/s); CTAs of four warps 76, one head a lane 79, one warp and one head 88.
+// position -> table row -> store (T small).  A warp's unit of work is either a token's latent row and
+// position key, or the position channels of 16 of its query heads (32 lanes = 8 heads x 4 quarters of the
+// pairs, two heads and 2 x 8 pairs a lane), so that small batches spread over 1 + H / 16 warps a token.  In
+// large ones each of the 16 warps that an SM holds walks on through the units, the numbers (position, slot)
+// two units ahead and the rows one: 32,768 tokens of 32 heads 68 us (386 MB, 5.6 TB/s), 64 tokens 2.8.  A
+// warp a unit and CTA took 72 and was bound by the launching of CTAs, 0.6 ns each.
 #include "latent.cuh"
+#include "sm100_ptx.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kWarps = 1;
+constexpr int kWarps = 2, kMaxBlocks = 152 * 8;  // 16 warps a SM: what 128 registers a thread leave room for
 
 // Eight consecutive elements as they lie in memory (16-byte aligned): what is neither normalised
 // nor rotated is stored again bit for bit.
@@ -82,12 +84,14 @@ __device__ __forceinline__ void quarter_at(int j, bool interleaved, int &lo, int
 
 // Rotates the 8 pairs held as row[lo..] and row[hi..] (see quarter_at).
 template <typename IO>
-__device__ __forceinline__ void rotate8(Raw8<IO> &rx, Raw8<IO> &ry, const float (&c)[8], const float (&s)[8],
+__device__ __forceinline__ void rotate8(Raw8<IO> &rx, Raw8<IO> &ry, const Raw8<float> &rc, const Raw8<float> &rs,
                                         bool interleaved)
 {
-    float x[8], y[8];
+    float x[8], y[8], c[8], s[8];
     widen(rx, x);
     widen(ry, y);
+    widen(rc, c);
+    widen(rs, s);
     if (interleaved) {  // pair i: elements 2i, 2i + 1 of x ++ y
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -109,82 +113,89 @@ __device__ __forceinline__ void rotate8(Raw8<IO> &rx, Raw8<IO> &ry, const float 
     narrow(y, ry);
 }
 
-constexpr int kRounds = 2;  // heads of a lane in a query unit
-constexpr int kUnitHeads = 8 * kRounds;
+constexpr int kUnitHeads = 16;  // heads of a query unit, two a lane
 
-// q_pe / q_pe_out, latent / latent_out and k_pe / k_pe_out may be the same rows: a lane reads
-// what it overwrites before it does.
+// A unit as its warp has it in flight: of a token's latent row and position key, r[0], r[1] the latent's
+// channels 8 lane and 256 + 8 lane, r[2], r[3] a quarter of the key (lanes 0 to 3); of its queries two
+// heads' quarters.
 template <typename IO>
-__global__ void __launch_bounds__(32 * kWarps)
-latent_append_kernel(const LatentAppend p)
-{
-    const int lane = threadIdx.x & 31;
-    const int units = 1 + (p.q_pe_out ? (p.heads + kUnitHeads - 1) / kUnitHeads : 0);
-    const int64_t work = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (work >= (int64_t)p.tokens * units) return;
-    const int t = (int)(work / units), unit = (int)(work - (int64_t)t * units);
-    const int j = lane & 3;
-    int lo, hi;
-    quarter_at(j, p.interleaved, lo, hi);
-    const int pos = p.cos_sin ? p.positions[t] : 0;
+struct Item {
+    int t, unit, pos, slot;
+    Raw8<IO> r[4];
+    Raw8<float> c, s;
+};
 
-    // the loads that depend on nothing, beside the chain position -> table row
-    Raw8<IO> x[kRounds], y[kRounds], x0, x1;
-    const int head = (unit - 1) * kUnitHeads + (lane >> 2);
-    int64_t slot = -1;
-    if (unit == 0) {
-        slot = p.slots[t];
-        const IO *row = static_cast<const IO *>(p.latent) + t * p.latent_stride;
-        load8(row + 8 * lane, x0);
-        load8(row + 256 + 8 * lane, x1);
+// The numbers of a unit: loaded two units ahead, as everything else hangs on the position.
+template <typename IO>
+__device__ __forceinline__ void ask_numbers(const LatentAppend &p, int64_t work, int64_t total, int units, Item<IO> &it)
+{
+    it.t = -1;
+    if (work >= total) return;
+    it.t = (int)(work / units);
+    it.unit = (int)(work - (int64_t)it.t * units);
+    it.pos = p.cos_sin ? p.positions[it.t] : 0;
+    it.slot = it.unit == 0 ? p.slots[it.t] : -1;
+}
+
+// Its rows and its row of the table: loaded one unit ahead.
+template <typename IO>
+__device__ __forceinline__ void ask_rows(const LatentAppend &p, Item<IO> &it, int lane, int lo, int hi)
+{
+    if (it.t < 0) return;
+    if (it.unit == 0) {
+        const IO *row = static_cast<const IO *>(p.latent) + it.t * p.latent_stride;
+        load8(row + 8 * lane, it.r[0]);
+        load8(row + 256 + 8 * lane, it.r[1]);
         if (lane < 4) {
-            const IO *kr = static_cast<const IO *>(p.k_pe) + t * p.k_pe_stride;
-            load8(kr + lo, x[0]);
-            load8(kr + hi, y[0]);
+            const IO *kr = static_cast<const IO *>(p.k_pe) + it.t * p.k_pe_stride;
+            load8(kr + lo, it.r[2]);
+            load8(kr + hi, it.r[3]);
         }
     } else {
+        const int head = (it.unit - 1) * kUnitHeads + (lane >> 2);
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-            if (head + 8 * r < p.heads) {
-                const IO *qr = static_cast<const IO *>(p.q_pe) + t * p.q_ts + (head + 8 * r) * p.q_hs;
-                load8(qr + lo, x[r]);
-                load8(qr + hi, y[r]);
+        for (int u = 0; u < 2; ++u)
+            if (head + 8 * u < p.heads) {
+                const IO *qr = static_cast<const IO *>(p.q_pe) + it.t * p.q_ts + (head + 8 * u) * p.q_hs;
+                load8(qr + lo, it.r[2 * u]);
+                load8(qr + hi, it.r[2 * u + 1]);
             }
     }
-    if (p.cos_sin && (pos < 0 || pos >= p.num_positions)) {  // the token is left out
-        if (unit == 0 && lane == 0 && p.errors) atomicOr(p.errors, DEV_ERR_POSITION);
+    if (p.cos_sin && it.pos >= 0 && it.pos < p.num_positions) {
+        const float *cs = p.cos_sin + (size_t)it.pos * kLatP + 8 * (lane & 3);
+        load8(cs, it.c);
+        load8(cs + kLatP / 2, it.s);
+    }
+}
+
+template <typename IO>
+__device__ __forceinline__ void finish(const LatentAppend &p, Item<IO> &it, int lane, int lo, int hi)
+{
+    if (p.cos_sin && (it.pos < 0 || it.pos >= p.num_positions)) {  // the token is left out
+        if (it.unit == 0 && lane == 0 && p.errors) atomicOr(p.errors, DEV_ERR_POSITION);
         return;
     }
-    if (p.cos_sin && (unit > 0 || lane < 4)) {
-        const float *cs = p.cos_sin + (size_t)pos * kLatP + 8 * j;
-        Raw8<float> rc, rs;
-        load8(cs, rc);
-        load8(cs + kLatP / 2, rs);
-        float c[8], s[8];
-        widen(rc, c);
-        widen(rs, s);
+    if (it.unit > 0) {
+        const int head = (it.unit - 1) * kUnitHeads + (lane >> 2);
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-            if (unit == 0 ? r == 0 : head + 8 * r < p.heads) rotate8(x[r], y[r], c, s, p.interleaved);
-    }
-    if (unit > 0) {
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-            if (head + 8 * r < p.heads) {
-                IO *qo = static_cast<IO *>(p.q_pe_out) + t * p.qo_ts + (head + 8 * r) * p.qo_hs;
-                store8(qo + lo, x[r]);
-                store8(qo + hi, y[r]);
+        for (int u = 0; u < 2; ++u)
+            if (head + 8 * u < p.heads) {
+                if (p.cos_sin) rotate8(it.r[2 * u], it.r[2 * u + 1], it.c, it.s, p.interleaved);
+                IO *qo = static_cast<IO *>(p.q_pe_out) + it.t * p.qo_ts + (head + 8 * u) * p.qo_hs;
+                store8(qo + lo, it.r[2 * u]);
+                store8(qo + hi, it.r[2 * u + 1]);
             }
         return;
     }
+    if (p.cos_sin && lane < 4) rotate8(it.r[2], it.r[3], it.c, it.s, p.interleaved);
     if (p.norm_weight) {
         const IO *w = static_cast<const IO *>(p.norm_weight);
         Raw8<IO> r0, r1;
         load8(w + 8 * lane, r0);
         load8(w + 256 + 8 * lane, r1);
         float a[8], b[8], w0[8], w1[8];
-        widen(x0, a);
-        widen(x1, b);
+        widen(it.r[0], a);
+        widen(it.r[1], b);
         widen(r0, w0);
         widen(r1, w1);
         float ss = 0.f;
@@ -198,29 +209,57 @@ latent_append_kernel(const LatentAppend p)
             a[i] *= rn * w0[i];
             b[i] *= rn * w1[i];
         }
-        narrow(a, x0);
-        narrow(b, x1);
+        narrow(a, it.r[0]);
+        narrow(b, it.r[1]);
     }
     if (p.latent_out) {
-        IO *out = static_cast<IO *>(p.latent_out) + t * p.lo_stride;
-        store8(out + 8 * lane, x0);
-        store8(out + 256 + 8 * lane, x1);
+        IO *out = static_cast<IO *>(p.latent_out) + it.t * p.lo_stride;
+        store8(out + 8 * lane, it.r[0]);
+        store8(out + 256 + 8 * lane, it.r[1]);
     }
     if (p.k_pe_out && lane < 4) {
-        IO *out = static_cast<IO *>(p.k_pe_out) + t * p.ko_stride;
-        store8(out + lo, x[0]);
-        store8(out + hi, y[0]);
+        IO *out = static_cast<IO *>(p.k_pe_out) + it.t * p.ko_stride;
+        store8(out + lo, it.r[2]);
+        store8(out + hi, it.r[3]);
     }
-    if (slot < 0 || slot >= p.num_slots) {  // -1: not cached
-        if (slot != -1 && lane == 0 && p.errors) atomicOr(p.errors, DEV_ERR_SLOT);
+    if (it.slot < 0 || it.slot >= p.num_slots) {  // -1: not cached
+        if (it.slot != -1 && lane == 0 && p.errors) atomicOr(p.errors, DEV_ERR_SLOT);
         return;
     }
-    IO *c = static_cast<IO *>(p.cache) + slot * kLatC;
-    store8(c + 8 * lane, x0);
-    store8(c + 256 + 8 * lane, x1);
+    IO *c = static_cast<IO *>(p.cache) + (int64_t)it.slot * kLatC;
+    store8(c + 8 * lane, it.r[0]);
+    store8(c + 256 + 8 * lane, it.r[1]);
     if (lane < 4) {
-        store8(c + kLatR + lo, x[0]);
-        store8(c + kLatR + hi, y[0]);
+        store8(c + kLatR + lo, it.r[2]);
+        store8(c + kLatR + hi, it.r[3]);
+    }
+}
+
+// q_pe / q_pe_out, latent / latent_out and k_pe / k_pe_out may be the same rows: a unit is read and written
+// by the same lanes, and no other unit touches its rows.
+template <typename IO>
+__global__ void __launch_bounds__(32 * kWarps)
+latent_append_kernel(const LatentAppend p)
+{
+    const int lane = threadIdx.x & 31;
+    const int units = 1 + (p.q_pe_out ? (p.heads + kUnitHeads - 1) / kUnitHeads : 0);
+    const int64_t total = (int64_t)p.tokens * units, step = (int64_t)gridDim.x * kWarps;
+    int64_t work = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    int lo, hi;
+    quarter_at(lane & 3, p.interleaved, lo, hi);
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    Item<IO> it, next, after;
+    ask_numbers(p, work, total, units, it);
+    ask_numbers(p, work + step, total, units, next);
+    ask_rows(p, it, lane, lo, hi);
+    while (it.t >= 0) {
+        work += step;
+        ask_numbers(p, work + step, total, units, after);
+        ask_rows(p, next, lane, lo, hi);
+        finish(p, it, lane, lo, hi);
+        it = next;
+        next = after;
     }
 }
 
@@ -229,14 +268,11 @@ latent_append_kernel(const LatentAppend p)
 cudaError_t launch_latent_append(const LatentAppend &p)
 {
     const int64_t units = 1 + (p.q_pe_out ? (p.heads + kUnitHeads - 1) / kUnitHeads : 0);
-    const int64_t blocks = (p.tokens * units + kWarps - 1) / kWarps;
-    if (blocks == 0) return cudaSuccess;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    if (p.dtype == KDA_DTYPE_BF16)
-        latent_append_kernel<__nv_bfloat16><<<(unsigned)blocks, 32 * kWarps, 0, p.stream>>>(p);
-    else
-        latent_append_kernel<float><<<(unsigned)blocks, 32 * kWarps, 0, p.stream>>>(p);
-    return cudaGetLastError();
+    const int64_t needed = (p.tokens * units + kWarps - 1) / kWarps;
+    if (needed == 0) return cudaSuccess;
+    const int blocks = (int)(needed < kMaxBlocks ? needed : kMaxBlocks);
+    return latent_launch(p.dtype == KDA_DTYPE_BF16 ? latent_append_kernel<__nv_bfloat16> : latent_append_kernel<float>,
+                         dim3((unsigned)blocks), 32 * kWarps, 0, p.stream, 1, p);
 }
 
 }  // namespace kda

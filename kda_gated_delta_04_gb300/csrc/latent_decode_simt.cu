@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kT, 2) latent_decode_simt_kernel(const LatentD
     Smem &sm = *reinterpret_cast<Smem *>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t capacity = (int64_t)p.table_width * p.page_size;
+    pdl_wait();
     LatentWalk w = latent_walk<kT, float>(p, kRows, kHeads, sm.scan);
     pdl_launch_dependents();
     if (w.cta >= w.ctas) return;
@@ -199,6 +200,7 @@ latent_join_kernel(const char *ws, int head_tile, int heads, IO *o, float *lse)
     __shared__ float s_red[4 * GROUPS];
     __shared__ float4 s_o[GROUPS > 1 ? GROUPS - 1 : 1][128];
     pdl_wait();  // launched early behind the kernel that wrote the parts
+    pdl_launch_dependents();
     const LatentJoin j = reinterpret_cast<const LatentJoin *>(ws)[blockIdx.x];
     const int hl = blockIdx.y, h = j.h0 + hl, tid = threadIdx.x, quad = tid & 127, group = tid >> 7;
     if (j.b < 0 || h >= heads) return;
@@ -272,17 +274,9 @@ cudaError_t launch_join(const LatentDecode &p, int head_tile, int grid)
     const int records = latent_join_by_unit(p.batch, p.heads, head_tile, grid) ? units : grid;
     const int heads = p.heads < head_tile ? p.heads : head_tile;
     const bool few = records * heads <= 4 * 152;  // one wave of 512 threads a CTA
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)records, (unsigned)heads);
-    cfg.blockDim = dim3(few ? 512 : 128);
-    cfg.stream = p.stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, few ? latent_join_kernel<IO, 4> : latent_join_kernel<IO, 1>,
-                              (const char *)p.workspace, head_tile, p.heads, static_cast<IO *>(p.o), p.lse);
+    return latent_launch(few ? latent_join_kernel<IO, 4> : latent_join_kernel<IO, 1>,
+                         dim3((unsigned)records, (unsigned)heads), few ? 512 : 128, 0, p.stream, 1,
+                         (const char *)p.workspace, head_tile, p.heads, static_cast<IO *>(p.o), p.lse);
 }
 
 int sm_count()
@@ -315,8 +309,8 @@ cudaError_t launch_latent_decode_simt(const LatentDecode &p)
     const int64_t most = per_seq * p.batch * ((p.heads + kHeads - 1) / kHeads);  // no more CTAs than there can be tiles
     int grid = 2 * sms < kLatMaxGrid ? 2 * sms : kLatMaxGrid;
     if (most < grid) grid = most > 0 ? (int)most : 1;
-    latent_decode_simt_kernel<<<grid, kT, sizeof(Smem), p.stream>>>(p);
-    const cudaError_t launched = cudaGetLastError();
+    const cudaError_t launched =
+        latent_launch(latent_decode_simt_kernel, dim3((unsigned)grid), kT, sizeof(Smem), p.stream, 1, p);
     return launched != cudaSuccess ? launched : launch_latent_join(p, kHeads, grid);
 }
 

@@ -537,6 +537,7 @@ latent_decode_tc_kernel(const LatentDecode p, const __grid_constant__ CUtensorMa
         tmem_alloc(&mi.tmem, C::COLS);
         tmem_relinquish();
     }
+    pdl_wait();
     const LatentWalk w = latent_walk<kT, __nv_bfloat16>(p, kRows, NH, mi.scan);
     tc_fence_before_sync();
     __syncthreads();
@@ -599,8 +600,8 @@ cudaError_t launch(const LatentDecode &p, int grid)
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    latent_decode_tc_kernel<NH><<<grid, kT, kSmemMax, p.stream>>>(p, tm, tq, piece, b_step, h_step);
-    err = cudaGetLastError();
+    err = latent_launch(latent_decode_tc_kernel<NH>, dim3((unsigned)grid), kT, kSmemMax, p.stream, 1, p, tm, tq, piece,
+                        b_step, h_step);
     return err != cudaSuccess ? err : launch_latent_join(p, NH, grid);
 }
 

@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int rank = CS > 1 ? (int)cluster_rank() : 0, unit = blockIdx.x / CS;
     const int h = unit % p.heads;
+    pdl_wait();
     // the tiles with the most keys first
     const int tile = (int)(gridDim.x / CS / p.heads) - 1 - unit / p.heads;
     const LatentTile at = latent_tile(p, tile, kM, tid & 31);
@@ -241,18 +242,7 @@ cudaError_t launch(const LatentPrefill &p, int64_t units)
     cudaError_t err = cudaFuncSetAttribute(latent_prefill_simt_kernel<CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)sizeof(Smem));
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * CS));
-    cfg.blockDim = dim3(kT);
-    cfg.dynamicSmemBytes = sizeof(Smem);
-    cfg.stream = p.stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = CS;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_prefill_simt_kernel<CS>, p);
+    return latent_launch(latent_prefill_simt_kernel<CS>, dim3((unsigned)(units * CS)), kT, sizeof(Smem), p.stream, CS, p);
 }
 
 }  // namespace

@@ -558,6 +558,7 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     tc_fence_before_sync();
     __syncthreads();
     cluster_sync();  // the other CTA's barriers are ready
+    pdl_wait();
     tc_fence_after_sync();
     const uint32_t tmem = mi.tmem;
     // registers: 384 x 168 = 64,512 at launch; 256 x 232 + 128 x 40 = 64,512 now
@@ -634,18 +635,8 @@ cudaError_t launch_latent_prefill_tc(const LatentPrefill &p)
     static int configured = -1;
     const cudaError_t err = tc::allow_smem(latent_prefill_tc_kernel, kSmem, &configured);
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kT);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = p.stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 2;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_prefill_tc_kernel, p, tq, tk, tp, tv, q_step, k_step, v_step);
+    return latent_launch(latent_prefill_tc_kernel, dim3((unsigned)blocks), kT, kSmem, p.stream, 2, p, tq, tk, tp, tv,
+                         q_step, k_step, v_step);
 }
 
 }  // namespace kda
