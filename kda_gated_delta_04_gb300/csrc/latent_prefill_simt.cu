@@ -65,9 +65,7 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
     const int rank = CS > 1 ? (int)cluster_rank() : 0, unit = blockIdx.x / CS;
     const int h = unit % p.heads;
     pdl_wait();
-    // the tiles with the most keys first
-    const int tile = (int)(gridDim.x / CS / p.heads) - 1 - unit / p.heads;
-    const LatentTile at = latent_tile(p, tile, kM, tid & 31);
+    const LatentTile at = latent_tile(p, unit / p.heads, (int)(gridDim.x / CS / p.heads), kM, tid & 31);
     if (blockIdx.x == 0 && tid < 32) {
         latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
         latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);

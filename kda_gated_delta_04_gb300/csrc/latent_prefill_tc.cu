@@ -38,7 +38,7 @@ constexpr uint32_t kPanelQ = 128 * 128;       // bytes: 128 queries x 64 channel
 constexpr uint32_t kPanelK = 64 * 128;        // half of a tile's keys x 64 channels
 constexpr uint32_t kTileK = 3 * kPanelK, kTileV = 128 * 128;  // a CTA's part of a K and a V tile
 constexpr int kStages = 3;                    // key tiles in shared memory
-constexpr int kAhead = 4;                     // key tiles brought into L2 before their copy
+constexpr int kAhead = 2;                     // key tiles brought into L2 before their copy
 constexpr uint32_t kOffQ = 0;                 // two tiles of three panels
 constexpr uint32_t kOffK = kOffQ + 6 * kPanelQ;
 constexpr uint32_t kOffV = kOffK + kStages * kTileK;
@@ -155,7 +155,7 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 __device__ __forceinline__ Job make_job(const LatentPrefill &p, int pair, int lane)
 {
     const int pairs = gridDim.x >> 1;
-    const LatentTile at = latent_tile(p, pairs / p.heads - 1 - pair / p.heads, kPairM, lane);
+    const LatentTile at = latent_tile(p, pair / p.heads, pairs / p.heads, kPairM, lane);
     Job j;
     j.h = pair % p.heads;
     j.q0 = at.q0;
@@ -561,9 +561,9 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     pdl_wait();
     tc_fence_after_sync();
     const uint32_t tmem = mi.tmem;
-    // registers: 384 x 168 = 64,512 at launch; 256 x 232 + 128 x 40 = 64,512 now
+    // registers: 384 x 168 = 64,512 at launch; 256 x 200 + 128 x 40 = 56,320 now
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         softmax_role(sm, mi, p, tmem, warp >> 2, rank);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
