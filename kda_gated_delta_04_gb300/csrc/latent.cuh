@@ -154,54 +154,78 @@ __device__ __forceinline__ void latent_range(const int32_t *cu, int n, int total
     t1 = (int)b;
 }
 
-// The order-th of `count` query tiles of m rows, by a whole warp, without a table.
+// The query tiles of m rows in the order in which they are worked on, by a whole warp, without a table.
 //  Up to 32 sequences (a lane each): the tiles with the highest index in their sequence first, so that
 //  those with the most keys (causal) start first and the numbers without a tile come last.  With C(x) the
 //  tiles of index x and more over all sequences, the index is the largest x with C(x) > order.
 //  More: sequence n's tiles are numbered from cu_q[n] / m + n, which increases with n and leaves room for
-//  all of them, and searched 32 candidates at a time (65,535 sequences: four rounds of one load); late
-//  numbers first.
+//  all of them, and searched 32 candidates at a time (65,535 sequences: four rounds of one load, the first
+//  of them here); late numbers first.
 // A malformed cu_q or cu_k is reported and held to the buffers.
-__device__ __forceinline__ LatentTile latent_tile(const LatentPrefill &p, int order, int count, int m, int lane)
+struct LatentLane {
+    int q0, q1, k0, k1;  // up to 32 sequences: the lane's
+    int first;           // more: the number of the first tile of the lane's candidate in the first round
+};
+__device__ __forceinline__ LatentLane latent_lane(const LatentPrefill &p, int m, int lane)
 {
-    int n = 0, q0, q1, k0, k1, index;
+    LatentLane l{};
+    const int step = (p.num_seqs + 31) / 32, at = lane * step;
+    if (at < p.num_seqs) {
+        latent_range(p.cu_q, at, (int)p.q_tokens, l.q0, l.q1);
+        if (step == 1) latent_range(p.cu_k, at, (int)p.k_tokens, l.k0, l.k1);
+        l.first = l.q0 / m + at;
+    } else {
+        l.first = 0x7fffffff;
+    }
+    return l;
+}
+
+// The order-th of `count` numbers.
+__device__ __forceinline__ LatentTile latent_tile(const LatentPrefill &p, const LatentLane &l, int order, int count,
+                                                  int m, int lane)
+{
+    int q0 = l.q0, q1 = l.q1, k0 = l.k0, k1 = l.k1, from, index;  // (from: the lane that has the sequence)
     if (p.num_seqs <= 32) {
-        latent_range(p.cu_q, lane < p.num_seqs ? lane : 0, (int)p.q_tokens, q0, q1);
-        const int tiles = lane < p.num_seqs ? (q1 - q0 + m - 1) / m : 0;
-        auto from = [&](int x) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)max(0, tiles - x)); };
+        const int tiles = (q1 - q0 + m - 1) / m;
+        auto above = [&](int x) { return (int)__reduce_add_sync(0xffffffffu, (unsigned)max(0, tiles - x)); };
         int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, (unsigned)tiles);  // C(hi) = 0
         while (lo + 1 < hi) {
             const int mid = (lo + hi) >> 1;
-            if (from(mid) > order) lo = mid;
+            if (above(mid) > order) lo = mid;
             else hi = mid;
         }
         index = lo;
-        const int rank = order - from(index + 1);  // among the sequences that have such a tile
+        const int rank = order - above(index + 1);  // among the sequences that have such a tile
         const uint32_t have = __ballot_sync(0xffffffffu, tiles > index);
         const uint32_t at = __ballot_sync(0xffffffffu, tiles > index && __popc(have & ((1u << lane) - 1u)) == rank);
         if (!at) return LatentTile{0, 0, 0, 0, 0, 0};
-        n = __ffs(at) - 1;
-        q0 = __shfl_sync(0xffffffffu, q0, n);
-        q1 = __shfl_sync(0xffffffffu, q1, n);
+        from = __ffs(at) - 1;
     } else {
         const int tile = count - 1 - order;
-        int left = p.num_seqs;  // the last sequence whose first tile is not after `tile` is in [n, n + left)
-        while (left > 1) {
-            const int step = (left + 31) / 32, at = n + lane * step;
+        // the last sequence whose first tile is not after `tile` is in [n, n + step)
+        int step = (p.num_seqs + 31) / 32;
+        from = 31 - __clz(__ballot_sync(0xffffffffu, l.first <= tile) | 1u);
+        int n = from * step, left = min(step, p.num_seqs - n), first = 0;
+        while (left > 1 || step > 1) {
+            step = (left + 31) / 32;
+            const int at = n + lane * step;
             bool before = false;
             if (lane * step < left) {
                 latent_range(p.cu_q, at, (int)p.q_tokens, q0, q1);
-                before = q0 / m + at <= tile;
+                if (step == 1) latent_range(p.cu_k, at, (int)p.k_tokens, k0, k1);
+                first = q0 / m + at;
+                before = first <= tile;
             }
-            const uint32_t set = __ballot_sync(0xffffffffu, before) | 1u;
-            const int k = 31 - __clz(set);
-            n += k * step;
-            left = min(step, left - k * step);
+            from = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);
+            n += from * step;
+            left = min(step, left - from * step);
         }
-        latent_range(p.cu_q, n, (int)p.q_tokens, q0, q1);
-        index = max(0, tile - (q0 / m + n));
+        index = max(0, tile - __shfl_sync(0xffffffffu, first, from));
     }
-    latent_range(p.cu_k, n, (int)p.k_tokens, k0, k1);
+    q0 = __shfl_sync(0xffffffffu, q0, from);
+    q1 = __shfl_sync(0xffffffffu, q1, from);
+    k0 = __shfl_sync(0xffffffffu, k0, from);
+    k1 = __shfl_sync(0xffffffffu, k1, from);
     LatentTile t;
     t.q0 = q0 + index * m;
     t.k0 = k0;

@@ -11,7 +11,7 @@
 //
 // With fewer query tiles than SMs a cluster of four CTAs shares a query tile, each taking every fourth
 // key tile, and the four results are joined through distributed shared memory (1,027 tokens, 4 heads:
-// XXX us; one CTA a tile: 216).
+// 65 us; one CTA a tile: 216).
 #include <math.h>
 
 #include "latent.cuh"
@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
     const int rank = CS > 1 ? (int)cluster_rank() : 0, unit = blockIdx.x / CS;
     const int h = unit % p.heads;
     pdl_wait();
-    const LatentTile at = latent_tile(p, unit / p.heads, (int)(gridDim.x / CS / p.heads), kM, tid & 31);
+    const LatentLane mine = latent_lane(p, kM, tid & 31);
+    const LatentTile at = latent_tile(p, mine, unit / p.heads, (int)(gridDim.x / CS / p.heads), kM, tid & 31);
     if (blockIdx.x == 0 && tid < 32) {
         latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
         latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);

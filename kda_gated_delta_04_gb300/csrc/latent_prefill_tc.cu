@@ -19,8 +19,8 @@
 // Tensor memory is full: two O, two S of 128 columns.  The two query tiles take turns: while one
 // tile's softmax runs (a warpgroup each, a thread per query, so that maximum and sum need no other
 // thread), the tensor cores run the other tile's products, O += P V of key tile j and S of j + 1.
-// Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10 and 11 make up
-// the warpgroup whose registers the softmax takes over.
+// Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10: the jobs; 11: a check of the
+// offsets (first CTA).
 #include <math.h>
 
 #include "latent.cuh"
@@ -38,6 +38,12 @@ constexpr uint32_t kPanelQ = 128 * 128;       // bytes: 128 queries x 64 channel
 constexpr uint32_t kPanelK = 64 * 128;        // half of a tile's keys x 64 channels
 constexpr uint32_t kTileK = 3 * kPanelK, kTileV = 128 * 128;  // a CTA's part of a K and a V tile
 constexpr int kStages = 3;                    // key tiles in shared memory
+constexpr int kJobs = 4;                      // records of jobs
+// Key tiles of a job during whose copies the next one is asked for already: what hides the 2,000 cycles that
+// asking for and finding it take.  A job taken sooner is one that a pair that comes free cannot have: with 4
+// for shared key tiles a prompt of 4,096 tokens took 129 us instead of 123 (its last jobs have 4), while 64
+// prompts of 150 to 250 tokens, side by side, take 88 us with 2 and 74 with 4 or 8 (16 heads).
+constexpr int kShort = 2, kShortApart = 8;
 constexpr int kAhead = 2;                     // key tiles brought into L2 before their copy
 constexpr uint32_t kOffQ = 0;                 // two tiles of three panels
 constexpr uint32_t kOffK = kOffQ + 6 * kPanelQ;
@@ -47,19 +53,28 @@ constexpr uint64_t kWait = tc::kWaitNs;
 constexpr float kSlack = 8.f;  // log2: how far scores may pass the held maximum before it is moved
 constexpr uint32_t kColO = 0, kColS = 256;    // + 128 x query tile
 
-// What a pair of CTAs works on: queries [q0, q0 + rows) of one head against the keys of their sequence,
-// klen from k0; the first query sees the keys up to `off` when causal.  n0, n1: key tiles that the two
-// query tiles see (with the second tile there is, it sees every key tile that the first does).
-struct alignas(16) Job {
-    int q0, k0, rows, klen, off, n0, n1;
-    int h;  // head; -1: no job, the pair is done
-    __device__ __forceinline__ int n(int i) const { return i ? n1 : n0; }
-    __device__ __forceinline__ int nmax() const { return max(n0, n1); }
-    // the last key tile reaches past the sequence's keys
-    __device__ __forceinline__ bool tail() const { return nmax() > 0 && nmax() * kN > klen; }
-    // first of this CTA's rows of tile i
-    __device__ __forceinline__ static int first(int i, int rank) { return 2 * kM * i + kM * rank; }
+// A query tile: queries [q0, q0 + rows) of a head (256 at most, 128 for each CTA) against the keys of their
+// sequence, klen from k0; the first query sees the keys up to `off` when causal; n key tiles.
+struct alignas(16) Part {
+    int q0, k0, rows, klen, off, h, n;
+    int tail;  // where the last key tile reaches past the sequence's keys: its V buffer + 4 x parity there
+    __device__ __forceinline__ bool has_tail() const { return n > 0 && n * kN > klen; }
 };
+
+// What a pair of CTAs works on: two query tiles of one sequence and head that share every key tile (the
+// second sees all that the first does), or, of sequences with no more than 256 queries left, one each of
+// two, whose key tiles come in turn.
+enum : int { kDone = 0, kShared = 1, kApart = 2 };
+struct Job {
+    Part part[2];
+    int kind, unused[3];
+};
+
+// Place of key tile j of query tile i among the job's key tiles.
+__device__ __forceinline__ int place(bool apart, int n0, int n1, int i, int j)
+{
+    return !apart ? j : (i ? j + min(j + 1, n0) : j + min(j, n1));
+}
 
 // Barriers of the leading CTA only: q_full, k_full, v_full (bytes that both CTAs copy), p_full,
 // o_empty and next_empty (a warp's arrival each, both CTAs).  The others each CTA has for itself; what the matrix
@@ -67,10 +82,10 @@ struct alignas(16) Job {
 struct Misc {
     uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], v_tail[kStages], drained;
-    uint64_t next_full, next_empty;  // the number of the next job: each CTA; both CTAs' copy warps, in the leading CTA
-    uint64_t job_full[2], job_empty[2];
+    uint64_t next_full, next_empty;  // the number asked for: each CTA; both CTAs have read it, in the leading one
+    uint64_t job_full[kJobs], job_empty[kJobs], copied[2];  // copied: all of a job's tiles
     alignas(16) uint4 next;
-    alignas(16) Job job[2];          // the present job and the next, for this CTA's other warps
+    alignas(16) Job job[kJobs];      // for this CTA's other warps
     uint32_t tmem;
     int abort;
 };
@@ -151,106 +166,209 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// The job of cluster `pair` of the grid: heads innermost, the tiles with the most keys first.  A whole warp.
-__device__ __forceinline__ Job make_job(const LatentPrefill &p, int pair, int lane)
+// Query tiles of cluster `pair` of the grid: heads innermost, the tiles with the most keys first.  A whole
+// warp; part[0].rows is 0 where the number has no tile.
+__device__ __forceinline__ void make_parts(const LatentPrefill &p, const LatentLane &mine, int count, uint32_t inverse,
+                                           int pair, int lane, Part (&part)[2])
 {
-    const int pairs = gridDim.x >> 1;
-    const LatentTile at = latent_tile(p, pair / p.heads, pairs / p.heads, kPairM, lane);
-    Job j;
-    j.h = pair % p.heads;
-    j.q0 = at.q0;
-    j.k0 = at.k0;
-    j.rows = at.rows;
-    j.klen = at.klen;
-    j.off = at.off;
-    auto tiles = [&](int i) {
-        const int rows = max(0, min(2 * kM, j.rows - 2 * kM * i));
-        int keys = j.klen;
-        if (p.causal) keys = max(0, min(keys, j.off + 2 * kM * i + rows));
-        return rows > 0 ? (keys + kN - 1) / kN : 0;
-    };
-    j.n0 = tiles(0);
-    j.n1 = tiles(1);
-    return j;
+    // pair / heads from floor((2^32 - 1) / heads), which is short by two at most
+    int order = (int)__umulhi((uint32_t)pair, inverse), h = pair - order * p.heads;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (h >= p.heads) {
+            h -= p.heads;
+            ++order;
+        }
+    const LatentTile at = latent_tile(p, mine, order, count, kPairM, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        Part &x = part[i];
+        x.q0 = at.q0 + 2 * kM * i;
+        x.k0 = at.k0;
+        x.rows = max(0, min(2 * kM, at.rows - 2 * kM * i));
+        x.klen = at.klen;
+        x.off = at.off + 2 * kM * i;
+        x.h = h;
+        const int keys = p.causal ? max(0, min(x.klen, x.off + x.rows)) : x.klen;
+        x.n = x.rows > 0 ? (keys + kN - 1) / kN : 0;
+        x.tail = 0;
+    }
 }
 
-// The jobs of this pair as the other warps of a CTA read them from its copy warp, which writes them one
-// job ahead.  Every warp of a role calls take in step.
+// The jobs of this pair as the other warps of a CTA read them.  Every warp of a role takes them in step.
 struct Jobs {
     Misc &mi;
     int count;
     __device__ __forceinline__ Jobs(Misc &m) : mi(m), count(0) {}
-    // false: there is none, or a wait gave up
-    __device__ __forceinline__ bool take(Job &job, int lane)
+    // The next job, to be read before done(); null: there is none, or a wait gave up
+    __device__ __forceinline__ const Job *take()
     {
-        const int slot = count & 1;
-        if (!all_wait<false>(&mi.job_full[slot], (count >> 1) & 1, &mi.abort)) return false;
-        job = mi.job[slot];
+        const Job *job = &mi.job[count % kJobs];
+        if (!all_wait<false>(&mi.job_full[count % kJobs], (count / kJobs) & 1, &mi.abort)) return nullptr;
+        return job->kind == kDone ? nullptr : job;
+    }
+    __device__ __forceinline__ void done(int lane)
+    {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&mi.job_empty[slot]);
+        if (lane == 0) mbar_arrive(&mi.job_empty[count % kJobs]);
         ++count;
-        return job.h >= 0;
     }
 };
 
-// One warp of each CTA: finds the jobs (its own cluster's, then those of clusters that were still
-// waiting to be launched) and copies their tiles.  The next one is asked for when the last copy of the
-// present one has been issued: early enough for the answer to be there, and no sooner, so that the last
-// jobs go to the pairs that are done first.
-__device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const LatentPrefill &p, const CUtensorMap &tq,
-                                          const CUtensorMap &tk, const CUtensorMap &tp, const CUtensorMap &tv,
-                                          int q_step, int k_step, int v_step, int rank, int lane)
+// One warp of each CTA: finds the jobs, its own cluster's, then those of clusters that were still waiting
+// to be launched.  The next one is asked for when the last copy of the present one has been issued: early
+// enough for the answer to be there, and no sooner, so that the last jobs go to the pairs that are done
+// first; a short job's successor is asked for when the copies of the one before are done.
+// A job of one query tile takes another such beside it (`beside`: the grid has more clusters than can run
+// at once), since alone it leaves the tensor cores to wait for its softmax and the other way round: 64
+// prompts of 150 to 250 tokens, 16 heads, 71 us instead of 97; 300 of 10 to 30 tokens 182 instead of 302.
+// Both CTAs of the pair come to the same jobs.
+__device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool beside, int rank, int lane)
+{
+    volatile int *abort = &mi.abort;
+    const bool lead = lane == 0, leader = rank == 0;
+    int t = 0, asked = 0;       // key tiles of the jobs before, numbers asked for so far
+    int at = blockIdx.x >> 1;   // the number at hand; -1: there is none left
+    bool used = false;          // it is in a job already
+    uint32_t tails = 0;         // parity of the tails so far in each V buffer
+    const LatentLane mine = latent_lane(p, kPairM, lane);
+    const int tiles = (int)(gridDim.x >> 1) / p.heads;
+    const uint32_t inverse = 0xffffffffu / (uint32_t)p.heads;
+    for (int count = 0;; ++count) {
+        Job &job = mi.job[count % kJobs];
+        if (count >= kJobs && !all_wait<false>(&mi.job_empty[count % kJobs], (count / kJobs - 1) & 1, abort)) return;
+        int kind = kDone, n0 = 0, n1 = 0;
+        bool tail0 = false, tail1 = false;
+        for (;;) {
+            if (used && at >= 0) {
+                if (lead) mbar_arrive_expect_tx(&mi.next_full, 16);
+                if (leader) {
+                    if (asked > 0 && !all_wait<true>(&mi.next_empty, (asked - 1) & 1, abort)) return;
+                    if (lead) cluster_take(&mi.next, &mi.next_full);
+                }
+                __syncwarp();
+                if (!all_wait<false>(&mi.next_full, asked & 1, abort)) return;
+                at = cluster_taken(&mi.next) >> 1;  // (-1 stays -1)
+                fence_proxy_async_smem();           // read before it is written again
+                __syncwarp();
+                if (lead) mbar_arrive_cluster(map_to_rank(&mi.next_empty, 0));
+                ++asked;
+                used = false;
+            }
+            if (at < 0) break;
+            Part part[2];
+            make_parts(p, mine, tiles, inverse, at, lane, part);
+            const bool lone = beside && part[1].rows == 0;
+            if (part[0].rows == 0) {
+                used = true;
+            } else if (kind == kDone) {
+                used = true;
+                if (lead) {
+                    job.part[0] = part[0];
+                    job.part[1] = part[1];
+                }
+                kind = kShared;
+                n0 = part[0].n, n1 = part[1].n;
+                tail0 = part[0].has_tail(), tail1 = part[1].has_tail();
+                if (!lone) break;
+            } else {  // a second one beside the first, or the next job
+                if (lone) {
+                    used = true;
+                    if (lead) job.part[1] = part[0];
+                    kind = kApart;
+                    n1 = part[0].n;
+                    tail1 = part[0].has_tail();
+                }
+                break;
+            }
+        }
+        const bool apart = kind == kApart;
+        const int all = apart ? n0 + n1 : max(n0, n1);
+        if (tail0 || tail1) {
+            // buffers and parities of the tails; of two, the one copied first counts first
+            const int e0 = place(apart, n0, n1, 0, n0 - 1), e1 = place(apart, n0, n1, 1, n1 - 1);
+            const bool swap = apart && e1 < e0;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+                const bool one = (k == 1) != swap;
+                if (!(one ? tail1 : tail0)) continue;
+                const int slot = (t + (one ? e1 : e0)) % kStages;
+                if (lead) job.part[one].tail = slot | (int)((tails >> slot) & 1) << 2;
+                // (where both share it, it is the second's)
+                if (apart || one || n1 == 0) tails ^= 1u << slot;
+            }
+        }
+        t += all;
+        if (lead) {
+            job.kind = kind;
+            mbar_arrive(&mi.job_full[count % kJobs]);
+        }
+        __syncwarp();
+        if (kind == kDone) return;
+        if (count > 0 && !all_wait<false>(&mi.copied[(count - 1) & 1], ((count - 1) >> 1) & 1, abort)) return;
+        if (all > (apart ? kShortApart : kShort) && !all_wait<false>(&mi.copied[count & 1], (count >> 1) & 1, abort)) return;
+    }
+}
+
+// One warp of each CTA: copies the tiles of the jobs.
+__device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const CUtensorMap &tq, const CUtensorMap &tk,
+                                          const CUtensorMap &tp, const CUtensorMap &tv, int q_step, int k_step,
+                                          int v_step, int rank, int lane)
 {
     volatile int *abort = &mi.abort;
     const bool lead = lane == 0, leader = rank == 0;
     int t = 0, nq0 = 0, nq1 = 0;  // key tiles and queries copied so far
-    int at = blockIdx.x >> 1;
-    bool ok = true;
-    for (int count = 0;; ++count) {
-        const int js = count & 1;
-        if (count >= 2 && !(ok = all_wait<false>(&mi.job_empty[js], (count / 2 - 1) & 1, abort))) break;
-        Job job;
-        job.h = -1;
-        if (at >= 0) job = make_job(p, at, lane);
-        if (lead) {
-            mi.job[js] = job;
-            mbar_arrive(&mi.job_full[js]);
-        }
-        if (at < 0) break;
-        const int k0 = job.k0, q0 = job.q0, h = job.h * q_step, kh = job.h * k_step, vh = job.h * v_step;
-        const int nmax = job.nmax();
-        auto ahead = [&](int j) {  // this CTA's part of key tile j into L2
-            if (!lead || j >= nmax) return;
-            const int k = k0 + kN * j;
+    Jobs jobs(mi);
+    while (const Job *next = jobs.take()) {
+        const Job &job = *next;
+        const bool apart = job.kind == kApart;
+        const int n0 = job.part[0].n, n1 = job.part[1].n, all = apart ? n0 + n1 : max(n0, n1);
+        bool ok = true;
+        auto ahead = [&](const Part &x, int j) {  // this CTA's part of a key tile into L2
+            if (!lead || j >= x.n) return;
+            const int k = x.k0 + kN * j, kh = x.h * k_step;
             tma_prefetch_3d(&tk, 0, kh, k + 64 * rank);
             tma_prefetch_3d(&tk, 64, kh, k + 64 * rank);
             tma_prefetch_3d(&tp, 0, 0, k + 64 * rank);
-            tma_prefetch_3d(&tv, 64 * rank, vh, k);
+            tma_prefetch_3d(&tv, 64 * rank, x.h * v_step, k);
         };
         auto queries = [&](int i, int &nq) -> bool {
-            if (job.n(i) == 0) return true;
+            const Part x = job.part[i];
+            if (x.n == 0) return true;
             if (nq > 0 && !all_wait<false>(&mi.q_empty[i], (nq - 1) & 1, abort)) return false;
             if (lead) {
                 if (leader) mbar_arrive_expect_tx(&mi.q_full[i], 2 * 3 * kPanelQ);
                 const uint32_t bar = map_to_rank(&mi.q_full[i], 0);
 #pragma unroll
                 for (int c = 0; c < 3; ++c)
-                    tma_load_3d_pair(sm + kOffQ + (3 * i + c) * kPanelQ, &tq, bar, 64 * c, h, q0 + job.first(i, rank));
+                    tma_load_3d_pair(sm + kOffQ + (3 * i + c) * kPanelQ, &tq, bar, 64 * c, x.h * q_step, x.q0 + kM * rank);
             }
             ++nq;
             return true;
         };
         if (lead) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (job.n(i) > 0)
+            for (int i = 0; i < 2; ++i) {
+                const Part x = job.part[i];
+                if (x.n > 0)
 #pragma unroll
-                    for (int c = 0; c < 3; ++c) tma_prefetch_3d(&tq, 64 * c, h, q0 + job.first(i, rank));
+                    for (int c = 0; c < 3; ++c) tma_prefetch_3d(&tq, 64 * c, x.h * q_step, x.q0 + kM * rank);
+            }
         }
-        for (int j = 0; j < kAhead; ++j) ahead(j);
-        for (int j = 0; j < nmax; ++j, ++t) {
-            ahead(j + kAhead);
-            const int slot = t % kStages, k = k0 + kN * j;
+        const int only = n1 > 0;  // shared key tiles: the second sees them all
+#pragma unroll 1
+        for (int u = 0; u < kAhead; ++u) {
+            const Part x = job.part[apart ? u & 1 : only];
+            ahead(x, apart ? u >> 1 : u);
+        }
+        int j0 = 0, j1 = 0;  // key tiles copied of each
+#pragma unroll 1
+        for (int u = 0; u < all; ++u, ++t) {
+            const int i = apart ? (j1 < n1 && (j0 > j1 || j0 == n0)) : only;
+            const int j = i ? j1++ : j0++;
+            const Part x = job.part[i];
+            ahead(x, j + (apart ? kAhead / 2 : kAhead));
+            const int slot = t % kStages, k = x.k0 + kN * j, kh = x.h * k_step;
             if (t >= kStages && !(ok = all_wait<false>(&mi.k_empty[slot], (t / kStages - 1) & 1, abort))) break;
             if (lead) {
                 if (leader) mbar_arrive_expect_tx(&mi.k_full[slot], 2 * kTileK);
@@ -260,34 +378,25 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const Lat
                 tma_load_3d_pair(dst + kPanelK, &tk, bar, 64, kh, k + 64 * rank);
                 tma_load_3d_pair(dst + 2 * kPanelK, &tp, bar, 0, 0, k + 64 * rank);
             }
-            if (j == 0 && !(ok = queries(0, nq0) && queries(1, nq1))) break;
+            if (u == 0 && !(ok = queries(0, nq0) && queries(1, nq1))) break;
             if (t >= kStages && !(ok = all_wait<false>(&mi.v_empty[slot], (t / kStages - 1) & 1, abort))) break;
             if (lead) {
                 unsigned char *dst = sm + kOffV + slot * kTileV;
-                if (job.tail() && j == nmax - 1) {
+                if (j + 1 == x.n && x.has_tail()) {
                     // each CTA's softmax waits for this part itself (it clears the rows past the end) and
                     // answers for it with its weights
                     if (leader) mbar_arrive(&mi.v_full[slot]);
                     mbar_arrive_expect_tx(&mi.v_tail[slot], kTileV);
-                    tma_load_3d(dst, &tv, &mi.v_tail[slot], 64 * rank, vh, k);
+                    tma_load_3d(dst, &tv, &mi.v_tail[slot], 64 * rank, x.h * v_step, k);
                 } else {
                     if (leader) mbar_arrive_expect_tx(&mi.v_full[slot], 2 * kTileV);
-                    tma_load_3d_pair(dst, &tv, map_to_rank(&mi.v_full[slot], 0), 64 * rank, vh, k);
+                    tma_load_3d_pair(dst, &tv, map_to_rank(&mi.v_full[slot], 0), 64 * rank, x.h * v_step, k);
                 }
             }
         }
         if (!ok) break;
-        if (lead) mbar_arrive_expect_tx(&mi.next_full, 16);
-        if (leader) {
-            if (count > 0 && !(ok = all_wait<true>(&mi.next_empty, (count - 1) & 1, abort))) break;
-            if (lead) cluster_take(&mi.next, &mi.next_full);
-        }
-        __syncwarp();
-        if (!(ok = all_wait<false>(&mi.next_full, count & 1, abort))) break;
-        at = cluster_taken(&mi.next) >> 1;  // (-1 stays -1)
-        fence_proxy_async_smem();           // read before it is written again
-        __syncwarp();
-        if (lead) mbar_arrive_cluster(map_to_rank(&mi.next_empty, 0));
+        if (lead) mbar_arrive(&mi.copied[jobs.count & 1]);
+        jobs.done(lane);
     }
     if (*abort && lead) {  // the copies in flight land before the pair goes (the other CTA stays for this one)
         if (leader) {
@@ -315,13 +424,17 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, i
     int np0 = 0, np1 = 0;        // products O += P V of each query tile so far
     int nj0 = 0, nj1 = 0;        // jobs of each query tile so far
     Jobs jobs(mi);
-    Job job;
-    while (jobs.take(job, lane)) {
-        const int nmax = job.nmax();
-        const bool two = job.n1 > 0;
-        auto k_ready = [&](int j) { return all_wait<true>(&mi.k_full[(t0 + j) % kStages], ((t0 + j) / kStages) & 1, abort); };
+    while (const Job *job = jobs.take()) {
+        const int n0 = job->part[0].n, n1 = job->part[1].n;
+        const bool apart = job->kind == kApart;
+        jobs.done(lane);
+        const bool back0 = apart || n1 == 0;  // a key tile is given back by the last query tile that reads it
+        auto k_ready = [&](int i, int j) {
+            const int t = t0 + place(apart, n0, n1, i, j);
+            return all_wait<true>(&mi.k_full[t % kStages], (t / kStages) & 1, abort);
+        };
         auto scores = [&](int i, int j) {  // S_i of key tile j
-            const int slot = (t0 + j) % kStages;
+            const int slot = (t0 + place(apart, n0, n1, i, j)) % kStages;
             const uint32_t d = tmem + kColS + 128 * i, a = sb + kOffQ + 3 * i * kPanelQ, b = sb + kOffK + slot * kTileK;
 #pragma unroll
             for (int c = 0; c < 3; ++c)
@@ -330,12 +443,12 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, i
                     mma_bf16_pair(lead, d, kdesc(a + c * kPanelQ + k * 32), kdesc(b + c * kPanelK + k * 32), id_s,
                                   c > 0 || k > 0);
             mma_commit_pair(lead, &mi.s_full[i]);
-            if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.k_empty[slot]);
-            if (j + 1 == job.n(i)) mma_commit_pair(lead, &mi.q_empty[i]);
+            if (i == 1 || back0) mma_commit_pair(lead, &mi.k_empty[slot]);
+            if (j + 1 == (i ? n1 : n0)) mma_commit_pair(lead, &mi.q_empty[i]);
         };
         auto step = [&](int i, int j, int &np, int nj) -> bool {  // O_i += P_i V of key tile j, S_i of the next
-            const int t = t0 + j, slot = t % kStages;
-            const bool more = j + 1 < job.n(i);
+            const int t = t0 + place(apart, n0, n1, i, j), slot = t % kStages;
+            const bool more = j + 1 < (i ? n1 : n0);
             if (j == 0 && nj > 0 && !all_wait<true>(&mi.o_empty[i], (nj - 1) & 1, abort)) return false;
             const uint32_t d = tmem + kColO + 128 * i, a = tmem + kColS + 128 * i, b = sb + kOffV + slot * kTileV;
 #pragma unroll
@@ -348,34 +461,34 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, i
                 mma_tmem_a_pair(lead, d, a + 8 * k, sdesc(b + k * 2048, kTileV, 1024, kSw128B), id_o, j > 0 || k > 0);
             }
             ++np;
-            if (i == (two ? 1 : 0)) mma_commit_pair(lead, &mi.v_empty[slot]);
+            if (i == 1 || back0) mma_commit_pair(lead, &mi.v_empty[slot]);
             if (!more) {
                 mma_commit_pair(lead, &mi.o_full[i]);
                 return true;
             }
-            if (!k_ready(j + 1)) return false;
+            if (!k_ready(i, j + 1)) return false;
             tc_fence_after_sync();
             scores(i, j + 1);
             return true;
         };
-        if (job.n0 > 0) {
-            if (!all_wait<true>(&mi.q_full[0], nj0 & 1, abort) || !k_ready(0)) return false;
+        if (n0 > 0) {
+            if (!all_wait<true>(&mi.q_full[0], nj0 & 1, abort) || !k_ready(0, 0)) return false;
             tc_fence_after_sync();
             scores(0, 0);
         }
-        if (two) {
-            if (!all_wait<true>(&mi.q_full[1], nj1 & 1, abort) || !k_ready(0)) return false;
+        if (n1 > 0) {
+            if (!all_wait<true>(&mi.q_full[1], nj1 & 1, abort) || !k_ready(1, 0)) return false;
             tc_fence_after_sync();
             scores(1, 0);
         }
 #pragma unroll 1
-        for (int j = 0; j < nmax; ++j) {
-            if (j < job.n0 && !step(0, j, np0, nj0)) return false;
-            if (j < job.n1 && !step(1, j, np1, nj1)) return false;
+        for (int j = 0; j < max(n0, n1); ++j) {
+            if (j < n0 && !step(0, j, np0, nj0)) return false;
+            if (j < n1 && !step(1, j, np1, nj1)) return false;
         }
-        t0 += nmax;
-        nj0 += job.n0 > 0;
-        nj1 += two;
+        t0 += apart ? n0 + n1 : max(n0, n1);
+        nj0 += n0 > 0;
+        nj1 += n1 > 0;
     }
     return !*abort;
 }
@@ -390,16 +503,16 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
     const uint32_t ts = tmem + kColS + 128 * i + quarter, to = tmem + kColO + 128 * i + quarter;
     const uint32_t p_full = map_to_rank(&mi.p_full[i][0], 0), o_empty = map_to_rank(&mi.o_empty[i], 0);
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-    int ns = 0, nj = 0, t0 = 0;  // score tiles and jobs of this query tile, key tiles so far
-    uint32_t tails = 0;          // parity of the tails so far in each V buffer
+    int ns = 0, nj = 0;  // score tiles and jobs of this query tile
     Jobs jobs(mi);
-    Job job;
-    while (jobs.take(job, lane)) {
-        const int klen = job.klen, n = job.n(i), first = job.first(i, rank) + row;
+    while (const Job *job = jobs.take()) {
+        const Part at = job->part[i];
+        jobs.done(lane);
+        const int klen = at.klen, n = at.n, mine = kM * rank + row;
         // last key this query sees
-        const int last = p.causal ? min(job.off + first, klen - 1) : klen - 1;
+        const int last = p.causal ? min(at.off + mine, klen - 1) : klen - 1;
         // this query's row of the output, or none
-        const int64_t out = first < job.rows ? (int64_t)(job.q0 + first) * p.heads + job.h : -1;
+        const int64_t out = mine < at.rows ? (int64_t)(at.q0 + mine) * p.heads + at.h : -1;
         float m = -INFINITY, l = 0.f;  // held maximum (log2 units) and the sum of the weights
         for (int j = 0; j < n; ++j, ++ns) {
             if (!all_wait<false>(&mi.s_full[i], ns & 1, abort)) return;
@@ -446,8 +559,8 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
                 // keys past the sequence's end are other sequences' rows: their weight is 0, so their values
                 // must be finite
                 if (left < kN) {
-                    const int slot = (t0 + j) % kStages;
-                    if (!all_wait<false>(&mi.v_tail[slot], (tails >> slot) & 1, abort)) return;
+                    const int slot = at.tail & 3;
+                    if (!all_wait<false>(&mi.v_tail[slot], at.tail >> 2, abort)) return;
                     for (int e = row; e < (kN - left) * 8; e += 128)
                         *reinterpret_cast<uint4 *>(sm + kOffV + slot * kTileV + (left + (e >> 3)) * 128 + (e & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
@@ -483,8 +596,6 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
             const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             l += all.x + all.y;
         }
-        if (job.tail()) tails ^= 1u << ((t0 + job.nmax() - 1) % kStages);
-        t0 += job.nmax();
         if (out >= 0 && p.lse) p.lse[out] = m * kLn2 + logf(l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + out * kLatN;
@@ -519,7 +630,7 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
 __global__ void __launch_bounds__(kT, 1)
 latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensorMap tq,
                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tp,
-                         const __grid_constant__ CUtensorMap tv, int q_step, int k_step, int v_step)
+                         const __grid_constant__ CUtensorMap tv, int q_step, int k_step, int v_step, bool beside)
 {
     extern __shared__ __align__(1024) unsigned char sm[];
     Misc &mi = *reinterpret_cast<Misc *>(sm + kOffMisc);
@@ -536,8 +647,7 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
             mbar_init(&mi.s_full[i], 1);
             mbar_init(&mi.p_full[i][0], 8);
             mbar_init(&mi.p_full[i][1], 8);
-            mbar_init(&mi.job_full[i], 1);
-            mbar_init(&mi.job_empty[i], rank == 0 ? 9 : 8);  // warps: softmax, matrix instructions
+            mbar_init(&mi.copied[i], 1);
             mbar_init(&mi.o_full[i], 1);
             mbar_init(&mi.o_empty[i], 8);
         }
@@ -547,6 +657,10 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
             mbar_init(&mi.v_full[i], 1);
             mbar_init(&mi.v_empty[i], 1);
             mbar_init(&mi.v_tail[i], 1);
+        }
+        for (int i = 0; i < kJobs; ++i) {
+            mbar_init(&mi.job_full[i], 1);
+            mbar_init(&mi.job_empty[i], rank == 0 ? 10 : 9);  // warps: softmax, copies, matrix instructions
         }
         mbar_init(&mi.drained, 1);
         mbar_init(&mi.next_full, 1);
@@ -561,14 +675,14 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     pdl_wait();
     tc_fence_after_sync();
     const uint32_t tmem = mi.tmem;
-    // registers: 384 x 168 = 64,512 at launch; 256 x 200 + 128 x 40 = 56,320 now
+    // registers: 384 x 168 = 64,512 at launch; 256 x 200 + 128 x 56 = 58,368 now
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         softmax_role(sm, mi, p, tmem, warp >> 2, rank);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 8) {
-            copy_role(sm, mi, p, tq, tk, tp, tv, q_step, k_step, v_step, rank, lane);
+            copy_role(sm, mi, tq, tk, tp, tv, q_step, k_step, v_step, rank, lane);
         } else if (warp == 9 && rank == 0) {
             // (the reduction's result is uniform to the compiler, the loaded word is not)
             if (!mma_role(smem_u32(sm), mi, __reduce_or_sync(0xffffffffu, tmem), lane)) {
@@ -576,7 +690,9 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
                 mma_commit_pair(lane == 0, &mi.drained);
                 if (lane == 0) mbar_wait_ns(&mi.drained, 0, kWait);
             }
-        } else if (warp == 10 && blockIdx.x == 0) {
+        } else if (warp == 10) {
+            job_role(mi, p, beside, rank, lane);
+        } else if (warp == 11 && blockIdx.x == 0) {
             latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
             latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);
         }
@@ -636,7 +752,7 @@ cudaError_t launch_latent_prefill_tc(const LatentPrefill &p)
     const cudaError_t err = tc::allow_smem(latent_prefill_tc_kernel, kSmem, &configured);
     if (err != cudaSuccess) return err;
     return latent_launch(latent_prefill_tc_kernel, dim3((unsigned)blocks), kT, kSmem, p.stream, 2, p, tq, tk, tp, tv,
-                         q_step, k_step, v_step);
+                         q_step, k_step, v_step, blocks > 152 /* CTAs at once */);
 }
 
 }  // namespace kda

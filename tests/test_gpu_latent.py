@@ -1,6 +1,7 @@
 """Latent attention on the GPU against its definition in float64 (latent_reference.py derives the
 bounds), at the sizes, strides and contents where such kernels go wrong."""
 import math
+import random
 
 import pytest
 import torch
@@ -383,6 +384,21 @@ def test_prefill_many_sequences(heads):
     q, kn, kp, v, cu, _ = prefill_inputs(g, heads, lens, lens, torch.bfloat16)
     o, lse = kda.latent_prefill(q, kn, kp, v, SCALE, cu)
     ref.check(o, lse, ref.prefill(q, kn, kp, v, SCALE, lens, lens, True), "1500 sequences")
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_prefill_short_sequences_side_by_side(causal):
+    """More query tiles than run at once, most of them the only one of their sequence: two such are worked
+    on in turn, with key tiles of their own, whose tails may meet in one buffer."""
+    rnd = random.Random(5)
+    lq = [rnd.choice([0, 1, 17, 64, 200, 256, 300, 512, 700]) for _ in range(70)]
+    lk = [l + rnd.choice([-3, 0, 0, 1, 63, 127, 128, 384, 500, 900]) if l else 0 for l in lq]
+    lk = [max(0, l) for l in lk]
+    q, kn, kp, v, cu_q, cu_k = prefill_inputs(gen(47), 3, lq, lk, torch.bfloat16)
+    err = errors()
+    o, lse = kda.latent_prefill(q, kn, kp, v, SCALE, cu_q, cu_k, causal=causal, errors=err)
+    ref.check(o, lse, ref.prefill(q, kn, kp, v, SCALE, lq, lk, causal), "side by side")
+    assert err.item() == 0
 
 
 def test_prefill_output_aligned_to_16_bytes_only():
