@@ -5,7 +5,9 @@
 //   s_hj = scale q_h . c_j  (576 channels),  o_h = sum_j softmax_j(s_h) c_j[:512],  j < len
 //
 // One pass over the cache rows with a running maximum m and sum l per head (base 2): a tile's rows
-// enter with p = 2^(s - m), and what is held is scaled by 2^(m_old - m) when m rises.
+// enter with p = 2^(s - m), and what is held is scaled by 2^(m_old - m) when m rises.  Bound by the chain of
+// a tile (copy, products, softmax, products) and not by the fp32 rate or HBM: 16 sequences of 1 to 2,048
+// rows, 8 heads, 24.6 us, of which HBM needs 5 and the products 3.6.
 #include <math.h>
 
 #include "latent.cuh"

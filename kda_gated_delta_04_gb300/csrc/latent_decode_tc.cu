@@ -21,7 +21,7 @@
 // in one, pairs of latent panels (read by both products) in the other.  S^T of tile t + 1 is issued
 // before O^T of tile t, so the softmax of one tile runs beside the products of its neighbours, and
 // the rings hold 2 to 2.7 tiles: while one is worked on, the others are in flight (100 KB and more a
-// SM; 45 KB cover HBM's latency at its full rate).
+// SM; 45 KB cover HBM's latency at its full rate).  256 sequences of 1 to 8,192 rows, 32 heads: 217 us, 5.9 TB/s.
 #include <math.h>
 
 #include "latent.cuh"
@@ -607,6 +607,11 @@ cudaError_t launch(const LatentDecode &p, int grid)
 
 // Heads per tile: the smallest of 16, 32 and 64 that holds them all, else tiles of 64 (each reads
 // the cache again, from L2).
+// Heads of a tile: the least power of two that holds them all, since a smaller tile leaves more shared memory
+// to the ring and costs the tensor cores less, and each further tile reads the cache rows once more (from L2).
+// 256 sequences of up to 8,192 rows: 16 heads 210 us in a tile of 16, 216 of 32, 243 of 64; 32 heads 217 in a
+// tile of 32, 249 of 64.  48 of up to 8,192 rows, 128 heads: 117 us in tiles of 64, 175 of 32.  The tile of 64
+// has a ring of two cache tiles, too short to hide a copy's latency: the tensor pipe is 42 % busy.
 int head_tile(int heads) { return heads <= 16 ? 16 : (heads <= 32 ? 32 : 64); }
 
 }  // namespace

