@@ -9,9 +9,10 @@
 // K and V have one buffer each: K of the next tile is copied (cp.async) while the softmax and the value
 // product run, V while the scores do.
 //
-// With fewer query tiles than SMs a cluster of four CTAs shares a query tile, each taking every fourth
-// key tile, and the four results are joined through distributed shared memory (1,027 tokens, 4 heads:
-// 65 us; one CTA a tile: 216).
+// With fewer query tiles than SMs a cluster of two or four CTAs shares a query tile, each taking every
+// second or fourth key tile, and the results are joined through distributed shared memory (1,027 tokens, 4
+// heads, 68 tiles: 60 us with four, 91 with two, 164 with one).  4,096 tokens, 8 heads: 1.1 ms, 39 TFLOP/s:
+// the products take half of the cycles, the reads of their operands from shared memory the rest.
 #include <math.h>
 
 #include "latent.cuh"
@@ -99,7 +100,8 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
     }
     copy_k(first);
     copy_v(first);
-    float m[4], l[4], acc[4][8];
+    float m[4], l[4];
+    alignas(8) float acc[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
@@ -110,7 +112,8 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
     for (int j0 = first; j0 < at.keys; j0 += step) {
         cp_async_wait<1>();  // K (V may still be on its way)
         __syncthreads();
-        float s[4][4] = {};
+        float s[4][4];
+        float2 s2[4][4] = {};  // channels two by two, added at the end
 #pragma unroll 4
         for (int c = 0; c < kLatQK; c += 4) {
             float4 a[4], b[4];
@@ -121,9 +124,15 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
+                for (int j = 0; j < 4; ++j) {
+                    s2[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), s2[i][j]);
+                    s2[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), s2[i][j]);
+                }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
         __syncthreads();  // K is read
         copy_k(j0 + step);
 #pragma unroll
@@ -165,8 +174,12 @@ __global__ void __launch_bounds__(kT, 1) latent_prefill_simt_kernel(const Latent
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
-                    acc[i][0] += x * va.x; acc[i][1] += x * va.y; acc[i][2] += x * va.z; acc[i][3] += x * va.w;
-                    acc[i][4] += x * vb.x; acc[i][5] += x * vb.y; acc[i][6] += x * vb.z; acc[i][7] += x * vb.w;
+                    const float2 xx = make_float2(x, x);
+                    float2 *o = reinterpret_cast<float2 *>(acc[i]);
+                    o[0] = fma2(xx, make_float2(va.x, va.y), o[0]);
+                    o[1] = fma2(xx, make_float2(va.z, va.w), o[1]);
+                    o[2] = fma2(xx, make_float2(vb.x, vb.y), o[2]);
+                    o[3] = fma2(xx, make_float2(vb.z, vb.w), o[3]);
                 }
             }
         }
@@ -251,8 +264,11 @@ cudaError_t launch_latent_prefill_simt(const LatentPrefill &p)
     const int64_t tiles = p.num_seqs == 1 ? (p.q_tokens + kM - 1) / kM : p.q_tokens / kM + p.num_seqs;
     const int64_t units = tiles * p.heads;
     if (4 * units > 0x7fffffff) return cudaErrorInvalidValue;
-    // four CTAs a tile up to two tiles an SM: the longest tile then no longer sets the time
-    return units <= 2 * 152 ? launch<4>(p, units) : launch<1>(p, units);
+    // Four CTAs a tile up to half a tile an SM, two up to one: each CTA costs some 13 us beside its key tiles
+    // (9 us each), one runs on an SM, and with more tiles than SMs they share the time out without it.  136
+    // tiles of 1,027 tokens 98 us with two CTAs, 119 with four, 165 with one; 272 of them 165 with one, 193
+    // with two; 112 tiles of sequences of 1 to 600 tokens 54 with two, 66 with four, 99 with one.
+    return units <= 152 / 2 ? launch<4>(p, units) : units <= 152 ? launch<2>(p, units) : launch<1>(p, units);
 }
 
 }  // namespace kda

@@ -401,6 +401,16 @@ def test_prefill_short_sequences_side_by_side(causal):
     assert err.item() == 0
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("heads", [5, 6, 11, 12])
+def test_prefill_f32_tiles_shared_by_four_two_or_one(heads, causal):
+    """13 query tiles a head: 65 are shared by four CTAs each, 78 and 143 by two, 156 by none."""
+    lq, lk = [5, 0, 130, 1, 300, 64], [5, 7, 200, 0, 310, 60]
+    q, kn, kp, v, cu_q, cu_k = prefill_inputs(gen(48 + heads), heads, lq, lk, torch.float32)
+    o, lse = kda.latent_prefill(q, kn, kp, v, SCALE, cu_q, cu_k, causal=causal)
+    ref.check(o, lse, ref.prefill(q, kn, kp, v, SCALE, lq, lk, causal), "shared tiles")
+
+
 def test_prefill_output_aligned_to_16_bytes_only():
     g = gen(48)
     q, kn, kp, v, cu, _ = prefill_inputs(g, 3, [300], [300], torch.bfloat16)
