@@ -39,22 +39,6 @@ struct Smem {
     float m[kM], l[kM];
 };
 
-// A float of this CTA's shared memory as CTA `rank` of the cluster has it.
-__device__ __forceinline__ float4 peer_load4(const float *p, uint32_t rank)
-{
-    float4 x;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                 : "r"(map_to_rank(p, rank)));
-    return x;
-}
-__device__ __forceinline__ float peer_load(const float *p, uint32_t rank)
-{
-    float x;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_to_rank(p, rank)));
-    return x;
-}
-
 // Threads are 16 x 16: thread (ty, tx) has queries 4 ty .. 4 ty + 3, and keys tx + 16 j or output
 // channels 4 tx + 64 j.  The 16 threads of a query row are half a warp.  CS: CTAs per query tile.
 template <int CS>

@@ -19,6 +19,8 @@
 // Tensor memory is full: two O, two S of 128 columns.  The two query tiles take turns: while one
 // tile's softmax runs (a warpgroup each, a thread per query, so that maximum and sum need no other
 // thread), the tensor cores run the other tile's products, O += P V of key tile j and S of j + 1.
+// Where there are few jobs and many keys, two or four pairs (one cluster) share the keys of a job and join their
+// parts through distributed shared memory.
 // Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10: the jobs; 11: a check of the
 // offsets (first CTA).
 //
@@ -207,16 +209,17 @@ struct Jobs {
 // at once), since alone it leaves the tensor cores to wait for its softmax and the other way round: 64
 // prompts of 150 to 250 tokens, 16 heads, 71 us instead of 97; 300 of 10 to 30 tokens 182 instead of 302.
 // Both CTAs of the pair come to the same jobs.
-__device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool beside, int rank, int lane)
+template <int SPLIT>
+__device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool beside, int rank, int team, int lane)
 {
     volatile int *abort = &mi.abort;
     const bool lead = lane == 0, leader = rank == 0;
     int t = 0, asked = 0;       // key tiles of the jobs before, numbers asked for so far
-    int at = blockIdx.x >> 1;   // the number at hand; -1: there is none left
+    int at = blockIdx.x / (2 * SPLIT);  // the number at hand; -1: there is none left
     bool used = false;          // it is in a job already
     uint32_t tails = 0;         // parity of the tails so far in each V buffer
     const LatentLane mine = latent_lane(p, kPairM, lane);
-    const int tiles = (int)(gridDim.x >> 1) / p.heads;
+    const int tiles = (int)(gridDim.x / (2 * SPLIT)) / p.heads;
     const uint32_t inverse = 0xffffffffu / (uint32_t)p.heads;
     for (int count = 0;; ++count) {
         Job &job = mi.job[count % kJobs];
@@ -224,7 +227,8 @@ __device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool 
         int kind = kDone, n0 = 0, n1 = 0;
         bool tail0 = false, tail1 = false;
         for (;;) {
-            if (used && at >= 0) {
+            if (SPLIT > 1 && used) at = -1;
+            if (SPLIT == 1 && used && at >= 0) {
                 if (lead) mbar_arrive_expect_tx(&mi.next_full, 16);
                 if (leader) {
                     if (asked > 0 && !all_wait<true>(&mi.next_empty, (asked - 1) & 1, abort)) return;
@@ -242,6 +246,17 @@ __device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool 
             if (at < 0) break;
             Part part[2];
             make_parts(p, mine, tiles, inverse, at, lane, part);
+            if constexpr (SPLIT > 1) {  // this pair's key tiles
+                const int n = max(part[0].n, part[1].n), from = n * team / SPLIT, to = n * (team + 1) / SPLIT;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    Part &x = part[i];
+                    x.n = max(0, min(to, x.n) - from);
+                    x.k0 += from * kN;
+                    x.klen -= from * kN;
+                    x.off -= from * kN;
+                }
+            }
             const bool lone = beside && part[1].rows == 0;
             if (part[0].rows == 0) {
                 used = true;
@@ -297,7 +312,7 @@ __device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool 
 // One warp of each CTA: copies the tiles of the jobs.
 __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const CUtensorMap &tq, const CUtensorMap &tk,
                                           const CUtensorMap &tp, const CUtensorMap &tv, int q_step, int k_step,
-                                          int v_step, int rank, int lane)
+                                          int v_step, int rank, int home, int lane)
 {
     volatile int *abort = &mi.abort;
     const bool lead = lane == 0, leader = rank == 0;
@@ -322,7 +337,7 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const CUt
             if (nq > 0 && !all_wait<false>(&mi.q_empty[i], (nq - 1) & 1, abort)) return false;
             if (lead) {
                 if (leader) mbar_arrive_expect_tx(&mi.q_full[i], 2 * 3 * kPanelQ);
-                const uint32_t bar = map_to_rank(&mi.q_full[i], 0);
+                const uint32_t bar = map_to_rank(&mi.q_full[i], home);
 #pragma unroll
                 for (int c = 0; c < 3; ++c)
                     tma_load_3d_pair(sm + kOffQ + (3 * i + c) * kPanelQ, &tq, bar, 64 * c, x.h * q_step, x.q0 + kM * rank);
@@ -356,7 +371,7 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const CUt
             if (t >= kStages && !(ok = all_wait<false>(&mi.k_empty[slot], (t / kStages - 1) & 1, abort))) break;
             if (lead) {
                 if (leader) mbar_arrive_expect_tx(&mi.k_full[slot], 2 * kTileK);
-                const uint32_t bar = map_to_rank(&mi.k_full[slot], 0);
+                const uint32_t bar = map_to_rank(&mi.k_full[slot], home);
                 unsigned char *dst = sm + kOffK + slot * kTileK;
                 tma_load_3d_pair(dst, &tk, bar, 0, kh, k + 64 * rank);
                 tma_load_3d_pair(dst + kPanelK, &tk, bar, 64, kh, k + 64 * rank);
@@ -374,7 +389,7 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const CUt
                     tma_load_3d(dst, &tv, &mi.v_tail[slot], 64 * rank, x.h * v_step, k);
                 } else {
                     if (leader) mbar_arrive_expect_tx(&mi.v_full[slot], 2 * kTileV);
-                    tma_load_3d_pair(dst, &tv, map_to_rank(&mi.v_full[slot], 0), 64 * rank, x.h * v_step, k);
+                    tma_load_3d_pair(dst, &tv, map_to_rank(&mi.v_full[slot], home), 64 * rank, x.h * v_step, k);
                 }
             }
         }
@@ -399,7 +414,7 @@ __device__ __forceinline__ void copy_role(unsigned char *sm, Misc &mi, const CUt
 // One warp of the leading CTA, in step: for each key tile and query tile in turn O += P V, then S of the
 // next key tile.  (A warp for each query tile: 6% slower; both tiles' softmax then run at the same time and
 // share the exponential units.)
-__device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, int lane)
+__device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, uint32_t pair, int lane)
 {
     constexpr uint32_t id_s = idesc_bf16(2 * kM, kN, false, false), id_o = idesc_bf16(2 * kM, 128, false, true);
     volatile int *abort = &mi.abort;
@@ -426,9 +441,9 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, i
                 for (int k = 0; k < 4; ++k)
                     mma_bf16_pair(lead, d, kdesc(a + c * kPanelQ + k * 32), kdesc(b + c * kPanelK + k * 32), id_s,
                                   c > 0 || k > 0);
-            mma_commit_pair(lead, &mi.s_full[i]);
-            if (i == 1 || back0) mma_commit_pair(lead, &mi.k_empty[slot]);
-            if (j + 1 == (i ? n1 : n0)) mma_commit_pair(lead, &mi.q_empty[i]);
+            mma_commit_pair(lead, &mi.s_full[i], pair);
+            if (i == 1 || back0) mma_commit_pair(lead, &mi.k_empty[slot], pair);
+            if (j + 1 == (i ? n1 : n0)) mma_commit_pair(lead, &mi.q_empty[i], pair);
         };
         auto step = [&](int i, int j, int &np, int nj) -> bool {  // O_i += P_i V of key tile j, S_i of the next
             const int t = t0 + place(apart, n0, n1, i, j), slot = t % kStages;
@@ -445,9 +460,9 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, i
                 mma_tmem_a_pair(lead, d, a + 8 * k, sdesc(b + k * 2048, kTileV, 1024, kSw128B), id_o, j > 0 || k > 0);
             }
             ++np;
-            if (i == 1 || back0) mma_commit_pair(lead, &mi.v_empty[slot]);
+            if (i == 1 || back0) mma_commit_pair(lead, &mi.v_empty[slot], pair);
             if (!more) {
-                mma_commit_pair(lead, &mi.o_full[i]);
+                mma_commit_pair(lead, &mi.o_full[i], pair);
                 return true;
             }
             if (!k_ready(i, j + 1)) return false;
@@ -477,15 +492,22 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, i
     return !*abort;
 }
 
+// What a thread has of its query's softmax at the end; any: there were keys.
+struct Held {
+    float m, l;
+    bool any;
+};
+
 // A warpgroup of each CTA per query tile, a thread per query.
+template <int SPLIT>
 __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const LatentPrefill &p, uint32_t tmem, int i,
-                                             int rank)
+                                             int rank, int home, Held &held)
 {
     volatile int *abort = &mi.abort;
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t quarter = (uint32_t)((row >> 5) * 32) << 16;
     const uint32_t ts = tmem + kColS + 128 * i + quarter, to = tmem + kColO + 128 * i + quarter;
-    const uint32_t p_full = map_to_rank(&mi.p_full[i][0], 0), o_empty = map_to_rank(&mi.o_empty[i], 0);
+    const uint32_t p_full = map_to_rank(&mi.p_full[i][0], home), o_empty = map_to_rank(&mi.o_empty[i], home);
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
     int ns = 0, nj = 0;  // score tiles and jobs of this query tile
     Jobs jobs(mi);
@@ -580,6 +602,11 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
             const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
             l += all.x + all.y;
         }
+        if constexpr (SPLIT > 1) {  // the only job: what it leaves is joined by all
+            held = Held{m, l, n > 0};
+            if (n > 0) all_wait<false>(&mi.o_full[i], 0, abort);
+            return;
+        }
         if (out >= 0 && p.lse) p.lse[out] = m * kLn2 + logf(l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + out * kLatN;
@@ -611,6 +638,67 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
     }
 }
 
+// The pairs of a cluster that had a share of the keys each: their unnormalised outputs (fp32) and sums, over
+// the tiles' buffers (256 rows of 512 bytes, the 16-byte pieces of a row in an order that spreads a column's
+// over the banks; then maximum and sum of each row), and their join.  The warps of the softmax.
+__device__ __forceinline__ void put_part(unsigned char *sm, uint32_t tmem, int i, int row, const Held &held)
+{
+    const uint32_t to = tmem + kColO + 128 * i + ((uint32_t)((row >> 5) * 32) << 16);
+    unsigned char *o = sm + (128 * i + row) * 512;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float x[32] = {};
+        if (held.any) {
+            tmem_ld32(to + 32 * c, x);
+            tmem_ld_wait();
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4 *>(o + (((8 * c + k) ^ (row & 31)) << 4)) =
+                make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+    }
+    *reinterpret_cast<float2 *>(sm + 256 * 512 + (128 * i + row) * 8) = make_float2(held.m, held.l);
+}
+template <int SPLIT>
+__device__ __forceinline__ void join_parts(const unsigned char *sm, const Misc &mi, const LatentPrefill &p, int rank,
+                                           int team, int warp, int lane)
+{
+    if (mi.job[0].kind == kDone) return;
+    constexpr int kShare = 256 / SPLIT;  // rows that this CTA writes
+#pragma unroll 1
+    for (int r = team * kShare + warp; r < (team + 1) * kShare; r += 8) {
+        const Part &x = mi.job[0].part[r >> 7];
+        const int mine = kM * rank + (r & 127);
+        if (mine >= x.rows) continue;
+        const float *stats = reinterpret_cast<const float *>(sm + 256 * 512 + r * 8);
+        const float *o = reinterpret_cast<const float *>(sm + r * 512 + ((lane ^ (r & 31)) << 4));
+        float m[SPLIT], top = -INFINITY, l = 0.f;
+        float4 part[SPLIT], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < SPLIT; ++u) {
+            m[u] = peer_load(stats, 2 * u + rank);
+            part[u] = peer_load4(o, 2 * u + rank);
+            top = fmaxf(top, m[u]);
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int u = 0; u < SPLIT; ++u) {
+            const float f = exp2f(m[u] - base);
+            l += f * peer_load(stats + 1, 2 * u + rank);
+            sum.x += f * part[u].x; sum.y += f * part[u].y; sum.z += f * part[u].z; sum.w += f * part[u].w;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t out = (int64_t)(x.q0 + mine) * p.heads + x.h;
+        uint2 w;
+        w.x = tc::pack_bf16x2(sum.x * inv, sum.y * inv);
+        w.y = tc::pack_bf16x2(sum.z * inv, sum.w * inv);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + out * kLatN + 4 * lane) = w;
+        if (p.lse && lane == 0) p.lse[out] = top * kLn2 + logf(l);
+    }
+}
+
+// SPLIT: pairs (in a cluster) that share a job's keys.
+template <int SPLIT>
 __global__ void __launch_bounds__(kT, 1)
 latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensorMap tq,
                          const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tp,
@@ -619,7 +707,8 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     extern __shared__ __align__(1024) unsigned char sm[];
     Misc &mi = *reinterpret_cast<Misc *>(sm + kOffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = (int)cluster_rank();
+    const int place = (int)cluster_rank(), rank = place & 1;
+    const int team = place >> 1, home = SPLIT > 1 ? place & ~1 : 0;  // which pair; its leading CTA
     if (smem_u32(sm) & 1023u) {    // the swizzled panels need it; never seen
         if (tid == 0 && p.errors) atomicOr(p.errors, DEV_ERR_TIMEOUT);
         return;
@@ -662,23 +751,39 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
     // registers: 384 x 168 = 64,512 at launch; 256 x 200 + 128 x 56 = 58,368 now
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        softmax_role(sm, mi, p, tmem, warp >> 2, rank);
+        Held held;
+        softmax_role<SPLIT>(sm, mi, p, tmem, warp >> 2, rank, home, held);
+        if constexpr (SPLIT > 1) {
+            __syncwarp();
+            __syncthreads();  // both query tiles' products are done
+            tc_fence_after_sync();
+            const bool whole = mi.job[0].kind != kDone && !mi.abort;
+            if (whole) put_part(sm, tmem, warp >> 2, tid & 127, held);
+            __syncwarp();
+            cluster_sync();
+            if (whole) join_parts<SPLIT>(sm, mi, p, rank, team, warp, lane);
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 8) {
-            copy_role(sm, mi, tq, tk, tp, tv, q_step, k_step, v_step, rank, lane);
+            copy_role(sm, mi, tq, tk, tp, tv, q_step, k_step, v_step, rank, home, lane);
         } else if (warp == 9 && rank == 0) {
             // (the reduction's result is uniform to the compiler, the loaded word is not)
-            if (!mma_role(smem_u32(sm), mi, __reduce_or_sync(0xffffffffu, tmem), lane)) {
+            if (!mma_role(smem_u32(sm), mi, __reduce_or_sync(0xffffffffu, tmem), 3u << home, lane)) {
                 // nothing in flight when tensor memory is given back
-                mma_commit_pair(lane == 0, &mi.drained);
+                mma_commit_pair(lane == 0, &mi.drained, 3u << home);
                 if (lane == 0) mbar_wait_ns(&mi.drained, 0, kWait);
             }
         } else if (warp == 10) {
-            job_role(mi, p, beside, rank, lane);
+            job_role<SPLIT>(mi, p, beside, rank, team, lane);
         } else if (warp == 11 && blockIdx.x == 0) {
             latent_check_cu(p.cu_q, p.num_seqs, p.q_tokens, p.errors);
             latent_check_cu(p.cu_k, p.num_seqs, p.k_tokens, p.errors);
+        }
+        if constexpr (SPLIT > 1) {
+            __syncwarp();
+            __syncthreads();
+            cluster_sync();
         }
     }
     __syncwarp();
@@ -713,6 +818,18 @@ bool make_map(CUtensorMap *m, const void *ptr, int channels, int64_t heads, int6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Pairs that share a job's keys: as many as leave every cluster an SM for each of its CTAs at once (15
+// clusters of eight CTAs or 36 of four do), where the share saves more than the larger cluster and the join
+// cost, 4 us.  512 queries behind 7,500 keys, us with one, two, four pairs: 15 heads 101, 63, 39; 16 heads 101,
+// 63, 73; 36 heads 103, 67, 114; 37 heads 103, 125, 114.  512 queries, 8 heads: no keys before them (4 tiles)
+// 15.5, 17.5, 13.8; 64 queries 9.4, 13.1, 13.5; 1,000 before 512 queries, 16 heads, 28, 26, 36; 512 before
+// them 21.7, 22.3, 31.
+int key_split(const LatentPrefill &p, int64_t jobs)
+{
+    const int64_t tiles = p.k_tokens / p.num_seqs / kN;  // key tiles of a sequence, on average
+    return jobs <= 15 && tiles >= 4 ? 4 : jobs <= 36 && tiles >= 10 ? 2 : 1;
+}
+
 }  // namespace
 
 cudaError_t launch_latent_prefill_tc(const LatentPrefill &p)
@@ -732,11 +849,17 @@ cudaError_t launch_latent_prefill_tc(const LatentPrefill &p)
         !make_map(&tp, kp, kLatP, 1, 0, tokens, p.kp_ts, 64, &one) ||
         !make_map(&tv, v, kLatN, p.heads, p.v_hs, tokens, p.v_ts, kN, &v_step))
         return cudaErrorInvalidValue;
-    static int configured = -1;
-    const cudaError_t err = tc::allow_smem(latent_prefill_tc_kernel, kSmem, &configured);
-    if (err != cudaSuccess) return err;
-    return latent_launch(latent_prefill_tc_kernel, dim3((unsigned)blocks), kT, kSmem, p.stream, 2, p, tq, tk, tp, tv,
-                         q_step, k_step, v_step, blocks > 152 /* CTAs at once */);
+    auto launch = [&](auto kernel, int split, int *configured) -> cudaError_t {
+        const cudaError_t err = tc::allow_smem(kernel, kSmem, configured);
+        if (err != cudaSuccess) return err;
+        return latent_launch(kernel, dim3((unsigned)(blocks * split)), kT, kSmem, p.stream, 2 * split, p, tq, tk, tp, tv,
+                             q_step, k_step, v_step, blocks > 152 /* CTAs at once */);
+    };
+    static int set1 = -1, set2 = -1, set4 = -1;
+    const int split = key_split(p, tiles * p.heads);
+    return split == 4   ? launch(latent_prefill_tc_kernel<4>, 4, &set4)
+           : split == 2 ? launch(latent_prefill_tc_kernel<2>, 2, &set2)
+                        : launch(latent_prefill_tc_kernel<1>, 1, &set1);
 }
 
 }  // namespace kda

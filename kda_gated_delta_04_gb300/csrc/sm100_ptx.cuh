@@ -505,6 +505,22 @@ __device__ __forceinline__ uint32_t map_to_rank(const void *p, uint32_t rank)
     return r;
 }
 
+// Floats of this CTA's shared memory as CTA `rank` of the cluster has it.
+__device__ __forceinline__ float4 peer_load4(const float *p, uint32_t rank)
+{
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(map_to_rank(p, rank)));
+    return x;
+}
+__device__ __forceinline__ float peer_load(const float *p, uint32_t rank)
+{
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_to_rank(p, rank)));
+    return x;
+}
+
 // Arrive on a barrier of the cluster.  Orders what tensor memory holds (after tc_fence_before_sync);
 // a release of shared-memory writes to the other CTA needs fence_cluster before it (a release at
 // cluster scope in the arrival itself costs 400 to 600 cycles whether or not there is anything to
@@ -554,7 +570,7 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 }
 
 // As mma_bf16_lead, mma_tmem_a_lead and mma_commit_lead, for the pair; the commit arrives on the
-// barrier of that offset in both CTAs.
+// barrier of that offset in both CTAs (mask: the CTAs of the cluster that are the pair).
 __device__ __forceinline__ void mma_bf16_pair(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate)
 {
@@ -575,13 +591,13 @@ __device__ __forceinline__ void mma_tmem_a_pair(uint32_t lead, uint32_t d_tmem, 
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit_pair(uint32_t lead, uint64_t *bar)
+__device__ __forceinline__ void mma_commit_pair(uint32_t lead, uint64_t *bar, uint32_t mask = 3)
 {
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
         "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::
             "r"(smem_u32(bar)),
-        "r"(lead), "h"((uint16_t)3)
+        "r"(lead), "h"((uint16_t)mask)
         : "memory");
 }
 

@@ -411,6 +411,41 @@ def test_prefill_f32_tiles_shared_by_four_two_or_one(heads, causal):
     ref.check(o, lse, ref.prefill(q, kn, kp, v, SCALE, lq, lk, causal), "shared tiles")
 
 
+# few queries behind many keys: the keys of a query tile are shared by several pairs of CTAs
+SPLIT = [
+    ("one_query", 1, [1], [1100]), ("chunk", 2, [300], [2000]), ("two_tiles", 3, [700], [1500]),
+    ("ragged", 2, [1, 600, 0, 40], [1500, 3001, 900, 5]), ("no_keys", 2, [9, 70, 3], [0, 6000, 2]),
+    ("fewer_keys", 2, [2100], [1700]), ("half_as_many", 20, [40], [1300]), ("thirty", 30, [513], [1409]),
+    ("all_in_one_tile", 1, [64, 64], [2100, 60]), ("ragged_two", 4, [1, 600, 0, 40], [1500, 3001, 900, 5]),
+    ("two_by_two", 17, [513], [1409]),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("name,heads,lq,lk", SPLIT, ids=[c[0] for c in SPLIT])
+def test_prefill_shared_keys(causal, name, heads, lq, lk):
+    q, kn, kp, v, cu_q, cu_k = prefill_inputs(gen(60 + heads), heads, lq, lk, torch.bfloat16)
+    err = errors()
+    o, lse = kda.latent_prefill(q, kn, kp, v, SCALE, cu_q, cu_k, causal=causal, errors=err)
+    ref.check(o, lse, ref.prefill(q, kn, kp, v, SCALE, lq, lk, causal), name)
+    assert err.item() == 0
+    for _ in range(3):
+        again, lse2 = kda.latent_prefill(q, kn, kp, v, SCALE, cu_q, cu_k, causal=causal)
+        assert torch.equal(o.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+
+
+def test_prefill_shared_keys_next_to_nan():
+    """Sequences of NaN and infinity on both sides: the shares of the one between them see none of it."""
+    lq, lk = [50, 91, 70], [1000, 1301, 1200]
+    q, kn, kp, v, cu_q, cu_k = prefill_inputs(gen(59), 2, lq, lk, torch.bfloat16)
+    qs, ks = slice(50, 141), slice(1000, 2301)
+    want = ref.prefill(q[qs], kn[ks], kp[ks], v[ks], SCALE, [91], [1301], True)
+    for t, at in ((q, qs), (kn, ks), (kp, ks), (v, ks)):
+        t[:at.start], t[at.stop:] = math.nan, math.inf
+    o, lse = kda.latent_prefill(q, kn, kp, v, SCALE, cu_q, cu_k)
+    ref.check(o[qs], lse[qs], want, "between")
+
+
 def test_prefill_output_aligned_to_16_bytes_only():
     g = gen(48)
     q, kn, kp, v, cu, _ = prefill_inputs(g, 3, [300], [300], torch.bfloat16)
