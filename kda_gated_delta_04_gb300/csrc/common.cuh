@@ -15,9 +15,7 @@ enum : uint32_t {
     DEV_ERR_TIMEOUT = 2u,  // a bounded mbarrier / flag wait gave up
     DEV_ERR_DECAY = 4u,    // |in-chunk cumulative log-decay| exceeded the supported range
     DEV_ERR_RANGE = 8u,    // a value kept in fp16 left the fp16 range
-    DEV_ERR_SLOT = 16u,    // a state- or cache-slot index outside [0, num_slots)
-    DEV_ERR_POSITION = 32u,  // a position outside the rotation table
-    DEV_ERR_PAGE = 64u,    // a page index outside the latent cache
+    DEV_ERR_SLOT = 16u,    // a state-slot index outside [0, num_slots)
 };
 
 constexpr int kChunk = KDA_CHUNK;

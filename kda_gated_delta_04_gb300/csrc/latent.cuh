@@ -7,6 +7,12 @@
 
 namespace kda {
 
+// Device-side error bits beside those of common.cuh.
+enum : uint32_t {
+    DEV_ERR_POSITION = 32u,  // a position outside the rotation table
+    DEV_ERR_PAGE = 64u,      // a page index outside the latent cache
+};
+
 // The supported widths (other values are refused by the entry points).
 constexpr int kLatR = KDA_LATENT_DIM;         // latent channels; the values of the absorbed form
 constexpr int kLatP = KDA_LATENT_PE_DIM;      // position channels

@@ -14,7 +14,7 @@
 // two units ahead and the rows one: 32,768 tokens of 32 heads 68 us (386 MB, 5.6 TB/s), 64 tokens 2.8.  A
 // warp a unit and CTA took 72 and was bound by the launching of CTAs, 0.6 ns each.
 #include "latent.cuh"
-#include "sm100_ptx.cuh"
+#include "latent_ptx.cuh"
 
 namespace kda {
 namespace {

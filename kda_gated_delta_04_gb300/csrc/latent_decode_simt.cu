@@ -11,7 +11,7 @@
 #include <math.h>
 
 #include "latent.cuh"
-#include "sm100_ptx.cuh"
+#include "latent_ptx.cuh"
 
 namespace kda {
 namespace {

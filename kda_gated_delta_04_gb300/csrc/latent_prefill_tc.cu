@@ -28,6 +28,7 @@
 #include <math.h>
 
 #include "latent.cuh"
+#include "latent_ptx.cuh"
 #include "tc_common.cuh"
 
 namespace kda {
