@@ -72,7 +72,9 @@ struct alignas(16) Part {
 enum : int { kDone = 0, kShared = 1, kApart = 2 };
 struct Job {
     Part part[2];
-    int kind, unused[3];
+    int kind;
+    int base[2];  // + j: key tile j of all jobs, where the query tile is alone (see alone_from)
+    int unused;
 };
 
 // Place of key tile j of query tile i among the job's key tiles.
@@ -81,12 +83,19 @@ __device__ __forceinline__ int place(bool apart, int n0, int n1, int i, int j)
     return !apart ? j : (i ? j + min(j + 1, n0) : j + min(j, n1));
 }
 
+// Where a query tile's key tiles outnumber the other's, S goes to the other's buffer and the own one in turn
+// from this key tile on, a key tile ahead, so that it is computed while the softmax before it runs: by then the
+// other's last product has been issued, and what a tile alone would wait for is half of its time.  256 queries
+// behind 15,000 keys, 8 heads: 36 us, with one buffer 49; 4 times 200 behind 3,000 32, with one 45.
+__device__ __forceinline__ int alone_from(int i, int n0, int n1) { return i ? n0 + 1 : n1 + 2; }
+__device__ __forceinline__ bool in_other(int alone, int j) { return j >= alone && !((j - alone) & 1); }
+
 // Barriers of the leading CTA only: q_full, k_full, v_full (bytes that both CTAs copy), p_full,
 // o_empty and next_empty (a warp's arrival each, both CTAs).  The others each CTA has for itself; what the matrix
 // instructions signal arrives in both.
 struct Misc {
     uint64_t q_full[2], q_empty[2], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], v_tail[kStages], drained;
+    uint64_t s_full[2], s_other[2], p_full[2][4], o_full[2], o_empty[2], v_tail[kStages], drained;
     uint64_t next_full, next_empty;  // the number asked for: each CTA; both CTAs have read it, in the leading one
     uint64_t job_full[kJobs], job_empty[kJobs], copied[2];  // copied: all of a job's tiles
     alignas(16) uint4 next;
@@ -298,11 +307,13 @@ __device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool 
                 if (apart || one || n1 == 0) tails ^= 1u << slot;
             }
         }
-        t += all;
         if (lead) {
             job.kind = kind;
+            job.base[0] = t + (apart ? n1 : 0);
+            job.base[1] = t + (apart ? n0 : 0);
             mbar_arrive(&mi.job_full[count % kJobs]);
         }
+        t += all;
         __syncwarp();
         if (kind == kDone) return;
         if (count > 0 && !all_wait<false>(&mi.copied[(count - 1) & 1], ((count - 1) >> 1) & 1, abort)) return;
@@ -421,7 +432,8 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, u
     volatile int *abort = &mi.abort;
     const uint32_t lead = elect_lead();
     int t0 = 0;                  // key tiles of the jobs before
-    int np0 = 0, np1 = 0;        // products O += P V of each query tile so far
+    int np0 = 0, np1 = 0;        // products O += P V of each query tile so far, P in its own buffer
+    int nother0 = 0, nother1 = 0;  // and in the other's
     int nj0 = 0, nj1 = 0;        // jobs of each query tile so far
     Jobs jobs(mi);
     while (const Job *job = jobs.take()) {
@@ -435,40 +447,46 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, u
         };
         auto scores = [&](int i, int j) {  // S_i of key tile j
             const int slot = (t0 + place(apart, n0, n1, i, j)) % kStages;
-            const uint32_t d = tmem + kColS + 128 * i, a = sb + kOffQ + 3 * i * kPanelQ, b = sb + kOffK + slot * kTileK;
+            const bool other = in_other(alone_from(i, n0, n1), j);
+            const uint32_t d = tmem + kColS + 128 * (i ^ (int)other), a = sb + kOffQ + 3 * i * kPanelQ;
+            const uint32_t b = sb + kOffK + slot * kTileK;
 #pragma unroll
             for (int c = 0; c < 3; ++c)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_bf16_pair(lead, d, kdesc(a + c * kPanelQ + k * 32), kdesc(b + c * kPanelK + k * 32), id_s,
                                   c > 0 || k > 0);
-            mma_commit_pair(lead, &mi.s_full[i], pair);
+            mma_commit_pair(lead, other ? &mi.s_other[i] : &mi.s_full[i], pair);
             if (i == 1 || back0) mma_commit_pair(lead, &mi.k_empty[slot], pair);
             if (j + 1 == (i ? n1 : n0)) mma_commit_pair(lead, &mi.q_empty[i], pair);
         };
-        auto step = [&](int i, int j, int &np, int nj) -> bool {  // O_i += P_i V of key tile j, S_i of the next
-            const int t = t0 + place(apart, n0, n1, i, j), slot = t % kStages;
-            const bool more = j + 1 < (i ? n1 : n0);
+        auto step = [&](int i, int j, int &np, int &nother, int nj, int &next) -> bool {
+            // O_i += P_i V of key tile j, S_i of the next (alone: the next two)
+            const int t = t0 + place(apart, n0, n1, i, j), slot = t % kStages, alone = alone_from(i, n0, n1);
+            const int n = i ? n1 : n0;
+            const bool other = in_other(alone, j);
+            const uint32_t parity = (other ? nother++ : np++) & 1;
             if (j == 0 && nj > 0 && !all_wait<true>(&mi.o_empty[i], (nj - 1) & 1, abort)) return false;
-            const uint32_t d = tmem + kColO + 128 * i, a = tmem + kColS + 128 * i, b = sb + kOffV + slot * kTileV;
+            const uint32_t d = tmem + kColO + 128 * i, a = tmem + kColS + 128 * (i ^ (int)other);
+            const uint32_t b = sb + kOffV + slot * kTileV;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 if (k == 0 && !all_wait<true>(&mi.v_full[slot], (t / kStages) & 1, abort)) return false;
                 if ((k & 3) == 0) {  // a half of the keys
-                    if (!all_wait<true>(&mi.p_full[i][k >> 2], np & 1, abort)) return false;
+                    if (!all_wait<true>(&mi.p_full[i][2 * (int)other + (k >> 2)], parity, abort)) return false;
                     tc_fence_after_sync();
                 }
                 mma_tmem_a_pair(lead, d, a + 8 * k, sdesc(b + k * 2048, kTileV, 1024, kSw128B), id_o, j > 0 || k > 0);
             }
-            ++np;
             if (i == 1 || back0) mma_commit_pair(lead, &mi.v_empty[slot], pair);
-            if (!more) {
-                mma_commit_pair(lead, &mi.o_full[i], pair);
-                return true;
+            if (j + 1 == n) mma_commit_pair(lead, &mi.o_full[i], pair);
+            const int to = min(n, j + 2 >= alone ? j + 3 : j + 2);
+#pragma unroll 1
+            for (; next < to; ++next) {
+                if (!k_ready(i, next)) return false;
+                tc_fence_after_sync();
+                scores(i, next);
             }
-            if (!k_ready(i, j + 1)) return false;
-            tc_fence_after_sync();
-            scores(i, j + 1);
             return true;
         };
         if (n0 > 0) {
@@ -481,10 +499,11 @@ __device__ __forceinline__ bool mma_role(uint32_t sb, Misc &mi, uint32_t tmem, u
             tc_fence_after_sync();
             scores(1, 0);
         }
+        int next0 = 1, next1 = 1;  // scores issued so far
 #pragma unroll 1
         for (int j = 0; j < max(n0, n1); ++j) {
-            if (j < n0 && !step(0, j, np0, nj0)) return false;
-            if (j < n1 && !step(1, j, np1, nj1)) return false;
+            if (j < n0 && !step(0, j, np0, nother0, nj0, next0)) return false;
+            if (j < n1 && !step(1, j, np1, nother1, nj1, next1)) return false;
         }
         t0 += apart ? n0 + n1 : max(n0, n1);
         nj0 += n0 > 0;
@@ -507,13 +526,14 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
     volatile int *abort = &mi.abort;
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t quarter = (uint32_t)((row >> 5) * 32) << 16;
-    const uint32_t ts = tmem + kColS + 128 * i + quarter, to = tmem + kColO + 128 * i + quarter;
+    const uint32_t to = tmem + kColO + 128 * i + quarter;
     const uint32_t p_full = map_to_rank(&mi.p_full[i][0], home), o_empty = map_to_rank(&mi.o_empty[i], home);
     const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-    int ns = 0, nj = 0;  // score tiles and jobs of this query tile
+    int ns = 0, nother = 0, nj = 0;  // score tiles in its own and in the other's buffer, jobs of this query tile
     Jobs jobs(mi);
     while (const Job *job = jobs.take()) {
         const Part at = job->part[i];
+        const int alone = alone_from(i, job->part[0].n, job->part[1].n), base = job->base[i];
         jobs.done(lane);
         const int klen = at.klen, n = at.n, mine = kM * rank + row;
         // last key this query sees
@@ -521,8 +541,10 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
         // this query's row of the output, or none
         const int64_t out = mine < at.rows ? (int64_t)(at.q0 + mine) * p.heads + at.h : -1;
         float m = -INFINITY, l = 0.f;  // held maximum (log2 units) and the sum of the weights
-        for (int j = 0; j < n; ++j, ++ns) {
-            if (!all_wait<false>(&mi.s_full[i], ns & 1, abort)) return;
+        for (int j = 0; j < n; ++j) {
+            const bool other = in_other(alone, j);
+            const uint32_t ts = tmem + kColS + 128 * (i ^ (int)other) + quarter;
+            if (!all_wait<false>(other ? &mi.s_other[i] : &mi.s_full[i], (other ? nother++ : ns++) & 1, abort)) return;
             tc_fence_after_sync();
             float s[128];
 #pragma unroll
@@ -551,8 +573,12 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
                     m = mx;
                     l *= f;
                 }
-                // what O holds follows (its last product finished before this S did)
+                // what O holds follows (its last product finished before this S did, but for a tile that is alone:
+                // there the product's end gives its V buffer back)
                 if (j > 0 && __any_sync(0xffffffffu, rise)) {
+                    const int t = base + j - 1;
+                    if (j >= alone && !all_wait<false>(&mi.v_empty[t % kStages], (t / kStages) & 1, abort)) return;
+                    tc_fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 16) {
                         float x[16];
@@ -594,7 +620,7 @@ __device__ __forceinline__ void softmax_role(unsigned char *sm, Misc &mi, const 
                     tmem_st_wait();
                     tc_fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(p_full + 8 * (c >> 1));
+                    if (lane == 0) mbar_arrive_cluster(p_full + 8 * (2 * (int)other + (c >> 1)));
                 }
             }
             float2 sum[4] = {};
@@ -719,8 +745,8 @@ latent_prefill_tc_kernel(const LatentPrefill p, const __grid_constant__ CUtensor
             mbar_init(&mi.q_full[i], 1);
             mbar_init(&mi.q_empty[i], 1);
             mbar_init(&mi.s_full[i], 1);
-            mbar_init(&mi.p_full[i][0], 8);
-            mbar_init(&mi.p_full[i][1], 8);
+            mbar_init(&mi.s_other[i], 1);
+            for (int k = 0; k < 4; ++k) mbar_init(&mi.p_full[i][k], 8);
             mbar_init(&mi.copied[i], 1);
             mbar_init(&mi.o_full[i], 1);
             mbar_init(&mi.o_empty[i], 8);

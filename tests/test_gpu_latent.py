@@ -446,6 +446,24 @@ def test_prefill_shared_keys_next_to_nan():
     ref.check(o[qs], lse[qs], want, "between")
 
 
+@pytest.mark.parametrize("name,heads,lq,lk", [
+    ("shared_keys", 2, [200], [2000]), ("one_at_a_time", 40, [200], [900]),
+    ("side_by_side", 12, [250, 100, 30, 256, 180, 1, 220, 90], [300, 1500, 30, 900, 181, 700, 1300, 89]),
+    ("second_tile", 40, [512], [700]),
+], ids=lambda x: x if isinstance(x, str) else "")
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_prefill_rising_scores_of_a_tile_alone(causal, name, heads, lq, lk):
+    """Scores that rise along the keys, so that the maximum is moved again and again while a query tile's
+    next scores are computed ahead."""
+    q, kn, kp, v, cu_q, cu_k = prefill_inputs(gen(70), heads, lq, lk, torch.bfloat16)
+    q[:, :, 0] = 5.0
+    kn[:, :, 0] = torch.cat([torch.linspace(-40, 40, n, device="cuda") for n in lk]).to(torch.bfloat16)[:, None]
+    err = errors()
+    o, lse = kda.latent_prefill(q, kn, kp, v, SCALE, cu_q, cu_k, causal=causal, errors=err)
+    ref.check(o, lse, ref.prefill(q, kn, kp, v, SCALE, lq, lk, causal), name)
+    assert err.item() == 0
+
+
 def test_prefill_output_aligned_to_16_bytes_only():
     g = gen(48)
     q, kn, kp, v, cu, _ = prefill_inputs(g, 3, [300], [300], torch.bfloat16)
