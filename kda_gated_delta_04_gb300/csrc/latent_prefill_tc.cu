@@ -16,11 +16,12 @@
 //   S [256 x 128] = Q [256 x 192] K^T          12 steps of K = 16, operands in shared memory
 //   O [256 x 128] += P [256 x 128] V            8 steps, P (bf16) in tensor memory over its S
 //
-// Tensor memory is full: two O, two S of 128 columns.  The two query tiles take turns: while one
-// tile's softmax runs (a warpgroup each, a thread per query, so that maximum and sum need no other
-// thread), the tensor cores run the other tile's products, O += P V of key tile j and S of j + 1.
-// Where there are few jobs and many keys, two or four pairs (one cluster) share the keys of a job and join their
-// parts through distributed shared memory.
+// Tensor memory is full: two O, two S of 128 columns (a tile that is alone has both S).  The two query
+// tiles take turns: while one tile's softmax runs (a warpgroup each, a thread per query, so that maximum
+// and sum need no other thread), the tensor cores run the other tile's products, O += P V of key tile j
+// and S of j + 1.
+// Where there are few jobs and many keys, two or four pairs (one cluster) share the keys of a job and join
+// their parts through distributed shared memory.
 // Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10: the jobs; 11: a check of the
 // offsets (first CTA).
 //
@@ -217,7 +218,7 @@ struct Jobs {
 // first; a short job's successor is asked for when the copies of the one before are done.
 // A job of one query tile takes another such beside it (`beside`: the grid has more clusters than can run
 // at once), since alone it leaves the tensor cores to wait for its softmax and the other way round: 64
-// prompts of 150 to 250 tokens, 16 heads, 71 us instead of 97; 300 of 10 to 30 tokens 182 instead of 302.
+// prompts of 150 to 250 tokens, 16 heads, 73 us instead of 97; 300 of 10 to 30 tokens 195 instead of 302.
 // Both CTAs of the pair come to the same jobs.
 template <int SPLIT>
 __device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool beside, int rank, int team, int lane)
@@ -847,10 +848,10 @@ bool make_map(CUtensorMap *m, const void *ptr, int channels, int64_t heads, int6
 
 // Pairs that share a job's keys: as many as leave every cluster an SM for each of its CTAs at once (15
 // clusters of eight CTAs or 36 of four do), where the share saves more than the larger cluster and the join
-// cost, 4 us.  512 queries behind 7,500 keys, us with one, two, four pairs: 15 heads 101, 63, 39; 16 heads 101,
-// 63, 73; 36 heads 103, 67, 114; 37 heads 103, 125, 114.  512 queries, 8 heads: no keys before them (4 tiles)
-// 15.5, 17.5, 13.8; 64 queries 9.4, 13.1, 13.5; 1,000 before 512 queries, 16 heads, 28, 26, 36; 512 before
-// them 21.7, 22.3, 31.
+// cost, 4 us.  512 queries behind 7,500 keys, us with one, two, four pairs: 15 heads 102, 62, 39; 16 heads 102,
+// 62, 72; 36 heads 104, 67, 112; 37 heads 104, 123, 112.  Few keys, 8 heads: 512 queries and keys (4 tiles)
+// 15.3, 17.6, 13.8; 64 queries and keys 9.4, 13.2, 13.4.  16 heads: 512 queries behind 1,000 keys 29, 25.5, 35,
+// behind 512 22.3, 21.9, 31; 200 behind 1,000 18.0, 20.1, 32.
 int key_split(const LatentPrefill &p, int64_t jobs)
 {
     const int64_t tiles = p.k_tokens / p.num_seqs / kN;  // key tiles of a sequence, on average
