@@ -22,10 +22,10 @@
 // and S of j + 1.
 // Where there are few jobs and many keys, two or four pairs (one cluster) share the keys of a job and join
 // their parts through distributed shared memory.
-// Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10: the jobs; 11: a check of the
-// offsets (first CTA).
+// Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10: the jobs;
+// 11: a check of the offsets (first CTA).
 //
-// 4,096 tokens, 32 heads, causal: 131 us, 1.31 PFLOP/s; with 15,000 keys before 1,024 tokens 204 us, 1.39.
+// 4,096 tokens, 32 heads, causal: 132 us, 1.30 PFLOP/s; with 15,000 keys before 1,024 tokens 207 us, 1.37.
 #include <math.h>
 
 #include "latent.cuh"
