@@ -556,6 +556,9 @@ kda_status_t kda_diag_tensor_phases(int32_t pass, int32_t reps, void *workspace,
  *               neither; may be the same rows
  *  latent_out, k_pe_out  the normalised latent and the rotated key again, for the
  *               expanded form's projections; each may be NULL or its input's rows
+ *               The rows of an output (q_pe_out, latent_out, k_pe_out) share no element:
+ *               a row's width fits into the smaller stride, and all rows along that one
+ *               into a step of the other.  Input rows may be shared (a stride of 0)
  *  cache        [num_slots, d_latent + d_pe] (pages of any size, one after the other)
  *  slots        [num_tokens] int32 device, distinct; -1: the row is not cached.  Others
  *               outside [0, num_slots): not cached, KDA_DEVICE_ERR_SLOT

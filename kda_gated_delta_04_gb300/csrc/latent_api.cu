@@ -11,6 +11,17 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // A stride in elements: not negative and a whole number of 16-byte pieces.
 bool stride_ok(int64_t s, size_t es) { return s >= 0 && s <= (int64_t)1 << 38 && (size_t)s * es % 16 == 0; }
 
+// Whether no two of the rows of `width` elements at i s0 + j s1 (i < n0, j < n1) share an element, as far as
+// nested strides show it: one dimension's whole extent lies within a step of the other's.
+bool rows_apart(int64_t s0, int64_t n0, int64_t s1, int64_t n1, int64_t width)
+{
+    if (n0 <= 1) return n1 <= 1 || s1 >= width;
+    if (n1 <= 1) return s0 >= width;
+    const bool first = s0 <= s1;
+    const int64_t inner = first ? s0 : s1, outer = first ? s1 : s0, steps = (first ? n0 : n1) - 1;
+    return inner >= width && (outer - width) / steps >= inner;
+}
+
 // Packed tokens are counted in int32, rounded up to tiles.
 constexpr int64_t kMaxTokens = INT32_MAX - 4096;
 
@@ -55,6 +66,12 @@ kda_status_t kda_latent_append(const void *latent, int64_t latent_stride, const 
         (q_pe && (!stride_ok(q_token_stride, es) || !stride_ok(q_head_stride, es) ||
                   !stride_ok(out_token_stride, es) || !stride_ok(out_head_stride, es))) ||
         (latent_out && !stride_ok(latent_out_stride, es)) || (k_pe_out && !stride_ok(k_pe_out_stride, es)))
+        return KDA_ERR_INVALID_ARG;
+    // rows are written by different warps, and where an output is its input a row is read as often as it is
+    // written: in shared rows the result would depend on the order
+    if ((q_pe && !rows_apart(out_token_stride, num_tokens, out_head_stride, num_heads, d_pe)) ||
+        (latent_out && !rows_apart(latent_out_stride, num_tokens, 0, 1, d_latent)) ||
+        (k_pe_out && !rows_apart(k_pe_out_stride, num_tokens, 0, 1, d_pe)))
         return KDA_ERR_INVALID_ARG;
     const kda_status_t st = kda::check_device();
     if (st != KDA_OK) return st;
