@@ -15,7 +15,7 @@ from test_latent_abi import FAKE, INVALID, append_args, kda  # noqa: F401 (a fix
     dict(num_heads=1, out_token_stride=0), dict(num_heads=1, out_token_stride=56),
     dict(num_tokens=1, out_head_stride=0), dict(num_tokens=1, out_head_stride=56),
     dict(latent_out_stride=0), dict(latent_out_stride=504), dict(k_pe_out_stride=0), dict(k_pe_out_stride=56),
-    dict(out_token_stride=2 ** 37, out_head_stride=2 ** 38, num_tokens=2 ** 30),  # (products past 64 bits)
+    dict(out_token_stride=2 ** 37, out_head_stride=2 ** 38, num_tokens=2 ** 29),  # (products past 64 bits)
 ])
 @pytest.mark.parametrize("dtype", [0, 1])
 def test_append_refuses_outputs_that_overlap(kda, over, dtype):  # noqa: F811
