@@ -593,14 +593,18 @@ def _flat(t, name, dtype, dev, shape):
 
 
 def _latent_like(t, name, dims):
-    """Type code, type and device index that every other tensor of the call shares with t."""
+    """Type code, type and device index that every other tensor of the call shares with t: the current
+    device, on which the entry points launch."""
     torch = _torch_module or _load_torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
-    dt = t.dtype
-    return KDA_DTYPE_BF16 if dt is torch.bfloat16 else _dtype_code(t), dt, t.get_device()
+    dt, dev = t.dtype, t.get_device()
+    now = torch._C._cuda_getDevice()  # torch.cuda.current_device()
+    if dev != now:
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{now}")
+    return KDA_DTYPE_BF16 if dt is torch.bfloat16 else _dtype_code(t), dt, dev
 
 
 def _raw_stream(stream, dev):
@@ -628,7 +632,8 @@ def latent_append(latent, k_pe, cache, slots, *, norm_weight=None, norm_eps=1e-6
     queries' position channels, is rotated in the same launch into q_pe_out (None: in place).
     latent_out [T, 512] and k_pe_out [T, 64] receive the normalised latent and the rotated key
     again.  Rows may be strided; all are bf16 or all fp32.  interleaved: the rotated pairs are
-    (2i, 2i + 1) instead of (i, i + 32).  errors: int32 [1] that collects KDA_DEVICE_ERR_* bits."""
+    (2i, 2i + 1) instead of (i, i + 32).  errors: int32 [1] that collects KDA_DEVICE_ERR_* bits.
+    The tensors are on the current device (this holds for every latent call)."""
     torch = _torch_module or _load_torch()
     if _native is not None:
         st = _native.append(latent, k_pe, cache, slots, norm_weight, norm_eps, cos_sin, positions, interleaved, q_pe,

@@ -7,6 +7,7 @@
 // the time of the entry point itself; this takes under one.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
@@ -39,6 +40,13 @@ struct Args {
         device = t->get_device();
         type = t->scalar_type();
         return t;
+    }
+    // Whether the tensors are where the entry points launch, on the current device (where there is none, the entry
+    // point says so).
+    bool here() const
+    {
+        c10::DeviceIndex now = -1;
+        return c10::cuda::GetDevice(&now) != cudaSuccess || now == device;
     }
     // a tensor of these sizes, its last dimension contiguous; the leading strides, 0 where there is one entry
     template <size_t D>
@@ -136,7 +144,7 @@ PyObject *append(PyObject *, PyObject *const *v, Py_ssize_t n)
         if (a.given(13)) err = a.flat(13, at::kInt, {1});
         const int inter = PyObject_IsTrue(v[8]);
         void *stream = a.stream(14);
-        if (!a.ok || inter < 0 || T > INT32_MAX || H > INT32_MAX || M > INT32_MAX) return kNo;
+        if (!a.ok || !a.here() || inter < 0 || T > INT32_MAX || H > INT32_MAX || M > INT32_MAX) return kNo;
         return kda_latent_append(x, xs, k, ks, w, (float)eps, static_cast<const float *>(cs), (int32_t)M,
                                  static_cast<const int32_t *>(pos), q, qs[0], qs[1], qo, os[0], os[1], lo, ls, ko, ps,
                                  (int32_t)T, (int32_t)H, KDA_LATENT_DIM, KDA_LATENT_PE_DIM, a.code(), c, pages * page,
@@ -163,7 +171,7 @@ PyObject *decode(PyObject *, PyObject *const *v, Py_ssize_t n)
         const double scale = a.number(4);
         void *o = a.flat(5, a.type, {B, H, KDA_LATENT_DIM}), *lse = a.flat(6, at::kFloat, {B, H});
         void *err = a.given(8) ? a.flat(8, at::kInt, {1}) : nullptr, *stream = a.stream(9);
-        if (!a.ok || B > INT32_MAX || H > INT32_MAX || page > INT32_MAX || W > INT32_MAX) return kNo;
+        if (!a.ok || !a.here() || B > INT32_MAX || H > INT32_MAX || page > INT32_MAX || W > INT32_MAX) return kNo;
         return kda_latent_decode(qp, qs[0], qs[1], c, pages, (int32_t)page, static_cast<const int32_t *>(tp), ts, (int32_t)W,
                                  static_cast<const int32_t *>(lens), (int32_t)B, (int32_t)H, KDA_LATENT_DIM,
                                  KDA_LATENT_PE_DIM, a.code(), (float)scale, o, static_cast<float *>(lse), ws->data_ptr(),
@@ -189,7 +197,7 @@ PyObject *prefill(PyObject *, PyObject *const *v, Py_ssize_t n)
         const int causal = PyObject_IsTrue(v[7]);
         void *o = a.flat(8, a.type, {Tq, H, D}), *lse = a.flat(9, at::kFloat, {Tq, H});
         void *err = a.given(10) ? a.flat(10, at::kInt, {1}) : nullptr, *stream = a.stream(11);
-        if (!a.ok || causal < 0 || H > INT32_MAX || N > INT32_MAX) return kNo;
+        if (!a.ok || !a.here() || causal < 0 || H > INT32_MAX || N > INT32_MAX) return kNo;
         return kda_latent_prefill(qp, qs[0], qs[1], kn, ns[0], ns[1], kpp, ps, vp, vs[0], vs[1],
                                   static_cast<const int32_t *>(cq), static_cast<const int32_t *>(ck), (int32_t)N, Tq, Tk,
                                   (int32_t)H, D, P, D, a.code(), (float)scale, o, static_cast<float *>(lse),

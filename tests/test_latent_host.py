@@ -37,3 +37,66 @@ def test_append_refuses_outputs_that_overlap(kda, over, dtype):  # noqa: F811
 def test_append_takes_outputs_that_do_not(kda, over):  # noqa: F811
     """Past the checks of the arguments the entry point finds that there is no device."""
     assert kda.kda_latent_append(*append_args(**over)) == kda.KDA_ERR_CUDA
+
+
+# ------------------------------------------------------------------ the device
+class Claimed(torch.Tensor):
+    """A tensor that says it is on the second GPU.  It holds nothing, and its address is no one's."""
+
+    @staticmethod
+    def __new__(cls, *size, dtype=torch.bfloat16):
+        return torch.Tensor._make_wrapper_subclass(cls, size, dtype=dtype, device="cuda:1")
+
+    def data_ptr(self):
+        return FAKE
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise AssertionError(f"{func} on a tensor without contents")
+
+
+class Recorded:
+    """Stands in for the loaded library: what is called, and nothing happens."""
+
+    def __init__(self):
+        self.called = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.called.append(name) or 0
+
+
+class Stream:
+    cuda_stream = 0
+
+
+def claimed_calls():
+    """(name, positional arguments, keywords, the native module's arguments without the stream)."""
+    t, i32, f32 = Claimed, torch.int32, torch.float32
+    a = (t(4, 512), t(4, 64), t(2, 8, 576), t(4, dtype=i32))
+    yield "latent_append", a, {}, (*a, None, 1e-6, None, None, False, None, None, None, None, None)
+    d = (t(2, 3, 576), t(2, 8, 576), t(2, 1, dtype=i32), t(2, dtype=i32), 0.1)
+    out = dict(o=t(2, 3, 512), lse=t(2, 3, dtype=f32))
+    ws = t(50331648, dtype=torch.uint8)
+    yield "latent_decode", d, dict(**out, workspace=ws), (*d, *out.values(), ws, None)
+    p = (t(5, 3, 192), t(5, 3, 128), t(5, 64), t(5, 3, 128), 0.1)
+    out = dict(o=t(5, 3, 128), lse=t(5, 3, dtype=f32))
+    yield "latent_prefill", p, out, (*p, None, None, True, *out.values(), None)
+
+
+@pytest.mark.parametrize("stream", [None, Stream()], ids=["current_stream", "given_stream"])
+@pytest.mark.parametrize("name,args,kw,native", list(claimed_calls()), ids=lambda x: x if isinstance(x, str) else "")
+def test_tensors_of_another_gpu_are_refused(kda, monkeypatch, name, args, kw, native, stream):  # noqa: F811
+    """The entry points launch on the current device: with another GPU's tensors the kernel would run on the
+    wrong one, on addresses that are not its own."""
+    fake = Recorded()
+    monkeypatch.setattr(kda, "_lib", fake)
+    monkeypatch.setattr(kda, "_native", None)
+    monkeypatch.setattr(kda, "_torch_module", torch)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+        getattr(kda, name)(*args, stream=stream, **kw)
+    assert not fake.called
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)  # made current: taken
+    getattr(kda, name)(*args, stream=stream, **kw)
+    assert fake.called == ["kda_" + name]
