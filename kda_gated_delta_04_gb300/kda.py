@@ -304,7 +304,12 @@ def _flags(log_alpha, qk_l2norm, seq_split=True, streamed=None):
 
 
 def _stream_handle(stream, device):
+    """The handle of the given stream, or of the current one; the entry points launch on the current
+    device, so `device`, where the tensors are, has to be that."""
     torch = _torch()
+    now = torch.cuda.current_device()
+    if device.index not in (None, now):
+        raise ValueError(f"the tensors are on {device}, but the current device is cuda:{now}")
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return s.cuda_stream
 
