@@ -95,6 +95,13 @@ struct Args {
     }
 };
 
+// The interpreter's lock let go during the entry point, as ctypes does: a launch waits where the GPU's queue is
+// full, maybe for a host function that needs the lock.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 template <class F>
 PyObject *answer(F &&f)
 {
@@ -145,6 +152,7 @@ PyObject *append(PyObject *, PyObject *const *v, Py_ssize_t n)
         const int inter = PyObject_IsTrue(v[8]);
         void *stream = a.stream(14);
         if (!a.ok || !a.here() || inter < 0 || T > INT32_MAX || H > INT32_MAX || M > INT32_MAX) return kNo;
+        const Unlocked unlocked;
         return kda_latent_append(x, xs, k, ks, w, (float)eps, static_cast<const float *>(cs), (int32_t)M,
                                  static_cast<const int32_t *>(pos), q, qs[0], qs[1], qo, os[0], os[1], lo, ls, ko, ps,
                                  (int32_t)T, (int32_t)H, KDA_LATENT_DIM, KDA_LATENT_PE_DIM, a.code(), c, pages * page,
@@ -172,10 +180,13 @@ PyObject *decode(PyObject *, PyObject *const *v, Py_ssize_t n)
         void *o = a.flat(5, a.type, {B, H, KDA_LATENT_DIM}), *lse = a.flat(6, at::kFloat, {B, H});
         void *err = a.given(8) ? a.flat(8, at::kInt, {1}) : nullptr, *stream = a.stream(9);
         if (!a.ok || !a.here() || B > INT32_MAX || H > INT32_MAX || page > INT32_MAX || W > INT32_MAX) return kNo;
+        void *scratch = ws->data_ptr();
+        const size_t scratch_bytes = ws->nbytes();
+        const Unlocked unlocked;
         return kda_latent_decode(qp, qs[0], qs[1], c, pages, (int32_t)page, static_cast<const int32_t *>(tp), ts, (int32_t)W,
                                  static_cast<const int32_t *>(lens), (int32_t)B, (int32_t)H, KDA_LATENT_DIM,
-                                 KDA_LATENT_PE_DIM, a.code(), (float)scale, o, static_cast<float *>(lse), ws->data_ptr(),
-                                 (size_t)ws->nbytes(), static_cast<uint32_t *>(err), stream);
+                                 KDA_LATENT_PE_DIM, a.code(), (float)scale, o, static_cast<float *>(lse), scratch, scratch_bytes,
+                                 static_cast<uint32_t *>(err), stream);
     });
 }
 
@@ -198,6 +209,7 @@ PyObject *prefill(PyObject *, PyObject *const *v, Py_ssize_t n)
         void *o = a.flat(8, a.type, {Tq, H, D}), *lse = a.flat(9, at::kFloat, {Tq, H});
         void *err = a.given(10) ? a.flat(10, at::kInt, {1}) : nullptr, *stream = a.stream(11);
         if (!a.ok || !a.here() || causal < 0 || H > INT32_MAX || N > INT32_MAX) return kNo;
+        const Unlocked unlocked;
         return kda_latent_prefill(qp, qs[0], qs[1], kn, ns[0], ns[1], kpp, ps, vp, vs[0], vs[1],
                                   static_cast<const int32_t *>(cq), static_cast<const int32_t *>(ck), (int32_t)N, Tq, Tk,
                                   (int32_t)H, D, P, D, a.code(), (float)scale, o, static_cast<float *>(lse),

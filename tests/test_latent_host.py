@@ -1,4 +1,9 @@
 """More of the latent calls' host side, without a GPU: calls whose outputs' rows overlap."""
+import importlib.machinery
+import importlib.util
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -100,3 +105,41 @@ def test_tensors_of_another_gpu_are_refused(kda, monkeypatch, name, args, kw, na
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)  # made current: taken
     getattr(kda, name)(*args, stream=stream, **kw)
     assert fake.called == ["kda_" + name]
+
+
+# ------------------------------------------------------------------ the native way
+STUB = """
+#include <stddef.h>
+int PyGILState_Check(void);
+int kda_latent_append() { return 100 + PyGILState_Check(); }
+int kda_latent_decode() { return 100 + PyGILState_Check(); }
+int kda_latent_prefill() { return 100 + PyGILState_Check(); }
+"""
+
+
+@pytest.fixture(scope="module")
+def stubbed(kda, tmp_path_factory):  # noqa: F811
+    """The native module over a library whose entry points do nothing but say whether the calling thread
+    holds the interpreter's lock (101) or not (100)."""
+    from kda_gated_delta_04_gb300 import build
+    obj = os.path.join(build.BUILD_DIR, "latent_args.o")
+    if not os.path.exists(build.ARGS_PATH):
+        pytest.skip("latent_args.cpp was left out of the build")
+    where = str(tmp_path_factory.mktemp("stub"))
+    with open(os.path.join(where, "stub.c"), "w") as f:
+        f.write(STUB)
+    run = lambda *cmd: subprocess.run(cmd, check=True, capture_output=True)
+    run("gcc", "-shared", "-fPIC", "-o", os.path.join(where, "libstub.so"), os.path.join(where, "stub.c"))
+    path = os.path.join(where, "_latent_args.so")
+    run("g++", "-shared", "-o", path, obj, "-L", where, "-lstub", f"-Wl,-rpath,{where}", "-Wl,-Bsymbolic", "-L",
+        os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda")
+    loader = importlib.machinery.ExtensionFileLoader("_latent_args", path)
+    return importlib.util.module_from_spec(importlib.util.spec_from_loader("_latent_args", loader))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="with a device the tensors' own is compared first")
+@pytest.mark.parametrize("name,native", [(c[0], c[3]) for c in claimed_calls()], ids=lambda x: x if isinstance(x, str) else "")
+def test_the_native_way_lets_other_threads_run(stubbed, name, native):
+    """A launch waits where the GPU's queue is full, maybe for a host function that needs the interpreter:
+    as in a call through ctypes, the lock is not held meanwhile."""
+    assert getattr(stubbed, name.removeprefix("latent_"))(*native, 0) == 100
