@@ -67,6 +67,15 @@ struct Args {
         void *p = rows(i, want, size, stride);
         return ok && tensor(i)->is_contiguous() ? p : fail();
     }
+    bool truth(int i)
+    {
+        const int x = PyObject_IsTrue(v[i]);
+        if (x < 0) {
+            PyErr_Clear();
+            ok = false;
+        }
+        return x > 0;
+    }
     double number(int i)
     {
         const double x = PyFloat_AsDouble(v[i]);
@@ -149,9 +158,9 @@ PyObject *append(PyObject *, PyObject *const *v, Py_ssize_t n)
         if (a.given(11)) lo = a.rows(11, a.type, {T, KDA_LATENT_DIM}, &ls);
         if (a.given(12)) ko = a.rows(12, a.type, {T, KDA_LATENT_PE_DIM}, &ps);
         if (a.given(13)) err = a.flat(13, at::kInt, {1});
-        const int inter = PyObject_IsTrue(v[8]);
+        const bool inter = a.truth(8);
         void *stream = a.stream(14);
-        if (!a.ok || !a.here() || inter < 0 || T > INT32_MAX || H > INT32_MAX || M > INT32_MAX) return kNo;
+        if (!a.ok || !a.here() || T > INT32_MAX || H > INT32_MAX || M > INT32_MAX) return kNo;
         const Unlocked unlocked;
         return kda_latent_append(x, xs, k, ks, w, (float)eps, static_cast<const float *>(cs), (int32_t)M,
                                  static_cast<const int32_t *>(pos), q, qs[0], qs[1], qo, os[0], os[1], lo, ls, ko, ps,
@@ -205,10 +214,10 @@ PyObject *prefill(PyObject *, PyObject *const *v, Py_ssize_t n)
         const void *kpp = a.rows(2, a.type, {Tk, P}, &ps), *vp = a.rows(3, a.type, {Tk, H, D}, vs);
         const double scale = a.number(4);
         const void *cq = cu ? a.flat(5, at::kInt, {N + 1}) : nullptr, *ck = a.given(6) ? a.flat(6, at::kInt, {N + 1}) : nullptr;
-        const int causal = PyObject_IsTrue(v[7]);
+        const bool causal = a.truth(7);
         void *o = a.flat(8, a.type, {Tq, H, D}), *lse = a.flat(9, at::kFloat, {Tq, H});
         void *err = a.given(10) ? a.flat(10, at::kInt, {1}) : nullptr, *stream = a.stream(11);
-        if (!a.ok || !a.here() || causal < 0 || H > INT32_MAX || N > INT32_MAX) return kNo;
+        if (!a.ok || !a.here() || H > INT32_MAX || N > INT32_MAX) return kNo;
         const Unlocked unlocked;
         return kda_latent_prefill(qp, qs[0], qs[1], kn, ns[0], ns[1], kpp, ps, vp, vs[0], vs[1],
                                   static_cast<const int32_t *>(cq), static_cast<const int32_t *>(ck), (int32_t)N, Tq, Tk,

@@ -143,3 +143,20 @@ def test_the_native_way_lets_other_threads_run(stubbed, name, native):
     """A launch waits where the GPU's queue is full, maybe for a host function that needs the interpreter:
     as in a call through ctypes, the lock is not held meanwhile."""
     assert getattr(stubbed, name.removeprefix("latent_"))(*native, 0) == 100
+
+
+class Unclear:
+    def __bool__(self):
+        raise RuntimeError("neither true nor false")
+
+
+@pytest.mark.parametrize("name,native", [(c[0], c[3]) for c in claimed_calls() if c[0] != "latent_decode"],
+                         ids=lambda x: x if isinstance(x, str) else "")
+def test_the_native_way_leaves_no_error_behind(stubbed, name, native):
+    """A flag without a truth value is handed back like any other bad argument; the error that asking for it
+    raised does not stay set, to come up at some later call."""
+    args = list(native)
+    args[8 if name == "latent_append" else 7] = Unclear()
+    call = getattr(stubbed, name.removeprefix("latent_"))
+    st, after = call(*args, None), [i for i in range(3)]
+    assert st == -1 and after == [0, 1, 2]
