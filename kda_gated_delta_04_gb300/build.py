@@ -6,8 +6,9 @@ runtime, so the library shares the process's runtime with PyTorch.
 
 Beside it goes ``_latent_args.so`` (g++, against this interpreter's and the
 installed torch's headers): the latent calls' arguments from tensors to the C
-entry points without ctypes.  Where those headers are missing it is left out,
-and kda.py passes the same arguments through ctypes.
+entry points without ctypes.  It is an option: where what it needs is missing, or
+it cannot be compiled or linked, it is left out with a message, and kda.py passes
+the same arguments through ctypes.
 """
 from __future__ import annotations
 
@@ -81,49 +82,56 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(ARGS_PATH):  # never beside a library that it was not built for
+        os.remove(ARGS_PATH)
     os.replace(tmp, LIB_PATH)
     _link_args(*args_obj.result())
     return LIB_PATH
 
 
 def _compile_args():
-    """The object file of latent_args.cpp and torch's library folder, or (None, why)."""
+    """The object file of latent_args.cpp and torch's library folder, or (None, why there is none)."""
     import sysconfig
     try:
         import torch
     except ImportError:
         return None, "torch is not installed"
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     py = sysconfig.get_paths()["include"]
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
-    for need in (os.path.join(py, "Python.h"), os.path.join(inc, "torch", "csrc", "autograd", "python_variable.h")):
+    for need in (os.path.join(py, "Python.h"), os.path.join(inc, "torch", "csrc", "autograd", "python_variable.h"),
+                 os.path.join(inc, "c10", "cuda", "CUDAStream.h"), os.path.join(libs, "libc10_cuda.so")):
         if not os.path.exists(need):
             return None, f"{need} is missing"
     obj = os.path.join(BUILD_DIR, "latent_args.o")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", py, "-isystem", inc,
-           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
-           "-c", ARGS_SRC, "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {ARGS_SRC}:\n{r.stdout}\n{r.stderr}")
-    return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
+    why = _gxx(["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", py, "-isystem", inc,
+                "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+                "-c", ARGS_SRC, "-o", obj])
+    return (None, why) if why else (obj, libs)
+
+
+def _gxx(args):
+    """None, or why g++ with these arguments did not do it."""
+    try:
+        r = subprocess.run(["g++", *args], capture_output=True, text=True)
+    except OSError as e:
+        return f"g++: {e}"
+    return None if r.returncode == 0 else f"g++ failed:\n{r.stdout}\n{r.stderr}"
 
 
 def _link_args(obj, where):
-    """_latent_args.so against the libkda.so that stands beside it."""
-    if os.path.exists(ARGS_PATH):
-        os.remove(ARGS_PATH)
-    if obj is None:
-        print(f"_latent_args left out ({where}): the latent calls go through ctypes", file=sys.stderr)
-        return
-    tmp = ARGS_PATH + f".{os.getpid()}.tmp"
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libkda.so", "-Wl,-rpath,$ORIGIN", "-L", where,
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of _latent_args failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, ARGS_PATH)
+    """_latent_args.so against the libkda.so that stands beside it; obj None: `where` says why not."""
+    why = where
+    if obj is not None:
+        tmp = ARGS_PATH + f".{os.getpid()}.tmp"
+        why = _gxx(["-shared", "-o", tmp, obj, "-L", os.path.dirname(LIB_PATH), "-l:libkda.so", "-Wl,-rpath,$ORIGIN",
+                    "-L", where, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+        if why is None:
+            os.replace(tmp, ARGS_PATH)
+            return
+    print(f"_latent_args left out ({why}): the latent calls go through ctypes", file=sys.stderr)
 
 
 if __name__ == "__main__":
