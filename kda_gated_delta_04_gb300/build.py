@@ -15,6 +15,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -26,6 +27,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libkda.so")
 ARGS_SRC = os.path.join(PKG, "native", "latent_args.cpp")
 ARGS_PATH = os.path.join(PKG, "_latent_args.so")
+HEADER = os.path.join(ROOT, "include", "kda.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,23 +42,56 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(ROOT, "include", "kda.h"), ARGS_SRC, os.path.abspath(__file__)]
+def _newer(path, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB_PATH, _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [HEADER, os.path.abspath(__file__)])
+
+
+def _torch_version():
+    import importlib.metadata
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _args_note():
+    """Where it is kept what _latent_args.so was built for, or why it was left out."""
+    return os.path.join(BUILD_DIR, "latent_args.txt")
+
+
+def _args_for() -> str:
+    return f"torch {_torch_version()}, {sys.implementation.cache_tag}, {platform.machine()}"
+
+
+def _args_left_out():
+    """Why the module was left out for this torch and interpreter, "" where it is there; None: it is to be built."""
+    if not _newer(_args_note(), [ARGS_SRC, HEADER, os.path.abspath(__file__)]):
+        return None
+    with open(_args_note()) as f:
+        made_for, _, why = f.read().partition("\n")
+    if made_for != _args_for() or (not why and not os.path.exists(ARGS_PATH)):
+        return None
+    return why
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _lib_up_to_date() and _args_left_out() is not None
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and up_to_date():
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    if not force and _lib_up_to_date():
+        why = _args_left_out()
+        if why is None:
+            _link_args(*_compile_args())
+        elif why:
+            _say_left_out(why)
         return LIB_PATH
     nvcc = nvcc_path()
-    os.makedirs(BUILD_DIR, exist_ok=True)
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                     "-I", os.path.join(ROOT, "include")]
     if ptxas_info:
@@ -94,12 +129,14 @@ def _compile_args():
     import sysconfig
     try:
         import torch
+        cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     except ImportError:
         return None, "torch is not installed"
+    except RuntimeError as e:
+        return None, str(e)
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     py = sysconfig.get_paths()["include"]
-    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     for need in (os.path.join(py, "Python.h"), os.path.join(inc, "torch", "csrc", "autograd", "python_variable.h"),
                  os.path.join(inc, "c10", "cuda", "CUDAStream.h"), os.path.join(libs, "libc10_cuda.so")):
         if not os.path.exists(need):
@@ -124,13 +161,21 @@ def _gxx(args):
 def _link_args(obj, where):
     """_latent_args.so against the libkda.so that stands beside it; obj None: `where` says why not."""
     why = where
+    if os.path.exists(ARGS_PATH):
+        os.remove(ARGS_PATH)
     if obj is not None:
         tmp = ARGS_PATH + f".{os.getpid()}.tmp"
         why = _gxx(["-shared", "-o", tmp, obj, "-L", os.path.dirname(LIB_PATH), "-l:libkda.so", "-Wl,-rpath,$ORIGIN",
                     "-L", where, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
         if why is None:
             os.replace(tmp, ARGS_PATH)
-            return
+    with open(_args_note(), "w") as f:
+        f.write(f"{_args_for()}\n{why or ''}")
+    if why:
+        _say_left_out(why)
+
+
+def _say_left_out(why):
     print(f"_latent_args left out ({why}): the latent calls go through ctypes", file=sys.stderr)
 
 

@@ -86,3 +86,64 @@ def test_no_old_module_while_the_library_is_replaced(bench, monkeypatch):
     monkeypatch.setattr(build.os, "replace", lambda a, b: (seen.append(b == bench.lib and os.path.exists(bench.args)), replace(a, b)))
     bench.build(force=True)
     assert seen and not any(seen)
+
+
+def test_nothing_runs_when_all_is_there(bench):
+    bench.build()
+    bench.ran.clear()
+    bench.build()
+    assert not bench.ran
+
+
+def test_a_missing_module_is_built_again(bench):
+    """By itself: the library stays as it is."""
+    bench.build()
+    os.remove(bench.args)
+    bench.ran.clear()
+    bench.build()
+    assert os.path.exists(bench.args) and [cmd[0] for cmd in bench.ran] == ["g++", "g++"]
+
+
+def test_a_module_for_another_torch_is_built_again(bench, monkeypatch):
+    bench.build()
+    before = os.path.getmtime(bench.lib)
+    monkeypatch.setattr(build, "_torch_version", lambda: "1.0", raising=False)
+    bench.ran.clear()
+    bench.build()
+    assert [cmd[0] for cmd in bench.ran] == ["g++", "g++"] and os.path.getmtime(bench.lib) == before
+    bench.ran.clear()
+    bench.build()
+    assert not bench.ran
+
+
+def test_a_module_left_out_is_not_tried_on_every_call(bench, capfd):
+    """But the reason is said again, and another torch is another chance."""
+    bench.fails = compiling
+    bench.build()
+    bench.ran.clear()
+    capfd.readouterr()
+    bench.build()
+    assert not bench.ran and "_latent_args left out" in capfd.readouterr().err
+
+
+def test_a_changed_module_source_leaves_the_library(bench, monkeypatch, tmp_path):
+    bench.build()
+    src = tmp_path / "changed.cpp"
+    src.write_text("")
+    os.utime(src, (os.path.getmtime(bench.lib) + 10,) * 2)
+    monkeypatch.setattr(build, "ARGS_SRC", str(src))
+    bench.ran.clear()
+    bench.build()
+    assert [cmd[0] for cmd in bench.ran] == ["g++", "g++"]
+
+
+def test_a_module_to_build_without_nvcc(bench, monkeypatch, capfd):
+    """The library is there; what the module's headers need is not."""
+    bench.build()
+    os.remove(bench.args)
+
+    def none():
+        raise RuntimeError("nvcc not found")
+
+    monkeypatch.setattr(build, "nvcc_path", none)
+    assert bench.build() == bench.lib and "nvcc not found" in capfd.readouterr().err
