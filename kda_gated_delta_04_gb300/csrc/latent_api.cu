@@ -52,7 +52,7 @@ kda_status_t kda_latent_append(const void *latent, int64_t latent_stride, const 
     if (!dtype_ok(dtype) || d_latent <= 0 || d_pe <= 0) return KDA_ERR_INVALID_ARG;
     if (d_latent != KDA_LATENT_DIM || d_pe != KDA_LATENT_PE_DIM) return KDA_ERR_UNSUPPORTED;
     if (num_tokens < 0 || num_heads < 0 || num_slots < 0) return KDA_ERR_INVALID_ARG;
-    if ((int64_t)num_tokens * (1 + (num_heads + 7) / 8) > INT32_MAX) return KDA_ERR_UNSUPPORTED;  // grid extent
+    if ((int64_t)num_tokens * (1 + (num_heads + 7) / 8) > INT32_MAX) return KDA_ERR_UNSUPPORTED;  // units of work
     if (num_tokens == 0) return KDA_OK;
     const size_t es = elem_size(dtype);
     if (!latent || !k_pe || !cache || !slots || !q_pe != !q_pe_out || (cos_sin && (!positions || num_positions <= 0)) ||

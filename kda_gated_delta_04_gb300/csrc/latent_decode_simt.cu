@@ -272,8 +272,8 @@ latent_join_kernel(const char *ws, int head_tile, int heads, IO *o, float *lse)
 template <typename IO>
 cudaError_t launch_join(const LatentDecode &p, int head_tile, int grid)
 {
-    const int units = p.batch * ((p.heads + head_tile - 1) / head_tile);
-    const int records = latent_join_by_unit(p.batch, p.heads, head_tile, grid) ? units : grid;
+    const int records = latent_join_by_unit(p.batch, p.heads, head_tile, grid)
+                            ? p.batch * ((p.heads + head_tile - 1) / head_tile) : grid;
     const int heads = p.heads < head_tile ? p.heads : head_tile;
     const bool few = records * heads <= 4 * 152;  // one wave of 512 threads a CTA
     return latent_launch(few ? latent_join_kernel<IO, 4> : latent_join_kernel<IO, 1>,

@@ -606,10 +606,9 @@ cudaError_t launch(const LatentDecode &p, int grid)
     return err != cudaSuccess ? err : launch_latent_join(p, NH, grid);
 }
 
-// Heads per tile: the smallest of 16, 32 and 64 that holds them all, else tiles of 64 (each reads
-// the cache again, from L2).
-// Heads of a tile: the least power of two that holds them all, since a smaller tile leaves more shared memory
-// to the ring and costs the tensor cores less, and each further tile reads the cache rows once more (from L2).
+// Heads of a tile: the least of 16, 32 and 64 that holds them all (else tiles of 64), since a smaller tile leaves
+// more shared memory to the ring and costs the tensor cores less, and each further tile reads the cache rows once
+// more (from L2).
 // 256 sequences of up to 8,192 rows: 16 heads 210 us in a tile of 16, 216 of 32, 243 of 64; 32 heads 217 in a
 // tile of 32, 249 of 64.  48 of up to 8,192 rows, 128 heads: 117 us in tiles of 64, 175 of 32.  The tile of 64
 // has a ring of two cache tiles, too short to hide a copy's latency: the tensor pipe is 42 % busy.

@@ -31,7 +31,7 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// mma_bf16, mma_tmem_a and mma_commit for a whole warp in step: every lane has the same operands and the one with
+// mma_bf16 and mma_commit for a whole warp in step: every lane has the same operands and the one with
 // `lead` set issues.  Control flow stays uniform, so that descriptors and addresses live in uniform
 // registers; issued by a lane alone in a branch, each operand is moved there anew, which made an
 // instruction take 127 cycles to issue against the 64 it runs for (M = N = 128).
@@ -42,16 +42,6 @@ __device__ __forceinline__ void mma_bf16_lead(uint32_t lead, uint32_t d_tmem, ui
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_tmem_a_lead(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
 
@@ -159,7 +149,7 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// As mma_bf16_lead, mma_tmem_a_lead and mma_commit_lead, for the pair; the commit arrives on the
+// As mma_bf16_lead and mma_commit_lead, for the pair, and A from tensor memory; the commit arrives on the
 // barrier of that offset in both CTAs (mask: the CTAs of the cluster that are the pair).
 __device__ __forceinline__ void mma_bf16_pair(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate)
