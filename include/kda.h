@@ -525,9 +525,11 @@ kda_status_t kda_diag_tensor_phases(int32_t pass, int32_t reps, void *workspace,
  * The projections themselves are plain matrix products and the caller's.  All of
  * them take bf16 or fp32 tensors (kda_dtype_t); bf16 attention runs on the tensor
  * cores, fp32 on the CUDA cores with exact fp32 products.  Scores, softmax
- * statistics and sums are fp32.  Strides are in elements and a multiple of 16 bytes,
- * the last dimension is contiguous, bases are 16-byte aligned.  device_errors is NULL
- * or a device uint32 that receives KDA_DEVICE_ERR_* bits (or-ed, never cleared).
+ * statistics and sums are fp32; in bf16 attention the softmax's weights are rounded
+ * to bf16 for their product with the values.  Strides are in elements and a multiple
+ * of 16 bytes, the last dimension is contiguous, bases are 16-byte aligned.
+ * device_errors is NULL or a device uint32 that receives KDA_DEVICE_ERR_* bits (or-ed,
+ * never cleared).  The kernels run on the current device, where all addresses have to be.
  */
 #define KDA_LATENT_DIM 512
 #define KDA_LATENT_PE_DIM 64

@@ -11,7 +11,7 @@
 // position key, or the position channels of 16 of its query heads (32 lanes = 8 heads x 4 quarters of the
 // pairs, two heads and 2 x 8 pairs a lane), so that small batches spread over 1 + H / 16 warps a token.  In
 // large ones each of the 16 warps that an SM holds walks on through the units, the numbers (position, slot)
-// two units ahead and the rows one: 32,768 tokens of 32 heads 68 us (386 MB, 5.6 TB/s), 64 tokens 2.8.  A
+// two units ahead and the rows one: 32,768 tokens of 32 heads 69 us (386 MB, 5.6 TB/s), 64 tokens 3.2.  A
 // warp a unit and CTA took 72 and was bound by the launching of CTAs, 0.6 ns each.
 #include "latent.cuh"
 #include "latent_ptx.cuh"

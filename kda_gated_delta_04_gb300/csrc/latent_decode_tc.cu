@@ -21,7 +21,10 @@
 // in one, pairs of latent panels (read by both products) in the other.  S^T of tile t + 1 is issued
 // before O^T of tile t, so the softmax of one tile runs beside the products of its neighbours, and
 // the rings hold 2 to 2.7 tiles: while one is worked on, the others are in flight (100 KB and more a
-// SM; 45 KB cover HBM's latency at its full rate).  256 sequences of 1 to 8,192 rows, 32 heads: 217 us, 5.9 TB/s.
+// SM; 45 KB cover HBM's latency at its full rate).  256 sequences of 1 to 8,192 rows, 32 heads: 217 to 222 us, 5.8 to
+// 5.9 TB/s.  That is with pages of 64 rows and more: a copy never leaves a page, and a tile of 9 copies of 8 KB takes
+// 36 of 2 KB with pages of 16 rows or 48 (215 us become 263) and 72 of 1 KB with 8 (380); pages of 32 are as good
+// as whole tiles (218).
 #include <math.h>
 
 #include "latent.cuh"

@@ -25,7 +25,10 @@
 // Warps 0 to 7: softmax; 8: copies (TMA); 9: matrix instructions (in the leading CTA); 10: the jobs;
 // 11: a check of the offsets (first CTA).
 //
-// 4,096 tokens, 32 heads, causal: 132 us, 1.30 PFLOP/s; with 15,000 keys before 1,024 tokens 207 us, 1.37.
+// 4,096 tokens, 32 heads, causal: 131 us, 1.31 PFLOP/s; 1,024 tokens behind 13,047 keys 207 us, 1.37 (other inputs
+// on every call).  The comparisons at the constants below repeat one call on the same inputs, in bursts of 2 ms after a
+// pause; the 4,096 tokens take 124 us so.  Cycles by that, over 4 to 32 key tiles and 1 to 6 jobs a pair, within 2 %:
+// 13,600 a call, 6,900 a job and 3,290 a key tile of a pair, for which the products need 2,560.
 #include <math.h>
 
 #include "latent.cuh"
@@ -47,8 +50,8 @@ constexpr int kStages = 3;                    // key tiles in shared memory
 constexpr int kJobs = 4;                      // records of jobs
 // Key tiles of a job during whose copies the next one is asked for already: what hides the 2,000 cycles that
 // asking for and finding it take.  A job taken sooner is one that a pair that comes free cannot have: with 4
-// for shared key tiles a prompt of 4,096 tokens took 129 us instead of 123 (its last jobs have 4), while 64
-// prompts of 150 to 250 tokens, side by side, take 88 us with 2 and 74 with 4 or 8 (16 heads).
+// for shared key tiles a prompt of 4,096 tokens takes 130 us instead of 124 (its last jobs have 4), while 64
+// prompts of 150 to 250 tokens, side by side, take 79 us with 2 and 74 with 4 or 8 (16 heads).
 constexpr int kShort = 2, kShortApart = 8;
 constexpr int kAhead = 2;                     // key tiles brought into L2 before their copy
 constexpr uint32_t kOffQ = 0;                 // two tiles of three panels
@@ -87,7 +90,9 @@ __device__ __forceinline__ int place(bool apart, int n0, int n1, int i, int j)
 // Where a query tile's key tiles outnumber the other's, S goes to the other's buffer and the own one in turn
 // from this key tile on, a key tile ahead, so that it is computed while the softmax before it runs: by then the
 // other's last product has been issued, and what a tile alone would wait for is half of its time.  256 queries
-// behind 15,000 keys, 8 heads: 36 us, with one buffer 49; 4 times 200 behind 3,000 32, with one 45.
+// behind 15,000 keys: 40 heads 118 us, with one buffer 180; 8 heads (their keys shared by four pairs) 39 and 55; 4
+// times 200 behind 3,000, 8 heads, 31.5 and 43.  What it costs: prompts of one key tile, which have nothing to
+// compute ahead, 300 of 10 to 30 tokens, 16 heads, 193 us and 182; 64 of 150 to 250 tokens 74 and 72.
 __device__ __forceinline__ int alone_from(int i, int n0, int n1) { return i ? n0 + 1 : n1 + 2; }
 __device__ __forceinline__ bool in_other(int alone, int j) { return j >= alone && !((j - alone) & 1); }
 
@@ -218,7 +223,7 @@ struct Jobs {
 // first; a short job's successor is asked for when the copies of the one before are done.
 // A job of one query tile takes another such beside it (`beside`: the grid has more clusters than can run
 // at once), since alone it leaves the tensor cores to wait for its softmax and the other way round: 64
-// prompts of 150 to 250 tokens, 16 heads, 73 us instead of 97; 300 of 10 to 30 tokens 195 instead of 302.
+// prompts of 150 to 250 tokens, 16 heads, 74 us instead of 97; 300 of 10 to 30 tokens 193 instead of 307.
 // Both CTAs of the pair come to the same jobs.
 template <int SPLIT>
 __device__ __forceinline__ void job_role(Misc &mi, const LatentPrefill &p, bool beside, int rank, int team, int lane)
@@ -848,10 +853,12 @@ bool make_map(CUtensorMap *m, const void *ptr, int channels, int64_t heads, int6
 
 // Pairs that share a job's keys: as many as leave every cluster an SM for each of its CTAs at once (15
 // clusters of eight CTAs or 36 of four do), where the share saves more than the larger cluster and the join
-// cost, 4 us.  512 queries behind 7,500 keys, us with one, two, four pairs: 15 heads 102, 62, 39; 16 heads 102,
-// 62, 72; 36 heads 104, 67, 112; 37 heads 104, 123, 112.  Few keys, 8 heads: 512 queries and keys (4 tiles)
-// 15.3, 17.6, 13.8; 64 queries and keys 9.4, 13.2, 13.4.  16 heads: 512 queries behind 1,000 keys 29, 25.5, 35,
-// behind 512 22.3, 21.9, 31; 200 behind 1,000 18.0, 20.1, 32.
+// cost, 4 us.  512 queries behind 7,500 keys, us with one, two, four pairs: 15 heads 115, 70, 42; 16 heads 115,
+// 69, 79; 36 heads 117, 74, 121; 37 heads 117, 136, 122.  Few keys, 8 heads: 512 queries and keys (4 tiles)
+// 14.8, 17.5, 13.7; 64 queries and keys 9.2, 13.0, 13.4.  16 heads: 512 queries behind 1,000 keys 29.7, 25.3, 35,
+// behind 512 21.7, 20.8, 30; 200 behind 1,000 18.4, 19.9, 32.  The key tiles are an average and the jobs include
+// numbers without a tile, since the lengths are on the device: one long history beside several short prompts is not
+// shared.
 int key_split(const LatentPrefill &p, int64_t jobs)
 {
     const int64_t tiles = p.k_tokens / p.num_seqs / kN;  // key tiles of a sequence, on average
