@@ -637,6 +637,115 @@ kda_status_t kda_latent_prefill(const void *q, int64_t q_token_stride, int64_t q
                                 int32_t d_nope, int32_t d_pe, int32_t d_v, kda_dtype_t dtype, float scale,
                                 void *o, float *lse, uint32_t *device_errors, void *stream, uint32_t flags);
 
+/*
+ * ---------------------------------------------------------------------------------
+ * What stands around the recurrence in a recurrent layer: the projections before and
+ * after it, the short causal convolution of their outputs ("K3 attention, three-piece
+ * set", KDA engineering notes: q and k pass a short causal convolution and then L2
+ * normalisation), and the selective scan, the sibling recurrence whose transition is
+ * diagonal.  The two recurrent calls share their packing and states:
+ *
+ *  cu_seqlens  [num_seqs + 1] int32 device offsets, 0 = cu[0] <= ... <= cu[num_seqs] <=
+ *              total_tokens; rows of y from cu[num_seqs] on are left as they were (the
+ *              padding of a captured batch).  NULL: num_seqs sequences of total_tokens /
+ *              num_seqs tokens each, which has to divide evenly: one prompt, a batch of
+ *              equal ones, or a generated token of every sequence.  A malformed array is
+ *              reported (KDA_DEVICE_ERR_SEQLENS) and held to the buffers; rows of
+ *              sequences that overlap are unspecified
+ *  init_state, init_slots    entry init_slots[n] (NULL: entry n) of init_state is what
+ *              sequence n starts from; -1, or init_state NULL: zero
+ *  final_state, final_slots  entry final_slots[n] (NULL: n) of final_state receives what
+ *              it ends in; -1, or final_state NULL: not kept.  A sequence without tokens
+ *              ends in what it starts from.  The entries that a call writes are distinct,
+ *              and none is another sequence's start; a sequence's own may be its start
+ *              (updated in place).  An index outside the num_init_slots (num_final_slots)
+ *              entries: KDA_DEVICE_ERR_SLOT; the sequence starts from zero and is not kept
+ *
+ * Tensors of a call are bf16 or fp32 (dtype) where nothing else is said, sums and states
+ * of the scan are fp32, and each output is rounded once.  device_errors as for the
+ * latent calls.  The kernels run on the current device, where all addresses have to be.
+ */
+typedef enum {
+    KDA_ACT_NONE = 0,
+    KDA_ACT_SILU = 1,     /* v / (1 + e^-v) */
+    KDA_ACT_GELU = 2,     /* v (1 + erf(v / sqrt 2)) / 2 */
+    KDA_ACT_SIGMOID = 3,  /* 1 / (1 + e^-v) */
+    KDA_ACT_SOFTPLUS = 4  /* log(1 + e^v) */
+} kda_activation_t;
+
+/*
+ * y_mn = act(sum_k x_mk w_nk + bias_n) + residual_mn: a projection with its bias, its
+ * activation and the residual stream that it is added to (beta of kda_prefill, for
+ * instance, is KDA_ACT_SIGMOID with fp32 outputs).
+ *
+ *  x         [rows, in_features], row stride; w [out_features, in_features], row stride
+ *            (rows may be shared or overlap); bias [out_features] dtype, or NULL
+ *  residual  [rows, out_features] out_dtype, row stride, or NULL; may be y itself
+ *  y         [rows, out_features] out_dtype, row stride >= out_features; overlaps no
+ *            other argument (the residual apart)
+ *  out_dtype dtype, or KDA_DTYPE_F32 for bf16 inputs
+ * Products are exact and sums fp32.  Addresses are aligned to their elements.  bf16 runs on
+ * the tensor cores where x and w start on 16 bytes and their strides (>= in_features) and
+ * in_features are multiples of 8, else, as fp32, on the CUDA cores.  The same arguments
+ * give the same bits on every call.
+ */
+kda_status_t kda_linear(const void *x, int64_t x_stride, const void *w, int64_t w_stride, const void *bias,
+                        const void *residual, int64_t residual_stride, void *y, int64_t y_stride, int64_t rows,
+                        int32_t out_features, int32_t in_features, kda_dtype_t dtype, kda_dtype_t out_dtype,
+                        kda_activation_t activation, void *stream);
+
+/*
+ * y_tc = act(bias_c + sum_{j < width} weight_cj x_{t - width + 1 + j, c}), per channel and
+ * causal within each sequence; rows before a sequence's first come from its state, the
+ * last width - 1 rows of what came before, oldest first.  The new state is the last width - 1
+ * rows of [state; x].  One token of every sequence is a call with cu_seqlens NULL and
+ * num_seqs = total_tokens.
+ *
+ *  x         [total_tokens, channels], row stride (part of a joint projection's rows);
+ *            channels a multiple of 8
+ *  weight    [channels, width] contiguous, width 2, 3 or 4; bias [channels] or NULL
+ *  y         [parts, total_tokens, channels / parts], part and row strides: channel c of
+ *            token t is in part c / (channels / parts), so that q, k and v of one joint
+ *            projection come out as kda_prefill takes them.  channels / parts is a multiple of 8;
+ *            y overlaps neither x nor the states
+ *  states    [entries, width - 1, channels] dtype, contiguous
+ *  activation  KDA_ACT_NONE or KDA_ACT_SILU
+ * Strides are in elements and a multiple of 16 bytes, bases 16-byte aligned.
+ */
+kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *weight, const void *bias, int32_t width,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t channels,
+                            int32_t parts, kda_dtype_t dtype, kda_activation_t activation, const void *init_state,
+                            const int32_t *init_slots, int64_t num_init_slots, void *final_state,
+                            const int32_t *final_slots, int64_t num_final_slots, void *y, int64_t y_part_stride,
+                            int64_t y_stride, uint32_t *device_errors, void *stream);
+
+/*
+ * Selective state space scan.  With d_tc = softplus(dt_tc + dt_bias_c), or dt_tc + dt_bias_c
+ * without KDA_SCAN_SOFTPLUS, per channel c of group g = c / (channels / num_groups) and
+ * state n < d_state:
+ *
+ *     h_cn <- exp(d_tc A_cn) h_cn + d_tc B_tgn x_tc
+ *     y_tc  = (sum_n C_tgn h_cn + D_c x_tc) silu(z_tc)
+ *
+ *  x, dt, z  [total_tokens, channels], row strides; z NULL: no gate
+ *  A         [channels, d_state] fp32; D, dt_bias [channels] fp32 or NULL (zero)
+ *  B, C      [total_tokens, num_groups, d_state], row strides (parts of one projection's rows)
+ *  states    [entries, channels, d_state] fp32, contiguous
+ *  y         [total_tokens, channels], row stride; overlaps none of the inputs
+ * channels / num_groups is a multiple of 8, d_state 8, 16, 32 or 64.  Strides are in elements
+ * and a multiple of 16 bytes, bases 16-byte aligned.  One token of every sequence is a call
+ * with cu_seqlens NULL and num_seqs = total_tokens.
+ */
+#define KDA_SCAN_SOFTPLUS 1u
+kda_status_t kda_selective_scan(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const float *A,
+                                const void *B, int64_t b_stride, const void *C, int64_t c_stride, const float *D,
+                                const void *z, int64_t z_stride, const float *dt_bias, const int32_t *cu_seqlens,
+                                int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t num_groups,
+                                int32_t d_state, kda_dtype_t dtype, const float *init_state, const int32_t *init_slots,
+                                int64_t num_init_slots, float *final_state, const int32_t *final_slots,
+                                int64_t num_final_slots, void *y, int64_t y_stride, uint32_t *device_errors,
+                                void *stream, uint32_t flags);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *kda_status_string(kda_status_t status);
 

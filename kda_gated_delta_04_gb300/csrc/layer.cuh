@@ -1,0 +1,117 @@
+// layer.cuh -- what stands around the recurrence in a recurrent layer (projections, short causal
+// convolution, selective scan): problem descriptions and device helpers shared by their kernels.
+#pragma once
+
+#include "latent.cuh"  // (kernel launches that overlap the end of the one before: latent_launch)
+
+namespace kda {
+
+struct Linear {
+    const void *x, *w, *bias, *residual;  // bias, residual may be null
+    int64_t xs, ws, rs, ys;               // row strides, elements
+    void *y;
+    int64_t rows;
+    int n, k;                             // outputs and inputs of a row
+    kda_dtype_t dtype, out_dtype;
+    kda_activation_t act;
+    cudaStream_t stream;
+};
+
+// Packed sequences and the entries that hold their states.
+struct Packed {
+    const int32_t *cu;                    // null: sequences of `each` tokens
+    int num_seqs;
+    int64_t tokens;
+    int each;
+    const void *init;
+    void *fin;                            // both may be null
+    const int32_t *init_slots, *fin_slots;
+    int64_t num_init, num_fin;
+    uint32_t *errors;
+};
+
+struct ShortConv {
+    Packed seq;
+    const void *x, *weight, *bias;        // bias may be null
+    int64_t xs;
+    int channels, width, part;            // part: channels of an output part
+    void *y;
+    int64_t part_stride, ys;
+    bool silu;
+    kda_dtype_t dtype;
+    cudaStream_t stream;
+};
+
+struct Scan {
+    Packed seq;
+    const void *x, *dt, *b, *c, *z;       // z may be null
+    const float *a, *d, *dt_bias;         // d, dt_bias may be null
+    int64_t xs, dts, bs, cs, zs, ys;
+    int channels, groups, states;
+    void *y;
+    bool softplus;
+    kda_dtype_t dtype;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_linear_simt(const Linear &p);
+cudaError_t launch_short_conv(const ShortConv &p);
+cudaError_t launch_scan(const Scan &p);
+cudaError_t launch_scan_step(const Scan &p);  // one token of every sequence (seq.cu null, seq.each 1)
+
+#ifdef __CUDACC__
+// Sequence n's tokens [first, end), held to the buffers whatever the offsets are.
+__device__ __forceinline__ void packed_range(const Packed &s, int n, int &first, int &end)
+{
+    if (!s.cu) {
+        first = n * s.each;
+        end = first + s.each;
+        return;
+    }
+    const int total = (int)s.tokens;
+    first = min(max(s.cu[n], 0), total);
+    end = min(max(s.cu[n + 1], first), total);
+}
+
+// Its state entries, -1 where it has none; false (both -1) for an index out of range.
+__device__ __forceinline__ bool packed_entries(const Packed &s, int n, int64_t &init, int64_t &fin)
+{
+    init = !s.init ? -1 : s.init_slots ? s.init_slots[n] : n;
+    fin = !s.fin ? -1 : s.fin_slots ? s.fin_slots[n] : n;
+    if (init >= -1 && init < s.num_init && fin >= -1 && fin < s.num_fin) return true;
+    init = fin = -1;
+    return false;
+}
+
+// One thread per entry of the offsets: whether they are a prefix sum within the tokens.
+__device__ __forceinline__ void packed_check(const Packed &s, int i)
+{
+    if (!s.cu || !s.errors || i > s.num_seqs) return;
+    const int a = s.cu[i];
+    if ((i == 0 && a != 0) || a > s.tokens || (i > 0 && a < s.cu[i - 1])) atomicOr(s.errors, DEV_ERR_SEQLENS);
+}
+
+// e^-v, 1 / x and so on as an output of type IO needs them: in fp32 correctly rounded to a few units, for
+// bf16 by the hardware's approximations (relative errors of 2^-21, against the rounding's 2^-9).
+template <typename IO>
+__device__ __forceinline__ float exp_io(float x) { return sizeof(IO) == 4 ? expf(x) : __expf(x); }
+template <typename IO>
+__device__ __forceinline__ float div_io(float a, float b) { return sizeof(IO) == 4 ? a / b : __fdividef(a, b); }
+template <typename IO>
+__device__ __forceinline__ float silu_io(float v) { return div_io<IO>(v, 1.f + exp_io<IO>(-v)); }
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+
+template <typename IO>
+__device__ __forceinline__ float activate(float v, int act)
+{
+    switch (act) {
+    case KDA_ACT_SILU: return silu_io<IO>(v);
+    case KDA_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);  // (1 + erf cancels for v << 0)
+    case KDA_ACT_SIGMOID: return div_io<IO>(1.f, 1.f + exp_io<IO>(-v));
+    case KDA_ACT_SOFTPLUS: return softplus(v);
+    default: return v;
+    }
+}
+#endif
+
+}  // namespace kda

@@ -1,0 +1,150 @@
+// layer_api.cu -- the extern "C" entry points of the projections, the short convolution and the
+// selective scan: argument validation and launches.  No compute happens here.
+#include "layer.cuh"
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool dtype_ok(kda_dtype_t dtype) { return dtype == KDA_DTYPE_BF16 || dtype == KDA_DTYPE_F32; }
+size_t elem_size(kda_dtype_t dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
+
+constexpr int64_t kMaxStride = (int64_t)1 << 38;
+// Packed tokens are counted in int32, rounded up to tiles.
+constexpr int64_t kMaxTokens = INT32_MAX - 4096;
+
+// A stride in elements: not negative and a whole number of 16-byte pieces.
+bool stride_ok(int64_t s, size_t es) { return s >= 0 && s <= kMaxStride && (size_t)s * es % 16 == 0; }
+
+// Rows of `width` elements `stride` apart share none.
+bool rows_apart(int64_t stride, int64_t rows, int64_t width) { return rows <= 1 || stride >= width; }
+
+// The packing and the states of a call; KDA_OK with num_seqs 0 where there is nothing to do.
+kda_status_t packed(kda::Packed &s, const int32_t *cu, int32_t num_seqs, int64_t tokens, const void *init,
+                    const int32_t *init_slots, int64_t num_init, void *fin, const int32_t *fin_slots, int64_t num_fin,
+                    uint32_t *errors)
+{
+    if (num_seqs < 0 || tokens < 0 || num_init < 0 || num_fin < 0) return KDA_ERR_INVALID_ARG;
+    if (num_seqs == 0 && tokens != 0) return KDA_ERR_INVALID_ARG;
+    if (!cu && num_seqs > 0 && tokens % num_seqs != 0) return KDA_ERR_INVALID_ARG;
+    if (tokens > kMaxTokens) return KDA_ERR_UNSUPPORTED;
+    if ((!init && init_slots) || (!fin && fin_slots)) return KDA_ERR_INVALID_ARG;
+    if ((init && !init_slots && num_init < num_seqs) || (fin && !fin_slots && num_fin < num_seqs)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(cu, 4) || !aligned(init, 16) || !aligned(fin, 16) || !aligned(init_slots, 4) || !aligned(fin_slots, 4) ||
+        !aligned(errors, 4))
+        return KDA_ERR_INVALID_ARG;
+    s.cu = cu; s.num_seqs = num_seqs; s.tokens = tokens; s.each = num_seqs > 0 ? (int)(tokens / num_seqs) : 0;
+    s.init = init; s.fin = fin; s.init_slots = init_slots; s.fin_slots = fin_slots;
+    s.num_init = num_init; s.num_fin = num_fin; s.errors = errors;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_linear(const void *x, int64_t x_stride, const void *w, int64_t w_stride, const void *bias,
+                        const void *residual, int64_t residual_stride, void *y, int64_t y_stride, int64_t rows,
+                        int32_t out_features, int32_t in_features, kda_dtype_t dtype, kda_dtype_t out_dtype,
+                        kda_activation_t activation, void *stream)
+{
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype) || activation < KDA_ACT_NONE || activation > KDA_ACT_SOFTPLUS)
+        return KDA_ERR_INVALID_ARG;
+    if (dtype == KDA_DTYPE_F32 && out_dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
+    if (rows < 0 || out_features < 0 || in_features <= 0) return KDA_ERR_INVALID_ARG;
+    if (rows > kMaxTokens || out_features > INT32_MAX - 4096 || in_features > INT32_MAX - 4096 ||
+        (rows / 64 + 1) * ((int64_t)out_features / 64 + 1) > INT32_MAX)  // tiles
+        return KDA_ERR_UNSUPPORTED;
+    if (rows == 0 || out_features == 0) return KDA_OK;
+    if (!x || !w || !y) return KDA_ERR_INVALID_ARG;
+    const size_t es = elem_size(dtype), eo = elem_size(out_dtype);
+    if (!aligned(x, es) || !aligned(w, es) || !aligned(bias, es) || !aligned(residual, eo) || !aligned(y, eo))
+        return KDA_ERR_INVALID_ARG;
+    auto in_range = [](int64_t s) { return s >= 0 && s <= kMaxStride; };
+    if (!in_range(x_stride) || !in_range(w_stride) || !in_range(y_stride) || (residual && !in_range(residual_stride)) ||
+        !rows_apart(y_stride, rows, out_features))
+        return KDA_ERR_INVALID_ARG;
+    // in place an element is read and written by the same thread: the rows have to be the same ones
+    if (residual == y && rows > 1 && residual_stride != y_stride) return KDA_ERR_INVALID_ARG;
+    const kda_status_t st = kda::check_device();
+    if (st != KDA_OK) return st;
+    kda::Linear p;
+    p.x = x; p.w = w; p.bias = bias; p.residual = residual; p.y = y;
+    p.xs = x_stride; p.ws = w_stride; p.rs = residual_stride; p.ys = y_stride;
+    p.rows = rows; p.n = out_features; p.k = in_features;
+    p.dtype = dtype; p.out_dtype = out_dtype; p.act = activation; p.stream = static_cast<cudaStream_t>(stream);
+    return kda::launch_linear_simt(p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *weight, const void *bias, int32_t width,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t channels,
+                            int32_t parts, kda_dtype_t dtype, kda_activation_t activation, const void *init_state,
+                            const int32_t *init_slots, int64_t num_init_slots, void *final_state,
+                            const int32_t *final_slots, int64_t num_final_slots, void *y, int64_t y_part_stride,
+                            int64_t y_stride, uint32_t *device_errors, void *stream)
+{
+    if (!dtype_ok(dtype) || width <= 0 || channels <= 0 || parts <= 0 || activation < KDA_ACT_NONE ||
+        activation > KDA_ACT_SOFTPLUS)
+        return KDA_ERR_INVALID_ARG;
+    if (width < 2 || width > 4 || channels % parts != 0 || channels / parts % 8 != 0 || activation > KDA_ACT_SILU)
+        return KDA_ERR_UNSUPPORTED;
+    kda::ShortConv p;
+    kda_status_t st = packed(p.seq, cu_seqlens, num_seqs, total_tokens, init_state, init_slots, num_init_slots, final_state,
+                             final_slots, num_final_slots, device_errors);
+    if (st != KDA_OK || num_seqs == 0) return st;
+    const size_t es = elem_size(dtype);
+    if (!weight || (total_tokens > 0 && (!x || !y))) return KDA_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(y, 16)) return KDA_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, es) || !stride_ok(y_stride, es) || (parts > 1 && !stride_ok(y_part_stride, es)))
+        return KDA_ERR_INVALID_ARG;
+    // rows of y are written by different threads: nested strides, one dimension within a step of the other
+    const int64_t part = channels / parts, ps = parts > 1 ? y_part_stride : 0;
+    const int64_t inner = parts <= 1 ? y_stride : total_tokens <= 1 ? ps : ps < y_stride ? ps : y_stride;
+    const int64_t outer = ps < y_stride ? y_stride : ps, steps = ps < y_stride ? parts - 1 : total_tokens - 1;
+    if ((parts > 1 || total_tokens > 1) && inner < part) return KDA_ERR_INVALID_ARG;
+    if (parts > 1 && total_tokens > 1 && (outer - part) / steps < inner) return KDA_ERR_INVALID_ARG;
+    st = kda::check_device();
+    if (st != KDA_OK) return st;
+    p.x = x; p.weight = weight; p.bias = bias; p.xs = x_stride;
+    p.channels = channels; p.width = width; p.part = (int)part;
+    p.y = y; p.part_stride = ps; p.ys = y_stride; p.silu = activation == KDA_ACT_SILU;
+    p.dtype = dtype; p.stream = static_cast<cudaStream_t>(stream);
+    return kda::launch_short_conv(p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status_t kda_selective_scan(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const float *A,
+                                const void *B, int64_t b_stride, const void *C, int64_t c_stride, const float *D,
+                                const void *z, int64_t z_stride, const float *dt_bias, const int32_t *cu_seqlens,
+                                int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t num_groups,
+                                int32_t d_state, kda_dtype_t dtype, const float *init_state, const int32_t *init_slots,
+                                int64_t num_init_slots, float *final_state, const int32_t *final_slots,
+                                int64_t num_final_slots, void *y, int64_t y_stride, uint32_t *device_errors,
+                                void *stream, uint32_t flags)
+{
+    if (flags & ~KDA_SCAN_SOFTPLUS) return KDA_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || channels <= 0 || num_groups <= 0 || d_state <= 0) return KDA_ERR_INVALID_ARG;
+    if ((d_state != 8 && d_state != 16 && d_state != 32 && d_state != 64) || channels % num_groups != 0 ||
+        channels / num_groups % 8 != 0)
+        return KDA_ERR_UNSUPPORTED;
+    kda::Scan p;
+    kda_status_t st = packed(p.seq, cu_seqlens, num_seqs, total_tokens, init_state, init_slots, num_init_slots, final_state,
+                             final_slots, num_final_slots, device_errors);
+    if (st != KDA_OK || num_seqs == 0) return st;
+    const size_t es = elem_size(dtype);
+    if (!A || (total_tokens > 0 && (!x || !dt || !B || !C || !y))) return KDA_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(dt, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(D, 16) ||
+        !aligned(z, 16) || !aligned(dt_bias, 16) || !aligned(y, 16))
+        return KDA_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, es) || !stride_ok(dt_stride, es) || !stride_ok(b_stride, es) || !stride_ok(c_stride, es) ||
+        (z && !stride_ok(z_stride, es)) || !stride_ok(y_stride, es) || !rows_apart(y_stride, total_tokens, channels))
+        return KDA_ERR_INVALID_ARG;
+    st = kda::check_device();
+    if (st != KDA_OK) return st;
+    p.x = x; p.dt = dt; p.b = B; p.c = C; p.z = z; p.a = A; p.d = D; p.dt_bias = dt_bias;
+    p.xs = x_stride; p.dts = dt_stride; p.bs = b_stride; p.cs = c_stride; p.zs = z_stride; p.ys = y_stride;
+    p.channels = channels; p.groups = num_groups; p.states = d_state; p.y = y;
+    p.softplus = (flags & KDA_SCAN_SOFTPLUS) != 0; p.dtype = dtype; p.stream = static_cast<cudaStream_t>(stream);
+    const bool step = !cu_seqlens && p.seq.each == 1;
+    return (step ? kda::launch_scan_step(p) : kda::launch_scan(p)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

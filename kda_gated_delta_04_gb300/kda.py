@@ -33,6 +33,8 @@ KDA_STREAM_RING_MIN = 8
 KDA_LATENT_DIM, KDA_LATENT_PE_DIM, KDA_LATENT_HEAD_DIM = 512, 64, 128
 KDA_LATENT_INTERLEAVED, KDA_LATENT_FULL = 1, 2
 KDA_LATENT_DECODE_WORKSPACE_MAX = 50331648
+KDA_ACT_NONE, KDA_ACT_SILU, KDA_ACT_GELU, KDA_ACT_SIGMOID, KDA_ACT_SOFTPLUS = range(5)
+KDA_SCAN_SOFTPLUS = 1
 
 _lib = None
 _lock = threading.Lock()
@@ -82,6 +84,15 @@ EXPORTS = {
                                       _VP, _c.c_int64, _c.c_int64, _VP, _VP, _c.c_int32, _c.c_int64, _c.c_int64,
                                       _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int, _c.c_float, _VP,
                                       _VP, _VP, _VP, _c.c_uint32]),
+    "kda_linear": (_c.c_int, [_VP, _c.c_int64, _VP, _c.c_int64, _VP, _VP, _c.c_int64, _VP, _c.c_int64, _c.c_int64,
+                              _c.c_int32, _c.c_int32, _c.c_int, _c.c_int, _c.c_int, _VP]),
+    "kda_short_conv": (_c.c_int, [_VP, _c.c_int64, _VP, _VP, _c.c_int32, _VP, _c.c_int32, _c.c_int64, _c.c_int32,
+                                  _c.c_int32, _c.c_int, _c.c_int, _VP, _VP, _c.c_int64, _VP, _VP, _c.c_int64, _VP,
+                                  _c.c_int64, _c.c_int64, _VP, _VP]),
+    "kda_selective_scan": (_c.c_int, [_VP, _c.c_int64, _VP, _c.c_int64, _VP, _VP, _c.c_int64, _VP, _c.c_int64, _VP,
+                                      _VP, _c.c_int64, _VP, _VP, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32,
+                                      _c.c_int32, _c.c_int, _VP, _VP, _c.c_int64, _VP, _VP, _c.c_int64, _VP,
+                                      _c.c_int64, _VP, _VP, _c.c_uint32]),
     "kda_prefill_slots": (_c.c_int, _PREFILL_ARGS[:12] + [_VP, _c.c_int32, _VP, _VP, _VP, _VP,
                                                           _c.c_size_t, _VP, _c.c_uint32]),
 }
@@ -232,6 +243,21 @@ def kda_latent_decode(*args):
 def kda_latent_prefill(*args):
     """The C entry point; arguments as in include/kda.h."""
     return lib().kda_latent_prefill(*args)
+
+
+def kda_linear(*args):
+    """The C entry point; arguments as in include/kda.h."""
+    return lib().kda_linear(*args)
+
+
+def kda_short_conv(*args):
+    """The C entry point; arguments as in include/kda.h."""
+    return lib().kda_short_conv(*args)
+
+
+def kda_selective_scan(*args):
+    """The C entry point; arguments as in include/kda.h."""
+    return lib().kda_selective_scan(*args)
 
 
 def kda_diag_tensor_phases(pass_, reps, workspace, stream, tflops):
@@ -769,3 +795,172 @@ def latent_prefill(q, k_nope, k_pe, v, scale, cu_q=None, cu_k=None, *, causal=Tr
     if st != KDA_OK:
         raise KdaError(st, "kda_latent_prefill")
     return o, lse
+
+
+# ------------------------------------------------------------------ around the recurrence
+_ACTIVATIONS = {None: KDA_ACT_NONE, "silu": KDA_ACT_SILU, "gelu": KDA_ACT_GELU, "sigmoid": KDA_ACT_SIGMOID,
+                "softplus": KDA_ACT_SOFTPLUS}
+
+
+def _activation(name):
+    try:
+        return _ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"activation must be None or one of {[a for a in _ACTIVATIONS if a]}, got {name!r}") from None
+
+
+def linear(x, w, bias=None, *, activation=None, residual=None, out=None, out_dtype=None, stream=None):
+    """act(x @ w.T + bias) + residual: x [M, K], w [N, K], bias [N], residual [M, N] (may be out itself:
+    added in place).  activation: None, "silu", "gelu" (erf), "sigmoid" or "softplus".  bf16 or fp32; of
+    bf16 inputs the output and the residual may be fp32 (out_dtype, or out's).  Rows may be strided.
+    bf16 runs on the tensor cores where the rows start on 16 bytes.  The tensors are on the current device (this
+    holds for every call of this section).  Returns out [M, N]."""
+    torch = _torch_module or _load_torch()
+    code, dt, dev = _latent_like(x, "x", 2)
+    M, K = x.shape
+    N = w.shape[0] if w.dim() == 2 else -1
+    if out is None:
+        out = _empty((M, N), out_dtype or dt, dev, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    odt = out.dtype
+    xp, xs = _rows2(x, "x", dt, dev, (M, K))
+    wp, ws = _rows2(w, "w", dt, dev, (N, K))
+    yp, ys = _rows2(out, "out", odt, dev, (M, N))
+    rp, rs = (None, 0) if residual is None else _rows2(residual, "residual", odt, dev, (M, N))
+    st = (_lib or lib()).kda_linear(
+        xp, xs, wp, ws, None if bias is None else _flat(bias, "bias", dt, dev, (N,)), rp, rs, yp, ys, M, N, K, code,
+        _dtype_code(out), _activation(activation), _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear")
+    return out
+
+
+def _entries(state, slots, name, dtype, dev, tail, seqs):
+    """Addresses of a state pool (or of a state per sequence) and of its slots, and its number of entries."""
+    if state is None:
+        if slots is not None:
+            raise ValueError(f"slots without {name}")
+        return None, None, 0
+    count = state.shape[0] if state.dim() > 0 else -1
+    return (_flat(state, name, dtype, dev, (count, *tail)),
+            None if slots is None else _flat(slots, f"slots of {name}", _torch_module.int32, dev, (seqs,)), count)
+
+
+def _short_conv(x, weight, bias, cu_seqlens, seqs, init_state, init_slots, final_state, final_slots, activation, parts, out,
+                errors, stream):
+    torch = _torch_module or _load_torch()
+    code, dt, dev = _latent_like(x, "x", 2)
+    T, C = x.shape
+    width = weight.shape[1] if weight.dim() == 2 else -1
+    if not isinstance(parts, int) or parts < 1 or C % parts:
+        raise ValueError(f"parts must divide the {C} channels, got {parts!r}")
+    shape = (T, C) if parts == 1 else (parts, T, C // parts)
+    if out is None:
+        out = _empty(shape, dt, dev, stream)
+    xp, xs = _rows2(x, "x", dt, dev, (T, C))
+    if parts == 1:
+        ps, (yp, ys) = 0, _rows2(out, "out", dt, dev, shape)
+    else:
+        yp, ps, ys = _rows3(out, "out", dt, dev, shape)
+    cu = None if cu_seqlens is None else _flat(cu_seqlens, "cu_seqlens", torch.int32, dev, (seqs + 1,))
+    ip, isl, inum = _entries(init_state, init_slots, "init_state", dt, dev, (width - 1, C), seqs)
+    fp, fsl, fnum = _entries(final_state, final_slots, "final_state", dt, dev, (width - 1, C), seqs)
+    st = (_lib or lib()).kda_short_conv(
+        xp, xs, _flat(weight, "weight", dt, dev, (C, width)), None if bias is None else _flat(bias, "bias", dt, dev, (C,)),
+        width, cu, seqs, T, C, parts, code, _activation(activation), ip, isl, inum, fp, fsl, fnum, yp, ps, ys,
+        None if errors is None else _flat(errors, "errors", torch.int32, dev, (1,)), _raw_stream(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_short_conv")
+    return out
+
+
+def short_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, activation="silu", parts=1, out=None,
+               final_state=None, init_slots=None, final_slots=None, errors=None, stream=None):
+    """Short causal convolution over packed sequences: x [T, C] (rows may be strided), weight [C, W] (W of
+    2 to 4 taps, the last one the token's own), bias [C], cu_seqlens int32 [N + 1] (None: one sequence; rows
+    from cu_seqlens[-1] on are left alone).  init_state and final_state [N, W - 1, C], the rows before a
+    sequence's first token and its last ones; with init_slots, final_slots (int32 [N], -1: none) entries of
+    a pool instead.  activation "silu" or None.  parts: the output is [parts, T, C / parts], q, k and v of a joint
+    projection one after the other, say; parts = 1: [T, C].  Returns (out, final_state); without final_state it is
+    allocated.  errors: int32 [1] that collects KDA_DEVICE_ERR_* bits."""
+    torch = _torch_module or _load_torch()
+    _, dt, dev = _latent_like(x, "x", 2)
+    seqs = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if final_state is None and final_slots is None:
+        final_state = _empty((seqs, weight.shape[-1] - 1, x.shape[1]), dt, dev, stream)
+    out = _short_conv(x, weight, bias, cu_seqlens, seqs, init_state, init_slots, final_state, final_slots, activation,
+                      parts, out, errors, stream)
+    return out, final_state
+
+
+def short_conv_step(x, weight, state, bias=None, *, activation="silu", parts=1, slots=None, new_state=None, out=None,
+                    errors=None, stream=None):
+    """short_conv of one token of every sequence: x [B, C], state [B, W - 1, C], or a pool of entries of
+    which slots (int32 [B], distinct; -1: none) are the sequences'.  The state is updated in place, or, with
+    new_state, read from state and written to the same entries there.  Returns out ([B, C], or [parts, B, C / parts])."""
+    return _short_conv(x, weight, bias, None, x.shape[0], state, slots, state if new_state is None else new_state, slots,
+                       activation, parts, out, errors, stream)
+
+
+def _selective_scan(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, seqs, init_state, init_slots, final_state, final_slots,
+                    softplus, out, errors, stream):
+    torch = _torch_module or _load_torch()
+    code, ty, dev = _latent_like(x, "x", 2)
+    f32 = torch.float32
+    T, channels = x.shape
+    n = A.shape[1] if A.dim() == 2 else -1
+    if out is None:
+        out = _empty((T, channels), ty, dev, stream)
+    xp, xs = _rows2(x, "x", ty, dev, (T, channels))
+    dp, ds = _rows2(dt, "dt", ty, dev, (T, channels))
+    zp, zs = (None, 0) if z is None else _rows2(z, "z", ty, dev, (T, channels))
+    yp, ys = _rows2(out, "out", ty, dev, (T, channels))
+    if B.dim() == 3:  # groups
+        groups = B.shape[1]
+        if B.stride(1) != n and groups > 1 or C.dim() == 3 and C.stride(1) != n and groups > 1:
+            raise ValueError("the groups of B and C must follow one another")
+        bp, bs, _ = _rows3(B, "B", ty, dev, (T, groups, n))
+        cp, cs, _ = _rows3(C, "C", ty, dev, (T, groups, n))
+    else:
+        groups = 1
+        bp, bs = _rows2(B, "B", ty, dev, (T, n))
+        cp, cs = _rows2(C, "C", ty, dev, (T, n))
+    cu = None if cu_seqlens is None else _flat(cu_seqlens, "cu_seqlens", torch.int32, dev, (seqs + 1,))
+    ip, isl, inum = _entries(init_state, init_slots, "init_state", f32, dev, (channels, n), seqs)
+    fp, fsl, fnum = _entries(final_state, final_slots, "final_state", f32, dev, (channels, n), seqs)
+    st = (_lib or lib()).kda_selective_scan(
+        xp, xs, dp, ds, _flat(A, "A", f32, dev, (channels, n)), bp, bs, cp, cs,
+        None if D is None else _flat(D, "D", f32, dev, (channels,)), zp, zs,
+        None if dt_bias is None else _flat(dt_bias, "dt_bias", f32, dev, (channels,)), cu, seqs, T, channels, groups, n,
+        code, ip, isl, inum, fp, fsl, fnum, yp, ys,
+        None if errors is None else _flat(errors, "errors", torch.int32, dev, (1,)), _raw_stream(stream, dev),
+        KDA_SCAN_SOFTPLUS if softplus else 0)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_selective_scan")
+    return out
+
+
+def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seqlens=None, init_state=None, *, softplus=True,
+                   out=None, final_state=None, init_slots=None, final_slots=None, errors=None, stream=None):
+    """Selective state space scan over packed sequences: h <- exp(d A) h + d B x, y = (C h + D x) silu(z) with
+    d = softplus(dt + dt_bias) (softplus=False: dt + dt_bias).  x, dt, z [T, channels]; A [channels, n] fp32; B, C
+    [T, n], or [T, groups, n] for channels in groups; D, dt_bias [channels] fp32; rows may be strided.  n: 8, 16, 32 or
+    64.  cu_seqlens, the states (fp32 [N, channels, n]), slots and errors as short_conv.  Returns (y, final_state)."""
+    torch = _torch_module or _load_torch()
+    _, _, dev = _latent_like(x, "x", 2)
+    seqs = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if final_state is None and final_slots is None:
+        final_state = _empty((seqs, *A.shape), torch.float32, dev, stream)
+    out = _selective_scan(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, seqs, init_state, init_slots, final_state, final_slots,
+                          softplus, out, errors, stream)
+    return out, final_state
+
+
+def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, *, softplus=True, slots=None, new_state=None,
+                        out=None, errors=None, stream=None):
+    """selective_scan of one token of every sequence (T = B of them): state [B, channels, n] fp32, or a pool of
+    entries of which slots (int32 [B], distinct; -1: none) are the sequences'; updated in place, or, with
+    new_state, read from state and written to the same entries there.  Returns y [B, channels]."""
+    return _selective_scan(x, dt, A, B, C, D, z, dt_bias, None, x.shape[0], state, slots,
+                           state if new_state is None else new_state, slots, softplus, out, errors, stream)
