@@ -692,7 +692,7 @@ typedef enum {
 kda_status_t kda_linear(const void *x, int64_t x_stride, const void *w, int64_t w_stride, const void *bias,
                         const void *residual, int64_t residual_stride, void *y, int64_t y_stride, int64_t rows,
                         int32_t out_features, int32_t in_features, kda_dtype_t dtype, kda_dtype_t out_dtype,
-                        kda_activation_t activation, void *stream);
+                        kda_activation_t activation, uint32_t *device_errors, void *stream);
 
 /*
  * y_tc = act(bias_c + sum_{j < width} weight_cj x_{t - width + 1 + j, c}), per channel and

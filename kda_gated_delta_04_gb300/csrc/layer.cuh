@@ -14,6 +14,7 @@ struct Linear {
     int n, k;                             // outputs and inputs of a row
     kda_dtype_t dtype, out_dtype;
     kda_activation_t act;
+    uint32_t *errors;
     cudaStream_t stream;
 };
 
@@ -55,6 +56,8 @@ struct Scan {
 };
 
 cudaError_t launch_linear_simt(const Linear &p);
+bool linear_tc_takes(const Linear &p);  // bf16 with rows that the tensor cores' copies can read
+cudaError_t launch_linear_tc(const Linear &p);
 cudaError_t launch_short_conv(const ShortConv &p);
 cudaError_t launch_scan(const Scan &p);
 cudaError_t launch_scan_step(const Scan &p);  // one token of every sequence (seq.cu null, seq.each 1)

@@ -45,7 +45,7 @@ extern "C" {
 kda_status_t kda_linear(const void *x, int64_t x_stride, const void *w, int64_t w_stride, const void *bias,
                         const void *residual, int64_t residual_stride, void *y, int64_t y_stride, int64_t rows,
                         int32_t out_features, int32_t in_features, kda_dtype_t dtype, kda_dtype_t out_dtype,
-                        kda_activation_t activation, void *stream)
+                        kda_activation_t activation, uint32_t *device_errors, void *stream)
 {
     if (!dtype_ok(dtype) || !dtype_ok(out_dtype) || activation < KDA_ACT_NONE || activation > KDA_ACT_SOFTPLUS)
         return KDA_ERR_INVALID_ARG;
@@ -57,7 +57,8 @@ kda_status_t kda_linear(const void *x, int64_t x_stride, const void *w, int64_t 
     if (rows == 0 || out_features == 0) return KDA_OK;
     if (!x || !w || !y) return KDA_ERR_INVALID_ARG;
     const size_t es = elem_size(dtype), eo = elem_size(out_dtype);
-    if (!aligned(x, es) || !aligned(w, es) || !aligned(bias, es) || !aligned(residual, eo) || !aligned(y, eo))
+    if (!aligned(x, es) || !aligned(w, es) || !aligned(bias, es) || !aligned(residual, eo) || !aligned(y, eo) ||
+        !aligned(device_errors, 4))
         return KDA_ERR_INVALID_ARG;
     auto in_range = [](int64_t s) { return s >= 0 && s <= kMaxStride; };
     if (!in_range(x_stride) || !in_range(w_stride) || !in_range(y_stride) || (residual && !in_range(residual_stride)) ||
@@ -71,8 +72,10 @@ kda_status_t kda_linear(const void *x, int64_t x_stride, const void *w, int64_t 
     p.x = x; p.w = w; p.bias = bias; p.residual = residual; p.y = y;
     p.xs = x_stride; p.ws = w_stride; p.rs = residual_stride; p.ys = y_stride;
     p.rows = rows; p.n = out_features; p.k = in_features;
-    p.dtype = dtype; p.out_dtype = out_dtype; p.act = activation; p.stream = static_cast<cudaStream_t>(stream);
-    return kda::launch_linear_simt(p) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    p.dtype = dtype; p.out_dtype = out_dtype; p.act = activation; p.errors = device_errors;
+    p.stream = static_cast<cudaStream_t>(stream);
+    return (kda::linear_tc_takes(p) ? kda::launch_linear_tc(p) : kda::launch_linear_simt(p)) == cudaSuccess ? KDA_OK
+                                                                                                            : KDA_ERR_CUDA;
 }
 
 kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *weight, const void *bias, int32_t width,

@@ -85,7 +85,7 @@ EXPORTS = {
                                       _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int, _c.c_float, _VP,
                                       _VP, _VP, _VP, _c.c_uint32]),
     "kda_linear": (_c.c_int, [_VP, _c.c_int64, _VP, _c.c_int64, _VP, _VP, _c.c_int64, _VP, _c.c_int64, _c.c_int64,
-                              _c.c_int32, _c.c_int32, _c.c_int, _c.c_int, _c.c_int, _VP]),
+                              _c.c_int32, _c.c_int32, _c.c_int, _c.c_int, _c.c_int, _VP, _VP]),
     "kda_short_conv": (_c.c_int, [_VP, _c.c_int64, _VP, _VP, _c.c_int32, _VP, _c.c_int32, _c.c_int64, _c.c_int32,
                                   _c.c_int32, _c.c_int, _c.c_int, _VP, _VP, _c.c_int64, _VP, _VP, _c.c_int64, _VP,
                                   _c.c_int64, _c.c_int64, _VP, _VP]),
@@ -809,12 +809,14 @@ def _activation(name):
         raise ValueError(f"activation must be None or one of {[a for a in _ACTIVATIONS if a]}, got {name!r}") from None
 
 
-def linear(x, w, bias=None, *, activation=None, residual=None, out=None, out_dtype=None, stream=None):
+def linear(x, w, bias=None, *, activation=None, residual=None, out=None, out_dtype=None, errors=None,
+           stream=None):
     """act(x @ w.T + bias) + residual: x [M, K], w [N, K], bias [N], residual [M, N] (may be out itself:
     added in place).  activation: None, "silu", "gelu" (erf), "sigmoid" or "softplus".  bf16 or fp32; of
     bf16 inputs the output and the residual may be fp32 (out_dtype, or out's).  Rows may be strided.
-    bf16 runs on the tensor cores where the rows start on 16 bytes.  The tensors are on the current device (this
-    holds for every call of this section).  Returns out [M, N]."""
+    bf16 runs on the tensor cores where the rows start on 16 bytes.  errors: int32 [1] that collects
+    KDA_DEVICE_ERR_* bits.  The tensors are on the current device (this holds for every call of this section).
+    Returns out [M, N]."""
     torch = _torch_module or _load_torch()
     code, dt, dev = _latent_like(x, "x", 2)
     M, K = x.shape
@@ -830,7 +832,8 @@ def linear(x, w, bias=None, *, activation=None, residual=None, out=None, out_dty
     rp, rs = (None, 0) if residual is None else _rows2(residual, "residual", odt, dev, (M, N))
     st = (_lib or lib()).kda_linear(
         xp, xs, wp, ws, None if bias is None else _flat(bias, "bias", dt, dev, (N,)), rp, rs, yp, ys, M, N, K, code,
-        _dtype_code(out), _activation(activation), _raw_stream(stream, dev))
+        _dtype_code(out), _activation(activation), None if errors is None else _flat(errors, "errors", torch.int32, dev, (1,)),
+        _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear")
     return out

@@ -11,7 +11,7 @@ BIG = 2 ** 31 - 1
 
 def linear_args(**over):
     a = dict(x=FAKE, x_stride=64, w=FAKE, w_stride=64, bias=FAKE, residual=2 * FAKE, residual_stride=32, y=FAKE, y_stride=32,
-             rows=4, out_features=32, in_features=64, dtype=0, out_dtype=0, activation=1, stream=None)
+             rows=4, out_features=32, in_features=64, dtype=0, out_dtype=0, activation=1, errors=FAKE, stream=None)
     assert set(over) <= set(a)
     a.update(over)
     return a.values()
@@ -20,7 +20,7 @@ def linear_args(**over):
 @pytest.mark.parametrize("over,expected", [
     (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(x=FAKE + 1), INVALID),
     (dict(w=FAKE + 2, dtype=1, out_dtype=1), INVALID), (dict(bias=FAKE + 1), INVALID), (dict(residual=FAKE + 2, out_dtype=1), INVALID),
-    (dict(y=FAKE + 1), INVALID), (dict(x_stride=-1), INVALID), (dict(w_stride=-64), INVALID), (dict(y_stride=31), INVALID),
+    (dict(y=FAKE + 1), INVALID), (dict(errors=FAKE + 2), INVALID), (dict(x_stride=-1), INVALID), (dict(w_stride=-64), INVALID), (dict(y_stride=31), INVALID),
     (dict(y_stride=0), INVALID), (dict(residual_stride=-1), INVALID), (dict(residual=FAKE, residual_stride=40), INVALID),
     (dict(y_stride=2 ** 39), INVALID), (dict(rows=-1), INVALID), (dict(out_features=-1), INVALID), (dict(in_features=0), INVALID),
     (dict(dtype=2), INVALID), (dict(out_dtype=-1), INVALID), (dict(activation=5), INVALID), (dict(activation=-1), INVALID),
