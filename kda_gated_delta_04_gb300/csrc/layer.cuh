@@ -2,6 +2,7 @@
 // convolution, selective scan): problem descriptions and device helpers shared by their kernels.
 #pragma once
 
+#include "latent_ptx.cuh"
 #include "latent.cuh"  // (kernel launches that overlap the end of the one before: latent_launch)
 
 namespace kda {
@@ -94,16 +95,43 @@ __device__ __forceinline__ void packed_check(const Packed &s, int i)
     if ((i == 0 && a != 0) || a > s.tokens || (i > 0 && a < s.cu[i - 1])) atomicOr(s.errors, DEV_ERR_SEQLENS);
 }
 
-// e^-v, 1 / x and so on as an output of type IO needs them: in fp32 correctly rounded to a few units, for
-// bf16 by the hardware's approximations (relative errors of 2^-21, against the rounding's 2^-9).
+// e^v, a / b and so on as an output of type IO needs them: in fp32 good to a few units, for bf16 by the hardware's
+// approximations (relative errors of 2^-21, against the rounding's 2^-9; what is subnormal becomes zero).
+__device__ __forceinline__ float exp_fast(float v)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v * kLatLog2e));
+    return y;
+}
 template <typename IO>
-__device__ __forceinline__ float exp_io(float x) { return sizeof(IO) == 4 ? expf(x) : __expf(x); }
+__device__ __forceinline__ float exp_io(float v) { return sizeof(IO) == 4 ? expf(v) : exp_fast(v); }
 template <typename IO>
-__device__ __forceinline__ float div_io(float a, float b) { return sizeof(IO) == 4 ? a / b : __fdividef(a, b); }
+__device__ __forceinline__ float div_io(float a, float b)
+{
+    if (sizeof(IO) == 4) return a / b;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+    return a * r;
+}
 template <typename IO>
 __device__ __forceinline__ float silu_io(float v) { return div_io<IO>(v, 1.f + exp_io<IO>(-v)); }
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
-
+// max(v, 0) + log1p(e^-|v|); log1p(u) / u on [0, 1] by the polynomial of degree 9 with the least relative error
+// (Remez exchange; 5e-9, in fp32 arithmetic 2.5 units of 2^-24), a quarter of the instructions of log1pf.
+__device__ __forceinline__ float softplus(float v)
+{
+    const float u = exp_fast(-fabsf(v));
+    float q = -3.244025167e-03f;
+    q = fmaf(q, u, 1.985146292e-02f);
+    q = fmaf(q, u, -5.695953593e-02f);
+    q = fmaf(q, u, 1.060365513e-01f);
+    q = fmaf(q, u, -1.530559212e-01f);
+    q = fmaf(q, u, 1.967593879e-01f);
+    q = fmaf(q, u, -2.495413423e-01f);
+    q = fmaf(q, u, 3.332996368e-01f);
+    q = fmaf(q, u, -4.999990165e-01f);
+    q = fmaf(q, u, 1.f);
+    return fmaf(u, q, fmaxf(v, 0.f));
+}
 template <typename IO>
 __device__ __forceinline__ float activate(float v, int act)
 {

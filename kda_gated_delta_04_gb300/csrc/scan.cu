@@ -4,13 +4,17 @@
 //   y_c = (sum_n C_n h_cn + D_c x_c) silu(z_c)
 //
 // Per token and channel d_state exponentials and 5 d_state other operations against 8 bytes of bf16: bound by
-// the exponential units (16 a cycle and SM).  Only h's product and sum are in order of the tokens, 4 cycles each,
-// so that the scan stays in order and the channels fill the GPU: 32 channels of 16 states a CTA, four states a
-// thread.
+// instructions and by the bytes that shared memory gives to registers.  Only h's products and sums are in order of
+// the tokens, 4 cycles each, so that a sequence stays in order and its channels fill the GPU.
 //
-// Warps 0 to 3 scan; warps 4 to 7 bring the tokens in and out, kChunk at a time, a chunk ahead and one behind:
-// d and d x, which all states of a channel share, are computed once and handed over in shared memory, as are
-// the sums, to which D x and the gate are applied where they are stored.
+// A CTA takes 8 to 32 channels of a sequence, each spread over the threads of N / S lanes with S states each; the
+// states that share a warp's loads of B and C and the channels that share those of d and d x are as many as registers
+// allow.  Four warps bring the tokens in and four take them out, a chunk ahead and one behind: d and d x, which all
+// states of a channel share, are made once and handed over in shared memory in pairs of tokens (register pairs for
+// two products an instruction), as are the sums of each thread's states, to which D x and the gate are applied where
+// they are stored.  What the steps before this form measured, 4,096 tokens of 4,096 channels, 16 states, bf16: a chunk
+// loaded through registers one ahead 283 us; asynchronous copies four ahead 188; the states of a channel over four warps
+// instead of four lanes 163; now 140: 34 ns a token, 180 instructions of a warp (45 a scheduler) in 70 cycles.
 #include "latent_ptx.cuh"
 #include "layer.cuh"
 #include "tc_common.cuh"
@@ -18,91 +22,102 @@
 namespace kda {
 namespace {
 
-constexpr int kScanThreads = 128, kThreads = 256;
-constexpr int kChunk = 32;  // tokens handed over at a time
+constexpr int kIn = 128, kOut = 128;  // threads that bring tokens in and take them out
 
-template <typename IO> struct Raw8 { uint4 q[sizeof(IO) / 2]; };
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return d;
+}
 
-template <typename IO>
-__device__ __forceinline__ Raw8<IO> load8(const IO *p)
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p)
 {
-    Raw8<IO> r;
-#pragma unroll
-    for (size_t i = 0; i < sizeof(IO) / 2; ++i) r.q[i] = reinterpret_cast<const uint4 *>(p)[i];
-    return r;
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-template <typename IO>
-__device__ __forceinline__ void store8(IO *p, const Raw8<IO> &r)
-{
-#pragma unroll
-    for (size_t i = 0; i < sizeof(IO) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = r.q[i];
-}
-template <typename IO>
-__device__ __forceinline__ void widen(const Raw8<IO> &r, float (&x)[8])
-{
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (sizeof(IO) == 2)
-            x[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-        else
-            x[i] = __uint_as_float(w[i]);
+__device__ __forceinline__ void store2(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float2 v) { *reinterpret_cast<uint32_t *>(p) = tc::pack_bf16x2(v.x, v.y); }
+
+// B and C of a state for two tokens: of bf16 as they come, half the bytes to load, widened where they are used.
+template <typename IO> struct Pair;
+template <> struct Pair<float> {
+    float4 v;  // B0, B1, C0, C1
+    __device__ __forceinline__ float2 b() const { return make_float2(v.x, v.y); }
+    __device__ __forceinline__ float2 c() const { return make_float2(v.z, v.w); }
+    // of states n and n + 1: what both tokens have, B0, B1, C0, C1
+    using Two = float2;
+    static __device__ __forceinline__ void make(Pair *to, Two p, Two q, Two r, Two s)
+    {
+        to[0].v = make_float4(p.x, q.x, r.x, s.x);
+        to[1].v = make_float4(p.y, q.y, r.y, s.y);
     }
-}
-template <typename IO>
-__device__ __forceinline__ Raw8<IO> narrow(const float (&x)[8])
-{
-    Raw8<IO> r;
-    uint32_t *w = reinterpret_cast<uint32_t *>(&r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (sizeof(IO) == 2) {
-            if (i & 1) w[i >> 1] = tc::pack_bf16x2(x[i - 1], x[i]);
-        } else {
-            w[i] = __float_as_uint(x[i]);
-        }
+};
+template <> struct Pair<__nv_bfloat16> {
+    uint2 v;  // B0 (low half) and B1; C0 and C1
+    __device__ __forceinline__ float2 b() const { return make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)); }
+    __device__ __forceinline__ float2 c() const { return make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)); }
+    using Two = uint32_t;
+    static __device__ __forceinline__ void make(Pair *to, Two p, Two q, Two r, Two s)
+    {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(__byte_perm(p, q, 0x5410), __byte_perm(r, s, 0x5410),
+                                                    __byte_perm(p, q, 0x7632), __byte_perm(r, s, 0x7632));
     }
-    return r;
-}
-
-// Channels of a CTA and the buffers of its chunks.
-template <typename IO, int N>
-struct Shape {
-    static constexpr int kLanes = N / 4;                    // lanes of a channel, four states each
-    static constexpr int kCh = kScanThreads / kLanes;       // channels
-    static constexpr int kRowY = kCh + 8;                   // (lanes of a channel store rows that follow one another)
-    static constexpr int kItems = (kChunk * kCh / 8 + 127) / 128;     // pieces of 8 channels a thread brings in
-    static constexpr int kItemsBC = (kChunk * 2 * N / 8 + 127) / 128;
-    float2 dd[2][kChunk][kCh];                              // d, d x
-    float bc[2][kChunk][2 * N];
-    float y[2][kChunk][kRowY];
-    alignas(16) IO x[3][kChunk][kCh], z[3][kChunk][kCh];
 };
 
-// Sums over the kLanes lanes of a channel of v[u], u < kLanes, to lane u.
-template <int L>
-__device__ __forceinline__ float spread_sums(float (&v)[L], int lane)
+// S of them, in loads of 16 bytes.
+template <typename IO, int S>
+__device__ __forceinline__ void load_pairs(Pair<IO> (&to)[S], const Pair<IO> *from)
 {
+    constexpr int kBytes = S * (int)sizeof(Pair<IO>);
+    if constexpr (kBytes == 8) {
+        *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(from);
+    } else {
 #pragma unroll
-    for (int m = L / 2; m; m >>= 1) {
-        const bool up = lane & m;
-#pragma unroll
-        for (int u = 0; u < m; ++u) {
-            const float give = up ? v[u] : v[u + m], keep = up ? v[u + m] : v[u];
-            v[u] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-        }
+        for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4 *>(to)[i] = reinterpret_cast<const uint4 *>(from)[i];
     }
-    return v[0];
 }
 
-template <typename IO, int N>
-__global__ void __launch_bounds__(kThreads)
+// A CTA: CH channels of N states each, S states a thread; its buffers.  Tokens lie in pairs, so that what a step
+// multiplies comes in register pairs.
+template <typename IO, int N, int CH, int S>
+struct Shape {
+    static constexpr int kScan = CH * N / S;                // threads that scan
+    static constexpr int kThreads = kScan + kIn + kOut;
+    static constexpr int kGroups = N / S;                   // threads of a channel
+    static constexpr int kWarpCh = CH < 16 ? CH : 16;       // channels of a warp
+    static constexpr int kChunk = CH == 8 && N == 16 ? 64 : 32;        // tokens handed over at a time
+    static constexpr int kPiece = 16 / (int)sizeof(IO);
+    struct Raw {                                            // as they come
+        alignas(16) IO x[kChunk][CH], dt[kChunk][CH], z[kChunk][CH], bc[kChunk][2 * N];
+    };
+    struct Ready {
+        // (rows more than there are: what is loaded ahead, and not used, at the end)
+        float4 dd[kChunk / 2 + 4][CH];                      // d, d x of two tokens: d0, d1, d0 x0, d1 x1
+        alignas(16) Pair<IO> bc[kChunk / 2 + 4][N];
+        float2 y[kGroups][kChunk / 2][CH];                  // sums over a thread's states
+    };
+    // chunks in shared memory: one going out, one scanned, one made ready, one that has come, the others on their way
+    static constexpr int kFit = (int)((232448 - 2 * sizeof(Ready)) / sizeof(Raw)), kRing = kFit < 6 ? kFit : 6;
+    static_assert(kRing >= 5 && kScan % 32 == 0);
+    Ready ready[2];
+    Raw raw[kRing];
+};
+
+template <typename IO, int N, int CH, int S>
+__global__ void __launch_bounds__(Shape<IO, N, CH, S>::kThreads, 2)
 scan_kernel(const Scan p, int group_blocks)
 {
-    using S = Shape<IO, N>;
-    constexpr int L = S::kLanes, CH = S::kCh;
+    using Sh = Shape<IO, N, CH, S>;
+    constexpr int T = Sh::kChunk, R = Sh::kRing, kScan = Sh::kScan;
     extern __shared__ __align__(16) unsigned char raw_smem[];
-    S &sm = *reinterpret_cast<S *>(raw_smem);
+    Sh &sm = *reinterpret_cast<Sh *>(raw_smem);
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const int blocks = p.groups * group_blocks, n = blockIdx.x / blocks, block = blockIdx.x % blocks;
@@ -111,10 +126,12 @@ scan_kernel(const Scan p, int group_blocks)
     const int held = min(CH, (group + 1) * per_group - c0);            // channels: a multiple of 8
     int first, end;
     packed_range(p.seq, n, first, end);
-    const int len = end - first, chunks = (len + kChunk - 1) / kChunk;
+    const int len = end - first, chunks = (len + T - 1) / T;
 
-    if (threadIdx.x < kScanThreads) {
-        const int lane = threadIdx.x % L, ch = threadIdx.x / L;
+    if (threadIdx.x < kScan) {
+        constexpr int CW = Sh::kWarpCh, PARTS = CH / CW;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int ch = warp % PARTS * CW + lane % CW, g = warp / PARTS * (32 / CW) + lane / CW;
         const bool mine = ch < held;
         int64_t init, fin;
         const bool good = packed_entries(p.seq, n, init, fin);
@@ -123,145 +140,238 @@ scan_kernel(const Scan p, int group_blocks)
             if (n == 0) packed_check(p.seq, p.seq.num_seqs);
             if (!good && p.seq.errors) atomicOr(p.seq.errors, DEV_ERR_SLOT);
         }
-        const int64_t at = (int64_t)(c0 + ch) * N + 4 * lane, all = (int64_t)p.channels * N;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), h = a;
-        if (mine) {
-            a = *reinterpret_cast<const float4 *>(p.a + at);
-            if (init >= 0) h = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.seq.init) + init * all + at);
+        const int64_t at = (int64_t)(c0 + ch) * N + g * S, all = (int64_t)p.channels * N;
+        float a[S], h[S];
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            a[i] = mine ? p.a[at + i] * tc::kLog2e : 0.f;
+            h[i] = mine && init >= 0 ? static_cast<const float *>(p.seq.init)[init * all + at + i] : 0.f;
         }
-        a.x *= tc::kLog2e; a.y *= tc::kLog2e; a.z *= tc::kLog2e; a.w *= tc::kLog2e;
         __syncthreads();
+        // B pairs of tokens at a time, of which all but h's own products and sums can be done side by side; their
+        // operands are loaded while the B before are worked on.  Tokens past the end leave h as it is (d = 0).
+        constexpr int B = S >= 4 ? 2 : 4;
+#pragma unroll 1
         for (int k = 0; k < chunks; ++k) {
-            const int buf = k & 1, count = min(kChunk, len - k * kChunk);
-            auto step = [&](int t) {
-                const float2 dd = sm.dd[buf][t][ch];
-                const float4 b = *reinterpret_cast<const float4 *>(&sm.bc[buf][t][4 * lane]);
-                const float4 c = *reinterpret_cast<const float4 *>(&sm.bc[buf][t][N + 4 * lane]);
-                h.x = fmaf(tc::exp2_approx(dd.x * a.x), h.x, dd.y * b.x);
-                h.y = fmaf(tc::exp2_approx(dd.x * a.y), h.y, dd.y * b.y);
-                h.z = fmaf(tc::exp2_approx(dd.x * a.z), h.z, dd.y * b.z);
-                h.w = fmaf(tc::exp2_approx(dd.x * a.w), h.w, dd.y * b.w);
-                return fmaf(h.x, c.x, h.y * c.y) + fmaf(h.z, c.z, h.w * c.w);
-            };
-#pragma unroll 2
-            for (int t = 0; t < count; t += L) {
-                float v[L];
-                if (t + L <= count) {
+            const int count = min(T, len - k * T);
+            const float4 *dd = &sm.ready[k & 1].dd[0][ch];
+            const Pair<IO> *bc = &sm.ready[k & 1].bc[0][g * S];
+            float2 *y = &sm.ready[k & 1].y[g][0][ch];
+            float4 d_next[B];
+            Pair<IO> bc_next[B][S];
 #pragma unroll
-                    for (int u = 0; u < L; ++u) v[u] = step(t + u);
-                } else {
+            for (int q = 0; q < B; ++q) {
+                d_next[q] = dd[q * CH];
+                load_pairs<IO, S>(bc_next[q], bc + q * N);
+            }
+#pragma unroll 1
+            for (int t = 0; t < count; t += 2 * B) {
+                float4 d[B];
+                Pair<IO> x[B][S];
+                float2 sum[B];
+                dd += B * CH;
+                bc += B * N;
 #pragma unroll
-                    for (int u = 0; u < L; ++u) v[u] = t + u < count ? step(t + u) : 0.f;
+                for (int q = 0; q < B; ++q) {
+                    d[q] = d_next[q];
+#pragma unroll
+                    for (int i = 0; i < S; ++i) x[q][i] = bc_next[q][i];
+                    d_next[q] = dd[q * CH];
+                    load_pairs<IO, S>(bc_next[q], bc + q * N);
                 }
-                sm.y[buf][t + lane][ch] = spread_sums<L>(v, lane);
+#pragma unroll
+                for (int q = 0; q < B; ++q)
+#pragma unroll
+                    for (int i = 0; i < S; ++i) {
+                        const float2 e = mul2(make_float2(d[q].x, d[q].y), make_float2(a[i], a[i]));
+                        const float2 b = mul2(make_float2(d[q].z, d[q].w), x[q][i].b());
+                        float2 hh;
+                        hh.x = fmaf(tc::exp2_approx(e.x), h[i], b.x);
+                        hh.y = fmaf(tc::exp2_approx(e.y), hh.x, b.y);
+                        h[i] = hh.y;
+                        sum[q] = i == 0 ? mul2(hh, x[q][i].c()) : ptx::fma2(hh, x[q][i].c(), sum[q]);
+                    }
+#pragma unroll
+                for (int q = 0; q < B; ++q) y[q * CH] = sum[q];
+                y += B * CH;
             }
             __syncthreads();
         }
-        if (fin >= 0 && mine) *reinterpret_cast<float4 *>(static_cast<float *>(p.seq.fin) + fin * all + at) = h;
-        return;
-    }
-
-    // tokens in and out
-    const int tid = threadIdx.x - kScanThreads;
-    Raw8<IO> rx[S::kItems], rdt[S::kItems], rz[S::kItems], rbc[S::kItemsBC];
-    auto ask = [&](int k) {  // a chunk's rows
+        if (fin >= 0 && mine)
 #pragma unroll
-        for (int i = 0; i < S::kItems; ++i) {
-            const int e = i * 128 + tid, t = k * kChunk + e / (CH / 8), c = e % (CH / 8) * 8;
-            if (e < kChunk * CH / 8 && t < len && c < held) {
-                const int64_t row = first + t;
-                rx[i] = load8(static_cast<const IO *>(p.x) + row * p.xs + c0 + c);
-                rdt[i] = load8(static_cast<const IO *>(p.dt) + row * p.dts + c0 + c);
-                if (p.z) rz[i] = load8(static_cast<const IO *>(p.z) + row * p.zs + c0 + c);
-            }
-        }
+            for (int i = 0; i < S; ++i) static_cast<float *>(p.seq.fin)[fin * all + at + i] = h[i];
+    } else if (threadIdx.x < kScan + kIn) {
+        const int tid = threadIdx.x - kScan;
+        // pieces of 16 bytes: a thread's are the same channels (states) of tokens that follow one another
+        constexpr int PE = Sh::kPiece, kRow = CH / PE, kRowBC = 2 * N / PE;
+        constexpr int kStep = kIn / kRow, kStepBC = kIn / kRowBC;
+        const int t0 = tid / kRow, c = tid % kRow * PE, b0 = tid / kRowBC, s = tid % kRowBC * PE;
+        const IO *x = static_cast<const IO *>(p.x) + (int64_t)(first + t0) * p.xs + c0 + c;
+        const IO *dt = static_cast<const IO *>(p.dt) + (int64_t)(first + t0) * p.dts + c0 + c;
+        const IO *z = static_cast<const IO *>(p.z) + (int64_t)(first + t0) * p.zs + c0 + c;
+        const int64_t bcs = s < N ? p.bs : p.cs;
+        const IO *bc = static_cast<const IO *>(s < N ? p.b : p.c) + (int64_t)(first + b0) * bcs + group * N + s % N;
+        int asked = 0;               // tokens so far
+        typename Sh::Raw *to = sm.raw;
+        auto ask = [&] {             // a chunk's rows
 #pragma unroll
-        for (int i = 0; i < S::kItemsBC; ++i) {
-            const int e = i * 128 + tid, t = k * kChunk + e / (N / 4), s = e % (N / 4) * 8;
-            if (e < kChunk * N / 4 && t < len) {
-                const int64_t row = first + t;
-                rbc[i] = s < N ? load8(static_cast<const IO *>(p.b) + row * p.bs + group * N + s)
-                               : load8(static_cast<const IO *>(p.c) + row * p.cs + group * N + s - N);
-            }
-        }
-    };
-    auto put = [&](int k) {
-        const int buf = k & 1;
-#pragma unroll
-        for (int i = 0; i < S::kItems; ++i) {
-            const int e = i * 128 + tid, t = e / (CH / 8), c = e % (CH / 8) * 8;
-            if (e < kChunk * CH / 8 && k * kChunk + t < len && c < held) {
-                float x[8], d[8], bias[8] = {};
-                widen(rx[i], x);
-                widen(rdt[i], d);
-                if (p.dt_bias) widen(load8(p.dt_bias + c0 + c), bias);
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    d[u] += bias[u];
-                    if (p.softplus) d[u] = softplus(d[u]);
-                    sm.dd[buf][t][c + u] = make_float2(d[u], d[u] * x[u]);
+            for (int i = 0; i < (T + kStep - 1) / kStep; ++i) {
+                const int t = i * kStep + t0;
+                if (t < T && asked + t < len && c < held) {
+                    ptx::cp_async16(&to->x[t][c], x + i * kStep * p.xs, true);
+                    ptx::cp_async16(&to->dt[t][c], dt + i * kStep * p.dts, true);
+                    if (p.z) ptx::cp_async16(&to->z[t][c], z + i * kStep * p.zs, true);
                 }
-                store8(&sm.x[k % 3][t][c], rx[i]);
-                if (p.z) store8(&sm.z[k % 3][t][c], rz[i]);
             }
-        }
 #pragma unroll
-        for (int i = 0; i < S::kItemsBC; ++i) {
-            const int e = i * 128 + tid, t = e / (N / 4), s = e % (N / 4) * 8;
-            if (e < kChunk * N / 4 && k * kChunk + t < len) {
-                float v[8];
-                widen(rbc[i], v);
-#pragma unroll
-                for (int u = 0; u < 8; u += 4)
-                    *reinterpret_cast<float4 *>(&sm.bc[buf][t][s + u]) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+            for (int i = 0; i < (T + kStepBC - 1) / kStepBC; ++i) {
+                const int t = i * kStepBC + b0;
+                if (t < T && asked + t < len) ptx::cp_async16(&to->bc[t][s], bc + i * kStepBC * bcs, true);
             }
-        }
-    };
-    auto out = [&](int k) {
-        const int buf = k & 1;
+            ptx::cp_async_commit();  // (a group for every chunk, empty past the last)
+            x += T * p.xs; dt += T * p.dts; z += T * p.zs; bc += T * bcs;
+            asked += T;
+            to = to + 1 == sm.raw + R ? sm.raw : to + 1;
+        };
+        // what is made ready by a thread: two tokens of two channels, two tokens of two states
+        constexpr int kPairs = kIn / (CH / 2), kPairsBC = kIn / (N / 2);
+        const int d0 = tid / (CH / 2), dc = tid % (CH / 2) * 2, e0 = tid / (N / 2), es = tid % (N / 2) * 2;
+        float2 bias = make_float2(0.f, 0.f);
+        if (p.dt_bias && dc < held) bias = load2(p.dt_bias + c0 + dc);
+        int made = 0;
+        const typename Sh::Raw *from = sm.raw;
+        auto put_some = [&](typename Sh::Ready &out, auto whole) {  // whole: all tokens are there
+            const float2 zero = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < S::kItems; ++i) {
-            const int e = i * 128 + tid, t = e / (CH / 8), c = e % (CH / 8) * 8;
-            if (e < kChunk * CH / 8 && k * kChunk + t < len && c < held) {
-                float x[8], z[8], skip[8] = {}, y[8];
-                widen(load8(&sm.x[k % 3][t][c]), x);
-                if (p.d) widen(load8(p.d + c0 + c), skip);
-                if (p.z) widen(load8(&sm.z[k % 3][t][c]), z);
+            for (int i = 0; i < (T / 2 + kPairs - 1) / kPairs; ++i) {
+                const int q = i * kPairs + d0, t = 2 * q;
+                if (q < T / 2 && dc < held) {
+                    float2 u[2] = {zero, zero}, v[2] = {zero, zero};
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    y[u] = fmaf(skip[u], x[u], sm.y[buf][t][c + u]);
-                    if (p.z) y[u] *= silu_io<IO>(z[u]);
+                    for (int j = 0; j < 2; ++j)
+                        if (whole.value || made + t + j < len) {
+                            v[j] = ptx::add2(load2(&from->dt[t + j][dc]), bias);
+                            if (p.softplus) v[j] = make_float2(softplus(v[j].x), softplus(v[j].y));
+                            u[j] = mul2(v[j], load2(&from->x[t + j][dc]));
+                        }
+                    out.dd[q][dc] = make_float4(v[0].x, v[1].x, u[0].x, u[1].x);
+                    out.dd[q][dc + 1] = make_float4(v[0].y, v[1].y, u[0].y, u[1].y);
                 }
-                store8(static_cast<IO *>(p.y) + (int64_t)(first + k * kChunk + t) * p.ys + c0 + c, narrow<IO>(y));
             }
-        }
-    };
-    if (chunks > 0) {
-        ask(0);
-        put(0);
-        if (chunks > 1) ask(1);
-    }
-    __syncthreads();
-    for (int k = 0; k < chunks; ++k) {  // while chunk k is scanned
-        if (k + 1 < chunks) put(k + 1);
-        if (k + 2 < chunks) ask(k + 2);
-        if (k > 0) out(k - 1);
+#pragma unroll
+            for (int i = 0; i < (T / 2 + kPairsBC - 1) / kPairsBC; ++i) {
+                const int q = i * kPairsBC + e0, t = 2 * q;
+                if (q < T / 2) {
+                    using Two = typename Pair<IO>::Two;
+                    auto two = [&](int j, int n) {
+                        return whole.value || made + t + j < len ? *reinterpret_cast<const Two *>(&from->bc[t + j][n]) : Two{};
+                    };
+                    Pair<IO>::make(&out.bc[q][es], two(0, es), two(1, es), two(0, N + es), two(1, N + es));
+                }
+            }
+        };
+        auto put = [&](typename Sh::Ready &out) {
+            if (made + T <= len) put_some(out, Yes());
+            else put_some(out, No());
+            made += T;
+            from = from + 1 == sm.raw + R ? sm.raw : from + 1;
+        };
+        auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kIn) : "memory"); };  // the threads that bring in
+#pragma unroll 1
+        for (int k = 0; k < R - 2; ++k) ask();
+        ptx::cp_async_wait<R - 4>();  // chunks 0 and 1 have come
+        meet();
+        if (chunks > 0) put(sm.ready[0]);
         __syncthreads();
+#pragma unroll 1
+        for (int k = 0; k < chunks; ++k) {  // while chunk k is scanned
+            ask();                          // to where chunk k - 2 was
+            if (k + 1 < chunks) put(sm.ready[(k + 1) & 1]);
+            ptx::cp_async_wait<R - 4>();    // chunk k + 2 has come
+            __syncthreads();
+        }
+    } else {
+        const int tid = threadIdx.x - kScan - kIn;
+        constexpr int kPairs = kOut / (CH / 2);
+        const int d0 = tid / (CH / 2), c = tid % (CH / 2) * 2;
+        IO *out = static_cast<IO *>(p.y) + (int64_t)(first + 2 * d0) * p.ys + c0 + c;
+        float2 skip = make_float2(0.f, 0.f);
+        if (p.d && c < held) skip = load2(p.d + c0 + c);
+        const typename Sh::Raw *raw = sm.raw;
+        __syncthreads();
+#pragma unroll 1
+        for (int k = 0; k <= chunks; ++k) {
+            if (k > 0) {  // chunk k - 1 goes out
+                const typename Sh::Ready &from = sm.ready[(k - 1) & 1];
+                const int left = len - (k - 1) * T;
+                auto give = [&](auto whole) {
+#pragma unroll
+                    for (int i = 0; i < (T / 2 + kPairs - 1) / kPairs; ++i) {
+                        const int q = i * kPairs + d0, t = 2 * q;
+                        if (q < T / 2 && (whole.value || t < left) && c < held) {
+                            float4 sum = *reinterpret_cast<const float4 *>(&from.y[0][q][c]);  // t, t + 1 of c; of c + 1
+#pragma unroll
+                            for (int j = 1; j < Sh::kGroups; ++j) {
+                                const float4 w = *reinterpret_cast<const float4 *>(&from.y[j][q][c]);
+                                sum.x += w.x; sum.y += w.y; sum.z += w.z; sum.w += w.w;
+                            }
+                            float2 y[2] = {make_float2(sum.x, sum.z), make_float2(sum.y, sum.w)};
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (j == 0 || whole.value || t + 1 < left) {
+                                    y[j] = ptx::fma2(skip, load2(&raw->x[t + j][c]), y[j]);
+                                    if (p.z) {
+                                        const float2 z = load2(&raw->z[t + j][c]);
+                                        y[j].x *= silu_io<IO>(z.x);
+                                        y[j].y *= silu_io<IO>(z.y);
+                                    }
+                                    store2(out + (2 * i * kPairs + j) * p.ys, y[j]);
+                                }
+                        }
+                    }
+                };
+                if (left >= T) give(Yes());
+                else give(No());
+                out += T * p.ys;
+                raw = raw + 1 == sm.raw + R ? sm.raw : raw + 1;
+            }
+            if (k < chunks) __syncthreads();
+        }
     }
-    if (chunks > 0) out(chunks - 1);
 }
 
-template <typename IO, int N>
+template <typename IO, int N, int CH, int S>
 cudaError_t launch(const Scan &p)
 {
-    using S = Shape<IO, N>;
+    using Sh = Shape<IO, N, CH, S>;
     static int configured = -1;
-    const cudaError_t err = tc::allow_smem(scan_kernel<IO, N>, (int)sizeof(S), &configured);
+    const cudaError_t err = tc::allow_smem(scan_kernel<IO, N, CH, S>, (int)sizeof(Sh), &configured);
     if (err != cudaSuccess) return err;
-    const int group_blocks = (p.channels / p.groups + S::kCh - 1) / S::kCh;
+    const int group_blocks = (p.channels / p.groups + CH - 1) / CH;
     const int64_t blocks = (int64_t)group_blocks * p.groups * p.seq.num_seqs;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return latent_launch(scan_kernel<IO, N>, dim3((unsigned)blocks), kThreads, sizeof(S), p.stream, 1, p, group_blocks);
+    return latent_launch(scan_kernel<IO, N, CH, S>, dim3((unsigned)blocks), Sh::kThreads, sizeof(Sh), p.stream, 1, p,
+                         group_blocks);
+}
+
+// Channels of a CTA and states of a thread: the fewest channels of which all CTAs run at once, one on an SM, since a
+// narrower CTA takes less time a token (16 states: 34 ns for 32 channels, 23 for 16, 17 for 8), else the most, which
+// take the least a channel (two on an SM).  4,096 tokens of 16 states in bf16, us with 32, 16, 8 channels: one sequence
+// of 1,024 channels 140, 96, 68; of 2,048 140, 96, 135; of 4,096 140, 151, 267; four sequences of 4,096 117, 135, 253.
+template <typename IO, int N>
+cudaError_t choose(const Scan &p)
+{
+    const int per_group = p.channels / p.groups;
+    auto at_once = [&](int ch) { return (int64_t)((per_group + ch - 1) / ch) * p.groups * p.seq.num_seqs <= 152; };
+    if constexpr (N == 8) {
+        return at_once(16) ? launch<IO, 8, 16, 1>(p) : launch<IO, 8, 32, 2>(p);
+    } else if constexpr (N == 16) {
+        return at_once(8) ? launch<IO, 16, 8, 1>(p) : at_once(16) ? launch<IO, 16, 16, 2>(p) : launch<IO, 16, 32, 4>(p);
+    } else if constexpr (N == 32) {
+        return at_once(8) ? launch<IO, 32, 8, 2>(p) : at_once(16) ? launch<IO, 32, 16, 2>(p) : launch<IO, 32, 32, 4>(p);
+    } else {
+        return at_once(8) ? launch<IO, 64, 8, 4>(p) : launch<IO, 64, 16, 4>(p);
+    }
 }
 
 }  // namespace
@@ -270,10 +380,10 @@ cudaError_t launch_scan(const Scan &p)
 {
     const bool half = p.dtype == KDA_DTYPE_BF16;
     switch (p.states) {
-    case 8: return half ? launch<__nv_bfloat16, 8>(p) : launch<float, 8>(p);
-    case 16: return half ? launch<__nv_bfloat16, 16>(p) : launch<float, 16>(p);
-    case 32: return half ? launch<__nv_bfloat16, 32>(p) : launch<float, 32>(p);
-    default: return half ? launch<__nv_bfloat16, 64>(p) : launch<float, 64>(p);
+    case 8: return half ? choose<__nv_bfloat16, 8>(p) : choose<float, 8>(p);
+    case 16: return half ? choose<__nv_bfloat16, 16>(p) : choose<float, 16>(p);
+    case 32: return half ? choose<__nv_bfloat16, 32>(p) : choose<float, 32>(p);
+    default: return half ? choose<__nv_bfloat16, 64>(p) : choose<float, 64>(p);
     }
 }
 
