@@ -59,6 +59,8 @@ struct Scan {
 cudaError_t launch_linear_simt(const Linear &p);
 bool linear_tc_takes(const Linear &p);  // bf16 with rows that the tensor cores' copies can read
 cudaError_t launch_linear_tc(const Linear &p);
+bool linear_few_takes(const Linear &p);  // of those, the ones of few rows
+cudaError_t launch_linear_few(const Linear &p);
 cudaError_t launch_short_conv(const ShortConv &p);
 cudaError_t launch_scan(const Scan &p);
 cudaError_t launch_scan_step(const Scan &p);  // one token of every sequence (seq.cu null, seq.each 1)

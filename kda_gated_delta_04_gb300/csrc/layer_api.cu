@@ -74,8 +74,10 @@ kda_status_t kda_linear(const void *x, int64_t x_stride, const void *w, int64_t 
     p.rows = rows; p.n = out_features; p.k = in_features;
     p.dtype = dtype; p.out_dtype = out_dtype; p.act = activation; p.errors = device_errors;
     p.stream = static_cast<cudaStream_t>(stream);
-    return (kda::linear_tc_takes(p) ? kda::launch_linear_tc(p) : kda::launch_linear_simt(p)) == cudaSuccess ? KDA_OK
-                                                                                                            : KDA_ERR_CUDA;
+    const cudaError_t err = kda::linear_few_takes(p)  ? kda::launch_linear_few(p)
+                            : kda::linear_tc_takes(p) ? kda::launch_linear_tc(p)
+                                                      : kda::launch_linear_simt(p);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *weight, const void *bias, int32_t width,

@@ -1,0 +1,144 @@
+// linear_few.cu -- projections of a few rows (generated tokens), bf16 rows on 16 bytes.
+//
+//   y_mn = act(sum_k x_mk w_nk + b_n) + r_mn,  m < 8 NT
+//
+// Bound by the bytes of w, which are read once, and by the latency of a short kernel: w goes straight from
+// memory to registers as the matrix instructions take it (mma.sync, 16 outputs x 16 inputs a warp), without the
+// set-up and the hand-over through shared and tensor memory.  A CTA has 16 outputs, and each of its warps every
+// kWarps-th block of 64 inputs, whose sums are joined at the end.
+//
+// Which inputs an instruction multiplies is free as long as w and x agree: a lane's 16 bytes of a row, inputs
+// 8 t to 8 t + 7 of 32 (t = lane % 4), are what it holds of two instructions' operands.
+#include "latent_ptx.cuh"
+#include "layer.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kBlock = 64;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// w is read once and by this CTA alone.
+__device__ __forceinline__ uint4 load_once(const __nv_bfloat16 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// A block's operands of a lane: its pieces of w's rows g and g + 8 and of x's row g (of each 8).
+template <int NT>
+struct Block {
+    uint4 w[2][2], x[NT][2];
+};
+
+template <typename OUT, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+linear_few_kernel(const Linear p)
+{
+    constexpr int F = 16, M = 8 * NT, D = NT == 1 ? 4 : 2;  // D: blocks in flight
+    __shared__ float part[kWarps][M][F + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n0 = blockIdx.x * F, blocks = (p.k + kBlock - 1) / kBlock;
+    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x) + 8 * t;
+    const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(p.w) + (int64_t)(n0 + g) * p.ws + 8 * t;
+    // the first blocks of w into L2 while the kernel before this one ends (whatever it writes, L2 has it)
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const int k = (warp + i * kWarps) * kBlock;
+            if (t == 0 && n0 + g + 8 * f < p.n && k < p.k)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(w + (int64_t)(8 * f) * p.ws + k));
+        }
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    auto ask = [&](Block<NT> &b, int block) {
+        const int k = block * kBlock;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const bool in = k + 32 * u + 8 * t < p.k;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                b.w[h][u] = make_uint4(0, 0, 0, 0);
+                if (in && n0 + g + 8 * h < p.n) b.w[h][u] = load_once(w + (int64_t)(8 * h) * p.ws + k + 32 * u);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                b.x[j][u] = make_uint4(0, 0, 0, 0);
+                if (in && 8 * j + g < p.rows)
+                    b.x[j][u] = *reinterpret_cast<const uint4 *>(x + (int64_t)(8 * j + g) * p.xs + k + 32 * u);
+            }
+        }
+    };
+    float acc[NT][4] = {};
+    Block<NT> b[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) ask(b[i], warp + i * kWarps);  // (past the last: zeros)
+#pragma unroll 1
+    for (int block = warp; block < blocks; block += D * kWarps) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint4 lo = b[i].w[0][u], hi = b[i].w[1][u], xx = b[i].x[j][u];
+                    mma16816(acc[j], lo.x, hi.x, lo.y, hi.y, xx.x, xx.y);
+                    mma16816(acc[j], lo.z, hi.z, lo.w, hi.w, xx.z, xx.w);
+                }
+            ask(b[i], block + (i + D) * kWarps);
+        }
+    }
+    // outputs g, g + 8 of rows 2 t, 2 t + 1
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[warp][8 * j + 2 * t + (e & 1)][g + (e >> 1) * 8] = acc[j][e];
+    __syncthreads();
+    for (int o = threadIdx.x; o < F * M; o += kThreads) {
+        const int m = o / F, f = o % F, n = n0 + f;
+        if (m >= p.rows || n >= p.n) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) v += part[i][m][f];
+        if (p.bias) v += load_io(static_cast<const __nv_bfloat16 *>(p.bias) + n);
+        v = activate<OUT>(v, p.act);
+        if (p.residual) v += load_io(static_cast<const OUT *>(p.residual) + m * p.rs + n);
+        store_io(static_cast<OUT *>(p.y) + m * p.ys + n, v);
+    }
+}
+
+template <typename OUT>
+cudaError_t launch(const Linear &p)
+{
+    auto go = [&](auto kernel) {
+        return latent_launch(kernel, dim3((unsigned)((p.n + 15) / 16)), kThreads, 0, p.stream, 1, p);
+    };
+    return p.rows <= 8 ? go(linear_few_kernel<OUT, 1>) : go(linear_few_kernel<OUT, 2>);
+}
+
+}  // namespace
+
+// Against the tensor-memory kernel, us, 4,096 inputs: 1 row 7.0 and 12.2 (4,096 outputs), 19.1 and 19.9 (12,288); 8
+// rows 7.5, 12.3 and 19.6, 19.9; 16 rows 8.8, 12.3 and 22.1, 19.9 (every CTA reads x); 32 rows 15.3, 12.5.
+bool linear_few_takes(const Linear &p)
+{
+    return linear_tc_takes(p) && (p.rows <= 8 || (p.rows <= 16 && p.n <= 8192));
+}
+
+cudaError_t launch_linear_few(const Linear &p)
+{
+    return p.out_dtype == KDA_DTYPE_F32 ? launch<float>(p) : launch<__nv_bfloat16>(p);
+}
+
+}  // namespace kda

@@ -2,12 +2,16 @@
 //
 //   y [rows x n] = act(x [rows x k] w^T [k x n] + b) + r
 //
-// A tile of y is 128 rows by `width` columns of one CTA, or 256 rows by `width` of a pair (a cluster of two):
-// there each CTA holds its 128 rows of x and half of w's rows, and an instruction spans both (M = 256).  The
-// accumulators, fp32 in tensor memory, are doubled, so that a tile's epilogue runs while the next one's
-// products do.
+// A tile of y is up to 128 rows by `width` columns of one CTA, or 256 rows by `width` of a pair (a cluster of two):
+// there each CTA holds its 128 rows of x and half of w's rows, and an instruction spans both (M = 256).  Many
+// tiles: CTAs stay and take one after the other, and the accumulators, fp32 in tensor memory, are doubled, so that a
+// tile's epilogue runs while the next one's products do.  Few tiles (few rows): the inputs of a tile are split among
+// the units (CTAs or pairs) of a cluster, each of which has all its columns, and joined through distributed
+// shared memory: what bounds such a call are the bytes that an SM takes in, about 40 a cycle, and wide tiles over
+// part of the inputs take in fewer than narrow ones over all.
 // Warp 0: copies (TMA); 1: matrix instructions (of a pair: in the leading CTA); 2: tensor memory; 4 to 7: the
 // epilogue, a thread a row.
+#include <type_traits>
 #include "latent_ptx.cuh"
 #include "layer.cuh"
 #include "tc_common.cuh"
@@ -19,7 +23,7 @@ using namespace ptx;
 using tc::kdesc;
 
 constexpr int kThreads = 256, kM = 128;
-constexpr int kMaxStages = 8, kMaxWidth = 256, kDepth = 64;  // kDepth: channels of a panel, a swizzled row of 128 bytes
+constexpr int kMaxStages = 12, kMaxWidth = 256, kDepth = 64;  // kDepth: channels of a panel, a swizzled row of 128 bytes
 constexpr int kSmem = 232448;
 constexpr uint64_t kWait = tc::kWaitNs;
 
@@ -29,18 +33,20 @@ struct Misc {
     uint32_t tmem;
     int abort;
 };
-// rows that an instruction reads behind those that a short last panel holds
-constexpr int kSlack = kM * 128;
-constexpr int kStageBytes = (kSmem - (int)sizeof(Misc) - kSlack) / 1024 * 1024;
+constexpr int kHead = 1024;  // Misc; the stages follow
+static_assert(sizeof(Misc) <= kHead);
 
 // What the host decides for a call.
 struct Plan {
-    int width;        // columns of a tile
-    int box;          // rows of x that a copy brings
+    int width, parts; // columns of a tile, in one or two instructions
+    int tall;         // rows of a tile: 256, or of one CTA at most 128
+    int box;          // rows of x that a CTA holds
     int panels;       // panels of a stage
     int stages;
     int tiles_m, tiles_n, group;  // tiles_m in groups that are worked on together
     uint32_t columns; // of tensor memory
+    uint32_t pitch;   // columns of it from one accumulator to the other: of the next tile, or the next part
+    int smem;
     bool vec;         // rows of y start on 16 bytes
     bool vec_r, vec_b;  // those of the residual; the bias
 };
@@ -64,6 +70,31 @@ __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity, volatil
         }
     }
     return __all_sync(0xffffffffu, ok);
+}
+
+// tma_load_2d; of a pair counted on a barrier of its leading CTA.
+template <bool PAIR>
+__device__ __forceinline__ void load_box(void *dst, const void *tmap, uint32_t bar_cluster_addr, int32_t x, int32_t y)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster_addr), "r"(x), "r"(y)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster_addr), "r"(x), "r"(y)
+            : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t *bar, uint32_t pair)
+{
+    if (PAIR) mma_commit_pair(lead, bar, pair);
+    else mma_commit_lead(lead, bar);
 }
 
 __device__ __forceinline__ void tile_at(const Plan &pl, int tile, int &m, int &n)
@@ -144,35 +175,83 @@ struct Raw16 {
     }
 };
 
+// A thread's row of a tile: where it is, and the columns that the epilogue has of it.
+template <typename OUT, bool PAIR>
+struct Row {
+    const OUT *r;
+    OUT *y;
+    const __nv_bfloat16 *bias;  // of the tile's first column
+    bool mine;                  // it is a row of y
+    __device__ __forceinline__ Row(const Linear &p, const Plan &pl, int m, int n, int rank)
+    {
+        const int row = threadIdx.x & 127, c0 = n * pl.width;
+        const int64_t at = (int64_t)m * pl.tall + rank * kM + row;
+        mine = at < p.rows && (PAIR || row < pl.tall);
+        r = p.residual ? static_cast<const OUT *>(p.residual) + at * p.rs + c0 : nullptr;
+        y = static_cast<OUT *>(p.y) + at * p.ys + c0;
+        bias = p.bias ? static_cast<const __nv_bfloat16 *>(p.bias) + c0 : nullptr;
+    }
+    // 16 columns from c on, `left` of which the row has; now: those of the residual, where vec and vec_r hold
+    __device__ __forceinline__ void finish(const Linear &p, const Plan &pl, float (&v)[16], int c, int left,
+                                           const Raw16<OUT> &now) const
+    {
+        if (bias) {
+            Raw16<__nv_bfloat16> b;
+            if (pl.vec_b && left >= 16) {
+                b.load(bias + c);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += b.get(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < left) v[i] += load_io(bias + c + i);
+            }
+        }
+        activate16<OUT>(v, p.act);
+        if (!mine) return;
+        if (left >= 16 && pl.vec && (!r || pl.vec_r)) {
+            if (r)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += now.get(i);
+            Raw16<OUT> out;
+            out.set(v);
+            out.store(y + c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < left) {
+                    if (r) v[i] += load_io(r + c + i);
+                    store_io(y + c + i, v[i]);
+                }
+        }
+    }
+};
+
 template <typename OUT, bool PAIR>
 __device__ __forceinline__ void epilogue_role(Misc &mi, const Linear &p, const Plan &pl, uint32_t tmem, int rank, int first,
                                               int step)
 {
     volatile int *abort = &mi.abort;
-    const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
-    const uint32_t quarter = (uint32_t)((row >> 5) * 32) << 16;
-    const __nv_bfloat16 *bias = static_cast<const __nv_bfloat16 *>(p.bias);
+    const int lane = threadIdx.x & 31;
+    const uint32_t quarter = (uint32_t)(threadIdx.x & 96) << 16;
     int count = 0;
     for (int tile = first; tile < pl.tiles_m * pl.tiles_n; tile += step, ++count) {
         int m, n;
         tile_at(pl, tile, m, n);
-        const int buf = count & 1, c0 = n * pl.width, left = min(pl.width, p.n - c0);
-        const int64_t at = (int64_t)m * (PAIR ? 2 * kM : kM) + rank * kM + row;
-        const bool mine = at < p.rows;
-        const OUT *r = static_cast<const OUT *>(p.residual) + at * p.rs + c0;
-        OUT *y = static_cast<OUT *>(p.y) + at * p.ys + c0;
+        const int buf = count & 1, left = min(pl.width, p.n - n * pl.width);
+        const Row<OUT, PAIR> row(p, pl, m, n, rank);
         // the residual's next 16 columns are on their way while these are worked on
-        const bool whole_r = p.residual && mine && pl.vec_r;
+        const bool whole_r = row.r && row.mine && pl.vec_r;
         Raw16<OUT> next;
-        if (whole_r && left >= 16) next.load(r);
+        if (whole_r && left >= 16) next.load(row.r);
         if (!all_wait<false>(&mi.done[buf], (count >> 1) & 1, abort)) return;
         tc_fence_after_sync();
 #pragma unroll 1
         for (int c = 0; c < left; c += 16) {
             float v[16];
-            tmem_ld16(tmem + buf * kMaxWidth + c + quarter, v);
+            tmem_ld16(tmem + buf * pl.pitch + c + quarter, v);
             const Raw16<OUT> now = next;
-            if (whole_r && left - c >= 32) next.load(r + c + 16);
+            if (whole_r && left - c >= 32) next.load(row.r + c + 16);
             tmem_ld_wait();
             if (c + 16 >= left) {  // the accumulators may be written again
                 tc_fence_before_sync();
@@ -182,51 +261,75 @@ __device__ __forceinline__ void epilogue_role(Misc &mi, const Linear &p, const P
                     else mbar_arrive(&mi.freed[buf]);
                 }
             }
-            if (bias) {
-                Raw16<__nv_bfloat16> b;
-                if (pl.vec_b && left - c >= 16) {
-                    b.load(bias + c0 + c);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] += b.get(i);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c + i < left) v[i] += load_io(bias + c0 + c + i);
-                }
-            }
-            activate16<OUT>(v, p.act);
-            if (!mine) continue;
-            if (left - c >= 16 && pl.vec && (!p.residual || pl.vec_r)) {
-                if (p.residual)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] += now.get(i);
-                Raw16<OUT> out;
-                out.set(v);
-                out.store(y + c);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c + i < left) {
-                        if (p.residual) v[i] += load_io(r + c + i);
-                        store_io(y + c + i, v[i]);
-                    }
-            }
+            row.finish(p, pl, v, c, left - c, now);
         }
     }
 }
 
-template <typename OUT, bool PAIR>
+// Where column c of a tile of one or two parts is in tensor memory.
+__device__ __forceinline__ uint32_t column(const Plan &pl, int c)
+{
+    const int w = pl.width / pl.parts;
+    return c < w ? c : pl.pitch + (c - w);
+}
+
+// Of a tile whose inputs S units have a part of each: the sums of this one to shared memory, all but its share of the
+// columns (column by column, 128 rows each), once its products are done ...
+__device__ __forceinline__ bool put_part(Misc &mi, const Plan &pl, float *part, uint32_t tmem, int from, int to)
+{
+    const int row = threadIdx.x & 127;
+    const uint32_t quarter = (uint32_t)(threadIdx.x & 96) << 16;
+    if (!all_wait<false>(&mi.done[0], 0, &mi.abort)) return false;
+    tc_fence_after_sync();
+#pragma unroll 1
+    for (int c = 0; c < pl.width; c += 16) {
+        if (c >= from && c < to) continue;
+        float v[16];
+        tmem_ld16(tmem + column(pl, c) + quarter, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[(c + i) * kM + row] = v[i];
+    }
+    return true;
+}
+// ... and the epilogue of its share, in the order of the inputs.
+template <typename OUT, bool PAIR, int S>
+__device__ __forceinline__ void join_parts(const Linear &p, const Plan &pl, const float *part, uint32_t tmem, int tile,
+                                           int rank, int unit, int from, int to)
+{
+    const uint32_t quarter = (uint32_t)(threadIdx.x & 96) << 16;
+    int m, n;
+    tile_at(pl, tile, m, n);
+    const Row<OUT, PAIR> row(p, pl, m, n, rank);
+    const int left = min(pl.width, p.n - n * pl.width);
+    const bool whole_r = row.r && row.mine && pl.vec_r;
+#pragma unroll 1
+    for (int c = from; c < min(to, left); c += 16) {
+        float v[16], sum[16] = {};
+        Raw16<OUT> now;
+        if (whole_r && left - c >= 16) now.load(row.r + c);
+        tmem_ld16(tmem + column(pl, c) + quarter, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int u = 0; u < S; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                sum[i] += u == unit ? v[i] : peer_load(part + (c + i) * kM + (threadIdx.x & 127), (PAIR ? 2 : 1) * u + rank);
+        row.finish(p, pl, sum, c, left - c, now);
+    }
+}
+
+// S: units (CTAs, or pairs) of a cluster, which share a tile's inputs (1: no cluster but the pair; many tiles).
+template <typename OUT, bool PAIR, int S>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_tc_kernel(const Linear p, const Plan pl, const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw)
 {
+    constexpr int kCtas = PAIR ? 2 : 1, kCluster = kCtas * S;
+    constexpr bool kClustered = kCluster > 1;
     extern __shared__ __align__(1024) unsigned char sm[];
-    Misc &mi = *reinterpret_cast<Misc *>(sm + kStageBytes + kSlack);
+    Misc &mi = *reinterpret_cast<Misc *>(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = PAIR ? (int)cluster_rank() : 0;
-    if (smem_u32(sm) & 1023u) {  // the swizzled panels need it; never seen
-        if (tid == 0 && p.errors) atomicOr(p.errors, DEV_ERR_TIMEOUT);
-        return;
-    }
+    const int place = kClustered ? (int)cluster_rank() : 0, rank = PAIR ? place & 1 : 0, unit = place / kCtas;
     if (tid == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&mi.full[i], 1);
@@ -234,11 +337,15 @@ linear_tc_kernel(const Linear p, const Plan pl, const __grid_constant__ CUtensor
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&mi.done[i], 1);
-            mbar_init(&mi.freed[i], PAIR ? 8 : 4);
+            mbar_init(&mi.freed[i], 4 * kCtas);
         }
         mbar_init(&mi.drained, 1);
         fence_mbar_init();
         mi.abort = 0;
+    }
+    if (tid == 32) {
+        prefetch_tmap(&tx);
+        prefetch_tmap(&tw);
     }
     if (warp == 2) {
         if (PAIR) {
@@ -250,96 +357,110 @@ linear_tc_kernel(const Linear p, const Plan pl, const __grid_constant__ CUtensor
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (PAIR) cluster_sync();
+    if (kClustered) cluster_sync();
     tc_fence_after_sync();
     // only now: a CTA of the next kernel must not take the tensor memory that one of this kernel is waiting for
     pdl_launch_dependents();
-    pdl_wait();
     const uint32_t tmem = mi.tmem;
-    const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+    const int first = blockIdx.x / kCluster, step = gridDim.x / kCluster;
     const int tiles = pl.tiles_m * pl.tiles_n, all_panels = (p.k + kDepth - 1) / kDepth;
-    const int steps = (all_panels + pl.panels - 1) / pl.panels;
-    const int half = PAIR ? pl.width / 2 : pl.width;  // rows of w that this CTA holds
-    const uint32_t panel_x = pl.box * 128, panel_w = half * 128, stage_bytes = pl.panels * (panel_x + panel_w);
+    const int k0 = all_panels * unit / S, panels = all_panels * (unit + 1) / S - k0;  // this unit's panels
+    const int steps = (panels + pl.panels - 1) / pl.panels;
+    const int part_w = pl.width / pl.parts, half = PAIR ? part_w / 2 : part_w;  // columns of an instruction; w's rows here
+    const uint32_t panel_x = pl.box * 128, panel_w = pl.parts * half * 128, stage_bytes = pl.panels * (panel_x + panel_w);
+    const uint32_t pair = (PAIR ? 3u : 1u) << (kCtas * unit);
+    float *part = reinterpret_cast<float *>(sm + kHead);
+    const int share = pl.width / S, from = unit * share, to = from + share;
     volatile int *abort = &mi.abort;
+    bool whole = true;  // (of the epilogue's warps)
 
-    if (warp == 0) {
+    if (smem_u32(sm) & 1023u) {  // the swizzled panels need it; never seen, and the same in every CTA
+        if (tid == 0) *abort = 1;
+        whole = false;
+    } else if (warp == 0) {
         const bool lead = elect_lead();
+        pdl_wait();
         int t = 0;  // stages so far
         for (int tile = first; tile < tiles; tile += step) {
             int m, n;
             tile_at(pl, tile, m, n);
-            const int row_x = m * (PAIR ? 2 * kM : kM) + rank * kM, row_w = n * pl.width + rank * half;
+            const int row_x = m * pl.tall + rank * kM, row_w = n * pl.width + rank * half;
             bool ok = true;
             for (int s = 0; s < steps; ++s, ++t) {
-                const int slot = t % pl.stages, count = min(pl.panels, all_panels - s * pl.panels);
+                const int slot = t % pl.stages, count = min(pl.panels, panels - s * pl.panels);
                 if (t >= pl.stages && !(ok = all_wait<PAIR>(&mi.empty[slot], (t / pl.stages - 1) & 1, abort))) break;
                 if (lead) {
-                    unsigned char *dst = sm + slot * stage_bytes;
-                    if (rank == 0) mbar_arrive_expect_tx(&mi.full[slot], (PAIR ? 2 : 1) * count * (panel_x + panel_w));
-                    const uint32_t bar = PAIR ? map_to_rank(&mi.full[slot], 0) : 0;
+                    unsigned char *dst = sm + kHead + slot * stage_bytes;
+                    if (rank == 0) mbar_arrive_expect_tx(&mi.full[slot], kCtas * count * (panel_x + panel_w));
+                    const uint32_t bar = PAIR ? map_to_rank(&mi.full[slot], kCtas * unit) : smem_u32(&mi.full[slot]);
                     for (int i = 0; i < count; ++i) {
-                        const int k = (s * pl.panels + i) * kDepth;
-                        unsigned char *dx = dst + i * panel_x, *dw = dst + pl.panels * panel_x + i * panel_w;
-                        if (PAIR) {
-                            tma_load_3d_pair(dx, &tx, bar, k, 0, row_x);
-                            tma_load_3d_pair(dw, &tw, bar, k, 0, row_w);
-                        } else {
-                            tma_load_3d(dx, &tx, &mi.full[slot], k, 0, row_x);
-                            tma_load_3d(dw, &tw, &mi.full[slot], k, 0, row_w);
-                        }
+                        const int k = (k0 + s * pl.panels + i) * kDepth;
+                        unsigned char *dw = dst + pl.panels * panel_x + i * panel_w;
+                        load_box<PAIR>(dst + i * panel_x, &tx, bar, k, row_x);
+                        for (int j = 0; j < pl.parts; ++j) load_box<PAIR>(dw + j * half * 128, &tw, bar, k, row_w + j * part_w);
                     }
                 }
                 __syncwarp();
             }
             if (!ok) break;
         }
-        // no copy in flight when the CTAs go, whatever became of the products
-        if (lead && rank == 0)
+        // No copy into this CTA is on its way when it goes: the stages that were copied last have been given back.  (After a
+        // wait that gave up, the first that is not ends this.)
+        if (lead)
             for (int k = max(0, t - pl.stages); k < t; ++k)
-                mbar_wait_ns(&mi.full[k % pl.stages], (k / pl.stages) & 1, kWait);
+                if (!mbar_wait_ns(&mi.empty[k % pl.stages], (k / pl.stages) & 1, kWait)) break;
     } else if (warp == 1 && rank == 0) {
-        const uint32_t lead = elect_lead(), base = __reduce_or_sync(0xffffffffu, tmem), sb = smem_u32(sm);
-        const uint32_t id = idesc_bf16(PAIR ? 2 * kM : kM, pl.width, false, false);
+        const uint32_t lead = elect_lead(), base = __reduce_or_sync(0xffffffffu, tmem), sb = smem_u32(sm) + kHead;
+        const uint32_t id = idesc_bf16(PAIR ? 2 * kM : kM, part_w, false, false);
         int t = 0, count = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step, ++count) {
             const int buf = count & 1;
             if (count >= 2 && !(ok = all_wait<PAIR>(&mi.freed[buf], ((count >> 1) - 1) & 1, abort))) break;
             tc_fence_after_sync();
-            const uint32_t d = base + buf * kMaxWidth;
+            const uint32_t d = base + buf * pl.pitch;
             for (int s = 0; s < steps; ++s, ++t) {
-                const int slot = t % pl.stages, held = min(pl.panels, all_panels - s * pl.panels);
+                const int slot = t % pl.stages, held = min(pl.panels, panels - s * pl.panels);
                 if (!(ok = all_wait<PAIR>(&mi.full[slot], (t / pl.stages) & 1, abort))) break;
                 tc_fence_after_sync();
                 const uint32_t a = sb + slot * stage_bytes, b = a + pl.panels * panel_x;
                 for (int i = 0; i < held; ++i)
+                    for (int j = 0; j < (S > 1 ? pl.parts : 1); ++j)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t da = kdesc(a + i * panel_x + k * 32), db = kdesc(b + i * panel_w + k * 32);
-                        if (PAIR) mma_bf16_pair(lead, d, da, db, id, s > 0 || i > 0 || k > 0);
-                        else mma_bf16_lead(lead, d, da, db, id, s > 0 || i > 0 || k > 0);
-                    }
-                if (PAIR) mma_commit_pair(lead, &mi.empty[slot]);
-                else mma_commit_lead(lead, &mi.empty[slot]);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t da = kdesc(a + i * panel_x + k * 32), db = kdesc(b + i * panel_w + j * half * 128 + k * 32);
+                            if (PAIR) mma_bf16_pair(lead, d + j * pl.pitch, da, db, id, s > 0 || i > 0 || k > 0);
+                            else mma_bf16_lead(lead, d + j * pl.pitch, da, db, id, s > 0 || i > 0 || k > 0);
+                        }
+                commit<PAIR>(lead, &mi.empty[slot], pair);
             }
             if (!ok) break;
-            if (PAIR) mma_commit_pair(lead, &mi.done[buf]);
-            else mma_commit_lead(lead, &mi.done[buf]);
+            commit<PAIR>(lead, &mi.done[buf], pair);
         }
         // nothing in flight when tensor memory is given back, whatever became of the epilogue
-        if (PAIR) mma_commit_pair(lead, &mi.drained);
-        else mma_commit_lead(lead, &mi.drained);
+        commit<PAIR>(lead, &mi.drained, pair);
+        if (lane == 0) mbar_wait_ns(&mi.drained, 0, kWait);
+    } else if (warp == 1) {
         if (lane == 0) mbar_wait_ns(&mi.drained, 0, kWait);
     } else if (warp >= 4) {
-        epilogue_role<OUT, PAIR>(mi, p, pl, tmem, rank, first, step);
+        pdl_wait();
+        if constexpr (S == 1) epilogue_role<OUT, PAIR>(mi, p, pl, tmem, rank, first, step);
+        else whole = put_part(mi, pl, part, tmem, from, to);
     }
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (PAIR) cluster_sync();  // neither CTA goes while the other's instructions use its memory
-    if (warp == 2) {
+    if (kClustered) cluster_sync();  // (no CTA goes while the other of the pair uses its memory)
+    tc_fence_after_sync();
+    if constexpr (S > 1) {
+        if (warp >= 4 && whole) join_parts<OUT, PAIR, S>(p, pl, part, tmem, first, rank, unit, from, to);
+        __syncwarp();
+        tc_fence_before_sync();
+        __syncthreads();
+        cluster_sync();
         tc_fence_after_sync();
+    }
+    if (warp == 2) {
         if (PAIR) tmem_dealloc_pair(tmem, pl.columns);
         else tmem_dealloc(tmem, pl.columns);
     }
@@ -350,10 +471,9 @@ bool make_map(CUtensorMap *m, const void *ptr, int k, int64_t rows, int64_t stri
 {
     tc::EncodeTiledFn enc = tc::encode_fn();
     if (!enc) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)k, 1, (cuuint64_t)rows};
-    const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {kDepth, 1, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
+    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {kDepth, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -363,19 +483,39 @@ bool rows_on(const void *p, int64_t stride, int64_t rows, size_t es)
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (size_t)stride * es % 16 == 0);
 }
 
-// The width of a tile: as few rounds of `at_once` tiles as possible, each as narrow as possible (`extra`: what a
-// round costs beside its columns, in columns).
-int tile_width(int n, int64_t tiles_m, int at_once, int extra)
+// A call's tiles: columns, in how many instructions, and the units among which the inputs are split.
+struct Tiles {
+    int width, parts, split;
+};
+
+// The least by what it takes, in cycles.  A panel of 64 inputs: its bytes into an SM at 40 a cycle, or its products;
+// a round of tiles: 20 a column for its epilogue; a split: 1,500 and 20 a column for its join.  All clusters of a split run at
+// once (of four CTAs 36, not 38; of eight 15).  us so and without a split, 4,096 inputs: 64 rows, 4,096 outputs
+// 13.4 and 18.7; 128 rows 13.7, 28.3; 256 rows 19.3, 28.7; 64 rows, 32 outputs 7.9, 14.0; 1,000 rows, 128 outputs 11.8,
+// 24.6; 128 rows, 12,288 outputs 25.9, 29.1.
+Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair)
 {
-    int best = 0;
-    int64_t least = 0;
-    for (int w = 16; w <= kMaxWidth; w += 16) {
-        const int64_t tiles = tiles_m * ((n + w - 1) / w), cost = (tiles + at_once - 1) / at_once * (w + extra);
-        if (best == 0 || cost < least) {
-            best = w;
-            least = cost;
-        }
-        if (w >= n) break;
+    const int64_t tiles_m = (rows + tall - 1) / tall, panels = (k + kDepth - 1) / kDepth;
+    Tiles best{};
+    int64_t least = INT64_MAX;
+    for (int split = 1; split <= 4; split *= 2) {
+        const int ctas = (pair ? 2 : 1) * split, at_once = ctas == 1 ? 152 : ctas == 2 ? 76 : ctas == 4 ? 36 : 15;
+        const int parts_max = split > 1 ? 2 : 1, unit = 16 * split;
+        if (split > 1 && panels < 4 * split) break;
+        for (int parts = 1; parts <= parts_max; ++parts)
+            for (int w = unit * parts; w <= kMaxWidth * parts; w += unit * parts) {
+                if (split > 1 && (w / parts % 16 != 0 || w * kM * 4 > kSmem - kHead)) continue;
+                const int64_t tiles = tiles_m * ((n + w - 1) / w), rounds = (tiles + at_once - 1) / at_once;
+                if (split > 1 && rounds > 1) continue;
+                const int64_t load = (int64_t)(box + (pair ? w / 2 : w)) * 128 / 40, mma = 4 * (w / 2 > 32 ? w / 2 : 32);
+                const int64_t cost = rounds * ((panels + split - 1) / split * (load > mma ? load : mma) + 20 * w) +
+                                     (split > 1 ? 1500 + 20 * w : 0);
+                if (cost < least) {
+                    least = cost;
+                    best = Tiles{w, parts, split};
+                }
+                if (w >= n) break;
+            }
     }
     return best;
 }
@@ -395,38 +535,55 @@ cudaError_t launch_linear_tc(const Linear &p)
     constexpr int kSms = 152;
     const bool pair = p.rows > kM && p.n > 64;
     Plan pl;
-    const int tall = pair ? 2 * kM : kM;
-    const int64_t tiles_m = (p.rows + tall - 1) / tall;
-    pl.width = tile_width(p.n, tiles_m, pair ? kSms / 2 : kSms, 32);
-    const int64_t tiles_n = (p.n + pl.width - 1) / pl.width;
-    if (tiles_m * tiles_n > INT32_MAX) return cudaErrorInvalidValue;
-    pl.tiles_m = (int)tiles_m; pl.tiles_n = (int)tiles_n;
-    pl.group = 8;
-    pl.box = (int)(p.rows < kM ? (p.rows + 7) / 8 * 8 : kM);
-    const int half = pair ? pl.width / 2 : pl.width, panel = (pl.box + half) * 128;
+    pl.tall = pair ? 2 * kM : p.rows < kM ? (int)((p.rows + 7) / 8 * 8) : kM;
+    // one CTA's tiles are lower where that lets all SMs take part
+    if (!pair && p.rows > kM && p.rows <= (int64_t)kM * kSms) pl.tall = (int)(((p.rows + kSms - 1) / kSms + 7) / 8 * 8);
+    pl.box = pair ? kM : pl.tall;
+    const Tiles at = choose_tiles(p.rows, p.n, p.k, pl.tall, pl.box, pair);
+    pl.width = at.width; pl.parts = at.parts;
+    const int64_t tiles_m = (p.rows + pl.tall - 1) / pl.tall, tiles_n = (p.n + pl.width - 1) / pl.width, tiles = tiles_m * tiles_n;
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    pl.tiles_m = (int)tiles_m; pl.tiles_n = (int)tiles_n; pl.group = 8;
+    const int rows_w = pair ? pl.width / 2 : pl.width, panel = (pl.box + rows_w) * 128;
     pl.panels = panel <= 8192 ? 4 : panel <= 16384 ? 2 : 1;
-    pl.stages = kStageBytes / (panel * pl.panels);
+    pl.pitch = 16;
+    while (pl.pitch < (uint32_t)(pl.width / pl.parts)) pl.pitch *= 2;
+    pl.columns = 2 * pl.pitch;
+    // rows that an instruction reads behind those that a short last panel holds
+    const int slack = (kM - pl.box) * 128, stage = panel * pl.panels;
+    pl.stages = (kSmem - kHead - slack) / stage;
     if (pl.stages > kMaxStages) pl.stages = kMaxStages;
-    pl.columns = 512;
+    pl.smem = kHead + pl.stages * stage + slack;
+    if (at.split > 1 && pl.smem < kHead + pl.width * kM * 4) pl.smem = kHead + pl.width * kM * 4;  // the parts
     const size_t eo = p.out_dtype == KDA_DTYPE_BF16 ? 2 : 4;
     pl.vec = rows_on(p.y, p.ys, p.rows, eo);
     pl.vec_r = rows_on(p.residual, p.rs, p.rows, eo);
     pl.vec_b = rows_on(p.bias, 0, 1, 2);
     CUtensorMap tx, tw;
     if (!make_map(&tx, p.x, p.k, p.rows, p.rows > 1 ? p.xs : p.k, pl.box) ||
-        !make_map(&tw, p.w, p.k, p.n, p.n > 1 ? p.ws : p.k, half))
+        !make_map(&tw, p.w, p.k, p.n, p.n > 1 ? p.ws : p.k, rows_w / pl.parts))
         return cudaErrorInvalidValue;
-    const int64_t at_once = pair ? kSms / 2 : kSms, tiles = tiles_m * tiles_n;
-    const unsigned blocks = (unsigned)((tiles < at_once ? tiles : at_once) * (pair ? 2 : 1));
+    const int ctas = (pair ? 2 : 1) * at.split;
+    const int64_t clusters = at.split > 1 || tiles < kSms / ctas ? tiles : kSms / ctas;
     auto launch = [&](auto kernel, int *configured) -> cudaError_t {
         const cudaError_t err = tc::allow_smem(kernel, kSmem, configured);
         if (err != cudaSuccess) return err;
-        return latent_launch(kernel, dim3(blocks), kThreads, kSmem, p.stream, pair ? 2 : 1, p, pl, tx, tw);
+        return latent_launch(kernel, dim3((unsigned)(clusters * ctas)), kThreads, (size_t)pl.smem, p.stream, ctas, p, pl, tx, tw);
     };
-    static int set[4] = {-1, -1, -1, -1};
-    const bool f32 = p.out_dtype == KDA_DTYPE_F32;
-    return pair ? f32 ? launch(linear_tc_kernel<float, true>, &set[0]) : launch(linear_tc_kernel<__nv_bfloat16, true>, &set[1])
-                : f32 ? launch(linear_tc_kernel<float, false>, &set[2]) : launch(linear_tc_kernel<__nv_bfloat16, false>, &set[3]);
+    static int set[12] = {-1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1};
+    auto of = [&](auto *out) {
+        using OUT = std::remove_pointer_t<decltype(out)>;
+        int *s = set + (sizeof(OUT) == 4 ? 6 : 0);
+        switch (2 * at.split + pair) {
+        case 2: return launch(linear_tc_kernel<OUT, false, 1>, s);
+        case 3: return launch(linear_tc_kernel<OUT, true, 1>, s + 1);
+        case 4: return launch(linear_tc_kernel<OUT, false, 2>, s + 2);
+        case 5: return launch(linear_tc_kernel<OUT, true, 2>, s + 3);
+        case 8: return launch(linear_tc_kernel<OUT, false, 4>, s + 4);
+        default: return launch(linear_tc_kernel<OUT, true, 4>, s + 5);
+        }
+    };
+    return p.out_dtype == KDA_DTYPE_F32 ? of(static_cast<float *>(nullptr)) : of(static_cast<__nv_bfloat16 *>(nullptr));
 }
 
 }  // namespace kda
