@@ -2,10 +2,10 @@
 //
 //   y_tc = act(b_c + sum_{j < W} w_cj x_{t - W + 1 + j, c}),   state: the last W - 1 rows of [state; x]
 //
-// Bound by memory: an element is read once and written once, W products between.  A thread has 16 bytes of
-// channels and walks along the tokens, the last W - 1 rows in registers.  The work is of two kinds, in one
-// launch:
-//  - runs of kRun tokens, whatever sequences they fall in: a token is computed here where all W rows of it
+// Bound by memory: an element is read once and written once, W products between.  A thread has four channels
+// (16 bytes of bf16 took 126 registers and 40 us where this takes 38) and walks along the tokens, the last W - 1 rows
+// in registers: 4,096 tokens of 12,288 channels in bf16 37.9 us, 5.3 TB/s.  The work is of two kinds, in one launch:
+//  - runs of tokens, whatever sequences they fall in: a token is computed here where all W rows of it
 //    are its sequence's;
 //  - heads, one for each sequence: its first W - 1 tokens, whose rows come from the state in part, and
 //    the new state.  A head reads and writes all that a sequence's state takes part in, thread by thread, so
@@ -17,62 +17,53 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRun = 16;   // tokens of a run
+// Tokens of a run.  4,096 tokens of 12,288 channels in bf16, us with 8, 16, 32: 41.4, 37.9, 40.6; 7,800 tokens of
+// 2,048 channels in fp32 28.1, 30.9, 34.7.
+template <typename IO> constexpr int kRun = sizeof(IO) == 2 ? 16 : 8;
 constexpr int kBatch = 8;  // rows asked for at once
+constexpr int kSeqs = 4;   // sequences of a thread that takes single tokens (256 of 12,288 channels 10.6 us; 1: 11.7)
 
-template <typename IO> constexpr int kVec = 16 / (int)sizeof(IO);
+// A thread's four channels of a row, as they lie in memory.
+constexpr int V = 4;
+template <typename IO> struct Raw;
+template <> struct Raw<__nv_bfloat16> { using Type = uint2; };
+template <> struct Raw<float> { using Type = uint4; };
+template <typename IO> using Raw4 = typename Raw<IO>::Type;
 
 template <typename IO>
-__device__ __forceinline__ void widen(const uint4 &r, float (&x)[kVec<IO>])
+__device__ __forceinline__ Raw4<IO> load_raw(const IO *p) { return *reinterpret_cast<const Raw4<IO> *>(p); }
+template <typename IO>
+__device__ __forceinline__ void store_raw(IO *p, const Raw4<IO> &r) { *reinterpret_cast<Raw4<IO> *>(p) = r; }
+__device__ __forceinline__ void widen(const uint2 &r, float (&x)[V])
 {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        if constexpr (sizeof(IO) == 2) {
-            x[2 * u] = __uint_as_float(w[u] << 16);
-            x[2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
-        } else {
-            x[u] = __uint_as_float(w[u]);
-        }
-    }
+    x[0] = __uint_as_float(r.x << 16); x[1] = __uint_as_float(r.x & 0xffff0000u);
+    x[2] = __uint_as_float(r.y << 16); x[3] = __uint_as_float(r.y & 0xffff0000u);
 }
-template <typename IO>
-__device__ __forceinline__ uint4 narrow(const float (&x)[kVec<IO>])
+__device__ __forceinline__ void widen(const uint4 &r, float (&x)[V])
 {
-    uint32_t w[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        if constexpr (sizeof(IO) == 2) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * u], x[2 * u + 1]);
-            w[u] = *reinterpret_cast<const uint32_t *>(&v);
-        } else {
-            w[u] = __float_as_uint(x[u]);
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
 }
 
 // A thread's channels: their taps and bias, and where their rows are.
 template <typename IO, int W>
 struct Channels {
-    static constexpr int V = kVec<IO>;
     float tap[V * W], bias[V];
     const IO *x;
     IO *y;
     __device__ __forceinline__ Channels(const ShortConv &p, int c)
     {
-        const uint4 *w = reinterpret_cast<const uint4 *>(static_cast<const IO *>(p.weight) + (int64_t)c * W);
+        const IO *w = static_cast<const IO *>(p.weight) + (int64_t)c * W;
 #pragma unroll
-        for (int j = 0; j < W; ++j) widen<IO>(__ldg(w + j), *reinterpret_cast<float(*)[V]>(&tap[V * j]));
+        for (int j = 0; j < W; ++j) widen(load_raw(w + V * j), *reinterpret_cast<float(*)[V]>(&tap[V * j]));
 #pragma unroll
         for (int v = 0; v < V; ++v) bias[v] = 0.f;
-        if (p.bias) widen<IO>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const IO *>(p.bias) + c)), bias);
+        if (p.bias) widen(load_raw(static_cast<const IO *>(p.bias) + c), bias);
         x = static_cast<const IO *>(p.x) + c;
         const int part = c / p.part;
         y = static_cast<IO *>(p.y) + part * p.part_stride + (c - part * p.part);
     }
-    // row[0 .. W - 1]: the rows of a token, the oldest first
-    __device__ __forceinline__ uint4 token(const float (&row)[W][V], bool silu) const
+    // Token t from its rows row[0 .. W - 1], the oldest first.
+    __device__ __forceinline__ void token(const ShortConv &p, const float (&row)[W][V], int64_t t) const
     {
         float a[V];
 #pragma unroll
@@ -80,16 +71,15 @@ struct Channels {
             a[v] = bias[v];
 #pragma unroll
             for (int j = 0; j < W; ++j) a[v] = fmaf(tap[v * W + j], row[j][v], a[v]);
-            if (silu) a[v] = silu_io<IO>(a[v]);
+            if (p.silu) a[v] = silu_io<IO>(a[v]);
         }
-        return narrow<IO>(a);
+        store_io4(y + t * p.ys, a);
     }
 };
 
 template <typename IO, int W>
 __device__ __forceinline__ void head(const ShortConv &p, int n, int c)
 {
-    constexpr int V = kVec<IO>;
     int first, end;
     int64_t init, fin;
     packed_range(p.seq, n, first, end);
@@ -97,21 +87,19 @@ __device__ __forceinline__ void head(const ShortConv &p, int n, int c)
     const int len = end - first, mine = min(len, W - 1);
     const IO *x = static_cast<const IO *>(p.x) + c;
     // the W - 1 rows of the state, and the sequence's first ones
-    uint4 raw[2 * W - 2], last[W - 1];
+    Raw4<IO> raw[2 * W - 2], last[W - 1];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-        raw[j] = make_uint4(0, 0, 0, 0);
-        if (init >= 0)
-            raw[j] = *reinterpret_cast<const uint4 *>(static_cast<const IO *>(p.seq.init) +
-                                                      (init * (W - 1) + j) * p.channels + c);
+        raw[j] = Raw4<IO>{};
+        if (init >= 0) raw[j] = load_raw(static_cast<const IO *>(p.seq.init) + (init * (W - 1) + j) * p.channels + c);
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-        if (j < mine) raw[W - 1 + j] = *reinterpret_cast<const uint4 *>(x + (int64_t)(first + j) * p.xs);
+        if (j < mine) raw[W - 1 + j] = load_raw(x + (int64_t)(first + j) * p.xs);
     // the last W - 1 rows of both
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-        if (len >= W - 1) last[j] = *reinterpret_cast<const uint4 *>(x + (int64_t)(end - (W - 1) + j) * p.xs);
+        if (len >= W - 1) last[j] = load_raw(x + (int64_t)(end - (W - 1) + j) * p.xs);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
         if (len == k)
@@ -120,7 +108,7 @@ __device__ __forceinline__ void head(const ShortConv &p, int n, int c)
     if (fin >= 0)
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            *reinterpret_cast<uint4 *>(static_cast<IO *>(p.seq.fin) + (fin * (W - 1) + j) * p.channels + c) = last[j];
+            store_raw(static_cast<IO *>(p.seq.fin) + (fin * (W - 1) + j) * p.channels + c, last[j]);
     if (mine == 0) return;
     const Channels<IO, W> ch(p, c);
 #pragma unroll
@@ -128,8 +116,8 @@ __device__ __forceinline__ void head(const ShortConv &p, int n, int c)
         if (t >= mine) break;
         float row[W][V];
 #pragma unroll
-        for (int j = 0; j < W; ++j) widen<IO>(raw[t + j], row[j]);
-        *reinterpret_cast<uint4 *>(ch.y + (int64_t)(first + t) * p.ys) = ch.token(row, p.silu);
+        for (int j = 0; j < W; ++j) widen(raw[t + j], row[j]);
+        ch.token(p, row, first + t);
     }
 }
 
@@ -146,12 +134,12 @@ __device__ __forceinline__ int sequence_of(const Packed &s, int t)
 }
 
 // Bit i: all W rows of token t0 + i are its sequence's.  A whole warp.
-template <int W>
+template <int W, int RUN>
 __device__ __forceinline__ uint32_t whole_tokens(const Packed &s, int t0, int lane)
 {
     const int t = t0 + lane;
     bool whole = false;
-    if (lane < kRun && t < s.tokens) {
+    if (lane < RUN && t < s.tokens) {
         int first, end;
         packed_range(s, s.cu ? sequence_of(s, t) : t / s.each, first, end);
         whole = t - first >= W - 1 && t < end;
@@ -162,35 +150,74 @@ __device__ __forceinline__ uint32_t whole_tokens(const Packed &s, int t0, int la
 template <typename IO, int W>
 __device__ __forceinline__ void run(const ShortConv &p, int t0, int c)
 {
-    constexpr int V = kVec<IO>;
     const Channels<IO, W> ch(p, c);
     const int total = (int)p.seq.tokens;
-    uint4 raw[kBatch];
+    constexpr int B = kBatch;
+    Raw4<IO> raw[B], before[W - 1];
     float row[W][V];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int t = max(t0 - (W - 1) + j, 0);
-        widen<IO>(*reinterpret_cast<const uint4 *>(ch.x + (int64_t)t * p.xs), row[j]);
-    }
+    for (int j = 0; j < W - 1; ++j) before[j] = load_raw(ch.x + (int64_t)max(t0 - (W - 1) + j, 0) * p.xs);
     uint32_t whole = 0;
 #pragma unroll
-    for (int b = 0; b < kRun; b += kBatch) {
+    for (int b = 0; b < kRun<IO>; b += B) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int t = min(t0 + b + i, total - 1);
-            raw[i] = *reinterpret_cast<const uint4 *>(ch.x + (int64_t)t * p.xs);
+        for (int i = 0; i < B; ++i) raw[i] = load_raw(ch.x + (int64_t)min(t0 + b + i, total - 1) * p.xs);
+        if (b == 0) {
+            whole = whole_tokens<W, kRun<IO>>(p.seq, t0, threadIdx.x & 31);  // (after the rows are on their way)
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) widen(before[j], row[j]);
         }
-        if (b == 0) whole = whole_tokens<W>(p.seq, t0, threadIdx.x & 31);  // (after the rows are on their way)
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            widen<IO>(raw[i], row[W - 1]);
-            if (whole >> (b + i) & 1)
-                *reinterpret_cast<uint4 *>(ch.y + (int64_t)(t0 + b + i) * p.ys) = ch.token(row, p.silu);
+        for (int i = 0; i < B; ++i) {
+            widen(raw[i], row[W - 1]);
+            if (whole >> (b + i) & 1) ch.token(p, row, t0 + b + i);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
                 for (int v = 0; v < V; ++v) row[j][v] = row[j + 1][v];
         }
+    }
+}
+
+// One token of each of kSeqs sequences: what head does where all sequences are one token, with everything of them
+// asked for at once.
+template <typename IO, int W>
+__global__ void __launch_bounds__(kThreads)
+short_conv_step_kernel(const ShortConv p, int channel_blocks)
+{
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    const int n0 = (int)(blockIdx.x / channel_blocks) * kSeqs;
+    const int c = ((blockIdx.x % channel_blocks) * kThreads + threadIdx.x) * V;
+    if (c >= p.channels) return;
+    int64_t init[kSeqs], fin[kSeqs];
+    Raw4<IO> raw[kSeqs][W];
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i) {
+        init[i] = fin[i] = -1;
+        if (n0 + i >= p.seq.num_seqs) continue;
+        if (!packed_entries(p.seq, n0 + i, init[i], fin[i]) && c == 0 && p.seq.errors) atomicOr(p.seq.errors, DEV_ERR_SLOT);
+        raw[i][W - 1] = load_raw(static_cast<const IO *>(p.x) + (int64_t)(n0 + i) * p.xs + c);
+    }
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i)
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            raw[i][j] = Raw4<IO>{};
+            if (init[i] >= 0) raw[i][j] = load_raw(static_cast<const IO *>(p.seq.init) + (init[i] * (W - 1) + j) * p.channels + c);
+        }
+    const Channels<IO, W> ch(p, c);
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i) {
+        if (n0 + i >= p.seq.num_seqs) break;
+        if (fin[i] >= 0)
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                store_raw(static_cast<IO *>(p.seq.fin) + (fin[i] * (W - 1) + j) * p.channels + c, raw[i][j + 1]);
+        float row[W][V];
+#pragma unroll
+        for (int j = 0; j < W; ++j) widen(raw[i][j], row[j]);
+        ch.token(p, row, n0 + i);
     }
 }
 
@@ -202,7 +229,7 @@ short_conv_kernel(const ShortConv p, int channel_blocks, int64_t head_blocks)
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const int64_t unit = blockIdx.x / channel_blocks;
-    const int c = ((blockIdx.x % channel_blocks) * kThreads + threadIdx.x) * kVec<IO>;
+    const int c = ((blockIdx.x % channel_blocks) * kThreads + threadIdx.x) * V;
     const bool mine = c < p.channels;
     if (unit < head_blocks) {
         if (blockIdx.x % channel_blocks == 0 && threadIdx.x == 0) {
@@ -212,17 +239,22 @@ short_conv_kernel(const ShortConv p, int channel_blocks, int64_t head_blocks)
         if (mine) head<IO, W>(p, (int)unit, c);
     } else {
         // (threads without channels keep the warp whole: the last channels, computed and stored again, the same)
-        run<IO, W>(p, (int)(unit - head_blocks) * kRun, mine ? c : p.channels - kVec<IO>);
+        run<IO, W>(p, (int)(unit - head_blocks) * kRun<IO>, mine ? c : p.channels - V);
     }
 }
 
 template <typename IO, int W>
 cudaError_t launch(const ShortConv &p)
 {
-    const int channel_blocks = (p.channels / kVec<IO> + kThreads - 1) / kThreads;
+    const int channel_blocks = (p.channels / V + kThreads - 1) / kThreads;
     const int64_t heads = p.seq.num_seqs;
+    if (!p.seq.cu && p.seq.each == 1) {
+        const int64_t blocks = (heads + kSeqs - 1) / kSeqs * channel_blocks;
+        if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+        return latent_launch(short_conv_step_kernel<IO, W>, dim3((unsigned)blocks), kThreads, 0, p.stream, 1, p, channel_blocks);
+    }
     // sequences of equal, few tokens have no others than their first W - 1
-    const int64_t runs = !p.seq.cu && p.seq.each < W ? 0 : (p.seq.tokens + kRun - 1) / kRun;
+    const int64_t runs = !p.seq.cu && p.seq.each < W ? 0 : (p.seq.tokens + kRun<IO> - 1) / kRun<IO>;
     const int64_t blocks = (heads + runs) * channel_blocks;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return latent_launch(short_conv_kernel<IO, W>, dim3((unsigned)blocks), kThreads, 0, p.stream, 1, p, channel_blocks, heads);
