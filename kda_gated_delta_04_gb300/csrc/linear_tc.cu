@@ -45,7 +45,9 @@ struct Plan {
     int stages;
     int tiles_m, tiles_n, group;  // tiles_m in groups that are worked on together
     uint32_t columns; // of tensor memory
-    uint32_t pitch;   // columns of it from one accumulator to the other: of the next tile, or the next part
+    uint32_t pitch;   // columns of it from one accumulator to the next: parts, then chains, then buffers
+    int chains;       // accumulators that a tile's inputs are shared out to
+    int buffers;      // tiles whose accumulators there is room for
     int smem;
     bool vec;         // rows of y start on 16 bytes
     bool vec_r, vec_b;  // those of the residual; the bias
@@ -227,32 +229,47 @@ struct Row {
     }
 };
 
+// 16 columns from c on of a tile, whose accumulators start at `base`: the chains' sums.  A warp in step.
+__device__ __forceinline__ void take16(const Plan &pl, uint32_t base, int c, float (&v)[16])
+{
+    const int w = pl.width / pl.parts;
+    const uint32_t at = base + (uint32_t)(threadIdx.x & 96) * 65536u + (c < w ? c : pl.pitch + (c - w));
+    tmem_ld16(at, v);
+    tmem_ld_wait();
+#pragma unroll 1
+    for (int i = 1; i < pl.chains; ++i) {
+        float u[16];
+        tmem_ld16(at + i * pl.parts * pl.pitch, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] += u[k];
+    }
+}
+
 template <typename OUT, bool PAIR>
 __device__ __forceinline__ void epilogue_role(Misc &mi, const Linear &p, const Plan &pl, uint32_t tmem, int rank, int first,
                                               int step)
 {
     volatile int *abort = &mi.abort;
     const int lane = threadIdx.x & 31;
-    const uint32_t quarter = (uint32_t)(threadIdx.x & 96) << 16;
     int count = 0;
     for (int tile = first; tile < pl.tiles_m * pl.tiles_n; tile += step, ++count) {
         int m, n;
         tile_at(pl, tile, m, n);
-        const int buf = count & 1, left = min(pl.width, p.n - n * pl.width);
+        const int buf = count % pl.buffers, left = min(pl.width, p.n - n * pl.width);
         const Row<OUT, PAIR> row(p, pl, m, n, rank);
         // the residual's next 16 columns are on their way while these are worked on
         const bool whole_r = row.r && row.mine && pl.vec_r;
         Raw16<OUT> next;
         if (whole_r && left >= 16) next.load(row.r);
-        if (!all_wait<false>(&mi.done[buf], (count >> 1) & 1, abort)) return;
+        if (!all_wait<false>(&mi.done[buf], (count / pl.buffers) & 1, abort)) return;
         tc_fence_after_sync();
 #pragma unroll 1
         for (int c = 0; c < left; c += 16) {
             float v[16];
-            tmem_ld16(tmem + buf * pl.pitch + c + quarter, v);
             const Raw16<OUT> now = next;
             if (whole_r && left - c >= 32) next.load(row.r + c + 16);
-            tmem_ld_wait();
+            take16(pl, tmem + buf * pl.chains * pl.pitch, c, v);
             if (c + 16 >= left) {  // the accumulators may be written again
                 tc_fence_before_sync();
                 __syncwarp();
@@ -266,27 +283,18 @@ __device__ __forceinline__ void epilogue_role(Misc &mi, const Linear &p, const P
     }
 }
 
-// Where column c of a tile of one or two parts is in tensor memory.
-__device__ __forceinline__ uint32_t column(const Plan &pl, int c)
-{
-    const int w = pl.width / pl.parts;
-    return c < w ? c : pl.pitch + (c - w);
-}
-
 // Of a tile whose inputs S units have a part of each: the sums of this one to shared memory, all but its share of the
 // columns (column by column, 128 rows each), once its products are done ...
 __device__ __forceinline__ bool put_part(Misc &mi, const Plan &pl, float *part, uint32_t tmem, int from, int to)
 {
     const int row = threadIdx.x & 127;
-    const uint32_t quarter = (uint32_t)(threadIdx.x & 96) << 16;
     if (!all_wait<false>(&mi.done[0], 0, &mi.abort)) return false;
     tc_fence_after_sync();
 #pragma unroll 1
     for (int c = 0; c < pl.width; c += 16) {
         if (c >= from && c < to) continue;
         float v[16];
-        tmem_ld16(tmem + column(pl, c) + quarter, v);
-        tmem_ld_wait();
+        take16(pl, tmem, c, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) part[(c + i) * kM + row] = v[i];
     }
@@ -297,7 +305,6 @@ template <typename OUT, bool PAIR, int S>
 __device__ __forceinline__ void join_parts(const Linear &p, const Plan &pl, const float *part, uint32_t tmem, int tile,
                                            int rank, int unit, int from, int to)
 {
-    const uint32_t quarter = (uint32_t)(threadIdx.x & 96) << 16;
     int m, n;
     tile_at(pl, tile, m, n);
     const Row<OUT, PAIR> row(p, pl, m, n, rank);
@@ -308,8 +315,7 @@ __device__ __forceinline__ void join_parts(const Linear &p, const Plan &pl, cons
         float v[16], sum[16] = {};
         Raw16<OUT> now;
         if (whole_r && left - c >= 16) now.load(row.r + c);
-        tmem_ld16(tmem + column(pl, c) + quarter, v);
-        tmem_ld_wait();
+        take16(pl, tmem, c, v);
 #pragma unroll
         for (int u = 0; u < S; ++u)
 #pragma unroll
@@ -415,23 +421,33 @@ linear_tc_kernel(const Linear p, const Plan pl, const __grid_constant__ CUtensor
         int t = 0, count = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step, ++count) {
-            const int buf = count & 1;
-            if (count >= 2 && !(ok = all_wait<PAIR>(&mi.freed[buf], ((count >> 1) - 1) & 1, abort))) break;
+            const int buf = count % pl.buffers;
+            if (count >= pl.buffers && !(ok = all_wait<PAIR>(&mi.freed[buf], (count / pl.buffers - 1) & 1, abort))) break;
             tc_fence_after_sync();
-            const uint32_t d = base + buf * pl.pitch;
+            uint32_t d = base + buf * pl.chains * pl.pitch;
+            int chain = 0, chain_end = panels / pl.chains;  // the panel that the next chain starts with
+            bool fresh = true;
             for (int s = 0; s < steps; ++s, ++t) {
                 const int slot = t % pl.stages, held = min(pl.panels, panels - s * pl.panels);
                 if (!(ok = all_wait<PAIR>(&mi.full[slot], (t / pl.stages) & 1, abort))) break;
                 tc_fence_after_sync();
                 const uint32_t a = sb + slot * stage_bytes, b = a + pl.panels * panel_x;
-                for (int i = 0; i < held; ++i)
+                for (int i = 0; i < held; ++i) {
+                    if (s * pl.panels + i == chain_end) {
+                        ++chain;
+                        chain_end = panels * (chain + 1) / pl.chains;
+                        d += pl.parts * pl.pitch;
+                        fresh = true;
+                    }
                     for (int j = 0; j < (S > 1 ? pl.parts : 1); ++j)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint64_t da = kdesc(a + i * panel_x + k * 32), db = kdesc(b + i * panel_w + j * half * 128 + k * 32);
-                            if (PAIR) mma_bf16_pair(lead, d + j * pl.pitch, da, db, id, s > 0 || i > 0 || k > 0);
-                            else mma_bf16_lead(lead, d + j * pl.pitch, da, db, id, s > 0 || i > 0 || k > 0);
+                            if (PAIR) mma_bf16_pair(lead, d + j * pl.pitch, da, db, id, !fresh || k > 0);
+                            else mma_bf16_lead(lead, d + j * pl.pitch, da, db, id, !fresh || k > 0);
                         }
+                    fresh = false;
+                }
                 commit<PAIR>(lead, &mi.empty[slot], pair);
             }
             if (!ok) break;
@@ -483,36 +499,55 @@ bool rows_on(const void *p, int64_t stride, int64_t rows, size_t es)
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (size_t)stride * es % 16 == 0);
 }
 
-// A call's tiles: columns, in how many instructions, and the units among which the inputs are split.
+// A call's tiles: columns, in how many instructions, the units among which the inputs are split, and the accumulators.
 struct Tiles {
-    int width, parts, split;
+    int width, parts, split, chains, buffers;
 };
+
+int pitch_of(int columns)
+{
+    int p = 16;
+    while (p < columns) p *= 2;
+    return p;
+}
+
+// The tensor cores cut sums off where fp32 arithmetic rounds, an error that grows with the additions in a row: 4,096
+// inputs leave 5e-6 of the sums' standard deviation.  That is nothing beside a bf16 output's rounding; for an fp32 output
+// the inputs are shared out to up to eight accumulators, 512 inputs each or more, which are added in fp32.
+int chains_of(bool f32, int width, int parts, int panels, int buffers)
+{
+    const int fit = 512 / (buffers * parts * pitch_of(width / parts)), most = panels / 8 < 8 ? panels / 8 : 8;
+    return !f32 || most < 1 ? 1 : fit < most ? fit : most;
+}
 
 // The least by what it takes, in cycles.  A panel of 64 inputs: its bytes into an SM at 40 a cycle, or its products;
 // a round of tiles: 20 a column for its epilogue; a split: 1,500 and 20 a column for its join.  All clusters of a split run at
 // once (of four CTAs 36, not 38; of eight 15).  us so and without a split, 4,096 inputs: 64 rows, 4,096 outputs
 // 13.4 and 18.7; 128 rows 13.7, 28.3; 256 rows 19.3, 28.7; 64 rows, 32 outputs 7.9, 14.0; 1,000 rows, 128 outputs 11.8,
 // 24.6; 128 rows, 12,288 outputs 25.9, 29.1.
-Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair)
+Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, bool f32)
 {
-    const int64_t tiles_m = (rows + tall - 1) / tall, panels = (k + kDepth - 1) / kDepth;
+    const int64_t tiles_m = (rows + tall - 1) / tall;
+    const int panels = (k + kDepth - 1) / kDepth;
     Tiles best{};
     int64_t least = INT64_MAX;
     for (int split = 1; split <= 4; split *= 2) {
         const int ctas = (pair ? 2 : 1) * split, at_once = ctas == 1 ? 152 : ctas == 2 ? 76 : ctas == 4 ? 36 : 15;
-        const int parts_max = split > 1 ? 2 : 1, unit = 16 * split;
+        const int parts_max = split > 1 ? 2 : 1, unit = 16 * split, each = panels / split;
         if (split > 1 && panels < 4 * split) break;
         for (int parts = 1; parts <= parts_max; ++parts)
             for (int w = unit * parts; w <= kMaxWidth * parts; w += unit * parts) {
-                if (split > 1 && (w / parts % 16 != 0 || w * kM * 4 > kSmem - kHead)) continue;
+                if (split > 1 && w * kM * 4 > kSmem - kHead) break;  // the parts that are joined
                 const int64_t tiles = tiles_m * ((n + w - 1) / w), rounds = (tiles + at_once - 1) / at_once;
                 if (split > 1 && rounds > 1) continue;
+                const int buffers = rounds > 1 && !f32 ? 2 : 1, chains = chains_of(f32, w, parts, each, buffers);
+                if (f32 && chains < 4 && chains < each / 8) break;
                 const int64_t load = (int64_t)(box + (pair ? w / 2 : w)) * 128 / 40, mma = 4 * (w / 2 > 32 ? w / 2 : 32);
                 const int64_t cost = rounds * ((panels + split - 1) / split * (load > mma ? load : mma) + 20 * w) +
                                      (split > 1 ? 1500 + 20 * w : 0);
                 if (cost < least) {
                     least = cost;
-                    best = Tiles{w, parts, split};
+                    best = Tiles{w, parts, split, chains, buffers};
                 }
                 if (w >= n) break;
             }
@@ -539,23 +574,24 @@ cudaError_t launch_linear_tc(const Linear &p)
     // one CTA's tiles are lower where that lets all SMs take part
     if (!pair && p.rows > kM && p.rows <= (int64_t)kM * kSms) pl.tall = (int)(((p.rows + kSms - 1) / kSms + 7) / 8 * 8);
     pl.box = pair ? kM : pl.tall;
-    const Tiles at = choose_tiles(p.rows, p.n, p.k, pl.tall, pl.box, pair);
-    pl.width = at.width; pl.parts = at.parts;
+    const bool f32 = p.out_dtype == KDA_DTYPE_F32;
+    const Tiles at = choose_tiles(p.rows, p.n, p.k, pl.tall, pl.box, pair, f32);
+    pl.width = at.width; pl.parts = at.parts; pl.chains = at.chains; pl.buffers = at.buffers;
     const int64_t tiles_m = (p.rows + pl.tall - 1) / pl.tall, tiles_n = (p.n + pl.width - 1) / pl.width, tiles = tiles_m * tiles_n;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     pl.tiles_m = (int)tiles_m; pl.tiles_n = (int)tiles_n; pl.group = 8;
     const int rows_w = pair ? pl.width / 2 : pl.width, panel = (pl.box + rows_w) * 128;
     pl.panels = panel <= 8192 ? 4 : panel <= 16384 ? 2 : 1;
-    pl.pitch = 16;
-    while (pl.pitch < (uint32_t)(pl.width / pl.parts)) pl.pitch *= 2;
-    pl.columns = 2 * pl.pitch;
+    pl.pitch = pitch_of(pl.width / pl.parts);
+    pl.columns = 32;
+    while (pl.columns < pl.pitch * pl.parts * pl.chains * pl.buffers) pl.columns *= 2;
     // rows that an instruction reads behind those that a short last panel holds
     const int slack = (kM - pl.box) * 128, stage = panel * pl.panels;
     pl.stages = (kSmem - kHead - slack) / stage;
     if (pl.stages > kMaxStages) pl.stages = kMaxStages;
     pl.smem = kHead + pl.stages * stage + slack;
     if (at.split > 1 && pl.smem < kHead + pl.width * kM * 4) pl.smem = kHead + pl.width * kM * 4;  // the parts
-    const size_t eo = p.out_dtype == KDA_DTYPE_BF16 ? 2 : 4;
+    const size_t eo = f32 ? 4 : 2;
     pl.vec = rows_on(p.y, p.ys, p.rows, eo);
     pl.vec_r = rows_on(p.residual, p.rs, p.rows, eo);
     pl.vec_b = rows_on(p.bias, 0, 1, 2);
@@ -583,7 +619,7 @@ cudaError_t launch_linear_tc(const Linear &p)
         default: return launch(linear_tc_kernel<OUT, true, 4>, s + 5);
         }
     };
-    return p.out_dtype == KDA_DTYPE_F32 ? of(static_cast<float *>(nullptr)) : of(static_cast<__nv_bfloat16 *>(nullptr));
+    return f32 ? of(static_cast<float *>(nullptr)) : of(static_cast<__nv_bfloat16 *>(nullptr));
 }
 
 }  // namespace kda
