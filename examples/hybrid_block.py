@@ -3,13 +3,15 @@ latent-attention layer, random weights.
 
     python examples/hybrid_block.py            # bf16; needs the GPU and the built library
 
-The prompts of several sequences are packed.  The KDA layer keeps a state per sequence
-(kda.prefill, kda.decode_step).  The latent layer keeps one row of 576 channels per token in a paged
-cache: kda.latent_append normalises, rotates and stores the rows and rotates the queries;
-kda.latent_prefill attends over the prompt with keys and values expanded per head; kda.latent_decode
-attends over the cache with the up-projections absorbed into the query and the output.  The script
-then prefills the prompts with the generated tokens' inputs appended and compares: the last rows of
-the expanded form must be what the absorbed steps gave.
+The prompts of several sequences are packed.  The KDA layer keeps two states per sequence: the last
+rows of its short convolution (kda.short_conv, kda.short_conv_step) and that of the recurrence
+(kda.prefill, kda.decode_step); its projections are kda.linear, with their activations and the residual.
+The latent layer keeps one row of 576 channels per token in a paged cache: kda.latent_append
+normalises, rotates and stores the rows and rotates the queries; kda.latent_prefill attends over the
+prompt with keys and values expanded per head; kda.latent_decode attends over the cache with the
+up-projections absorbed into the query and the output.  The script then prefills the prompts with the
+generated tokens' inputs appended and compares: the last rows of the expanded form must be what the
+absorbed steps gave.
 """
 import argparse
 import os
@@ -28,24 +30,29 @@ def rms(x, eps=1e-6):
 
 
 class KdaLayer:
-    """q, k, v, the decay and beta from the block's input; the state is the library's."""
+    """The projections to q, k, v, the decay and beta, the short convolution of q, k and v, the recurrence, and the
+    projection back onto the residual stream; the states, of the convolution and of the recurrence, are the library's."""
 
     def __init__(self, dim, heads, g, dt):
-        self.heads, d = heads, 128
-        self.w = [(torch.randn(dim, heads * d, generator=g, device="cuda") * dim ** -0.5).to(dt) for _ in range(4)]
-        self.w_beta = (torch.randn(dim, heads, generator=g, device="cuda") * dim ** -0.5).to(dt)
-        self.out = (torch.randn(heads * d, dim, generator=g, device="cuda") * (heads * d) ** -0.5).to(dt)
+        def normal(n, k):
+            return (torch.randn(n, k, generator=g, device="cuda") * k ** -0.5).to(dt)
+        self.heads, width = heads, heads * 128
+        self.w_qkv, self.w_decay, self.w_beta = normal(3 * width, dim), normal(width, dim), normal(heads, dim)
+        self.taps, self.out = normal(3 * width, 4), normal(dim, width)
 
-    def inputs(self, x):
-        q, k, v, a = ((x @ w).view(-1, self.heads, 128) for w in self.w)
-        return q, k, v, -0.1 * torch.sigmoid(a.float()), torch.sigmoid((x @ self.w_beta).float())
+    def gates(self, x):
+        decay = kda.linear(x, self.w_decay, activation="sigmoid", out_dtype=torch.float32)
+        return -0.1 * decay.view(-1, self.heads, 128), kda.linear(x, self.w_beta, activation="sigmoid", out_dtype=torch.float32)
 
     def prefill(self, x, cu):
-        o, self.state = kda.prefill(*self.inputs(x), cu, qk_l2norm=True)
-        return o.flatten(1) @ self.out
+        qkv, self.rows = kda.short_conv(kda.linear(x, self.w_qkv), self.taps, None, cu, parts=3)
+        o, self.state = kda.prefill(*qkv.unflatten(2, (self.heads, 128)), *self.gates(x), cu, qk_l2norm=True)
+        return kda.linear(o.flatten(1), self.out, residual=x)
 
     def step(self, x):
-        return kda.decode_step(*self.inputs(x), self.state, qk_l2norm=True).flatten(1) @ self.out
+        qkv = kda.short_conv_step(kda.linear(x, self.w_qkv), self.taps, self.rows, parts=3)
+        o = kda.decode_step(*qkv.unflatten(2, (self.heads, 128)), *self.gates(x), self.state, qk_l2norm=True)
+        return kda.linear(o.flatten(1), self.out, residual=x)
 
 
 class LatentLayer:
@@ -112,12 +119,12 @@ def run(lens=(300, 77, 5), steps=4, dim=512, heads=4, dtype=torch.bfloat16, page
 
     cu, pos, slots = packed(lens)
     x = torch.cat(prompts)
-    h = rms(x + first.prefill(x, cu))
+    h = rms(first.prefill(x, cu))
     second.prefill(h, cu, pos, slots)
     inputs, outputs = [h], []  # the latent layer's
     held = torch.tensor(lens, dtype=torch.int32, device="cuda")
     for t in range(steps):
-        h = rms(tokens[t] + first.step(tokens[t]))
+        h = rms(first.step(tokens[t]))
         y = second.step(h, held, slots_of(torch.arange(n, device="cuda"), held.long()).int(), table, held + 1)
         held += 1
         inputs.append(h)

@@ -5,8 +5,8 @@ then linked into ``kda_gated_delta_04_gb300/libkda.so`` against the shared CUDA
 runtime, so the library shares the process's runtime with PyTorch.
 
 Beside it goes ``_latent_args.so`` (g++, against this interpreter's and the
-installed torch's headers): the latent calls' arguments from tensors to the C
-entry points without ctypes.  It is an option: where what it needs is missing, or
+installed torch's headers): the arguments of the latent calls, and of those around
+the recurrence, from tensors to the C entry points without ctypes.  It is an option: where what it needs is missing, or
 it cannot be compiled or linked, it is left out with a message, and kda.py passes
 the same arguments through ctypes.
 """

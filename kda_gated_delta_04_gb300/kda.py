@@ -551,8 +551,9 @@ def decode_step(q, k, v, log_alpha, beta, state, *, o=None, stream=None, qk_l2no
 # These calls are made once per layer and generated token, where the host's time counts: a tensor
 # that is as it should be is checked with a handful of comparisons, and only one that is not is
 # looked at again for the message.
-# Where latent_args.cpp has been built (against the torch that runs), a call whose every argument is as
-# it should be goes through it; the checks here are then for naming what is not.
+# Where latent_args.cpp has been built (against the torch that runs), a call (of these, and of those around
+# the recurrence below) whose every argument is as it should be goes through it; the checks here are then
+# for naming what is not.
 _torch_module = None
 _native = None
 
@@ -825,6 +826,13 @@ def linear(x, w, bias=None, *, activation=None, residual=None, out=None, out_dty
         out = _empty((M, N), out_dtype or dt, dev, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    act = _activation(activation)
+    if _native is not None:
+        st = _native.linear(x, w, bias, residual, act, out, errors, None if stream is None else stream.cuda_stream)
+        if st == KDA_OK:
+            return out
+        if st > 0:
+            raise KdaError(st, "kda_linear")
     odt = out.dtype
     xp, xs = _rows2(x, "x", dt, dev, (M, K))
     wp, ws = _rows2(w, "w", dt, dev, (N, K))
@@ -832,7 +840,7 @@ def linear(x, w, bias=None, *, activation=None, residual=None, out=None, out_dty
     rp, rs = (None, 0) if residual is None else _rows2(residual, "residual", odt, dev, (M, N))
     st = (_lib or lib()).kda_linear(
         xp, xs, wp, ws, None if bias is None else _flat(bias, "bias", dt, dev, (N,)), rp, rs, yp, ys, M, N, K, code,
-        _dtype_code(out), _activation(activation), None if errors is None else _flat(errors, "errors", torch.int32, dev, (1,)),
+        _dtype_code(out), act, None if errors is None else _flat(errors, "errors", torch.int32, dev, (1,)),
         _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear")
@@ -861,6 +869,14 @@ def _short_conv(x, weight, bias, cu_seqlens, seqs, init_state, init_slots, final
     shape = (T, C) if parts == 1 else (parts, T, C // parts)
     if out is None:
         out = _empty(shape, dt, dev, stream)
+    act = _activation(activation)
+    if _native is not None:
+        st = _native.conv(x, weight, bias, cu_seqlens, seqs, init_state, init_slots, final_state, final_slots, act, parts, out,
+                          errors, None if stream is None else stream.cuda_stream)
+        if st == KDA_OK:
+            return out
+        if st > 0:
+            raise KdaError(st, "kda_short_conv")
     xp, xs = _rows2(x, "x", dt, dev, (T, C))
     if parts == 1:
         ps, (yp, ys) = 0, _rows2(out, "out", dt, dev, shape)
@@ -871,7 +887,7 @@ def _short_conv(x, weight, bias, cu_seqlens, seqs, init_state, init_slots, final
     fp, fsl, fnum = _entries(final_state, final_slots, "final_state", dt, dev, (width - 1, C), seqs)
     st = (_lib or lib()).kda_short_conv(
         xp, xs, _flat(weight, "weight", dt, dev, (C, width)), None if bias is None else _flat(bias, "bias", dt, dev, (C,)),
-        width, cu, seqs, T, C, parts, code, _activation(activation), ip, isl, inum, fp, fsl, fnum, yp, ps, ys,
+        width, cu, seqs, T, C, parts, code, act, ip, isl, inum, fp, fsl, fnum, yp, ps, ys,
         None if errors is None else _flat(errors, "errors", torch.int32, dev, (1,)), _raw_stream(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_short_conv")
@@ -915,6 +931,13 @@ def _selective_scan(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, seqs, init_state,
     n = A.shape[1] if A.dim() == 2 else -1
     if out is None:
         out = _empty((T, channels), ty, dev, stream)
+    if _native is not None:
+        st = _native.scan(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, seqs, init_state, init_slots, final_state, final_slots,
+                          softplus, out, errors, None if stream is None else stream.cuda_stream)
+        if st == KDA_OK:
+            return out
+        if st > 0:
+            raise KdaError(st, "kda_selective_scan")
     xp, xs = _rows2(x, "x", ty, dev, (T, channels))
     dp, ds = _rows2(dt, "dt", ty, dev, (T, channels))
     zp, zs = (None, 0) if z is None else _rows2(z, "z", ty, dev, (T, channels))

@@ -1,5 +1,5 @@
-// latent_args.cpp -- the latent calls' arguments from torch tensors to the C entry points, for calls
-// whose every argument is as it should be.  Returns the entry point's status, or -1 when some
+// latent_args.cpp -- the arguments of the latent calls, and of those around the recurrence, from torch tensors to the
+// C entry points, for calls whose every argument is as it should be.  Returns the entry point's status, or -1 when some
 // argument is not: kda.py then checks them one by one and names the one.  Nothing is computed here, and
 // nothing is kept between calls.
 //
@@ -13,6 +13,13 @@
 #include <torch/version.h>
 
 #include "../../include/kda.h"
+
+// Weak: a library that has the latent calls alone is served too.
+extern "C" {
+extern __attribute__((weak)) decltype(kda_linear) kda_linear;
+extern __attribute__((weak)) decltype(kda_short_conv) kda_short_conv;
+extern __attribute__((weak)) decltype(kda_selective_scan) kda_selective_scan;
+}
 
 namespace {
 
@@ -75,6 +82,30 @@ struct Args {
             ok = false;
         }
         return x > 0;
+    }
+    int64_t whole(int i)
+    {
+        const long long x = PyLong_Check(v[i]) ? PyLong_AsLongLong(v[i]) : -1;
+        if (x == -1) {
+            PyErr_Clear();
+            ok = false;
+        }
+        return x;
+    }
+    // a pool of states, or None: contiguous entries of these sizes, and how many
+    void *pool(int i, at::ScalarType want, const int64_t (&size)[2], int64_t *count)
+    {
+        if (!given(i)) return nullptr;
+        const at::Tensor *t = tensor(i);
+        if (!t || t->dim() != 3) return fail();
+        *count = t->size(0);
+        return flat(i, want, {*count, size[0], size[1]});
+    }
+    // which of its entries are the sequences', or None
+    void *slots(int i, int of, int64_t seqs)
+    {
+        if (!given(i)) return nullptr;
+        return given(of) ? flat(i, at::kInt, {seqs}) : fail();
     }
     double number(int i)
     {
@@ -226,10 +257,110 @@ PyObject *prefill(PyObject *, PyObject *const *v, Py_ssize_t n)
     });
 }
 
+// x, w, bias, residual, activation (code), out, errors, stream
+PyObject *linear(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    return answer([&]() -> long {
+        if (n != 8 || !kda_linear) return kNo;
+        Args a{v};
+        const at::Tensor *x = a.like(0, 2), *w = a.tensor(1), *y = a.tensor(5);
+        if (!x || !w || w->dim() != 2 || !y) return kNo;
+        const at::ScalarType out = y->scalar_type();
+        if (out != at::kBFloat16 && out != at::kFloat) return kNo;
+        const int64_t M = x->size(0), K = x->size(1), N = w->size(0);
+        int64_t xs = 0, ws = 0, rs = 0, ys = 0;
+        const void *xp = a.rows(0, a.type, {M, K}, &xs), *wp = a.rows(1, a.type, {N, K}, &ws);
+        const void *b = a.given(2) ? a.flat(2, a.type, {N}) : nullptr, *r = a.given(3) ? a.rows(3, out, {M, N}, &rs) : nullptr;
+        const int64_t act = a.whole(4);
+        void *yp = a.rows(5, out, {M, N}, &ys), *err = a.given(6) ? a.flat(6, at::kInt, {1}) : nullptr, *stream = a.stream(7);
+        if (!a.ok || !a.here() || K > INT32_MAX || N > INT32_MAX) return kNo;
+        const Unlocked unlocked;
+        return kda_linear(xp, xs, wp, ws, b, r, rs, yp, ys, M, (int32_t)N, (int32_t)K, a.code(),
+                          out == at::kBFloat16 ? KDA_DTYPE_BF16 : KDA_DTYPE_F32, (kda_activation_t)act,
+                          static_cast<uint32_t *>(err), stream);
+    });
+}
+
+// x, weight, bias, cu_seqlens, num_seqs, init_state, init_slots, final_state, final_slots, activation (code), parts, out,
+// errors, stream
+PyObject *conv(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    return answer([&]() -> long {
+        if (n != 14 || !kda_short_conv) return kNo;
+        Args a{v};
+        const at::Tensor *x = a.like(0, 2), *w = a.tensor(1);
+        if (!x || !w || w->dim() != 2) return kNo;
+        const int64_t T = x->size(0), C = x->size(1), W = w->size(1), seqs = a.whole(4), act = a.whole(9), parts = a.whole(10);
+        if (!a.ok || parts < 1 || C % parts != 0 || seqs < 0) return kNo;
+        int64_t xs = 0, ys[2] = {};
+        const void *xp = a.rows(0, a.type, {T, C}, &xs), *wp = a.flat(1, a.type, {C, W});
+        const void *b = a.given(2) ? a.flat(2, a.type, {C}) : nullptr, *cu = a.given(3) ? a.flat(3, at::kInt, {seqs + 1}) : nullptr;
+        int64_t num_init = 0, num_fin = 0;
+        const void *init = a.pool(5, a.type, {W - 1, C}, &num_init), *is = a.slots(6, 5, seqs);
+        void *fin = a.pool(7, a.type, {W - 1, C}, &num_fin);
+        const void *fs = a.slots(8, 7, seqs);
+        void *y = parts == 1 ? a.rows(11, a.type, {T, C}, ys + 1) : a.rows(11, a.type, {parts, T, C / parts}, ys);
+        void *err = a.given(12) ? a.flat(12, at::kInt, {1}) : nullptr, *stream = a.stream(13);
+        if (!a.ok || !a.here() || C > INT32_MAX || W > INT32_MAX || seqs > INT32_MAX) return kNo;
+        const Unlocked unlocked;
+        return kda_short_conv(xp, xs, wp, b, (int32_t)W, static_cast<const int32_t *>(cu), (int32_t)seqs, T, (int32_t)C,
+                              (int32_t)parts, a.code(), (kda_activation_t)act, init, static_cast<const int32_t *>(is), num_init,
+                              fin, static_cast<const int32_t *>(fs), num_fin, y, ys[0], ys[1], static_cast<uint32_t *>(err),
+                              stream);
+    });
+}
+
+// x, dt, A, B, C, D, z, dt_bias, cu_seqlens, num_seqs, init_state, init_slots, final_state, final_slots, softplus, out,
+// errors, stream
+PyObject *scan(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    return answer([&]() -> long {
+        if (n != 18 || !kda_selective_scan) return kNo;
+        Args a{v};
+        const at::Tensor *x = a.like(0, 2), *A = a.tensor(2), *B = a.tensor(3);
+        if (!x || !A || A->dim() != 2 || !B || (B->dim() != 2 && B->dim() != 3)) return kNo;
+        const int64_t T = x->size(0), C = x->size(1), N = A->size(1), G = B->dim() == 3 ? B->size(1) : 1, seqs = a.whole(9);
+        if (!a.ok || seqs < 0) return kNo;
+        int64_t xs = 0, ds = 0, zs = 0, ys = 0, bs[2] = {}, cs[2] = {};
+        const void *xp = a.rows(0, a.type, {T, C}, &xs), *dp = a.rows(1, a.type, {T, C}, &ds);
+        const void *ap = a.flat(2, at::kFloat, {C, N});
+        const void *bp, *cp;
+        if (B->dim() == 3) {
+            bp = a.rows(3, a.type, {T, G, N}, bs);
+            cp = a.rows(4, a.type, {T, G, N}, cs);
+            if (G > 1 && (bs[1] != N || cs[1] != N)) return kNo;
+        } else {
+            bp = a.rows(3, a.type, {T, N}, bs);
+            cp = a.rows(4, a.type, {T, N}, cs);
+        }
+        const void *skip = a.given(5) ? a.flat(5, at::kFloat, {C}) : nullptr;
+        const void *z = a.given(6) ? a.rows(6, a.type, {T, C}, &zs) : nullptr;
+        const void *bias = a.given(7) ? a.flat(7, at::kFloat, {C}) : nullptr;
+        const void *cu = a.given(8) ? a.flat(8, at::kInt, {seqs + 1}) : nullptr;
+        int64_t num_init = 0, num_fin = 0;
+        const void *init = a.pool(10, at::kFloat, {C, N}, &num_init), *is = a.slots(11, 10, seqs);
+        void *fin = a.pool(12, at::kFloat, {C, N}, &num_fin);
+        const void *fs = a.slots(13, 12, seqs);
+        const bool softplus = a.truth(14);
+        void *y = a.rows(15, a.type, {T, C}, &ys), *err = a.given(16) ? a.flat(16, at::kInt, {1}) : nullptr, *stream = a.stream(17);
+        if (!a.ok || !a.here() || C > INT32_MAX || N > INT32_MAX || G > INT32_MAX || seqs > INT32_MAX) return kNo;
+        const Unlocked unlocked;
+        return kda_selective_scan(xp, xs, dp, ds, static_cast<const float *>(ap), bp, bs[0], cp, cs[0],
+                                  static_cast<const float *>(skip), z, zs, static_cast<const float *>(bias),
+                                  static_cast<const int32_t *>(cu), (int32_t)seqs, T, (int32_t)C, (int32_t)G, (int32_t)N, a.code(),
+                                  static_cast<const float *>(init), static_cast<const int32_t *>(is), num_init,
+                                  static_cast<float *>(fin), static_cast<const int32_t *>(fs), num_fin, y, ys,
+                                  static_cast<uint32_t *>(err), stream, softplus ? KDA_SCAN_SOFTPLUS : 0);
+    });
+}
+
 PyMethodDef methods[] = {
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode)), METH_FASTCALL, nullptr},
     {"prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefill)), METH_FASTCALL, nullptr},
+    {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear)), METH_FASTCALL, nullptr},
+    {"conv", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(conv)), METH_FASTCALL, nullptr},
+    {"scan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scan)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_latent_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

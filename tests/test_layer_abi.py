@@ -1,5 +1,10 @@
 """The host side of the projections, the short convolution and the selective scan: every refusal before
 anything touches a GPU."""
+import importlib.machinery
+import importlib.util
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -111,3 +116,66 @@ def test_tensors_of_another_gpu_are_refused(kda, monkeypatch, name, args, kw):  
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)  # made current: taken
     getattr(kda, name)(*args, stream=Stream(), **kw)
     assert fake.called == ["kda_" + name.removesuffix("_step")]
+
+
+# ------------------------------------------------------------------ the native way
+STUB = """
+int PyGILState_Check(void);
+int kda_latent_append() { return 0; }
+int kda_latent_decode() { return 0; }
+int kda_latent_prefill() { return 0; }
+int kda_linear() { return 100 + PyGILState_Check(); }
+int kda_short_conv() { return 100 + PyGILState_Check(); }
+int kda_selective_scan() { return 100 + PyGILState_Check(); }
+"""
+
+
+@pytest.fixture(scope="module")
+def stubbed(kda, tmp_path_factory):  # noqa: F811
+    """The native module over a library whose entry points do nothing but say whether the calling thread
+    holds the interpreter's lock (101) or not (100)."""
+    from kda_gated_delta_04_gb300 import build
+    if not os.path.exists(build.ARGS_PATH):
+        pytest.skip("latent_args.cpp was left out of the build")
+    where = str(tmp_path_factory.mktemp("stub"))
+    with open(os.path.join(where, "stub.c"), "w") as f:
+        f.write(STUB)
+    run = lambda *cmd: subprocess.run(cmd, check=True, capture_output=True)
+    run("gcc", "-shared", "-fPIC", "-o", os.path.join(where, "liblayerstub.so"), os.path.join(where, "stub.c"))
+    path = os.path.join(where, "_latent_args.so")
+    run("g++", "-shared", "-o", path, os.path.join(build.BUILD_DIR, "latent_args.o"), "-L", where, "-llayerstub",
+        f"-Wl,-rpath,{where}", "-Wl,-Bsymbolic", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+        "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda")
+    loader = importlib.machinery.ExtensionFileLoader("_latent_args", path)
+    return importlib.util.module_from_spec(importlib.util.spec_from_loader("_latent_args", loader))
+
+
+def native_calls():
+    """Each call's arguments without the stream; where its numbers are, and its flag."""
+    t, f32, i32 = Claimed, torch.float32, torch.int32
+    yield "linear", [t(4, 64), t(32, 64), None, None, 1, t(4, 32), None], [4], None
+    yield "conv", [t(10, 48), t(48, 4), None, None, 1, None, None, t(1, 3, 48), None, 1, 3, t(3, 10, 16), None], [4, 9, 10], None
+    yield "scan", [t(10, 48), t(10, 48), t(48, 16, dtype=f32), t(10, 16), t(10, 16), None, None, None, t(3, dtype=i32), 2, None, None,
+                   t(2, 48, 16, dtype=f32), None, True, t(10, 48), None], [9], 14
+
+
+class Unclear:
+    def __bool__(self):
+        raise RuntimeError("neither true nor false")
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="with a device the tensors' own is compared first")
+@pytest.mark.parametrize("name,args,numbers,flag", list(native_calls()), ids=lambda x: x if isinstance(x, str) else "")
+def test_the_native_way(stubbed, name, args, numbers, flag):
+    """The lock is let go during the entry point; what is no number, or a flag without a truth value, is handed back
+    like any other bad argument, and leaves no error set."""
+    call = getattr(stubbed, name)
+    assert call(*args, 0) == 100
+    for at, bad in [(n, b) for n in numbers for b in (None, 1.5, "1", 2 ** 70, -1)] + ([] if flag is None else [(flag, Unclear())]):
+        st, after = call(*args[:at], bad, *args[at + 1:], 0), [i for i in range(3)]
+        assert st == -1 and after == [0, 1, 2], (at, bad)
+    assert call(*args) == -1 and call(*args, 0, 0) == -1
+    for at in range(len(args)):  # a tensor where none belongs, and none where one does
+        if isinstance(args[at], torch.Tensor) and at not in (7, 8, 12):
+            assert call(*args[:at], None, *args[at + 1:], 0) == -1, at
+        assert call(*args[:at], object(), *args[at + 1:], 0) in (-1, 100 if at == flag else -1), at
