@@ -4,8 +4,8 @@
 //
 // A tile of y is up to 128 rows by `width` columns of one CTA, or 256 rows by `width` of a pair (a cluster of two):
 // there each CTA holds its 128 rows of x and half of w's rows, and an instruction spans both (M = 256).  Many
-// tiles: CTAs stay and take one after the other, and the accumulators, fp32 in tensor memory, are doubled, so that a
-// tile's epilogue runs while the next one's products do.  Few tiles (few rows): the inputs of a tile are split among
+// tiles: CTAs stay and take one after the other; the accumulators, fp32 in tensor memory, are either doubled, so that
+// a tile's epilogue runs while the next one's products do, or fill it with up to 512 columns of one tile.  Few tiles (few rows): the inputs of a tile are split among
 // the units (CTAs or pairs) of a cluster, each of which has all its columns, and joined through distributed
 // shared memory: what bounds such a call are the bytes that an SM takes in, about 40 a cycle, and wide tiles over
 // part of the inputs take in fewer than narrow ones over all.
@@ -29,7 +29,7 @@ constexpr uint64_t kWait = tc::kWaitNs;
 
 struct Misc {
     uint64_t full[kMaxStages], empty[kMaxStages];  // full: of a pair, the leading CTA's
-    uint64_t done[2], drained, freed[2];           // done: in both CTAs; freed: the leading one's
+    uint64_t done[2], drained, freed[2];           // of a buffer (freed: or a part); done: in both CTAs; freed: the leading one's
     uint32_t tmem;
     int abort;
 };
@@ -251,7 +251,8 @@ __device__ __forceinline__ void epilogue_role(Misc &mi, const Linear &p, const P
                                               int step)
 {
     volatile int *abort = &mi.abort;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, part_w = pl.width / pl.parts;
+    const bool two = pl.parts == 2;
     int count = 0;
     for (int tile = first; tile < pl.tiles_m * pl.tiles_n; tile += step, ++count) {
         int m, n;
@@ -264,20 +265,27 @@ __device__ __forceinline__ void epilogue_role(Misc &mi, const Linear &p, const P
         if (whole_r && left >= 16) next.load(row.r);
         if (!all_wait<false>(&mi.done[buf], (count / pl.buffers) & 1, abort)) return;
         tc_fence_after_sync();
+        auto give_back = [&](int i) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(map_to_rank(&mi.freed[i], 0));
+                else mbar_arrive(&mi.freed[i]);
+            }
+        };
+        bool first_back = false;
 #pragma unroll 1
         for (int c = 0; c < left; c += 16) {
             float v[16];
             const Raw16<OUT> now = next;
             if (whole_r && left - c >= 32) next.load(row.r + c + 16);
             take16(pl, tmem + buf * pl.chains * pl.pitch, c, v);
-            if (c + 16 >= left) {  // the accumulators may be written again
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(map_to_rank(&mi.freed[buf], 0));
-                    else mbar_arrive(&mi.freed[buf]);
-                }
+            // the accumulators may be written again: one part's, or all of this tile's
+            if (two && !first_back && c + 16 >= min(left, part_w)) {
+                give_back(0);
+                first_back = true;
             }
+            if (c + 16 >= left) give_back(two ? 1 : buf);
             row.finish(p, pl, v, c, left - c, now);
         }
     }
@@ -422,8 +430,13 @@ linear_tc_kernel(const Linear p, const Plan pl, const __grid_constant__ CUtensor
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step, ++count) {
             const int buf = count % pl.buffers;
-            if (count >= pl.buffers && !(ok = all_wait<PAIR>(&mi.freed[buf], (count / pl.buffers - 1) & 1, abort))) break;
-            tc_fence_after_sync();
+            // the accumulators are free: of two parts the second's only where it is needed
+            auto free = [&](int i) {
+                if (count >= pl.buffers && !all_wait<PAIR>(&mi.freed[i], (count / pl.buffers - 1) & 1, abort)) return false;
+                tc_fence_after_sync();
+                return true;
+            };
+            if (!(ok = free(buf))) break;
             uint32_t d = base + buf * pl.chains * pl.pitch;
             int chain = 0, chain_end = panels / pl.chains;  // the panel that the next chain starts with
             bool fresh = true;
@@ -439,15 +452,18 @@ linear_tc_kernel(const Linear p, const Plan pl, const __grid_constant__ CUtensor
                         d += pl.parts * pl.pitch;
                         fresh = true;
                     }
-                    for (int j = 0; j < (S > 1 ? pl.parts : 1); ++j)
+                    for (int j = 0; j < pl.parts; ++j) {
+                        if (S == 1 && j == 1 && s == 0 && i == 0 && !(ok = free(1))) break;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint64_t da = kdesc(a + i * panel_x + k * 32), db = kdesc(b + i * panel_w + j * half * 128 + k * 32);
                             if (PAIR) mma_bf16_pair(lead, d + j * pl.pitch, da, db, id, !fresh || k > 0);
                             else mma_bf16_lead(lead, d + j * pl.pitch, da, db, id, !fresh || k > 0);
                         }
+                    }
                     fresh = false;
                 }
+                if (!ok) break;
                 commit<PAIR>(lead, &mi.empty[slot], pair);
             }
             if (!ok) break;
@@ -520,11 +536,14 @@ int chains_of(bool f32, int width, int parts, int panels, int buffers)
     return !f32 || most < 1 ? 1 : fit < most ? fit : most;
 }
 
-// The least by what it takes, in cycles.  A panel of 64 inputs: its bytes into an SM at 40 a cycle, or its products;
-// a round of tiles: 20 a column for its epilogue; a split: 1,500 and 20 a column for its join.  All clusters of a split run at
-// once (of four CTAs 36, not 38; of eight 15).  us so and without a split, 4,096 inputs: 64 rows, 4,096 outputs
-// 13.4 and 18.7; 128 rows 13.7, 28.3; 256 rows 19.3, 28.7; 64 rows, 32 outputs 7.9, 14.0; 1,000 rows, 128 outputs 11.8,
-// 24.6; 128 rows, 12,288 outputs 25.9, 29.1.
+// The least by what it takes, in cycles.  A panel of 64 inputs: its bytes into an SM at 46 a cycle, or its products (the
+// copies alone, without a product, take 281 of the 287 us of 4,096 rows, 4,096 inputs and 12,288 outputs in tiles of 240
+// columns: wider tiles take in less).  A tile's epilogue: 33 a column, beside the next tile's products where there are
+// two buffers (16,384 rows, 1,024 inputs, 4,096 outputs: tiles of 256 and two buffers 105 us, of 512 and one 131; 4,096
+// inputs, 4,096 rows, 12,288 outputs: of 240 and two 262, of 448 and one 238).  A split: 1,500 and 20 a column for its
+// join; all clusters of a split run at once (of four CTAs 36, not 38; of eight 15).  us with and without a split, 4,096
+// inputs: 64 rows, 4,096 outputs 13.4 and 18.7; 128 rows 13.7, 28.3; 256 rows 19.3, 28.7; 64 rows, 32 outputs 7.9, 14.0;
+// 1,000 rows, 128 outputs 11.8, 24.6; 128 rows, 12,288 outputs 25.9, 29.1.
 Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, bool f32)
 {
     const int64_t tiles_m = (rows + tall - 1) / tall;
@@ -533,17 +552,18 @@ Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, boo
     int64_t least = INT64_MAX;
     for (int split = 1; split <= 4; split *= 2) {
         const int ctas = (pair ? 2 : 1) * split, at_once = ctas == 1 ? 152 : ctas == 2 ? 76 : ctas == 4 ? 36 : 15;
-        const int parts_max = split > 1 ? 2 : 1, unit = 16 * split, each = panels / split;
+        const int unit = 16 * split, each = panels / split;
         if (split > 1 && panels < 4 * split) break;
-        for (int parts = 1; parts <= parts_max; ++parts)
+        for (int parts = 1; parts <= 2; ++parts)
             for (int w = unit * parts; w <= kMaxWidth * parts; w += unit * parts) {
                 if (split > 1 && w * kM * 4 > kSmem - kHead) break;  // the parts that are joined
                 const int64_t tiles = tiles_m * ((n + w - 1) / w), rounds = (tiles + at_once - 1) / at_once;
                 if (split > 1 && rounds > 1) continue;
-                const int buffers = rounds > 1 && !f32 ? 2 : 1, chains = chains_of(f32, w, parts, each, buffers);
+                const int buffers = rounds > 1 && !f32 && parts == 1 ? 2 : 1, chains = chains_of(f32, w, parts, each, buffers);
                 if (f32 && chains < 4 && chains < each / 8) break;
-                const int64_t load = (int64_t)(box + (pair ? w / 2 : w)) * 128 / 40, mma = 4 * (w / 2 > 32 ? w / 2 : 32);
-                const int64_t cost = rounds * ((panels + split - 1) / split * (load > mma ? load : mma) + 20 * w) +
+                const int64_t load = (int64_t)(box + (pair ? w / 2 : w)) * 128 / 46, mma = 4 * (w / 2 > 32 ? w / 2 : 32);
+                const int64_t main = (panels + split - 1) / split * (load > mma ? load : mma), out = 33 * w / split;
+                const int64_t cost = (buffers == 2 ? rounds * ((main > out ? main : out) + out / 4) + out : rounds * (main + out)) +
                                      (split > 1 ? 1500 + 20 * w : 0);
                 if (cost < least) {
                     least = cost;

@@ -36,7 +36,7 @@ def offsets(lens):
 SHAPES = [(1, 1, 1), (1, 8, 8), (1, 4096, 128), (3, 33, 72), (5, 1000, 264), (16, 128, 64), (17, 129, 1024), (64, 64, 64),
           (100, 32, 512), (128, 256, 128), (129, 257, 200), (255, 511, 136), (256, 4096, 256), (300, 4104, 96),
           (513, 1, 640), (300, 72, 64), (700, 100, 256), (1000, 128, 512), (5000, 96, 72), (1000, 40, 2048), (40, 4096, 512),
-          (33, 100, 64), (128, 5000, 256), (12, 9000, 64), (1024, 1024, 1024), (2049, 384, 64), (2500, 777, 320)]
+          (33, 100, 64), (128, 5000, 256), (12, 9000, 64), (4200, 4300, 192), (9000, 3900, 72), (1024, 1024, 1024), (2049, 384, 64), (2500, 777, 320)]
 
 
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
