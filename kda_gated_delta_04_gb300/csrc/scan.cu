@@ -5,7 +5,8 @@
 //
 // Per token and channel d_state exponentials and 5 d_state other operations against 8 bytes of bf16: bound by
 // instructions and by the bytes that shared memory gives to registers.  Only h's products and sums are in order of
-// the tokens, 4 cycles each, so that a sequence stays in order and its channels fill the GPU.
+// the tokens, 4 cycles each, so that a sequence stays in order where its channels fill the GPU; where they do not, up
+// to eight CTAs of a cluster have a part of it each (see scan_kernel).
 //
 // A CTA takes 8 to 32 channels of a sequence, each spread over the threads of N / S lanes with S states each; the
 // states that share a warp's loads of B and C and the channels that share those of d and d x are as many as registers
@@ -93,26 +94,31 @@ struct Shape {
     static constexpr int kGroups = N / S;                   // threads of a channel
     static constexpr int kWarpCh = CH < 16 ? CH : 16;       // channels of a warp
     static constexpr int kChunk = CH == 8 && N == 16 ? 64 : 32;        // tokens handed over at a time
+    static constexpr int kAhead = S >= 4 ? 2 : 4;           // pairs of tokens worked on at a time, and loaded ahead
     static constexpr int kPiece = 16 / (int)sizeof(IO);
     struct Raw {                                            // as they come
         alignas(16) IO x[kChunk][CH], dt[kChunk][CH], z[kChunk][CH], bc[kChunk][2 * N];
     };
     struct Ready {
         // (rows more than there are: what is loaded ahead, and not used, at the end)
-        float4 dd[kChunk / 2 + 4][CH];                      // d, d x of two tokens: d0, d1, d0 x0, d1 x1
-        alignas(16) Pair<IO> bc[kChunk / 2 + 4][N];
+        float4 dd[kChunk / 2 + kAhead][CH];                      // d, d x of two tokens: d0, d1, d0 x0, d1 x1
+        alignas(16) Pair<IO> bc[kChunk / 2 + kAhead][N];
         float2 y[kGroups][kChunk / 2][CH];                  // sums over a thread's states
     };
     // chunks in shared memory: one going out, one scanned, one made ready, one that has come, the others on their way
-    static constexpr int kFit = (int)((232448 - 2 * sizeof(Ready)) / sizeof(Raw)), kRing = kFit < 6 ? kFit : 6;
+    static constexpr int kFit = (int)((232448 - 8 * S * kScan - 2 * sizeof(Ready)) / sizeof(Raw)), kRing = kFit < 6 ? kFit : 6;
     static_assert(kRing >= 5 && kScan % 32 == 0);
     Ready ready[2];
     Raw raw[kRing];
+    float2 ends[S][kScan];  // of a part of the sequence: its states' ends E, and the root of P (see below)
 };
 
+// parts: the CTAs of a cluster, which have a part each of a sequence's tokens.  Each first scans its own without a
+// start (the first part: from the sequence's), to learn its end E and, from the sum of its steps, what a start is worth
+// there, P = exp(A sum d); then all but the first start from  h = P h + E  over the parts before, and scan again.
 template <typename IO, int N, int CH, int S>
 __global__ void __launch_bounds__(Shape<IO, N, CH, S>::kThreads, 2)
-scan_kernel(const Scan p, int group_blocks)
+scan_kernel(const Scan p, int group_blocks, int parts)
 {
     using Sh = Shape<IO, N, CH, S>;
     constexpr int T = Sh::kChunk, R = Sh::kRing, kScan = Sh::kScan;
@@ -120,13 +126,20 @@ scan_kernel(const Scan p, int group_blocks)
     Sh &sm = *reinterpret_cast<Sh *>(raw_smem);
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
-    const int blocks = p.groups * group_blocks, n = blockIdx.x / blocks, block = blockIdx.x % blocks;
+    const int part = blockIdx.x % parts, unit = blockIdx.x / parts;
+    const int blocks = p.groups * group_blocks, n = unit / blocks, block = unit % blocks;
     const int group = block / group_blocks, per_group = p.channels / p.groups;
     const int c0 = group * per_group + (block % group_blocks) * CH;   // first channel
     const int held = min(CH, (group + 1) * per_group - c0);            // channels: a multiple of 8
     int first, end;
     packed_range(p.seq, n, first, end);
+    if (parts > 1) {  // whole chunks each
+        const int each = ((end - first + parts - 1) / parts + T - 1) / T * T;
+        first = min(first + part * each, end);
+        end = min(first + each, end);
+    }
     const int len = end - first, chunks = (len + T - 1) / T;
+    const int early = parts > 1 && part + 1 < parts ? chunks : 0;  // chunks of the first scan (nothing follows the last part)
 
     if (threadIdx.x < kScan) {
         constexpr int CW = Sh::kWarpCh, PARTS = CH / CW;
@@ -135,7 +148,7 @@ scan_kernel(const Scan p, int group_blocks)
         const bool mine = ch < held;
         int64_t init, fin;
         const bool good = packed_entries(p.seq, n, init, fin);
-        if (threadIdx.x == 0 && block == 0) {
+        if (threadIdx.x == 0 && block == 0 && part == 0) {
             packed_check(p.seq, n);
             if (n == 0) packed_check(p.seq, p.seq.num_seqs);
             if (!good && p.seq.errors) atomicOr(p.seq.errors, DEV_ERR_SLOT);
@@ -145,59 +158,89 @@ scan_kernel(const Scan p, int group_blocks)
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             a[i] = mine ? p.a[at + i] * tc::kLog2e : 0.f;
-            h[i] = mine && init >= 0 ? static_cast<const float *>(p.seq.init)[init * all + at + i] : 0.f;
+            h[i] = part == 0 && mine && init >= 0 ? static_cast<const float *>(p.seq.init)[init * all + at + i] : 0.f;
         }
-        __syncthreads();
         // B pairs of tokens at a time, of which all but h's own products and sums can be done side by side; their
         // operands are loaded while the B before are worked on.  Tokens past the end leave h as it is (d = 0).
-        constexpr int B = S >= 4 ? 2 : 4;
+        constexpr int B = Sh::kAhead;
+        auto scan = [&](int chunks, auto ends) {  // ends: no sums are wanted, but that of the steps
+            float steps = 0.f;
+            __syncthreads();
 #pragma unroll 1
-        for (int k = 0; k < chunks; ++k) {
-            const int count = min(T, len - k * T);
-            const float4 *dd = &sm.ready[k & 1].dd[0][ch];
-            const Pair<IO> *bc = &sm.ready[k & 1].bc[0][g * S];
-            float2 *y = &sm.ready[k & 1].y[g][0][ch];
-            float4 d_next[B];
-            Pair<IO> bc_next[B][S];
-#pragma unroll
-            for (int q = 0; q < B; ++q) {
-                d_next[q] = dd[q * CH];
-                load_pairs<IO, S>(bc_next[q], bc + q * N);
-            }
-#pragma unroll 1
-            for (int t = 0; t < count; t += 2 * B) {
-                float4 d[B];
-                Pair<IO> x[B][S];
-                float2 sum[B];
-                dd += B * CH;
-                bc += B * N;
+            for (int k = 0; k < chunks; ++k) {
+                const int count = min(T, len - k * T);
+                const float4 *dd = &sm.ready[k & 1].dd[0][ch];
+                const Pair<IO> *bc = &sm.ready[k & 1].bc[0][g * S];
+                float2 *y = &sm.ready[k & 1].y[g][0][ch];
+                float4 d_next[B];
+                Pair<IO> bc_next[B][S];
+                float2 step_sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int q = 0; q < B; ++q) {
-                    d[q] = d_next[q];
-#pragma unroll
-                    for (int i = 0; i < S; ++i) x[q][i] = bc_next[q][i];
                     d_next[q] = dd[q * CH];
                     load_pairs<IO, S>(bc_next[q], bc + q * N);
                 }
+#pragma unroll 1
+                for (int t = 0; t < count; t += 2 * B) {
+                    float4 d[B];
+                    Pair<IO> x[B][S];
+                    float2 sum[B];
+                    dd += B * CH;
+                    bc += B * N;
 #pragma unroll
-                for (int q = 0; q < B; ++q)
+                    for (int q = 0; q < B; ++q) {
+                        d[q] = d_next[q];
 #pragma unroll
-                    for (int i = 0; i < S; ++i) {
-                        const float2 e = mul2(make_float2(d[q].x, d[q].y), make_float2(a[i], a[i]));
-                        const float2 b = mul2(make_float2(d[q].z, d[q].w), x[q][i].b());
-                        float2 hh;
-                        hh.x = fmaf(tc::exp2_approx(e.x), h[i], b.x);
-                        hh.y = fmaf(tc::exp2_approx(e.y), hh.x, b.y);
-                        h[i] = hh.y;
-                        sum[q] = i == 0 ? mul2(hh, x[q][i].c()) : ptx::fma2(hh, x[q][i].c(), sum[q]);
+                        for (int i = 0; i < S; ++i) x[q][i] = bc_next[q][i];
+                        d_next[q] = dd[q * CH];
+                        load_pairs<IO, S>(bc_next[q], bc + q * N);
                     }
 #pragma unroll
-                for (int q = 0; q < B; ++q) y[q * CH] = sum[q];
-                y += B * CH;
+                    for (int q = 0; q < B; ++q) {
+                        if (ends.value) step_sum = ptx::add2(step_sum, make_float2(d[q].x, d[q].y));
+#pragma unroll
+                        for (int i = 0; i < S; ++i) {
+                            const float2 e = mul2(make_float2(d[q].x, d[q].y), make_float2(a[i], a[i]));
+                            const float2 b = mul2(make_float2(d[q].z, d[q].w), x[q][i].b());
+                            float2 hh;
+                            hh.x = fmaf(tc::exp2_approx(e.x), h[i], b.x);
+                            hh.y = fmaf(tc::exp2_approx(e.y), hh.x, b.y);
+                            h[i] = hh.y;
+                            if (!ends.value) sum[q] = i == 0 ? mul2(hh, x[q][i].c()) : ptx::fma2(hh, x[q][i].c(), sum[q]);
+                        }
+                    }
+                    if (!ends.value)
+#pragma unroll
+                        for (int q = 0; q < B; ++q) y[q * CH] = sum[q];
+                    y += B * CH;
+                }
+                steps += step_sum.x + step_sum.y;
+                __syncthreads();
             }
-            __syncthreads();
+            return steps;
+        };
+        if (parts > 1) {
+            float start[S];
+#pragma unroll
+            for (int i = 0; i < S; ++i) start[i] = h[i];
+            const float steps = scan(early, Yes());
+#pragma unroll
+            for (int i = 0; i < S; ++i) sm.ends[i][threadIdx.x] = make_float2(h[i], tc::exp2_approx(0.5f * a[i] * steps));
+            ptx::cluster_sync();
+#pragma unroll
+            for (int i = 0; i < S; ++i) h[i] = start[i];
+#pragma unroll 1
+            for (int before = 0; before < part; ++before)
+#pragma unroll
+                for (int i = 0; i < S; ++i) {
+                    const float *from = &sm.ends[i][threadIdx.x].x;
+                    // P in two factors, whose range holds whatever a start may grow by; nothing grows to nothing
+                    const float root = ptx::peer_load(from + 1, before), e = ptx::peer_load(from, before);
+                    h[i] = h[i] == 0.f ? e : fmaf(h[i] * root, root, e);
+                }
         }
-        if (fin >= 0 && mine)
+        scan(chunks, No());
+        if (fin >= 0 && mine && part + 1 == parts)
 #pragma unroll
             for (int i = 0; i < S; ++i) static_cast<float *>(p.seq.fin)[fin * all + at + i] = h[i];
     } else if (threadIdx.x < kScan + kIn) {
@@ -277,19 +320,34 @@ scan_kernel(const Scan p, int group_blocks)
             from = from + 1 == sm.raw + R ? sm.raw : from + 1;
         };
         auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kIn) : "memory"); };  // the threads that bring in
+        auto bring = [&](int chunks) {
 #pragma unroll 1
-        for (int k = 0; k < R - 2; ++k) ask();
-        ptx::cp_async_wait<R - 4>();  // chunks 0 and 1 have come
-        meet();
-        if (chunks > 0) put(sm.ready[0]);
-        __syncthreads();
-#pragma unroll 1
-        for (int k = 0; k < chunks; ++k) {  // while chunk k is scanned
-            ask();                          // to where chunk k - 2 was
-            if (k + 1 < chunks) put(sm.ready[(k + 1) & 1]);
-            ptx::cp_async_wait<R - 4>();    // chunk k + 2 has come
+            for (int k = 0; k < R - 2; ++k) ask();
+            ptx::cp_async_wait<R - 4>();  // chunks 0 and 1 have come
+            meet();
+            if (chunks > 0) put(sm.ready[0]);
             __syncthreads();
+#pragma unroll 1
+            for (int k = 0; k < chunks; ++k) {  // while chunk k is scanned
+                ask();                          // to where chunk k - 2 was
+                if (k + 1 < chunks) put(sm.ready[(k + 1) & 1]);
+                ptx::cp_async_wait<R - 4>();    // chunk k + 2 has come
+                __syncthreads();
+            }
+        };
+        if (parts > 1) {
+            bring(early);
+            ptx::cluster_sync();
+            // from the start again; no copy of the first scan is on its way
+            ptx::cp_async_wait<0>();
+            meet();
+            const int64_t back = asked;
+            x -= back * p.xs; dt -= back * p.dts; z -= back * p.zs; bc -= back * bcs;
+            asked = made = 0;
+            to = sm.raw;
+            from = sm.raw;
         }
+        bring(chunks);
     } else {
         const int tid = threadIdx.x - kScan - kIn;
         constexpr int kPairs = kOut / (CH / 2);
@@ -298,6 +356,11 @@ scan_kernel(const Scan p, int group_blocks)
         float2 skip = make_float2(0.f, 0.f);
         if (p.d && c < held) skip = load2(p.d + c0 + c);
         const typename Sh::Raw *raw = sm.raw;
+        if (parts > 1) {
+#pragma unroll 1
+            for (int k = 0; k <= early; ++k) __syncthreads();
+            ptx::cluster_sync();
+        }
         __syncthreads();
 #pragma unroll 1
         for (int k = 0; k <= chunks; ++k) {
@@ -338,40 +401,82 @@ scan_kernel(const Scan p, int group_blocks)
             if (k < chunks) __syncthreads();
         }
     }
+    if (parts > 1) ptx::cluster_sync();  // no CTA goes while another may read its ends
 }
 
 template <typename IO, int N, int CH, int S>
-cudaError_t launch(const Scan &p)
+cudaError_t launch(const Scan &p, int parts)
 {
     using Sh = Shape<IO, N, CH, S>;
     static int configured = -1;
     const cudaError_t err = tc::allow_smem(scan_kernel<IO, N, CH, S>, (int)sizeof(Sh), &configured);
     if (err != cudaSuccess) return err;
     const int group_blocks = (p.channels / p.groups + CH - 1) / CH;
-    const int64_t blocks = (int64_t)group_blocks * p.groups * p.seq.num_seqs;
+    const int64_t blocks = (int64_t)group_blocks * p.groups * p.seq.num_seqs * parts;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return latent_launch(scan_kernel<IO, N, CH, S>, dim3((unsigned)blocks), Sh::kThreads, sizeof(Sh), p.stream, 1, p,
-                         group_blocks);
+    return latent_launch(scan_kernel<IO, N, CH, S>, dim3((unsigned)blocks), Sh::kThreads, sizeof(Sh), p.stream, parts, p,
+                         group_blocks, parts);
 }
 
-// Channels of a CTA and states of a thread: the fewest channels of which all CTAs run at once, one on an SM, since a
-// narrower CTA takes less time a token (16 states: 34 ns for 32 channels, 23 for 16, 17 for 8), else the most, which
-// take the least a channel (two on an SM).  4,096 tokens of 16 states in bf16, us with 32, 16, 8 channels: one sequence
-// of 1,024 channels 140, 96, 68; of 2,048 140, 96, 135; of 4,096 140, 151, 267; four sequences of 4,096 117, 135, 253.
+// What a call takes, in ns, with so many channels a CTA and so many parts of a sequence: a token `token_ns` with a CTA on
+// an SM; two on an SM (where they fit) take 1.74 times that each; the first scan of parts 0.75 times; joining them 3 us.
+// All clusters' CTAs at once: 152 of one or two, 144 of four, 120 of eight; two on an SM twice that (of eight 256).  The
+// lengths are on the device: the sequences count as equally long.
+double scan_ns(const Scan &p, int channels, int chunk, size_t smem, double token_ns, int parts)
+{
+    const int64_t ctas = (int64_t)((p.channels / p.groups + channels - 1) / channels) * p.groups * p.seq.num_seqs * parts;
+    const int64_t mean = (p.seq.tokens + p.seq.num_seqs - 1) / p.seq.num_seqs;
+    const int64_t each = ((mean + parts - 1) / parts + chunk - 1) / chunk * chunk;
+    const int64_t one = parts == 8 ? 120 : parts == 4 ? 144 : 152, two = parts == 8 ? 256 : 2 * one;
+    const bool fits = 2 * (smem + 1024) <= 233472;
+    const double crowd = ctas <= one ? 1 : fits ? 1.74 * ((ctas + two - 1) / two) : (double)((ctas + one - 1) / one);
+    return each * token_ns * crowd * (parts > 1 ? 1.75 : 1) + (parts > 1 ? 3000 : 0);
+}
+
+// The form that takes the least by that.  16 states in bf16, us with the form that is chosen and without parts: 16,384
+// tokens of 1,024 channels 212 (32 channels a CTA, eight parts) and 263 (8 channels), of 512 135 (16, eight) and 271; 4,096
+// tokens of 256 31 (8, four) and 66, of 64 18 (8, eight) and 66, of 2,048 96 (16 channels; in parts 107), of 4,096 140
+// (32 channels; 16 take 151, parts more); four sequences of 2,048 tokens and 256 channels 33 (32, eight) and 36.
+template <typename IO, int N>
+struct Chooser {
+    const Scan &p;
+    double least = 1e300;
+    int parts = 1;
+    cudaError_t (*go)(const Scan &, int) = nullptr;
+    template <int CH, int S>
+    void consider(double token_ns)
+    {
+        using Sh = Shape<IO, N, CH, S>;
+        for (int k = 1; k <= 8; k *= 2) {
+            const double ns = scan_ns(p, CH, Sh::kChunk, sizeof(Sh), token_ns, k);
+            if (ns >= least) continue;
+            least = ns;
+            parts = k;
+            go = launch<IO, N, CH, S>;
+        }
+    }
+};
+
 template <typename IO, int N>
 cudaError_t choose(const Scan &p)
 {
-    const int per_group = p.channels / p.groups;
-    auto at_once = [&](int ch) { return (int64_t)((per_group + ch - 1) / ch) * p.groups * p.seq.num_seqs <= 152; };
+    Chooser<IO, N> c{p};
     if constexpr (N == 8) {
-        return at_once(16) ? launch<IO, 8, 16, 1>(p) : launch<IO, 8, 32, 2>(p);
+        c.template consider<16, 1>(16.5);
+        c.template consider<32, 2>(24.5);
     } else if constexpr (N == 16) {
-        return at_once(8) ? launch<IO, 16, 8, 1>(p) : at_once(16) ? launch<IO, 16, 16, 2>(p) : launch<IO, 16, 32, 4>(p);
+        c.template consider<8, 1>(16.5);
+        c.template consider<16, 2>(23);
+        c.template consider<32, 4>(34);
     } else if constexpr (N == 32) {
-        return at_once(8) ? launch<IO, 32, 8, 2>(p) : at_once(16) ? launch<IO, 32, 16, 2>(p) : launch<IO, 32, 32, 4>(p);
+        c.template consider<8, 2>(21.5);
+        c.template consider<16, 2>(34.7);
+        c.template consider<32, 4>(51);
     } else {
-        return at_once(8) ? launch<IO, 64, 8, 4>(p) : launch<IO, 64, 16, 4>(p);
+        c.template consider<8, 4>(33);
+        c.template consider<16, 4>(48);
     }
+    return c.go(p, c.parts);
 }
 
 }  // namespace

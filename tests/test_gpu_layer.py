@@ -292,6 +292,42 @@ def test_scan_step(batch, channels, groups, n, dtype):
     assert torch.equal(kda.selective_scan_step(**s, state=dense), y)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,channels,lens", [
+    (8, 24, [700]), (8, 200, [900, 3, 0, 640]), (16, 8, [1100]), (16, 64, [520]), (16, 136, [1000, 1, 0, 1010]), (16, 264, [2000]),
+    (32, 16, [700]), (32, 72, [650, 0, 900]), (64, 8, [800]), (64, 40, [513, 600])], ids=str)
+def test_scan_in_parts(n, channels, lens, dtype):
+    """Few channels and long sequences, of which several CTAs have a part each (parts without tokens among them); states
+    in place, a sequence that starts from zero, another that is not kept; the same bits again."""
+    dt = DT[dtype]
+    g = gen(sum(lens) + channels)
+    s = scan_inputs(g, sum(lens) + 7, channels, n, dt)
+    s["A"] = s["A"] * torch.where(torch.arange(channels, device="cuda")[:, None] % 3 == 0, 0.01, 1.0)  # long memories too
+    first = normal(g, len(lens) + 1, channels, n, dtype=torch.float32)
+    at = torch.arange(len(lens), dtype=torch.int32, device="cuda")
+    start, keep = at.clone(), at.clone()
+    if len(lens) > 1:
+        start[-1], keep[0] = -1, -1
+    state = torch.stack([first[i] if i >= 0 else torch.zeros_like(first[0]) for i in start.tolist()])
+    cut = {k: v[:sum(lens)] if v is not None and k in ("x", "dt", "z", "B", "C") else v for k, v in s.items()}
+    wy, e, wn, ne = reference(cut, lens, state)
+    results = []
+    for _ in range(2):
+        pool, err = first.clone(), errors()
+        y = torch.full((sum(lens) + 7, channels), 7.0, dtype=dt, device="cuda")
+        kda.selective_scan(**s, cu_seqlens=offsets(lens), init_state=pool, init_slots=start, final_state=pool, final_slots=keep,
+                           out=y, errors=err)
+        assert err.item() == 0 and (y[sum(lens):] == 7).all() and torch.equal(pool[-1], first[-1])
+        ref.check(y[:sum(lens)], wy, e, f"{lens} {channels}")
+        for i, k in enumerate(keep.tolist()):
+            if k >= 0:
+                ref.check(pool[k], wn[i], ne[i], f"{lens} {channels} state {i}")
+            else:
+                assert torch.equal(pool[i], first[i])
+        results.append((y, pool))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 def test_scan_slots():
     """-1: from zero, not kept; out of range: reported, from zero, not kept."""
     g = gen(12)
