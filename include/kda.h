@@ -687,7 +687,8 @@ typedef enum {
  * Products are exact and sums fp32.  Addresses are aligned to their elements.  bf16 runs on
  * the tensor cores where x and w start on 16 bytes and their strides (>= in_features) and
  * in_features are multiples of 8, else, as fp32, on the CUDA cores.  The same arguments
- * give the same bits on every call.
+ * give the same bits on every call.  device_errors receives KDA_DEVICE_ERR_TIMEOUT when a bounded
+ * device-side wait expired (y is then incomplete).
  */
 kda_status_t kda_linear(const void *x, int64_t x_stride, const void *w, int64_t w_stride, const void *bias,
                         const void *residual, int64_t residual_stride, void *y, int64_t y_stride, int64_t rows,
@@ -728,7 +729,7 @@ kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *weight,
  *     y_tc  = (sum_n C_tgn h_cn + D_c x_tc) silu(z_tc)
  *
  *  x, dt, z  [total_tokens, channels], row strides; z NULL: no gate
- *  A         [channels, d_state] fp32; D, dt_bias [channels] fp32 or NULL (zero)
+ *  A         [channels, d_state] fp32, finite; D, dt_bias [channels] fp32 or NULL (zero)
  *  B, C      [total_tokens, num_groups, d_state], row strides (parts of one projection's rows)
  *  states    [entries, channels, d_state] fp32, contiguous
  *  y         [total_tokens, channels], row stride; overlaps none of the inputs

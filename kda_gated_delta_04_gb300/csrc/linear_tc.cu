@@ -9,8 +9,9 @@
 // the units (CTAs or pairs) of a cluster, each of which has all its columns, and joined through distributed
 // shared memory: what bounds such a call are the bytes that an SM takes in, about 40 a cycle, and wide tiles over
 // part of the inputs take in fewer than narrow ones over all.
-// Warp 0: copies (TMA); 1: matrix instructions (of a pair: in the leading CTA); 2: tensor memory; 4 to 7: the
-// epilogue, a thread a row.
+// Warp 0: copies (TMA); 1: matrix instructions (of a pair: in the leading CTA); 2: tensor memory; 4 to 11: the
+// epilogue, two threads a row, which take 16 columns in turn (one thread a row: 4,096 x 4,096 x 12,288 with a bias
+// and SiLU 297 us instead of EP).
 #include <type_traits>
 #include "latent_ptx.cuh"
 #include "layer.cuh"
@@ -22,7 +23,7 @@ namespace {
 using namespace ptx;
 using tc::kdesc;
 
-constexpr int kThreads = 256, kM = 128;
+constexpr int kThreads = 384, kM = 128;
 constexpr int kMaxStages = 12, kMaxWidth = 256, kDepth = 64;  // kDepth: channels of a panel, a swizzled row of 128 bytes
 constexpr int kSmem = 232448;
 constexpr uint64_t kWait = tc::kWaitNs;
@@ -193,16 +194,24 @@ struct Row {
         y = static_cast<OUT *>(p.y) + at * p.ys + c0;
         bias = p.bias ? static_cast<const __nv_bfloat16 *>(p.bias) + c0 : nullptr;
     }
-    // 16 columns from c on, `left` of which the row has; now: those of the residual, where vec and vec_r hold
+    // What the epilogue needs of 16 columns from c on, `left` of which the row has, asked for ahead.
+    struct Ahead {
+        Raw16<OUT> r;
+        Raw16<__nv_bfloat16> bias;
+    };
+    __device__ __forceinline__ void ask(const Plan &pl, Ahead &to, int c, int left) const
+    {
+        if (left < 16) return;
+        if (bias && pl.vec_b) to.bias.load(bias + c);
+        if (r && mine && pl.vec_r) to.r.load(r + c);
+    }
     __device__ __forceinline__ void finish(const Linear &p, const Plan &pl, float (&v)[16], int c, int left,
-                                           const Raw16<OUT> &now) const
+                                           const Ahead &ahead) const
     {
         if (bias) {
-            Raw16<__nv_bfloat16> b;
             if (pl.vec_b && left >= 16) {
-                b.load(bias + c);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] += b.get(i);
+                for (int i = 0; i < 16; ++i) v[i] += ahead.bias.get(i);
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -214,7 +223,7 @@ struct Row {
         if (left >= 16 && pl.vec && (!r || pl.vec_r)) {
             if (r)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] += now.get(i);
+                for (int i = 0; i < 16; ++i) v[i] += ahead.r.get(i);
             Raw16<OUT> out;
             out.set(v);
             out.store(y + c);
@@ -251,42 +260,41 @@ __device__ __forceinline__ void epilogue_role(Misc &mi, const Linear &p, const P
                                               int step)
 {
     volatile int *abort = &mi.abort;
-    const int lane = threadIdx.x & 31, part_w = pl.width / pl.parts;
-    const bool two = pl.parts == 2;
+    const int lane = threadIdx.x & 31, part_w = pl.width / pl.parts, turn = 16 * ((threadIdx.x >> 7) - 1);
     int count = 0;
     for (int tile = first; tile < pl.tiles_m * pl.tiles_n; tile += step, ++count) {
         int m, n;
         tile_at(pl, tile, m, n);
         const int buf = count % pl.buffers, left = min(pl.width, p.n - n * pl.width);
         const Row<OUT, PAIR> row(p, pl, m, n, rank);
-        // the residual's next 16 columns are on their way while these are worked on
-        const bool whole_r = row.r && row.mine && pl.vec_r;
-        Raw16<OUT> next;
-        if (whole_r && left >= 16) next.load(row.r);
+        typename Row<OUT, PAIR>::Ahead next;  // for the columns that come after these
+        row.ask(pl, next, turn, left - turn);
         if (!all_wait<false>(&mi.done[buf], (count / pl.buffers) & 1, abort)) return;
         tc_fence_after_sync();
-        auto give_back = [&](int i) {
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(map_to_rank(&mi.freed[i], 0));
-                else mbar_arrive(&mi.freed[i]);
-            }
-        };
-        bool first_back = false;
+        for (int j = 0; j < pl.parts; ++j) {
+            const int end = min(left, (j + 1) * part_w);
+            bool back = false;
+            auto give_back = [&] {  // the accumulators may be written again: this part's, or (one part) this tile's
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    uint64_t *bar = &mi.freed[pl.parts == 2 ? j : buf];
+                    if (PAIR) mbar_arrive_cluster(map_to_rank(bar, 0));
+                    else mbar_arrive(bar);
+                }
+                back = true;
+            };
 #pragma unroll 1
-        for (int c = 0; c < left; c += 16) {
-            float v[16];
-            const Raw16<OUT> now = next;
-            if (whole_r && left - c >= 32) next.load(row.r + c + 16);
-            take16(pl, tmem + buf * pl.chains * pl.pitch, c, v);
-            // the accumulators may be written again: one part's, or all of this tile's
-            if (two && !first_back && c + 16 >= min(left, part_w)) {
-                give_back(0);
-                first_back = true;
+            for (int c = j * part_w + turn; c < end; c += 32) {
+                float v[16];
+                const typename Row<OUT, PAIR>::Ahead now = next;
+                const int then = c + 32 < end ? c + 32 : (j + 1) * part_w + turn;
+                if (then < left) row.ask(pl, next, then, left - then);
+                take16(pl, tmem + buf * pl.chains * pl.pitch, c, v);
+                if (c + 32 >= end) give_back();
+                row.finish(p, pl, v, c, left - c, now);
             }
-            if (c + 16 >= left) give_back(two ? 1 : buf);
-            row.finish(p, pl, v, c, left - c, now);
+            if (!back) give_back();
         }
     }
 }
@@ -299,7 +307,7 @@ __device__ __forceinline__ bool put_part(Misc &mi, const Plan &pl, float *part, 
     if (!all_wait<false>(&mi.done[0], 0, &mi.abort)) return false;
     tc_fence_after_sync();
 #pragma unroll 1
-    for (int c = 0; c < pl.width; c += 16) {
+    for (int c = 16 * ((threadIdx.x >> 7) - 1); c < pl.width; c += 32) {
         if (c >= from && c < to) continue;
         float v[16];
         take16(pl, tmem, c, v);
@@ -317,12 +325,11 @@ __device__ __forceinline__ void join_parts(const Linear &p, const Plan &pl, cons
     tile_at(pl, tile, m, n);
     const Row<OUT, PAIR> row(p, pl, m, n, rank);
     const int left = min(pl.width, p.n - n * pl.width);
-    const bool whole_r = row.r && row.mine && pl.vec_r;
 #pragma unroll 1
-    for (int c = from; c < min(to, left); c += 16) {
+    for (int c = from + 16 * ((threadIdx.x >> 7) - 1); c < min(to, left); c += 32) {
         float v[16], sum[16] = {};
-        Raw16<OUT> now;
-        if (whole_r && left - c >= 16) now.load(row.r + c);
+        typename Row<OUT, PAIR>::Ahead now;
+        row.ask(pl, now, c, left - c);
         take16(pl, tmem, c, v);
 #pragma unroll
         for (int u = 0; u < S; ++u)
@@ -351,7 +358,7 @@ linear_tc_kernel(const Linear p, const Plan pl, const __grid_constant__ CUtensor
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&mi.done[i], 1);
-            mbar_init(&mi.freed[i], 4 * kCtas);
+            mbar_init(&mi.freed[i], 8 * kCtas);
         }
         mbar_init(&mi.drained, 1);
         fence_mbar_init();
@@ -540,7 +547,7 @@ int chains_of(bool f32, int width, int parts, int panels, int buffers)
 // copies alone, without a product, take 281 of the 287 us of 4,096 rows, 4,096 inputs and 12,288 outputs in tiles of 240
 // columns: wider tiles take in less).  A tile's epilogue: 33 a column, beside the next tile's products where there are
 // two buffers (16,384 rows, 1,024 inputs, 4,096 outputs: tiles of 256 and two buffers 105 us, of 512 and one 131; 4,096
-// inputs, 4,096 rows, 12,288 outputs: of 240 and two 262, of 448 and one 238).  A split: 1,500 and 20 a column for its
+// inputs, 4,096 rows, 12,288 outputs: of 240 and two 262, of 448 and one 238).  A split: 3,000 and 25 a column for its
 // join; all clusters of a split run at once (of four CTAs 36, not 38; of eight 15).  us with and without a split, 4,096
 // inputs: 64 rows, 4,096 outputs 13.4 and 18.7; 128 rows 13.7, 28.3; 256 rows 19.3, 28.7; 64 rows, 32 outputs 7.9, 14.0;
 // 1,000 rows, 128 outputs 11.8, 24.6; 128 rows, 12,288 outputs 25.9, 29.1.
@@ -552,10 +559,11 @@ Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, boo
     int64_t least = INT64_MAX;
     for (int split = 1; split <= 4; split *= 2) {
         const int ctas = (pair ? 2 : 1) * split, at_once = ctas == 1 ? 152 : ctas == 2 ? 76 : ctas == 4 ? 36 : 15;
-        const int unit = 16 * split, each = panels / split;
+        const int each = panels / split;
         if (split > 1 && panels < 4 * split) break;
-        for (int parts = 1; parts <= 2; ++parts)
-            for (int w = unit * parts; w <= kMaxWidth * parts; w += unit * parts) {
+        for (int parts = 1; parts <= 2; ++parts) {
+            const int unit = 16 * (split > parts ? split : parts);  // each unit's share and each part in 16 columns
+            for (int w = unit; w <= kMaxWidth * parts; w += unit) {
                 if (split > 1 && w * kM * 4 > kSmem - kHead) break;  // the parts that are joined
                 const int64_t tiles = tiles_m * ((n + w - 1) / w), rounds = (tiles + at_once - 1) / at_once;
                 if (split > 1 && rounds > 1) continue;
@@ -564,13 +572,14 @@ Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, boo
                 const int64_t load = (int64_t)(box + (pair ? w / 2 : w)) * 128 / 46, mma = 4 * (w / 2 > 32 ? w / 2 : 32);
                 const int64_t main = (panels + split - 1) / split * (load > mma ? load : mma), out = 33 * w / split;
                 const int64_t cost = (buffers == 2 ? rounds * ((main > out ? main : out) + out / 4) + out : rounds * (main + out)) +
-                                     (split > 1 ? 1500 + 20 * w : 0);
+                                     (split > 1 ? 3000 + 25 * w : 0);
                 if (cost < least) {
                     least = cost;
                     best = Tiles{w, parts, split, chains, buffers};
                 }
                 if (w >= n) break;
             }
+        }
     }
     return best;
 }

@@ -821,7 +821,9 @@ def linear(x, w, bias=None, *, activation=None, residual=None, out=None, out_dty
     torch = _torch_module or _load_torch()
     code, dt, dev = _latent_like(x, "x", 2)
     M, K = x.shape
-    N = w.shape[0] if w.dim() == 2 else -1
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        _refuse(w, "w", dt, dev, ("N", K))
+    N = w.shape[0]
     if out is None:
         out = _empty((M, N), out_dtype or dt, dev, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
@@ -845,6 +847,15 @@ def linear(x, w, bias=None, *, activation=None, residual=None, out=None, out_dty
     if st != KDA_OK:
         raise KdaError(st, "kda_linear")
     return out
+
+
+def _sequences(cu_seqlens):
+    """How many sequences the offsets have (None: one)."""
+    if cu_seqlens is None:
+        return 1
+    if not isinstance(cu_seqlens, _torch_module.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] == 0:
+        raise ValueError("cu_seqlens must be a CUDA tensor of one dimension, [sequences + 1]")
+    return cu_seqlens.shape[0] - 1
 
 
 def _entries(state, slots, name, dtype, dev, tail, seqs):
@@ -905,9 +916,11 @@ def short_conv(x, weight, bias=None, cu_seqlens=None, init_state=None, *, activa
     allocated.  errors: int32 [1] that collects KDA_DEVICE_ERR_* bits."""
     torch = _torch_module or _load_torch()
     _, dt, dev = _latent_like(x, "x", 2)
-    seqs = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    seqs = _sequences(cu_seqlens)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        _refuse(weight, "weight", dt, dev, (x.shape[1], "W"))
     if final_state is None and final_slots is None:
-        final_state = _empty((seqs, weight.shape[-1] - 1, x.shape[1]), dt, dev, stream)
+        final_state = _empty((seqs, max(0, weight.shape[1] - 1), x.shape[1]), dt, dev, stream)
     out = _short_conv(x, weight, bias, cu_seqlens, seqs, init_state, init_slots, final_state, final_slots, activation,
                       parts, out, errors, stream)
     return out, final_state
@@ -975,7 +988,9 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, cu_seqlens=None
     64.  cu_seqlens, the states (fp32 [N, channels, n]), slots and errors as short_conv.  Returns (y, final_state)."""
     torch = _torch_module or _load_torch()
     _, _, dev = _latent_like(x, "x", 2)
-    seqs = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    seqs = _sequences(cu_seqlens)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        _refuse(A, "A", torch.float32, dev, (x.shape[1], "n"))
     if final_state is None and final_slots is None:
         final_state = _empty((seqs, *A.shape), torch.float32, dev, stream)
     out = _selective_scan(x, dt, A, B, C, D, z, dt_bias, cu_seqlens, seqs, init_state, init_slots, final_state, final_slots,

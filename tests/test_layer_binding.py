@@ -25,7 +25,7 @@ def calls():
             ("out type", (x, w), dict(out=r(6, 48).half())), ("out_dtype", (x, w), dict(out=r(6, 48), out_dtype=torch.float32)),
             ("activation", (x, w), dict(activation="relu")), ("last stride", (x, r(64, 48).T), {}), ("on the CPU", (x, w.cpu()), {}),
             ("shared output rows", (x, w), dict(out=r(1, 48).expand(6, 48))), ("fp32 to bf16", (x.float(), w.float()), dict(out_dtype=torch.bfloat16)),
-            ("one dimension", (x[0], w), {}), ("half", (x.half(), w.half()), {})]:
+            ("one dimension", (x[0], w), {}), ("no weight", (x, None), {}), ("weight of one dimension", (x, w[0]), {}), ("half", (x.half(), w.half()), {})]:
         yield "linear, " + name, kda.linear, args, kw
     c, t, b = r(10, 56)[:, :48], r(48, 4), r(48)
     yield "conv", kda.short_conv, (c, t, b, i(0, 3, 10), r(2, 3, 48)), dict(parts=3, out=r(3, 10, 16), final_state=r(2, 3, 48))
@@ -34,7 +34,7 @@ def calls():
     yield "conv step", kda.short_conv_step, (c, t, r(10, 3, 48), b), {}
     for name, args, kw in [
             ("taps", (c, r(48, 5)), {}), ("channels", (r(10, 44), r(44, 4)), {}), ("parts", (c, t), dict(parts=5)),
-            ("narrow parts", (c, t), dict(parts=12)), ("offsets type", (c, t, None, i(0, 10).long()), {}), ("state", (c, t, None, None, r(1, 4, 48)), {}),
+            ("narrow parts", (c, t), dict(parts=12)), ("offsets type", (c, t, None, i(0, 10).long()), {}), ("no offsets", (c, t, None, i()), {}), ("taps of one dimension", (c, t[:, 0]), {}), ("state", (c, t, None, None, r(1, 4, 48)), {}),
             ("states", (c, t, None, i(0, 3, 10), r(1, 3, 48)), {}), ("state type", (c, t, None, None, f(1, 3, 48)), {}),
             ("slots alone", (c, t), dict(init_slots=i(0))), ("slots shape", (c, t, None, None, r(4, 3, 48)), dict(init_slots=i(0, 1))),
             ("activation", (c, t), dict(activation="gelu")), ("misaligned", (r(10, 57)[:, 1:49], t), {}), ("bias type", (c, t, b.float()), {})]:
@@ -46,7 +46,7 @@ def calls():
     yield "scan groups", kda.selective_scan, (*s, A, bc[:, :32].unflatten(1, (2, 16)), bc[:, 32:64].unflatten(1, (2, 16))), dict(softplus=False)
     yield "scan step", kda.selective_scan_step, (*s, A, B, C, f(12, 48, 16)), dict(slots=i(*range(10)), new_state=f(12, 48, 16))
     for name, args, kw in [
-            ("states", (*s, f(48, 24), r(10, 24), r(10, 24)), {}), ("A type", (*s, A.bfloat16(), B, C), {}), ("B type", (*s, A, B.float(), C), {}),
+            ("states", (*s, f(48, 24), r(10, 24), r(10, 24)), {}), ("A type", (*s, A.bfloat16(), B, C), {}), ("A of one dimension", (*s, A[:, 0], B, C), {}), ("offsets of two", (*s, A, B, C, None, None, None, i(0, 10)[None]), {}), ("B type", (*s, A, B.float(), C), {}),
             ("groups apart", (*s, A, r(10, 4, 16)[:, ::2], r(10, 4, 16)[:, ::2]), {}), ("groups differ", (*s, A, r(10, 2, 16), C), {}),
             ("D shape", (*s, A, B, C, f(47)), {}), ("z type", (*s, A, B, C, None, f(10, 48)), {}), ("dt rows", (s[0], r(9, 48), A, B, C), {}),
             ("state type", (*s, A, B, C, None, None, None, None, r(1, 48, 16)), {}), ("errors", (*s, A, B, C), dict(errors=i(0, 0))),
