@@ -11,7 +11,7 @@
 // part of the inputs take in fewer than narrow ones over all.
 // Warp 0: copies (TMA); 1: matrix instructions (of a pair: in the leading CTA); 2: tensor memory; 4 to 11: the
 // epilogue, two threads a row, which take 16 columns in turn (one thread a row: 4,096 x 4,096 x 12,288 with a bias
-// and SiLU 297 us instead of EP).
+// and SiLU 297 us instead of 238).
 #include <type_traits>
 #include "latent_ptx.cuh"
 #include "layer.cuh"
@@ -543,14 +543,23 @@ int chains_of(bool f32, int width, int parts, int panels, int buffers)
     return !f32 || most < 1 ? 1 : fit < most ? fit : most;
 }
 
-// The least by what it takes, in cycles.  A panel of 64 inputs: its bytes into an SM at 46 a cycle, or its products (the
-// copies alone, without a product, take 281 of the 287 us of 4,096 rows, 4,096 inputs and 12,288 outputs in tiles of 240
-// columns: wider tiles take in less).  A tile's epilogue: 33 a column, beside the next tile's products where there are
-// two buffers (16,384 rows, 1,024 inputs, 4,096 outputs: tiles of 256 and two buffers 105 us, of 512 and one 131; 4,096
-// inputs, 4,096 rows, 12,288 outputs: of 240 and two 262, of 448 and one 238).  A split: 3,000 and 25 a column for its
-// join; all clusters of a split run at once (of four CTAs 36, not 38; of eight 15).  us with and without a split, 4,096
-// inputs: 64 rows, 4,096 outputs 13.4 and 18.7; 128 rows 13.7, 28.3; 256 rows 19.3, 28.7; 64 rows, 32 outputs 7.9, 14.0;
-// 1,000 rows, 128 outputs 11.8, 24.6; 128 rows, 12,288 outputs 25.9, 29.1.
+// Panels of a stage: rows of more than 128 bytes at a time, as long as there are three stages.  us with (and with one
+// panel): 256 rows, 4,096 inputs, 12,288 outputs 23.8 (30.4); 16,384 rows, 1,024 inputs, 4,096 outputs 81 (102).
+int stage_panels(int panel, int box)
+{
+    int n = 1;
+    while (n < 4 && 2 * n * panel * 3 <= kSmem - kHead - (kM - box) * 128) n *= 2;
+    return n;
+}
+
+// The least by what it takes, in cycles.  A panel of 64 inputs: its bytes into an SM, 44 a cycle, or 62 and 120 cycles
+// where a stage has more than one, or its products (the copies alone, without a product, took 281 of the 287 us of 4,096
+// rows, 4,096 inputs and 12,288 outputs in tiles of 240 columns and stages of one panel).  A tile's epilogue: 20 a
+// column, beside the next tile's products where there are two buffers.  A split: 1,200 and 32 a column for its join; all
+// clusters of a split run at once (of four CTAs 36, not 38; of eight 15).  us with and without a split, 4,096
+// inputs: 64 rows, 4,096 outputs 13.2 and 18.7; 128 rows 13.8, 28.3; 256 rows 16, 28.7; 64 rows, 32 outputs 8.3, 14.0;
+// 1,000 rows, 128 outputs 11.8, 24.6.  Of 21 shapes from 32 x 4,096 x 4,096 to 4,096 x 12,288 x 4,096 the choice takes
+// within a tenth of the best of all widths, parts and splits.
 Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, bool f32)
 {
     const int64_t tiles_m = (rows + tall - 1) / tall;
@@ -569,10 +578,11 @@ Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, boo
                 if (split > 1 && rounds > 1) continue;
                 const int buffers = rounds > 1 && !f32 && parts == 1 ? 2 : 1, chains = chains_of(f32, w, parts, each, buffers);
                 if (f32 && chains < 4 && chains < each / 8) break;
-                const int64_t load = (int64_t)(box + (pair ? w / 2 : w)) * 128 / 46, mma = 4 * (w / 2 > 32 ? w / 2 : 32);
-                const int64_t main = (panels + split - 1) / split * (load > mma ? load : mma), out = 33 * w / split;
+                const int panel = (box + (pair ? w / 2 : w)) * 128;
+                const int64_t load = stage_panels(panel, box) > 1 ? 120 + panel / 62 : panel / 44, mma = 4 * (w / 2 > 32 ? w / 2 : 32);
+                const int64_t main = (panels + split - 1) / split * (load > mma ? load : mma), out = 20 * w / split;
                 const int64_t cost = (buffers == 2 ? rounds * ((main > out ? main : out) + out / 4) + out : rounds * (main + out)) +
-                                     (split > 1 ? 3000 + 25 * w : 0);
+                                     (split > 1 ? 1200 + 32 * w : 0);
                 if (cost < least) {
                     least = cost;
                     best = Tiles{w, parts, split, chains, buffers};
@@ -610,7 +620,7 @@ cudaError_t launch_linear_tc(const Linear &p)
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     pl.tiles_m = (int)tiles_m; pl.tiles_n = (int)tiles_n; pl.group = 8;
     const int rows_w = pair ? pl.width / 2 : pl.width, panel = (pl.box + rows_w) * 128;
-    pl.panels = panel <= 8192 ? 4 : panel <= 16384 ? 2 : 1;
+    pl.panels = stage_panels(panel, pl.box);
     pl.pitch = pitch_of(pl.width / pl.parts);
     pl.columns = 32;
     while (pl.columns < pl.pitch * pl.parts * pl.chains * pl.buffers) pl.columns *= 2;
