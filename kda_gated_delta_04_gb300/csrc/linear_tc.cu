@@ -555,12 +555,12 @@ int stage_panels(int panel, int box)
 // The least by what it takes, in cycles.  A panel of 64 inputs: its bytes into an SM, 44 a cycle, or 62 and 120 cycles
 // where a stage has more than one, or its products (the copies alone, without a product, took 281 of the 287 us of 4,096
 // rows, 4,096 inputs and 12,288 outputs in tiles of 240 columns and stages of one panel).  A tile's epilogue: 20 a
-// column, beside the next tile's products where there are two buffers.  A split: 1,200 and 32 a column for its join; all
-// clusters of a split run at once (of four CTAs 36, not 38; of eight 15).  us with and without a split, 4,096
-// inputs: 64 rows, 4,096 outputs 13.2 and 18.7; 128 rows 13.8, 28.3; 256 rows 16, 28.7; 64 rows, 32 outputs 8.3, 14.0;
-// 1,000 rows, 128 outputs 11.8, 24.6.  Of 21 shapes from 32 x 4,096 x 4,096 to 4,096 x 12,288 x 4,096 the choice takes
-// within a tenth of the best of all widths, parts and splits.
-Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, bool f32)
+// column, 60 with an activation, beside the next tile's products where there are two buffers.  A split: 1,200 and
+// 32 a column for its join; all clusters of a split run at once (of four CTAs 36, not 38; of eight 15).  us with and
+// without a split, 4,096 inputs: 64 rows, 4,096 outputs 13.2 and 18.7; 128 rows 13.8, 28.3; 256 rows 16, 28.7; 64 rows,
+// 32 outputs 8.3, 14.0; 1,000 rows, 128 outputs 11.8, 24.6.  Of 21 shapes from 32 x 4,096 x 4,096 to 4,096 x 12,288 x
+// 4,096 the choice takes within a tenth of the best of all widths, parts and splits.
+Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, bool f32, bool act)
 {
     const int64_t tiles_m = (rows + tall - 1) / tall;
     const int panels = (k + kDepth - 1) / kDepth;
@@ -580,7 +580,7 @@ Tiles choose_tiles(int64_t rows, int n, int k, int tall, int box, bool pair, boo
                 if (f32 && chains < 4 && chains < each / 8) break;
                 const int panel = (box + (pair ? w / 2 : w)) * 128;
                 const int64_t load = stage_panels(panel, box) > 1 ? 120 + panel / 62 : panel / 44, mma = 4 * (w / 2 > 32 ? w / 2 : 32);
-                const int64_t main = (panels + split - 1) / split * (load > mma ? load : mma), out = 20 * w / split;
+                const int64_t main = (panels + split - 1) / split * (load > mma ? load : mma), out = (act ? 60 : 20) * w / split;
                 const int64_t cost = (buffers == 2 ? rounds * ((main > out ? main : out) + out / 4) + out : rounds * (main + out)) +
                                      (split > 1 ? 1200 + 32 * w : 0);
                 if (cost < least) {
@@ -614,7 +614,7 @@ cudaError_t launch_linear_tc(const Linear &p)
     if (!pair && p.rows > kM && p.rows <= (int64_t)kM * kSms) pl.tall = (int)(((p.rows + kSms - 1) / kSms + 7) / 8 * 8);
     pl.box = pair ? kM : pl.tall;
     const bool f32 = p.out_dtype == KDA_DTYPE_F32;
-    const Tiles at = choose_tiles(p.rows, p.n, p.k, pl.tall, pl.box, pair, f32);
+    const Tiles at = choose_tiles(p.rows, p.n, p.k, pl.tall, pl.box, pair, f32, p.act != KDA_ACT_NONE);
     pl.width = at.width; pl.parts = at.parts; pl.chains = at.chains; pl.buffers = at.buffers;
     const int64_t tiles_m = (p.rows + pl.tall - 1) / pl.tall, tiles_n = (p.n + pl.width - 1) / pl.width, tiles = tiles_m * tiles_n;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
