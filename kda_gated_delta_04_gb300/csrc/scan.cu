@@ -163,6 +163,7 @@ scan_kernel(const Scan p, int group_blocks, int parts)
         // B pairs of tokens at a time, of which all but h's own products and sums can be done side by side; their
         // operands are loaded while the B before are worked on.  Tokens past the end leave h as it is (d = 0).
         constexpr int B = Sh::kAhead;
+        const float2 middle = make_float2(kDecayMiddle, kDecayMiddle);
         auto scan = [&](int chunks, auto ends) {  // ends: no sums are wanted, but that of the steps
             float steps = 0.f;
             __syncthreads();
@@ -200,7 +201,7 @@ scan_kernel(const Scan p, int group_blocks, int parts)
                         if (ends.value) step_sum = ptx::add2(step_sum, make_float2(d[q].x, d[q].y));
 #pragma unroll
                         for (int i = 0; i < S; ++i) {
-                            const float2 e = mul2(make_float2(d[q].x, d[q].y), make_float2(a[i], a[i]));
+                            const float2 e = ptx::fma2(make_float2(d[q].x, d[q].y), make_float2(a[i], a[i]), middle);
                             const float2 b = mul2(make_float2(d[q].z, d[q].w), x[q][i].b());
                             float2 hh;
                             hh.x = fmaf(tc::exp2_approx(e.x), h[i], b.x);

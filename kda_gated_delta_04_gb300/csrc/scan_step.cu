@@ -86,10 +86,10 @@ scan_step_kernel(const Scan p, int channel_blocks)
         load_io4(static_cast<const IO *>(p.c) + n * p.cs + group * N + 4 * lane, cc);
         const float di = __shfl_sync(0xffffffffu, d[i / L], i % L, L);
         const float dx = di * __shfl_sync(0xffffffffu, x[i / L], i % L, L);
-        h[i].x = fmaf(tc::exp2_approx(di * a.x), h[i].x, dx * b[0]);
-        h[i].y = fmaf(tc::exp2_approx(di * a.y), h[i].y, dx * b[1]);
-        h[i].z = fmaf(tc::exp2_approx(di * a.z), h[i].z, dx * b[2]);
-        h[i].w = fmaf(tc::exp2_approx(di * a.w), h[i].w, dx * b[3]);
+        h[i].x = fmaf(tc::exp2_approx(fmaf(di, a.x, kDecayMiddle)), h[i].x, dx * b[0]);
+        h[i].y = fmaf(tc::exp2_approx(fmaf(di, a.y, kDecayMiddle)), h[i].y, dx * b[1]);
+        h[i].z = fmaf(tc::exp2_approx(fmaf(di, a.z, kDecayMiddle)), h[i].z, dx * b[2]);
+        h[i].w = fmaf(tc::exp2_approx(fmaf(di, a.w, kDecayMiddle)), h[i].w, dx * b[3]);
         y[i] = fmaf(h[i].x, cc[0], h[i].y * cc[1]) + fmaf(h[i].z, cc[2], h[i].w * cc[3]);
         if (mine && fin[i] >= 0)
             *reinterpret_cast<float4 *>(static_cast<float *>(p.seq.fin) + fin[i] * all + at) = h[i];
