@@ -97,6 +97,15 @@ __device__ __forceinline__ void packed_check(const Packed &s, int i)
     if ((i == 0 && a != 0) || a > s.tokens || (i > 0 && a < s.cu[i - 1])) atomicOr(s.errors, DEV_ERR_SEQLENS);
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return d;
+}
+
 // A scan's decay is exp2(d A' + kDecayMiddle), A' = A log2 e.  ex2.approx is right to 2.5 units of 2^-24, but of decays
 // near one mostly below: by 0.1 of a unit on average for exponents over -0.004, by 0.35 from there to -0.3 (expf: by
 // 0.2 above, and 0.1 above).  What a state remembers, 1 / (1 - decay) tokens, adds such a lean up.  The addend costs

@@ -25,15 +25,6 @@ namespace {
 
 constexpr int kIn = 128, kOut = 128;  // threads that bring tokens in and take them out
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<unsigned long long &>(d))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return d;
-}
-
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
 

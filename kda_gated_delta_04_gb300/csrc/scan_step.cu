@@ -5,7 +5,9 @@
 // Bound by memory: the states, fp32, are read and written once.  A thread has four states of a channel, so that
 // a warp's states are 512 bytes in a row, and kSeqs sequences, whose states are asked for at once; A is
 // read once for them.  What all states of a channel share is done by one of its lanes for each sequence: the step, D x
-// and the gate; 256 sequences of 4,096 channels, 16 states, bf16 take 31.8 us so (64 registers, eight CTAs an SM) and took 38.6 when every lane did it.
+// and the gate; a sequence's entries are read by one lane of a warp.  256 sequences of 4,096 channels, 16 states, bf16:
+// 26.2 us, 5.5 TB/s (48 registers, ten CTAs an SM; with 64 and eight 30; two sequences a thread 30; 31.8 when every lane
+// read the entries and found each row's address by a product; 38.6 when every lane did the shared part as well).
 #include "latent_ptx.cuh"
 #include "layer.cuh"
 #include "tc_common.cuh"
@@ -38,7 +40,7 @@ __device__ __forceinline__ void spread_sums(float (&v)[kSeqs], int lane)
 }
 
 template <typename IO, int N>
-__global__ void __launch_bounds__(kThreads, 8)
+__global__ void __launch_bounds__(kThreads, 10)
 scan_step_kernel(const Scan p, int channel_blocks)
 {
     constexpr int L = N / 4, CH = kThreads / L, R = (kSeqs + L - 1) / L;  // R: sequences of which a lane has x, dt, z
@@ -47,18 +49,21 @@ scan_step_kernel(const Scan p, int channel_blocks)
     const int n0 = (int)(blockIdx.x / channel_blocks) * kSeqs, lane = threadIdx.x % L;
     const int ch = (blockIdx.x % channel_blocks) * CH + threadIdx.x / L, c = min(ch, p.channels - 1);
     const bool mine = ch < p.channels;
-    const int group = c / (p.channels / p.groups);
+    const int group = p.groups == 1 ? 0 : c / (p.channels / p.groups);
     const int64_t at = (int64_t)c * N + 4 * lane, all = (int64_t)p.channels * N;
-    int64_t fin[kSeqs];
+    // lane i of a warp reads sequence i's entries
+    const int in_warp = threadIdx.x & 31;
+    int64_t own_init = -1, own_fin = -1;
+    if (in_warp < kSeqs && n0 + in_warp < p.seq.num_seqs &&
+        !packed_entries(p.seq, n0 + in_warp, own_init, own_fin) && blockIdx.x % channel_blocks == 0 && threadIdx.x < 32 && p.seq.errors)
+        atomicOr(p.seq.errors, DEV_ERR_SLOT);
+    int fin[kSeqs];
     float4 h[kSeqs];
 #pragma unroll
     for (int i = 0; i < kSeqs; ++i) {
-        int64_t init = -1;
-        fin[i] = -1;
+        const int init = __shfl_sync(0xffffffffu, (int)own_init, i);
+        fin[i] = __shfl_sync(0xffffffffu, (int)own_fin, i);
         h[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n0 + i >= p.seq.num_seqs) continue;
-        if (!packed_entries(p.seq, n0 + i, init, fin[i]) && blockIdx.x % channel_blocks == 0 && threadIdx.x == 0 && p.seq.errors)
-            atomicOr(p.seq.errors, DEV_ERR_SLOT);
         if (init >= 0) h[i] = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.seq.init) + init * all + at);
     }
     float x[R], d[R], z[R];
@@ -77,22 +82,31 @@ scan_step_kernel(const Scan p, int channel_blocks)
         d[r] += bias;
         if (p.softplus) d[r] = softplus(d[r]);
     }
+    const float2 middle = make_float2(kDecayMiddle, kDecayMiddle);
+    const IO *bn = static_cast<const IO *>(p.b) + n0 * p.bs + group * N + 4 * lane;
+    const IO *cn = static_cast<const IO *>(p.c) + n0 * p.cs + group * N + 4 * lane;
     float y[kSeqs];
 #pragma unroll
     for (int i = 0; i < kSeqs; ++i) {
-        const int64_t n = min(n0 + i, p.seq.num_seqs - 1);
         float b[4], cc[4];
-        load_io4(static_cast<const IO *>(p.b) + n * p.bs + group * N + 4 * lane, b);
-        load_io4(static_cast<const IO *>(p.c) + n * p.cs + group * N + 4 * lane, cc);
+        load_io4(bn, b);
+        load_io4(cn, cc);
+        if (n0 + i + 1 < p.seq.num_seqs) {
+            bn += p.bs;
+            cn += p.cs;
+        }
         const float di = __shfl_sync(0xffffffffu, d[i / L], i % L, L);
         const float dx = di * __shfl_sync(0xffffffffu, x[i / L], i % L, L);
-        h[i].x = fmaf(tc::exp2_approx(fmaf(di, a.x, kDecayMiddle)), h[i].x, dx * b[0]);
-        h[i].y = fmaf(tc::exp2_approx(fmaf(di, a.y, kDecayMiddle)), h[i].y, dx * b[1]);
-        h[i].z = fmaf(tc::exp2_approx(fmaf(di, a.z, kDecayMiddle)), h[i].z, dx * b[2]);
-        h[i].w = fmaf(tc::exp2_approx(fmaf(di, a.w, kDecayMiddle)), h[i].w, dx * b[3]);
-        y[i] = fmaf(h[i].x, cc[0], h[i].y * cc[1]) + fmaf(h[i].z, cc[2], h[i].w * cc[3]);
+        const float2 d2 = make_float2(di, di), dx2 = make_float2(dx, dx);
+        const float2 e0 = ptx::fma2(d2, make_float2(a.x, a.y), middle), e1 = ptx::fma2(d2, make_float2(a.z, a.w), middle);
+        const float2 h0 = ptx::fma2(make_float2(tc::exp2_approx(e0.x), tc::exp2_approx(e0.y)), make_float2(h[i].x, h[i].y),
+                                    mul2(dx2, make_float2(b[0], b[1])));
+        const float2 h1 = ptx::fma2(make_float2(tc::exp2_approx(e1.x), tc::exp2_approx(e1.y)), make_float2(h[i].z, h[i].w),
+                                    mul2(dx2, make_float2(b[2], b[3])));
+        const float2 sum = ptx::fma2(h0, make_float2(cc[0], cc[1]), mul2(h1, make_float2(cc[2], cc[3])));
+        y[i] = sum.x + sum.y;
         if (mine && fin[i] >= 0)
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.seq.fin) + fin[i] * all + at) = h[i];
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.seq.fin) + fin[i] * all + at) = make_float4(h0.x, h0.y, h1.x, h1.y);
     }
     spread_sums<L>(y, lane);
 #pragma unroll

@@ -21,7 +21,7 @@ constexpr int kThreads = 128;
 // 2,048 channels in fp32 28.1, 30.9, 34.7.
 template <typename IO> constexpr int kRun = sizeof(IO) == 2 ? 16 : 8;
 constexpr int kBatch = 8;  // rows asked for at once
-constexpr int kSeqs = 4;   // sequences of a thread that takes single tokens (256 of 12,288 channels 10.6 us; 1: 11.7)
+constexpr int kSeqs = 4;   // sequences of a thread that takes single tokens (256 of 12,288 channels 10.0 us; 1: 11.7)
 
 // A thread's four channels of a row, as they lie in memory.
 constexpr int V = 4;
@@ -182,38 +182,49 @@ __device__ __forceinline__ void run(const ShortConv &p, int t0, int c)
 // One token of each of kSeqs sequences: what head does where all sequences are one token, with everything of them
 // asked for at once.
 template <typename IO, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 6 : 4)
 short_conv_step_kernel(const ShortConv p, int channel_blocks)
 {
     ptx::pdl_wait();
     ptx::pdl_launch_dependents();
     const int n0 = (int)(blockIdx.x / channel_blocks) * kSeqs;
-    const int c = ((blockIdx.x % channel_blocks) * kThreads + threadIdx.x) * V;
-    if (c >= p.channels) return;
-    int64_t init[kSeqs], fin[kSeqs];
+    const int own = ((blockIdx.x % channel_blocks) * kThreads + threadIdx.x) * V, c = min(own, p.channels - V);
+    const bool mine = own < p.channels;
+    // lane i of a warp reads sequence i's entries
+    const int lane = threadIdx.x & 31;
+    int64_t own_init = -1, own_fin = -1;
+    if (lane < kSeqs && n0 + lane < p.seq.num_seqs &&
+        !packed_entries(p.seq, n0 + lane, own_init, own_fin) && blockIdx.x % channel_blocks == 0 && threadIdx.x < 32 && p.seq.errors)
+        atomicOr(p.seq.errors, DEV_ERR_SLOT);
+    int fin[kSeqs];
     Raw4<IO> raw[kSeqs][W];
+    const IO *x = static_cast<const IO *>(p.x) + n0 * p.xs + c;
 #pragma unroll
     for (int i = 0; i < kSeqs; ++i) {
-        init[i] = fin[i] = -1;
-        if (n0 + i >= p.seq.num_seqs) continue;
-        if (!packed_entries(p.seq, n0 + i, init[i], fin[i]) && c == 0 && p.seq.errors) atomicOr(p.seq.errors, DEV_ERR_SLOT);
-        raw[i][W - 1] = load_raw(static_cast<const IO *>(p.x) + (int64_t)(n0 + i) * p.xs + c);
+        raw[i][W - 1] = load_raw(x);
+        if (n0 + i + 1 < p.seq.num_seqs) x += p.xs;
     }
 #pragma unroll
-    for (int i = 0; i < kSeqs; ++i)
+    for (int i = 0; i < kSeqs; ++i) {
+        const int init = __shfl_sync(0xffffffffu, (int)own_init, i);
+        fin[i] = __shfl_sync(0xffffffffu, (int)own_fin, i);
+        const IO *from = static_cast<const IO *>(p.seq.init) + (int64_t)init * (W - 1) * p.channels + c;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             raw[i][j] = Raw4<IO>{};
-            if (init[i] >= 0) raw[i][j] = load_raw(static_cast<const IO *>(p.seq.init) + (init[i] * (W - 1) + j) * p.channels + c);
+            if (init >= 0) raw[i][j] = load_raw(from + (int64_t)j * p.channels);
         }
+    }
+    if (!mine) return;
     const Channels<IO, W> ch(p, c);
 #pragma unroll
     for (int i = 0; i < kSeqs; ++i) {
         if (n0 + i >= p.seq.num_seqs) break;
-        if (fin[i] >= 0)
+        if (fin[i] >= 0) {
+            IO *to = static_cast<IO *>(p.seq.fin) + (int64_t)fin[i] * (W - 1) * p.channels + c;
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-                store_raw(static_cast<IO *>(p.seq.fin) + (fin[i] * (W - 1) + j) * p.channels + c, raw[i][j + 1]);
+            for (int j = 0; j < W - 1; ++j) store_raw(to + (int64_t)j * p.channels, raw[i][j + 1]);
+        }
         float row[W][V];
 #pragma unroll
         for (int j = 0; j < W; ++j) widen(raw[i][j], row[j]);
