@@ -431,3 +431,31 @@ def test_streams_graphs_and_repeats():
     fresh()
     d = layer()
     assert all(torch.equal(p, q) for p, q in zip((d, conv_state, scan_state), got))
+
+
+@pytest.mark.parametrize("m", [1, 4, 12, 64, 300])
+def test_weights_written_by_the_call_before(m):
+    """A call whose weights (and rows) the call before it wrote in place, with the ends and beginnings of all of them
+    overlapping in a replayed graph: as with a synchronisation between any two."""
+    g = gen(100 + m)
+    a, b, x = normal(g, 512, 64, scale=0.1), normal(g, 256, 64, scale=0.1), normal(g, m, 256)
+    first = normal(g, 512, 256)
+    w, y = first.clone(), torch.zeros(m, 512, dtype=torch.bfloat16, device="cuda")
+
+    def run(between):
+        for _ in range(8):
+            kda.linear(a, b, residual=w, out=w)
+            between()
+            kda.linear(x, w, residual=y, out=y)
+            between()
+
+    run(torch.cuda.synchronize)
+    want = [w.clone(), y.clone()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(lambda: None)
+    for _ in range(3):
+        w.copy_(first)
+        y.zero_()
+        graph.replay()
+        assert torch.equal(w, want[0]) and torch.equal(y, want[1])
