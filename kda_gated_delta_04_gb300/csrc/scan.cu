@@ -15,7 +15,8 @@
 // two products an instruction), as are the sums of each thread's states, to which D x and the gate are applied where
 // they are stored.  What the steps before this form measured, 4,096 tokens of 4,096 channels, 16 states, bf16: a chunk
 // loaded through registers one ahead 283 us; asynchronous copies four ahead 188; the states of a channel over four warps
-// instead of four lanes 163; now 140: 34 ns a token, 180 instructions of a warp (45 a scheduler) in 70 cycles.
+// instead of four lanes 163; two rounds of the loop at a time, so that operands stay in the registers that they were
+// loaded to, 145 to 135.  INSTR
 #include "latent_ptx.cuh"
 #include "layer.cuh"
 #include "tc_common.cuh"
@@ -85,7 +86,9 @@ struct Shape {
     static constexpr int kGroups = N / S;                   // threads of a channel
     static constexpr int kWarpCh = CH < 16 ? CH : 16;       // channels of a warp
     static constexpr int kChunk = CH == 8 && N == 16 ? 64 : 32;        // tokens handed over at a time
-    static constexpr int kAhead = S >= 4 ? 2 : 4;           // pairs of tokens worked on at a time, and loaded ahead
+    // Pairs of tokens worked on at a time, and loaded ahead: us of 4,096 tokens in bf16 with 2 and 4, 8 states and 4,096
+    // channels (S = 2) 99, 107; 32 and 2,048 (2) 135, 143; 16 and 2,048 (2) 98, 94.
+    static constexpr int kAhead = S >= 4 || (S == 2 && N != 16) ? 2 : 4;
     static constexpr int kPiece = 16 / (int)sizeof(IO);
     struct Raw {                                            // as they come
         alignas(16) IO x[kChunk][CH], dt[kChunk][CH], z[kChunk][CH], bc[kChunk][2 * N];
@@ -164,47 +167,49 @@ scan_kernel(const Scan p, int group_blocks, int parts)
                 const float4 *dd = &sm.ready[k & 1].dd[0][ch];
                 const Pair<IO> *bc = &sm.ready[k & 1].bc[0][g * S];
                 float2 *y = &sm.ready[k & 1].y[g][0][ch];
-                float4 d_next[B];
-                Pair<IO> bc_next[B][S];
                 float2 step_sum = make_float2(0.f, 0.f);
+                float4 d[2][B];
+                Pair<IO> x[2][B][S];
+                auto load = [&](int side) {
 #pragma unroll
-                for (int q = 0; q < B; ++q) {
-                    d_next[q] = dd[q * CH];
-                    load_pairs<IO, S>(bc_next[q], bc + q * N);
-                }
-#pragma unroll 1
-                for (int t = 0; t < count; t += 2 * B) {
-                    float4 d[B];
-                    Pair<IO> x[B][S];
-                    float2 sum[B];
+                    for (int q = 0; q < B; ++q) {
+                        d[side][q] = dd[q * CH];
+                        load_pairs<IO, S>(x[side][q], bc + q * N);
+                    }
                     dd += B * CH;
                     bc += B * N;
+                };
+                auto step = [&](int side) {
+                    float2 sum[B];
 #pragma unroll
                     for (int q = 0; q < B; ++q) {
-                        d[q] = d_next[q];
-#pragma unroll
-                        for (int i = 0; i < S; ++i) x[q][i] = bc_next[q][i];
-                        d_next[q] = dd[q * CH];
-                        load_pairs<IO, S>(bc_next[q], bc + q * N);
-                    }
-#pragma unroll
-                    for (int q = 0; q < B; ++q) {
-                        if (ends.value) step_sum = ptx::add2(step_sum, make_float2(d[q].x, d[q].y));
+                        const float4 at = d[side][q];
+                        if (ends.value) step_sum = ptx::add2(step_sum, make_float2(at.x, at.y));
 #pragma unroll
                         for (int i = 0; i < S; ++i) {
-                            const float2 e = ptx::fma2(make_float2(d[q].x, d[q].y), make_float2(a[i], a[i]), middle);
-                            const float2 b = mul2(make_float2(d[q].z, d[q].w), x[q][i].b());
+                            const float2 e = ptx::fma2(make_float2(at.x, at.y), make_float2(a[i], a[i]), middle);
+                            const float2 b = mul2(make_float2(at.z, at.w), x[side][q][i].b());
                             float2 hh;
                             hh.x = fmaf(tc::exp2_approx(e.x), h[i], b.x);
                             hh.y = fmaf(tc::exp2_approx(e.y), hh.x, b.y);
                             h[i] = hh.y;
-                            if (!ends.value) sum[q] = i == 0 ? mul2(hh, x[q][i].c()) : ptx::fma2(hh, x[q][i].c(), sum[q]);
+                            if (!ends.value) sum[q] = i == 0 ? mul2(hh, x[side][q][i].c()) : ptx::fma2(hh, x[side][q][i].c(), sum[q]);
                         }
                     }
                     if (!ends.value)
 #pragma unroll
                         for (int q = 0; q < B; ++q) y[q * CH] = sum[q];
                     y += B * CH;
+                };
+                load(0);
+                // (two rounds at a time, so that operands stay in the registers they were loaded to; a chunk has whole ones)
+                static_assert(T % (4 * B) == 0);
+#pragma unroll 1
+                for (int t = 0; t < count; t += 4 * B) {
+                    load(1);
+                    step(0);
+                    load(0);
+                    step(1);
                 }
                 steps += step_sum.x + step_sum.y;
                 __syncthreads();
@@ -248,6 +253,7 @@ scan_kernel(const Scan p, int group_blocks, int parts)
         const IO *bc = static_cast<const IO *>(s < N ? p.b : p.c) + (int64_t)(first + b0) * bcs + group * N + s % N;
         int asked = 0;               // tokens so far
         typename Sh::Raw *to = sm.raw;
+        bool gate = p.z && parts == 1;  // (z is wanted where outputs are made)
         auto ask = [&] {             // a chunk's rows
 #pragma unroll
             for (int i = 0; i < (T + kStep - 1) / kStep; ++i) {
@@ -255,7 +261,7 @@ scan_kernel(const Scan p, int group_blocks, int parts)
                 if (t < T && asked + t < len && c < held) {
                     ptx::cp_async16(&to->x[t][c], x + i * kStep * p.xs, true);
                     ptx::cp_async16(&to->dt[t][c], dt + i * kStep * p.dts, true);
-                    if (p.z) ptx::cp_async16(&to->z[t][c], z + i * kStep * p.zs, true);
+                    if (gate) ptx::cp_async16(&to->z[t][c], z + i * kStep * p.zs, true);
                 }
             }
 #pragma unroll
@@ -336,6 +342,7 @@ scan_kernel(const Scan p, int group_blocks, int parts)
             const int64_t back = asked;
             x -= back * p.xs; dt -= back * p.dts; z -= back * p.zs; bc -= back * bcs;
             asked = made = 0;
+            gate = p.z;
             to = sm.raw;
             from = sm.raw;
         }
@@ -426,9 +433,9 @@ double scan_ns(const Scan &p, int channels, int chunk, size_t smem, double token
 }
 
 // The form that takes the least by that.  16 states in bf16, us with the form that is chosen and without parts: 16,384
-// tokens of 1,024 channels 212 (32 channels a CTA, eight parts) and 263 (8 channels), of 512 135 (16, eight) and 271; 4,096
-// tokens of 256 31 (8, four) and 66, of 64 18 (8, eight) and 66, of 2,048 96 (16 channels; in parts 107), of 4,096 140
-// (32 channels; 16 take 151, parts more); four sequences of 2,048 tokens and 256 channels 33 (32, eight) and 36.
+// tokens of 1,024 channels 197 (32 channels a CTA, eight parts) and 276 (8 channels), of 512 128 (16, eight) and 276; 4,096
+// tokens of 256 31 (8, four) and 70, of 64 18 (8, eight) and 69, of 2,048 94 (16 channels; in parts 107), of 4,096 135
+// (32 channels; 16 take 150, parts more); four sequences of 2,048 tokens and 256 channels 32 (32, eight) and 36.
 template <typename IO, int N>
 struct Chooser {
     const Scan &p;
