@@ -16,7 +16,7 @@
 // they are stored.  What the steps before this form measured, 4,096 tokens of 4,096 channels, 16 states, bf16: a chunk
 // loaded through registers one ahead 283 us; asynchronous copies four ahead 188; the states of a channel over four warps
 // instead of four lanes 163; two rounds of the loop at a time, so that operands stay in the registers that they were
-// loaded to, 145 to 135.  INSTR
+// loaded to, 145 to 135: 33 ns a token, 156 instructions of a warp (39 a scheduler) in 63 cycles.
 #include "latent_ptx.cuh"
 #include "layer.cuh"
 #include "tc_common.cuh"
