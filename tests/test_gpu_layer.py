@@ -459,3 +459,75 @@ def test_weights_written_by_the_call_before(m):
         y.zero_()
         graph.replay()
         assert torch.equal(w, want[0]) and torch.equal(y, want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_32_bits(dtype):
+    """Rows and entries of pools more than 2^32 elements apart: the bits of the same calls on compact tensors."""
+    dt, rows, stride = DT[dtype], 65, (1 << 26) + 64
+    g = gen(16)
+    try:
+        wide = torch.empty(rows * stride, dtype=dt, device="cuda")
+    except torch.cuda.OutOfMemoryError:
+        pytest.skip("not enough memory")
+
+    def far(t, column):
+        view = wide.as_strided((t.shape[0], t.shape[1]), (stride, 1), column)
+        view.copy_(t)
+        return view
+
+    x, w, r = normal(g, rows, 64, dtype=dt), normal(g, 40, 64, dtype=dt, scale=0.125), normal(g, rows, 40, dtype=dt)
+    out = torch.zeros(rows, 40, dtype=dt, device="cuda")
+    for m in (4, rows):  # (few rows, many)
+        y = far(out[:m], 1024)
+        kda.linear(far(x[:m], 0), far(w, 128), residual=far(r[:m], 256), out=y)
+        assert torch.equal(y, kda.linear(x[:m], w, residual=r[:m]))
+    conv_w, cu = normal(g, 64, 4, dtype=dt), ints(0, 20, 21, rows)
+    z, b, c = normal(g, rows, 64, dtype=dt), normal(g, rows, 8, dtype=dt), normal(g, rows, 8, dtype=dt)
+    dts = normal(g, rows, 64, dtype=dt)
+    A = -torch.rand(64, 8, generator=g, device="cuda") - 0.1
+    for offsets, step in ((cu, False), (None, True)):
+        y = far(torch.zeros_like(x), 1024)
+        if step:
+            kda.short_conv_step(far(x, 0), conv_w, torch.zeros(rows, 3, 64, dtype=dt, device="cuda"), out=y)
+            want = kda.short_conv_step(x, conv_w, torch.zeros(rows, 3, 64, dtype=dt, device="cuda"))
+        else:
+            kda.short_conv(far(x, 0), conv_w, None, offsets, out=y)
+            want = kda.short_conv(x, conv_w, None, offsets)[0]
+        assert torch.equal(y, want)
+        y = far(torch.zeros_like(x), 1024)
+        f = [far(t, 128 * i) for i, t in enumerate((x, dts, b, c, z))]
+        if step:
+            kda.selective_scan_step(f[0], f[1], A, f[2], f[3], torch.zeros(rows, 64, 8, device="cuda"), z=f[4], out=y)
+            want = kda.selective_scan_step(x, dts, A, b, c, torch.zeros(rows, 64, 8, device="cuda"), z=z)
+        else:
+            kda.selective_scan(f[0], f[1], A, f[2], f[3], None, f[4], None, offsets, out=y)
+            want = kda.selective_scan(x, dts, A, b, c, None, z, None, offsets)[0]
+        assert torch.equal(y, want)
+    del wide, y, f
+    # the last entries of pools
+    n, ch = 9000, 4096 * 8
+    x, dts = normal(g, 2, ch, dtype=dt), normal(g, 2, ch, dtype=dt)
+    slots = ints(n - 1, 7)
+    pool, few = torch.empty(n, ch, 8, device="cuda"), torch.zeros(2, ch, 8, device="cuda")
+    pool[n - 1] = pool[7] = 0
+    A = -torch.rand(ch, 8, generator=g, device="cuda") - 0.1
+    for _ in range(2):
+        got = kda.selective_scan_step(x, dts, A, b[:2], c[:2], pool, slots=slots)
+        assert torch.equal(got, kda.selective_scan_step(x, dts, A, b[:2], c[:2], few))
+        kda.selective_scan(x, dts, A, b[:2], c[:2], None, None, None, ints(0, 1, 2), pool, init_slots=slots, final_state=pool,
+                           final_slots=slots)
+        kda.selective_scan(x, dts, A, b[:2], c[:2], None, None, None, ints(0, 1, 2), few, final_state=few)
+        assert torch.equal(pool[n - 1], few[0]) and torch.equal(pool[7], few[1])
+    del pool, few
+    n = 24000
+    conv_w = normal(g, ch, 4, dtype=dt)
+    slots = ints(n - 1, 7)
+    pool, few = torch.empty(n, 3, ch, dtype=dt, device="cuda"), torch.zeros(2, 3, ch, dtype=dt, device="cuda")
+    pool[n - 1] = pool[7] = 0
+    for _ in range(2):
+        got = kda.short_conv_step(x, conv_w, pool, slots=slots)
+        assert torch.equal(got, kda.short_conv_step(x, conv_w, few))
+        kda.short_conv(x, conv_w, None, ints(0, 1, 2), pool, init_slots=slots, final_state=pool, final_slots=slots)
+        kda.short_conv(x, conv_w, None, ints(0, 1, 2), few, final_state=few)
+        assert torch.equal(pool[n - 1], few[0]) and torch.equal(pool[7], few[1])
