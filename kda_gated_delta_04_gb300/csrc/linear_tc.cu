@@ -628,6 +628,8 @@ cudaError_t launch_linear_tc(const Linear &p)
     const int slack = (kM - pl.box) * 128, stage = panel * pl.panels;
     pl.stages = (kSmem - kHead - slack) / stage;
     if (pl.stages > kMaxStages) pl.stages = kMaxStages;
+    // (Over half of an SM's shared memory, whatever the plan: were two calls' CTAs on an SM, one could wait there for
+    // tensor memory that the other holds while it waits for its own partner, and so on around.)
     pl.smem = kHead + pl.stages * stage + slack;
     if (at.split > 1 && pl.smem < kHead + pl.width * kM * 4) pl.smem = kHead + pl.width * kM * 4;  // the parts
     const size_t eo = f32 ? 4 : 2;

@@ -531,3 +531,32 @@ def test_offsets_past_32_bits(dtype):
         kda.short_conv(x, conv_w, None, ints(0, 1, 2), pool, init_slots=slots, final_state=pool, final_slots=slots)
         kda.short_conv(x, conv_w, None, ints(0, 1, 2), few, final_state=few)
         assert torch.equal(pool[n - 1], few[0]) and torch.equal(pool[7], few[1])
+
+
+def test_calls_on_streams_at_once():
+    """Calls of all forms (pairs, split inputs, single CTAs, few rows, fp32) on four streams at once, and the convolution
+    and the scan in parts beside them: as one after the other."""
+    g = gen(17)
+    w = normal(g, 1024, 1024, scale=1 / 32)
+    xs = [normal(g, m, 1024) for m in (4, 64, 128, 300, 1500)]
+    wf, xf = w[:100].float(), xs[2].float()
+    cw, A = normal(g, 1024, 4), -torch.rand(1024, 16, generator=g, device="cuda") - 0.1
+    bc = normal(g, 1500, 32)
+
+    def run(stream):
+        out = [kda.linear(x, w, activation="silu", stream=stream) for x in xs]
+        out += [kda.linear(xs[3], w, out_dtype=torch.float32, stream=stream), kda.linear(xf, wf, stream=stream)]
+        out += [kda.short_conv(xs[4], cw, stream=stream)[0]]
+        return out + [kda.selective_scan(xs[4], xs[4], A, bc[:, :16], bc[:, 16:], stream=stream)[0]]
+
+    want = run(None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(run(s))
+    torch.cuda.synchronize()
+    for out in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
